@@ -20,6 +20,8 @@ __all__ = [
     "expert_grouped", "ExpertCall", "STATIC_SCRATCH_BYTES", "test_block_isum", "ERR_BITS", "F_PDL",
     "LayerCall", "layer_sync_ints", "router_topk", "combine", "F_SYNC_PAIR", "F_SYNC_ODD", "F_TEST_EXPIRE",
     "qsa_block_scores", "grouped_fused_sync_ints", "stage_blobs",
+    "kv8_block_bytes", "kv8_pool", "kv8_write", "kv8_read", "kv8_attention", "kv8_attention_workspace",
+    "add_rms_norm_q8_1", "dequantize_q8_1",
 ]
 
 Q8_0, Q4B, NL4, CB2, CB3, CB3X, CB2X = 1, 2, 3, 4, 5, 6, 7
@@ -29,7 +31,7 @@ F_SYNC_ODD = 4   # ... and this call uses the second half
 F_TEST_EXPIRE = 8  # test hook: the down staging waits for a flag no call writes (timeout path)
 STATIC_SCRATCH_BYTES = 4 << 20
 ERR_BITS = {1: "NGROUPS", 2: "EXPERT", 4: "START", 8: "ENTRY", 16: "ALIGN", 32: "CODEBOOK",
-            64: "TIMEOUT", 128: "ROUTE"}
+            64: "TIMEOUT", 128: "ROUTE", 256: "PAGE", 512: "LEN"}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmoe_grouped.so")
@@ -71,6 +73,41 @@ class LayerCallC(ctypes.Structure):
     ]
 
 
+class KV8CacheC(ctypes.Structure):
+    _fields_ = [
+        ("pool", _P), ("n_pages", _I64), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32), ("page_table", _P), ("table_stride", _I64),
+        ("max_pages", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+    ]
+
+
+class KV8RowsC(ctypes.Structure):
+    _fields_ = [
+        ("k", _P), ("v", _P), ("type", ctypes.c_int32), ("n_tokens", _I64),
+        ("k_token_stride", _I64), ("k_head_stride", _I64), ("v_token_stride", _I64), ("v_head_stride", _I64),
+    ]
+
+
+class KV8AttentionC(ctypes.Structure):
+    _fields_ = [
+        ("cache", KV8CacheC), ("q", _P), ("type", ctypes.c_int32), ("T", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32), ("q_seq_stride", _I64), ("q_token_stride", _I64), ("q_head_stride", _I64),
+        ("lens", _P), ("tree", _P), ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("out", _P),
+        ("lse", _P), ("workspace", _P), ("workspace_bytes", _I64), ("err", _P),
+    ]
+
+
+class NormCallC(ctypes.Structure):
+    _fields_ = [
+        ("x", _P), ("residual", _P), ("weight", _P), ("sum", _P), ("y", _P), ("xq", _P),
+        ("type", ctypes.c_int32), ("w_type", ctypes.c_int32), ("rows", _I64), ("x_stride", _I64),
+        ("residual_stride", _I64), ("cols", ctypes.c_int32), ("eps", ctypes.c_float),
+    ]
+
+
+_ELEM = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
 def lib():
     """Load the CUDA library (raises if it has not been built)."""
     global _LIB
@@ -102,10 +139,20 @@ def lib():
         L.moe_grouped_fused_sync_ints.argtypes = [_I, _I, _I]
         L.moe_grouped_fused_sync_ints.restype = _I64
         L.moe_stage_blobs.argtypes = [_P, _P, _P, _I, _P]
+        L.moe_kv8_block_bytes.argtypes = [_I]
+        L.moe_kv8_block_bytes.restype = _I64
+        L.moe_kv8_write.argtypes = [_P, _P, _P, _P, _P, _P]
+        L.moe_kv8_read.argtypes = [_P, _P, _P, _P, _P, _P]
+        L.moe_kv8_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
+        L.moe_kv8_attention_workspace_bytes.restype = _I64
+        L.moe_kv8_attention.argtypes = [_P, _P]
+        L.moe_add_rms_norm_q8_1.argtypes = [_P, _P]
+        L.moe_dequantize_q8_1.argtypes = [_P, _I64, _I64, _P, _I, _P]
         for f in ("moe_quantize_q8_1", "moe_route_group", "moe_grouped_gu", "moe_swiglu_q8_1",
                   "moe_grouped_down", "moe_expert_grouped", "moe_expert_grouped_static", "moe_test_block_isum",
                   "moe_transcode_cb", "moe_expert_layer", "moe_router_topk", "moe_combine",
-                  "moe_qsa_block_scores", "moe_expert_grouped_fused", "moe_stage_blobs"):
+                  "moe_qsa_block_scores", "moe_expert_grouped_fused", "moe_stage_blobs", "moe_kv8_write",
+                  "moe_kv8_read", "moe_kv8_attention", "moe_add_rms_norm_q8_1", "moe_dequantize_q8_1"):
             getattr(L, f).restype = _I
         _LIB = L
     return _LIB
@@ -284,6 +331,205 @@ def qsa_block_scores(q, keys, key_scale, scores=None, stream=None):
         scores = torch.empty((T, nb), dtype=torch.float32, device=q.device)
     _check(lib().moe_qsa_block_scores(_dp(q), T, _dp(keys), _dp(key_scale), nb, _dp(scores), _stream(stream)))
     return scores
+
+
+# ---------------------------------------------------------------- the attention side (moe_kv8.h)
+# These calls return tensors that they allocate when none are given, so a small call's time is the
+# binding's: it passes plain integers and checks only what the library cannot see (devices, types,
+# shapes and strides of tensors). Everything else is checked by the library.
+
+def _elem(t):
+    try:
+        return _ELEM[t.dtype]
+    except KeyError:
+        raise MoeError(f"float32, float16 or bfloat16 expected, got {t.dtype}") from None
+
+
+def _ptr(t):
+    if t is None:
+        return 0
+    if not t.is_cuda:
+        raise MoeError("device tensor expected")
+    return t.data_ptr()
+
+
+def _ints(t, name, numel):
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != numel:
+        raise MoeError(f"{name}: a contiguous int32 tensor of {numel} elements expected")
+    return _ptr(t)
+
+
+def _err(err):
+    return None if err is None else _ints(err, "err", err.numel())
+
+
+def _raw_stream(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _on(stream, *tensors):
+    """Tensors of the caching allocator that are used on another stream than their own."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _kv8_cache(pool, page_table):
+    if pool.dtype != torch.uint8 or pool.dim() != 4 or not pool.is_contiguous():
+        raise MoeError("pool: contiguous uint8 [pages, kv heads, page tokens / 32, block bytes] expected")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise MoeError("page_table: int32 [sequences, pages] with contiguous rows expected")
+    n_pages, hkv, nb, rec = pool.shape
+    if rec < 16 or (rec - 16) % 64:
+        raise MoeError(f"pool: records of {rec} bytes are of no head size")
+    return KV8CacheC(_ptr(pool), n_pages, hkv, (rec - 16) // 64, nb * 32, _ptr(page_table),
+                     page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1], page_table.shape[1],
+                     page_table.shape[0])
+
+
+def kv8_block_bytes(head_dim: int) -> int:
+    """Bytes of one record of the cache: 32 tokens of one key/value head."""
+    return int(lib().moe_kv8_block_bytes(head_dim))
+
+
+def kv8_pool(n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda") -> torch.Tensor:
+    """A zeroed cache pool: uint8 [n_pages, n_kv_heads, page_tokens / 32, block bytes]."""
+    rec = kv8_block_bytes(head_dim)
+    if not rec or page_tokens <= 0 or page_tokens % 32:
+        raise MoeError("head_dim: a multiple of 32 up to 256; page_tokens: a multiple of 32")
+    return torch.zeros((n_pages, n_kv_heads, page_tokens // 32, rec), dtype=torch.uint8, device=device)
+
+
+def _kv8_rows(c, k, v):
+    if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype or k.shape[1] != c.n_kv_heads or \
+            k.shape[2] != c.head_dim or k.stride(2) != 1 or v.stride(2) != 1:
+        raise MoeError(f"k, v: [tokens, {c.n_kv_heads}, {c.head_dim}] of one type, contiguous in the last dimension, expected")
+    return KV8RowsC(_ptr(k), _ptr(v), _elem(k), k.shape[0], k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+
+
+def kv8_write(k, v, pool, page_table, cu_tokens, start, err=None, stream=None):
+    """Quantise rows k, v [tokens, kv heads, head_dim] into the cache: rows cu_tokens[b] ..
+    cu_tokens[b+1] become positions start[b] .. of sequence b, which ends with them. cu_tokens int32
+    [sequences + 1], start int32 [sequences], page_table int32 [sequences, pages]; all on the device."""
+    c = _kv8_cache(pool, page_table)
+    r = _kv8_rows(c, k, v)
+    _check(lib().moe_kv8_write(ctypes.byref(c), ctypes.byref(r), _ints(cu_tokens, "cu_tokens", c.n_seqs + 1),
+                               _ints(start, "start", c.n_seqs), _err(err), _raw_stream(stream)))
+    _on(stream, k, v, pool, page_table, cu_tokens, start, err)
+
+
+def kv8_read(pool, page_table, cu_tokens, start, n_tokens, dtype=torch.bfloat16, k=None, v=None, err=None,
+             stream=None):
+    """Read positions start[b] .. of each sequence back as rows cu_tokens[b] .. cu_tokens[b+1] of
+    k, v [n_tokens, kv heads, head_dim] (allocated as `dtype` when not given). n_tokens is
+    cu_tokens' last value. Rows of a sequence or block that is refused (err) are left as they were."""
+    c = _kv8_cache(pool, page_table)
+    shape = (n_tokens, c.n_kv_heads, c.head_dim)
+    if k is None or v is None:
+        with torch.cuda.stream(stream):
+            k = torch.empty(shape, dtype=dtype, device=pool.device) if k is None else k
+            v = torch.empty(shape, dtype=k.dtype, device=pool.device) if v is None else v
+    if k.shape[0] != n_tokens:
+        raise MoeError(f"k, v: {n_tokens} rows expected")
+    r = _kv8_rows(c, k, v)
+    _check(lib().moe_kv8_read(ctypes.byref(c), ctypes.byref(r), _ints(cu_tokens, "cu_tokens", c.n_seqs + 1),
+                              _ints(start, "start", c.n_seqs), _err(err), _raw_stream(stream)))
+    _on(stream, k, v, pool, page_table, cu_tokens, start, err)
+    return k, v
+
+
+def kv8_attention_workspace(n_seqs: int, T: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                            device="cuda") -> torch.Tensor:
+    """A zeroed workspace for kv8_attention calls of these sizes or smaller ones, to be kept between
+    calls (one for each stream that calls run on at the same time)."""
+    n = int(lib().moe_kv8_attention_workspace_bytes(n_seqs, T, n_heads, n_kv_heads, head_dim))
+    if not n:
+        raise MoeError(strerror(-3))
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def kv8_attention(q, pool, page_table, lens, scale=None, window=0, tree=None, workspace=None, out=None, lse=None,
+                  with_lse=False, err=None, stream=None):
+    """Attention of q [sequences, T, heads, head_dim] (the last T of lens[b] cached positions; T <= 32)
+    over the cache. window: a query sees that many positions up to its own (0: all); tree: int32
+    [sequences, T], bit j of tree[b, t] lets query t see window token j (else: causal). Returns out
+    [sequences, T, heads, head_dim] of q's type, and with_lse (or a given lse) also the log of the
+    softmax sums, fp32 [sequences, T, heads]; a query that sees nothing gives zeros and -inf."""
+    c = _kv8_cache(pool, page_table)
+    if q.dim() != 4 or q.shape[0] != c.n_seqs or q.shape[3] != c.head_dim or q.stride(3) != 1:
+        raise MoeError(f"q: [{c.n_seqs}, T, heads, {c.head_dim}], contiguous in the last dimension, expected")
+    B, T, hq, D = q.shape
+    if workspace is None or out is None or (with_lse and lse is None):
+        with torch.cuda.stream(stream):
+            if workspace is None:
+                workspace = kv8_attention_workspace(B, T, hq, c.n_kv_heads, D, q.device)
+            if out is None:
+                out = torch.empty((B, T, hq, D), dtype=q.dtype, device=q.device)
+            if with_lse and lse is None:
+                lse = torch.empty((B, T, hq), dtype=torch.float32, device=q.device)
+    if out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        raise MoeError("out: contiguous, of q's shape and type, expected")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, T, hq) or not lse.is_contiguous()):
+        raise MoeError("lse: contiguous float32 [sequences, T, heads] expected")
+    if not workspace.is_contiguous():
+        raise MoeError("workspace: a contiguous tensor expected")
+    a = KV8AttentionC(c, _ptr(q), _elem(q), T, hq, q.stride(0), q.stride(1), q.stride(2),
+                      _ints(lens, "lens", B), None if tree is None else _ints(tree, "tree", B * T), window,
+                      D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse) or None, _ptr(workspace),
+                      workspace.numel() * workspace.element_size(), _err(err))
+    _check(lib().moe_kv8_attention(ctypes.byref(a), _raw_stream(stream)))
+    _on(stream, q, pool, page_table, lens, tree, out, lse, workspace, err)
+    return (out, lse) if lse is not None else out
+
+
+def add_rms_norm_q8_1(x, weight, residual=None, eps=1e-6, sum_out=None, y=None, xq=None, with_y=False, stream=None):
+    """h = x + residual, y = h * (1 / sqrt(mean(h^2) + eps)) * weight, and y's q8_1 rows, in one pass.
+    x, residual [rows, cols] of one type, weight [cols]. Returns (sum, y, xq): h in x's type (None
+    without a residual, unless sum_out is given; sum_out may be the residual itself), y in x's type
+    (with_y or a given y, else None), xq uint8 [rows, cols/32, 36]."""
+    if x.dim() != 2 or x.stride(1) != 1 or weight.shape != x.shape[1:] or not weight.is_contiguous():
+        raise MoeError("x: [rows, cols] with contiguous rows, weight: contiguous [cols], expected")
+    rows, cols = x.shape
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or residual.stride(1) != 1):
+        raise MoeError("residual: x's shape and type, with contiguous rows, expected")
+    with_sum = residual is not None and sum_out is None
+    if with_sum or (with_y and y is None) or xq is None:
+        with torch.cuda.stream(stream):
+            if with_sum:
+                sum_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+            if with_y and y is None:
+                y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+            if xq is None:
+                xq = torch.empty((rows, cols // 32, 36), dtype=torch.uint8, device=x.device)
+    for t in (sum_out, y):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or not t.is_contiguous()):
+            raise MoeError("sum_out, y: contiguous, of x's shape and type, expected")
+    if xq.dtype != torch.uint8 or xq.shape != (rows, cols // 32, 36) or not xq.is_contiguous():
+        raise MoeError("xq: contiguous uint8 [rows, cols/32, 36] expected")
+    c = NormCallC(_ptr(x), _ptr(residual) or None, _ptr(weight), _ptr(sum_out) or None, _ptr(y) or None,
+                  _ptr(xq) or None, _elem(x), _elem(weight), rows, x.stride(0),
+                  0 if residual is None else residual.stride(0), cols, eps)
+    if rows:
+        _check(lib().moe_add_rms_norm_q8_1(ctypes.byref(c), _raw_stream(stream)))
+        _on(stream, x, residual, weight, sum_out, y, xq)
+    return sum_out, y, xq
+
+
+def dequantize_q8_1(xq, dtype=torch.float32, out=None, stream=None):
+    """The values that q8_1 rows [rows, cols/32, 36] stand for, [rows, cols] of `dtype`."""
+    if xq.dtype != torch.uint8 or xq.dim() != 3 or xq.shape[2] != 36 or not xq.is_contiguous():
+        raise MoeError("xq: contiguous uint8 [rows, cols/32, 36] expected")
+    rows, cols = xq.shape[0], xq.shape[1] * 32
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = torch.empty((rows, cols), dtype=dtype, device=xq.device)
+    if out.shape != (rows, cols) or not out.is_contiguous():
+        raise MoeError("out: contiguous [rows, cols] expected")
+    if rows:
+        _check(lib().moe_dequantize_q8_1(_ptr(xq), rows, cols, _ptr(out), _elem(out), _raw_stream(stream)))
+        _on(stream, xq, out)
+    return out
 
 
 def expert_grouped(*args, stream=None, **kw):

@@ -1,0 +1,163 @@
+// kv8.cuh - the 8-bit key/value cache's record layout and the dense rows' element types, shared by
+// the cache, attention and norm kernels. Internal header (not part of the C ABI).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "moe_kv8.h"
+
+namespace moe {
+
+constexpr int kKvBlock = 32;                  // tokens of a record
+constexpr int kKvHead = 16;                   // record header: f32 k_scale, f32 v_scale, 8 unused
+constexpr float kKvTiny = 7.888609052210118e-31f;  // 2^-100: a block below it is stored as zeros
+
+__host__ __device__ constexpr int kv8_record_bytes(int D) { return kKvHead + 2 * kKvBlock * D; }
+
+// byte of the key code (token t, dim d) and of the value code in a record
+__device__ __forceinline__ int kv8_k_at(int D, int t, int d) {
+    return kKvHead + ((((t >> 1) & 3) * (D >> 5) + (d >> 5)) * 8 + 2 * (t >> 3) + (t & 1)) * 32 + (d & 31);
+}
+__device__ __forceinline__ int kv8_v_at(int D, int t, int d) { return kKvHead + kKvBlock * D + d * kKvBlock + t; }
+
+template <int TYPE>
+struct Elem;
+template <>
+struct Elem<MOE_F32> {
+    using T = float;
+    static __device__ __forceinline__ float get(float v) { return v; }
+    static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <>
+struct Elem<MOE_F16> {
+    using T = __half;
+    static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+};
+template <>
+struct Elem<MOE_BF16> {
+    using T = __nv_bfloat16;
+    static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+
+// Eight consecutive elements; vec: p is 16-byte aligned.
+template <int TYPE>
+__device__ __forceinline__ void load8(const typename Elem<TYPE>::T* p, bool vec, float (&v)[8]) {
+    using E = Elem<TYPE>;
+    constexpr int kB = 8 * sizeof(typename E::T);
+    union {
+        typename E::T e[8];
+        uint4 w[kB / 16];
+    } u;
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < kB / 16; ++i) u.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u.e[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = E::get(u.e[i]);
+}
+
+template <int TYPE>
+__device__ __forceinline__ void store8(typename Elem<TYPE>::T* p, bool vec, const float (&v)[8]) {
+    using E = Elem<TYPE>;
+    constexpr int kB = 8 * sizeof(typename E::T);
+    union U {
+        typename E::T e[8];
+        uint4 w[kB / 16];
+        __device__ U() {}
+    } u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u.e[i] = E::put(v[i]);
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < kB / 16; ++i) reinterpret_cast<uint4*>(p)[i] = u.w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = u.e[i];
+    }
+}
+
+// Device copy of moe_kv8_cache.
+struct KvCache {
+    uint8_t* pool;
+    const int32_t* table;
+    int64_t table_stride;
+    int64_t n_pages;
+    int n_kv, D, page_blocks, max_pages, n_seqs, rec;
+};
+
+// The record of (sequence b, block j, head h), or nullptr (*err gets MOE_ERR_PAGE).
+__device__ __forceinline__ uint8_t* kv8_record(const KvCache& c, int b, int j, int h, int32_t* err) {
+    const int pi = j / c.page_blocks, pb = j - pi * c.page_blocks;
+    if (pi < c.max_pages) {
+        const int32_t pg = __ldg(c.table + b * c.table_stride + pi);
+        if (pg >= 0 && pg < c.n_pages)
+            return c.pool + ((static_cast<int64_t>(pg) * c.n_kv + h) * c.page_blocks + pb) * c.rec;
+    }
+    set_err(err, MOE_ERR_PAGE);
+    return nullptr;
+}
+
+// The blocks that ragged rows touch, as a flat list with gaps: sequence b's first block has index
+// floor(cu[b] / 32) + 2 b. A sequence of n tokens touches at most floor((n + 30) / 32) + 1 blocks,
+// which is no more than the distance to the next sequence's index, and all indices lie below
+// floor(n_tokens / 32) + 2 n_seqs.
+__host__ __device__ inline int64_t kv8_slots(int64_t n_tokens, int n_seqs) { return n_tokens / 32 + 2LL * n_seqs; }
+
+struct KvSlot {
+    int b;             // sequence, -1: none
+    int blk;           // block of the sequence
+    int t0, t1;        // the block's tokens in the range: t0 <= t < t1
+    int64_t row;       // dense row of token t: row + t
+};
+
+// Find slot `s`. All threads of a warp call it with the same s; the sequence is found by a 32-way
+// search over its lanes (one round of loads per factor of 32 in n_seqs).
+__device__ __forceinline__ KvSlot kv8_slot(int64_t s, const int32_t* __restrict__ cu, const int32_t* __restrict__ start,
+                                           int n_seqs, int64_t n_tokens, int32_t* err) {
+    KvSlot r;
+    r.b = -1;
+    r.blk = r.t0 = r.t1 = 0;
+    r.row = 0;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = n_seqs;  // the last b in [lo, lo + n) whose first index is <= s
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int i = lo + lane * step;
+        const bool ok = lane * step < n && (static_cast<int64_t>(__ldg(cu + i)) >> 5) + 2LL * i <= s;
+        const unsigned m = __ballot_sync(0xffffffffu, ok);
+        const int k = m ? 31 - __clz(m) : 0;
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    const int64_t c0 = __ldg(cu + lo), c1 = __ldg(cu + lo + 1), p0 = __ldg(start + lo);
+    if (c0 < 0 || c1 < c0 || c1 > n_tokens || p0 < 0 || p0 + (c1 - c0) > 0x7fffffff) {
+        set_err(err, MOE_ERR_LEN);
+        return r;
+    }
+    const int64_t k = s - ((c0 >> 5) + 2LL * lo);
+    const int64_t blk = (p0 >> 5) + k, p1 = p0 + (c1 - c0);
+    if (k < 0 || c1 == c0 || blk * 32 >= p1) return r;
+    r.b = lo;
+    r.blk = static_cast<int>(blk);
+    r.t0 = static_cast<int>(p0 > blk * 32 ? p0 - blk * 32 : 0);
+    r.t1 = static_cast<int>(p1 < blk * 32 + 32 ? p1 - blk * 32 : 32);
+    r.row = c0 + blk * 32 - p0;
+    return r;
+}
+
+// Dense rows of one of keys or values.
+template <typename T>
+struct KvRows {
+    T* p;
+    int64_t ts, hs;
+    bool vec;  // 16-byte vectors
+};
+
+}  // namespace moe

@@ -1,0 +1,153 @@
+// rms_norm_q8_1.cu - residual addition, root-mean-square norm and the experts' q8_1 rows in one
+// pass, and reading q8_1 rows back.
+//
+//   h = x + residual;  y = h * (1 / sqrt(mean(h^2) + eps)) * weight;  xq = q8_1(y)
+//
+// One CTA per row; a thread holds eight consecutive values of up to four chunks in registers, so
+// the row is read once and the outputs may overwrite the inputs. A q8_1 block of 32 values is four
+// neighbouring threads. The sum of squares is fp32: per thread, then over the warp's lanes, then
+// over the warps in order.
+#include "internal.h"
+#include "kv8.cuh"
+#include "kv8_api.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxChunks = 4;
+
+// the q8_1 block of four neighbouring lanes' values (32 in all): the lane's codes and header word
+__device__ __forceinline__ void quad_q8_1(const float (&y)[8], uint32_t (&code)[2], uint32_t& hdr) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float v = fabsf(y[e]);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(v));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        const float v = __shfl_xor_sync(0xffffffffu, amax, o);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(v));
+    }
+    const float d = __fdiv_rn(amax, 127.0f);
+    int S = 0;
+    code[0] = code[1] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int q = d == 0.0f ? 0 : static_cast<int>(roundf(__fdiv_rn(y[e], d)));
+        S += q;
+        code[e >> 2] |= static_cast<uint32_t>(q & 255) << (8 * (e & 3));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+    hdr = __half_as_ushort(__float2half_rn(d)) |
+          static_cast<uint32_t>(__half_as_ushort(__float2half_rn(__fmul_rn(d, static_cast<float>(S))))) << 16;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void weight8(const void* w, int w_type, int col, float (&v)[8]) {
+    if (w_type == MOE_F32) load8<MOE_F32>(static_cast<const float*>(w) + col, true, v);
+    else if (w_type == MOE_F16) load8<MOE_F16>(static_cast<const __half*>(w) + col, true, v);
+    else load8<MOE_BF16>(static_cast<const __nv_bfloat16*>(w) + col, true, v);
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(1024) add_rms_norm_q8_1_kernel(moe_norm_call c) {
+    using E = Elem<TYPE>;
+    using T = typename E::T;
+    __shared__ float red[32];
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const T* x = static_cast<const T*>(c.x) + row * c.x_stride;
+    const T* r = c.residual ? static_cast<const T*>(c.residual) + row * c.residual_stride : nullptr;
+    float h[kMaxChunks][8], ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMaxChunks; ++k) {
+        const int col = (k * blockDim.x + threadIdx.x) * 8;
+        if (col >= c.cols) continue;
+        load8<TYPE>(x + col, true, h[k]);
+        if (r) {
+            float v[8];
+            load8<TYPE>(r + col, true, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[k][e] += v[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(h[k][e], h[k][e], ss);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (lane == 0) red[wid] = ss;
+    __syncthreads();  // also: every thread's reads of the row lie before the writes below
+    ss = 0.0f;
+    for (int w = 0; w < nw; ++w) ss += red[w];
+    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(c.cols)) + c.eps));
+#pragma unroll
+    for (int k = 0; k < kMaxChunks; ++k) {
+        // a warp's columns are whole q8_1 blocks, and lanes past the row carry zeros into its shuffles
+        const int col = (k * blockDim.x + threadIdx.x) * 8;
+        const bool in = col < c.cols;
+        if (!__any_sync(0xffffffffu, in)) continue;
+        float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (in) {
+            if (c.sum) store8<TYPE>(static_cast<T*>(c.sum) + row * c.cols + col, true, h[k]);
+            weight8<TYPE>(c.weight, c.w_type, col, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = h[k][e] * inv * y[e];
+            if (c.y) store8<TYPE>(static_cast<T*>(c.y) + row * c.cols + col, true, y);
+        }
+        if (c.xq) {
+            uint32_t code[2], hdr;
+            quad_q8_1(y, code, hdr);
+            if (in) {
+                uint32_t* blk = reinterpret_cast<uint32_t*>(c.xq + row * (c.cols / 32) + col / 32);
+                const int part = (col >> 3) & 3;
+                blk[1 + 2 * part] = code[0];
+                blk[2 + 2 * part] = code[1];
+                if (part == 0) blk[0] = hdr;
+            }
+        }
+    }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(256) dequantize_q8_1_kernel(const moe_q8_1* __restrict__ xq, int64_t n_blocks,
+                                                              typename Elem<TYPE>::T* __restrict__ out) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n_blocks * 4) return;
+    const uint32_t* blk = reinterpret_cast<const uint32_t*>(xq + (i >> 2));
+    const int part = static_cast<int>(i & 3);
+    const float d = h2f_bits(__ldg(blk));
+    const uint32_t w[2] = {__ldg(blk + 1 + 2 * part), __ldg(blk + 2 + 2 * part)};
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = d * static_cast<float>(static_cast<int8_t>(w[e >> 2] >> (8 * (e & 3))));
+    store8<TYPE>(out + i * 8, true, v);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rms_norm_q8_1(const moe_norm_call& c, cudaStream_t st) {
+    if (c.rows == 0) return cudaSuccess;
+    int threads = (c.cols / 8 + 31) / 32 * 32;
+    if (threads > 1024) threads = 1024;
+    const unsigned grid = static_cast<unsigned>(c.rows);
+    if (c.type == MOE_F32) add_rms_norm_q8_1_kernel<MOE_F32><<<grid, threads, 0, st>>>(c);
+    else if (c.type == MOE_F16) add_rms_norm_q8_1_kernel<MOE_F16><<<grid, threads, 0, st>>>(c);
+    else add_rms_norm_q8_1_kernel<MOE_BF16><<<grid, threads, 0, st>>>(c);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_dequantize_q8_1(const moe_q8_1* xq, int64_t n_blocks, void* out, int type, cudaStream_t st) {
+    if (n_blocks == 0) return cudaSuccess;
+    const unsigned grid = static_cast<unsigned>((n_blocks * 4 + 255) / 256);
+    if (type == MOE_F32) dequantize_q8_1_kernel<MOE_F32><<<grid, 256, 0, st>>>(xq, n_blocks, static_cast<float*>(out));
+    else if (type == MOE_F16)
+        dequantize_q8_1_kernel<MOE_F16><<<grid, 256, 0, st>>>(xq, n_blocks, static_cast<__half*>(out));
+    else
+        dequantize_q8_1_kernel<MOE_BF16><<<grid, 256, 0, st>>>(xq, n_blocks, static_cast<__nv_bfloat16*>(out));
+    return cudaGetLastError();
+}
+
+}  // namespace moe
