@@ -75,7 +75,7 @@ int64_t moe_kv8_attention_workspace_bytes(int n_seqs, int T, int n_heads, int n_
     if (n_seqs <= 0 || T < 1 || T > 32 || n_kv_heads <= 0 || n_heads <= 0 || n_heads % n_kv_heads ||
         moe_kv8_block_bytes(head_dim) == 0)
         return 0;
-    return 16;
+    return attn_workspace_bytes(n_seqs, T, n_heads, n_kv_heads, head_dim);
 }
 
 int moe_kv8_attention(const moe_kv8_attention_call* call, cudaStream_t stream) {

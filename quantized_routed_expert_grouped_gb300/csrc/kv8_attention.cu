@@ -1,107 +1,136 @@
-// kv8_attention.cu - attention of a verify window over the 8-bit cache.
-//
-// For a row (query token t, head h) and the positions j it sees: s_j = scale * q . k_j,
-// m = max s_j, out = sum e^(s_j - m) v_j / sum e^(s_j - m), kept as a running maximum, sum and
-// weighted row that are rescaled when the maximum grows.
-#include "internal.h"
-#include "kv8.cuh"
-#include "kv8_api.h"
+// kv8_attention.cu - planning the attention call, and the kernel that joins the parts of sequences
+// that several CTAs worked on.
+#include "kv8_attention.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kWarps = 4;
-
-// One CTA per (sequence, query token, head); a warp takes every fourth block of 32 tokens, lane =
-// token for the scores and lane = dims lane, lane + 32, .. for the weighted values.
-template <int TYPE>
-__global__ void __launch_bounds__(kWarps * 32) kv8_attention_kernel(AttnArgs a) {
-    using E = Elem<TYPE>;
-    extern __shared__ float sm[];
-    const int D = a.c.D, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int h = blockIdx.x % a.n_heads, t = blockIdx.x / a.n_heads % a.T, b = blockIdx.x / a.n_heads / a.T;
-    float* qs = sm;               // [D]
-    float* part = sm + D;         // [kWarps][D + 2]
-    const typename E::T* q = static_cast<const typename E::T*>(a.q) + b * a.qs + t * a.qt + h * a.qh;
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) qs[d] = E::get(q[d]);
-    __syncthreads();
-    int len = a.lens[b];
-    const int64_t cap = static_cast<int64_t>(a.c.max_pages) * a.c.page_blocks * 32;
-    if (len < 0) {
-        set_err(a.err, MOE_ERR_LEN);
-        len = 0;
+// WPR warps take one output row's parts in turn; a part is (row / l, m, l), its weight l 2^(m - M) / L.
+// Rows of a segment that one CTA held whole are in out already; a sequence without blocks gives
+// zeros here.
+template <int WPR>
+__global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
+    constexpr int kRows = 8 / WPR;
+    __shared__ float acc[WPR > 1 ? 8 : 1][256];
+    pdl_wait();
+    const AttnArgs& a = p.a;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, sub = wid / WPR, w = wid - sub * WPR, D = a.c.D;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub;
+    const int64_t rows = static_cast<int64_t>(a.c.n_seqs) * a.T * a.n_heads;
+    if (row >= rows) return;  // WPR == 1 where more than one row shares the CTA
+    const int h = static_cast<int>(row % a.n_heads), t = static_cast<int>(row / a.n_heads % a.T);
+    const int b = static_cast<int>(row / a.n_heads / a.T);
+    const int kv = h / a.G, r = t * a.G + h - kv * a.G, rb = r / p.g.RP, rr = r - rb * p.g.RP;
+    const int64_t at = p.plan[b], n = p.plan[b + 1] - at, chunk = p.plan[a.c.n_seqs + 1];
+    const int64_t s0 = at * p.segs + (static_cast<int64_t>(kv) * p.g.RB + rb) * n;
+    int i0 = 0, cnt = 0;
+    bool head = false;
+    if (n > 0) {
+        i0 = static_cast<int>(s0 / chunk);
+        cnt = static_cast<int>((s0 + n - 1) / chunk) - i0 + 1;
+        head = s0 == i0 * chunk;
+        if (cnt == 1) return;
     }
-    if (len > cap) {
-        set_err(a.err, MOE_ERR_PAGE);
-        len = static_cast<int>(cap);
-    }
-    const int pos = len - a.T + t;
-    const uint32_t bits = a.tree ? static_cast<uint32_t>(a.tree[b * a.T + t]) : 0u;
-    float m = -INFINITY, l = 0.0f, o[8];
-    for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-    const int nblk = pos < 0 ? 0 : (len + 31) / 32;
-    for (int j = wid; j < nblk; j += kWarps) {
-        const uint8_t* rec = kv8_record(a.c, b, j, h / a.G, a.err);
-        if (!rec) continue;
-        const float ks = reinterpret_cast<const float*>(rec)[0], vs = reinterpret_cast<const float*>(rec)[1];
-        const int key = j * 32 + lane;
-        float dot = 0.0f;
-        for (int d = 0; d < D; ++d) dot += qs[d] * (rec[kv8_k_at(D, lane, d)] - 128);
-        float s = dot * ks * a.scale;
-        const int w = key - (len - a.T);
-        const bool see = key < len && (a.tree ? (w < 0 || (bits >> w & 1u)) : key <= pos) &&
-                         (a.window == 0 || key > pos - a.window);
-        if (!see) s = -INFINITY;
-        float bm = s;
-        for (int x = 16; x > 0; x >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
-        if (!__any_sync(0xffffffffu, see)) continue;
-        const float nm = fmaxf(m, bm), base = nm == -INFINITY ? 0.0f : nm;
-        const float al = expf(m - base);
-        const float p = see ? expf(s - base) : 0.0f;
-        float sum = p;
-        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        l = l * al + sum;
-        m = nm;
-        for (int i = 0; i < D / 32; ++i) {
-            float acc = 0.0f;
-            for (int x = 0; x < 32; ++x) {
-                const float px = __shfl_sync(0xffffffffu, p, x);
-                if (px != 0.0f) acc += px * (rec[kv8_v_at(D, x, i * 32 + lane)] - 128);
+    const int64_t pf = attn_part_floats(p.g.RP, D), ml = static_cast<int64_t>(p.g.RP) * D + rr;
+    auto part = [&](int j) { return p.parts + (2LL * (i0 + j) + (j == 0 && !head ? 1 : 0)) * pf; };
+    float M = -INFINITY, Ls = 0.0f;
+    for (int j = lane; j < cnt; j += 32) M = fmaxf(M, part(j)[ml]);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -INFINITY ? 0.0f : M;
+    for (int j = lane; j < cnt; j += 32) Ls += part(j)[ml + p.g.RP] * ex2(part(j)[ml] - base);
+    for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+    const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
+    float4 v[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+    for (int j0 = w; j0 < cnt; j0 += WPR * 4) {
+        float4 y[4][2];
+        float wt[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = j0 + k * WPR;
+            wt[k] = 0.0f;
+            if (j >= cnt) continue;
+            const float* q = part(j);
+            wt[k] = q[ml + p.g.RP] * ex2(q[ml] - base) * inv;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (i * 128 + lane * 4 < D) y[k][i] = *reinterpret_cast<const float4*>(q + static_cast<int64_t>(rr) * D + i * 128 + lane * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (j0 + k * WPR < cnt) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (i * 128 + lane * 4 < D) {
+                        v[i].x = fmaf(wt[k], y[k][i].x, v[i].x);
+                        v[i].y = fmaf(wt[k], y[k][i].y, v[i].y);
+                        v[i].z = fmaf(wt[k], y[k][i].z, v[i].z);
+                        v[i].w = fmaf(wt[k], y[k][i].w, v[i].w);
+                    }
             }
-            o[i] = o[i] * al + acc * vs;
+    }
+    if (WPR > 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (i * 128 + lane * 4 < D) *reinterpret_cast<float4*>(&acc[wid][i * 128 + lane * 4]) = v[i];
+        __syncthreads();
+        if (w) return;
+        for (int k = 1; k < WPR; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (i * 128 + lane * 4 < D) {
+                    const float4 y = *reinterpret_cast<const float4*>(&acc[wid + k][i * 128 + lane * 4]);
+                    v[i].x += y.x;
+                    v[i].y += y.y;
+                    v[i].z += y.z;
+                    v[i].w += y.w;
+                }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int d = i * 128 + lane * 4;
+        if (d >= D) continue;
+        if (p.out_type == MOE_F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + d) = v[i];
+        } else if (p.out_type == MOE_F16) {
+            __half2* q = reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + row * D + d);
+            q[0] = __floats2half2_rn(v[i].x, v[i].y);
+            q[1] = __floats2half2_rn(v[i].z, v[i].w);
+        } else {
+            __nv_bfloat162* q = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d);
+            q[0] = __floats2bfloat162_rn(v[i].x, v[i].y);
+            q[1] = __floats2bfloat162_rn(v[i].z, v[i].w);
         }
     }
-    float* mine = part + wid * (D + 2);
-    for (int i = 0; i < D / 32; ++i) mine[i * 32 + lane] = o[i];
-    if (lane == 0) {
-        mine[D] = m;
-        mine[D + 1] = l;
-    }
-    __syncthreads();
-    float mx = -INFINITY, total = 0.0f;
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, part[w * (D + 2) + D]);
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    for (int w = 0; w < kWarps; ++w) total += part[w * (D + 2) + D + 1] * expf(part[w * (D + 2) + D] - base);
-    const int64_t row = (static_cast<int64_t>(b) * a.T + t) * a.n_heads + h;
-    typename E::T* out = static_cast<typename E::T*>(a.out) + row * D;
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-        float acc = 0.0f;
-        for (int w = 0; w < kWarps; ++w) acc += part[w * (D + 2) + d] * expf(part[w * (D + 2) + D] - base);
-        out[d] = E::put(total == 0.0f ? 0.0f : acc / total);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = base + logf(total);
+    if (a.lse && lane == 0) a.lse[row] = Ls == 0.0f ? -INFINITY : (M - kAttnShift) * kLn2 + logf(Ls);
 }
 
 }  // namespace
 
+int64_t attn_workspace_bytes(int n_seqs, int T, int n_heads, int n_kv, int D) {
+    const AttnGeom g = attn_geom(T * (n_heads / n_kv), D);
+    return attn_plan_bytes(n_seqs) + 2LL * kAttnMaxCtas * attn_part_floats(g.RP, D) * 4;
+}
+
+cudaError_t launch_attn_combine(const AttnPlan& p, cudaStream_t st) {
+    const int64_t rows = static_cast<int64_t>(p.a.c.n_seqs) * p.a.T * p.a.n_heads;
+    // few rows have many parts each
+    if (rows <= 1024)
+        return launch_kernel(kv8_combine_kernel<8>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, true, p);
+    return launch_kernel(kv8_combine_kernel<1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, true, p);
+}
+
 cudaError_t launch_kv8_attention(const AttnArgs& a, int type, cudaStream_t st) {
-    const unsigned grid = static_cast<unsigned>(a.c.n_seqs * a.T * a.n_heads);
-    const int smem = (a.c.D + kWarps * (a.c.D + 2)) * 4;
-    if (type == MOE_F32) kv8_attention_kernel<MOE_F32><<<grid, kWarps * 32, smem, st>>>(a);
-    else if (type == MOE_F16) kv8_attention_kernel<MOE_F16><<<grid, kWarps * 32, smem, st>>>(a);
-    else kv8_attention_kernel<MOE_BF16><<<grid, kWarps * 32, smem, st>>>(a);
-    return cudaGetLastError();
+    AttnPlan p{};
+    p.a = a;
+    p.R = a.T * a.G;
+    p.g = attn_geom(p.R, a.c.D);
+    p.segs = a.c.n_kv * p.g.RB;
+    p.out_type = type;
+    p.plan = static_cast<int64_t*>(a.workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + attn_plan_bytes(a.c.n_seqs));
+    const cudaError_t e = type == MOE_F32 ? launch_attn_f32(p, st) : launch_attn_16(p, st);
+    return e == cudaSuccess ? launch_attn_combine(p, st) : e;
 }
 
 }  // namespace moe

@@ -1,0 +1,716 @@
+// kv8_attention.cuh - attention of a verify window over the 8-bit cache.
+//
+// Mathematics. The rows of a key/value head are its queries (token t, head h of its group): R = T *
+// n_heads / n_kv_heads of them share every key and value. For a row, in base 2 (log2 e is in the
+// row's factor), s_j = f * (q . (c_j - 128)) with f = scale * log2 e * k_scale * (the query's own
+// power of two), m = max s_j, l = sum 2^(s_j - m + 15), o = sum 2^(s_j - m + 15) (v_scale / vref)
+// (c_j - 128), out = o * vref / l. m, vref (the largest v_scale so far) and with them l and o are
+// kept running, block by block of 32 tokens. The 2^15 uses fp16's range for the weights from 2^15
+// down to 2^-24, so that a long tail of small ones keeps its sum; v_scale / vref <= 1 joins the
+// weights because blocks differ in scale. Codes and, after a shift by a power of two, 16-bit queries
+// are exact in fp16; an fp32 query and its weights are two fp16 parts each (SPLIT). Sums are fp32.
+//
+// Layout. A matrix instruction (m16n8k16) takes 16 rows; its other operand is the record itself: a
+// lane's eight bytes of a 256-byte tile are its part of two instructions' keys (eight dims of one
+// token) or values (eight tokens of one dim), and the tokens whose scores a lane receives are the
+// ones whose weights it must supply, so neither scores nor weights leave the registers. Four codes
+// become two half2 with two byte permutes (0x64 above a byte is 1024 + code) and two subtractions.
+// The row count is small and the cache is read once, so the work is a stream of records through
+// registers, not a tile product: the matrix instructions that take register operands fit it, while
+// operands staged for tcgen05 would have to be widened to fp16 in shared memory first (twice the
+// bytes written and read there again).
+//
+// Split. The call's blocks, over all sequences, heads and groups of rows, are one list; each CTA
+// takes an equal range of it, and its four warps the range's blocks in turn, each with its own ring
+// of shared-memory stages that bulk copies fill (one copy a block: keys, values and scales are
+// one record). A CTA joins its warps' results in warp order. Ranges that end inside a sequence
+// leave a part (rows, m, l) in the workspace, and a second kernel joins the parts in list order:
+// the result does not depend on timing.
+#pragma once
+
+#include <atomic>
+
+#include "internal.h"
+#include "kv8.cuh"
+#include "kv8_api.h"
+
+namespace moe {
+
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr int kAttnStages = 32;          // ring stages of a CTA, at most
+constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many CTAs
+constexpr float kAttnShift = 15.0f;      // weights are held times 2^15
+constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
+
+// Row tiles of a pass over the blocks: MT tiles of 16 rows per warp, RTW warps share a ring.
+struct AttnGeom {
+    int MT, RTW, RP, RB;  // RP = 16 MT RTW rows a pass, RB passes
+};
+inline __host__ __device__ AttnGeom attn_geom(int R, int D) {
+    AttnGeom g;
+    g.MT = D <= 128 && R > 16 ? 2 : 1;
+    const int tiles = (R + 16 * g.MT - 1) / (16 * g.MT);
+    g.RTW = tiles >= 3 ? 4 : tiles;
+    g.RP = 16 * g.MT * g.RTW;
+    g.RB = (R + g.RP - 1) / g.RP;
+    return g;
+}
+// workspace: int64 plan[n_seqs + 2] (units before each sequence; the chunk), then two parts per CTA
+inline __host__ __device__ int64_t attn_plan_bytes(int n_seqs) { return (static_cast<int64_t>(n_seqs) + 2 + 1) / 2 * 16; }
+inline __host__ __device__ int64_t attn_part_floats(int RP, int D) { return static_cast<int64_t>(RP) * (D + 2); }
+
+struct AttnPlan {
+    AttnArgs a;
+    AttnGeom g;
+    int R, segs;     // rows of a key/value head; segments (head, pass) of a sequence
+    int out_type;
+    int stages;      // ring stages per group of RTW warps
+    int min_chunk;
+    int smem;
+    int64_t* plan;
+    float* parts;
+};
+
+cudaError_t launch_attn_f32(const AttnPlan& p, cudaStream_t st);
+cudaError_t launch_attn_16(const AttnPlan& p, cudaStream_t st);
+cudaError_t launch_attn_combine(const AttnPlan& p, cudaStream_t st);
+
+// Blocks that a sequence's queries can see: n blocks from `first`.
+__device__ __forceinline__ void attn_seq(const AttnArgs& a, int b, int& len, int& first, int& n, bool report) {
+    len = __ldg(a.lens + b);
+    const int64_t cap = static_cast<int64_t>(a.c.max_pages) * a.c.page_blocks * kKvBlock;
+    if (len < 0) {
+        if (report) set_err(a.err, MOE_ERR_LEN);
+        len = 0;
+    }
+    if (len > cap) {
+        if (report) set_err(a.err, MOE_ERR_PAGE);
+        len = static_cast<int>(cap);
+    }
+    first = 0;
+    if (a.window > 0) {
+        const int64_t lo = static_cast<int64_t>(len) - a.T - a.window + 1;  // the first query's first position
+        if (lo > 0) first = static_cast<int>(lo >> 5);
+    }
+    n = len > 0 ? ((len - 1) >> 5) + 1 - first : 0;
+}
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// four codes -> two half2 of code - 128 (exact)
+__device__ __forceinline__ void codes_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t a = prmt(w, 0x64646464u, 0x4140u), b = prmt(w, 0x64646464u, 0x4342u);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+
+// A run of blocks [blk, end) of one segment within the CTA's range.
+struct AttnPiece {
+    int b, seg, len, first, n, blk, end;
+    int64_t left;  // units of the CTA's range after this piece
+};
+
+__device__ __forceinline__ bool attn_next(const AttnPlan& p, AttnPiece& x) {
+    if (x.left <= 0) return false;
+    if (++x.seg == p.segs) {
+        x.seg = 0;
+        do {
+            if (++x.b >= p.a.c.n_seqs) return false;
+            attn_seq(p.a, x.b, x.len, x.first, x.n, false);
+        } while (x.n == 0);
+    }
+    const int take = x.left < x.n ? static_cast<int>(x.left) : x.n;
+    x.blk = x.first;
+    x.end = x.first + take;
+    x.left -= take;
+    return true;
+}
+
+template <int D, int MT, bool SPLIT>
+struct AttnSmem {
+    static constexpr int kRec = kv8_record_bytes(D);
+    static constexpr int kTileQ = D * 32 * (SPLIT ? 2 : 1);  // fragments of 16 rows
+    static constexpr int kRowO = D + 8;                      // floats of a row in the joining buffer
+    static __host__ __device__ int buf_bytes(int RTW) {
+        const int q = kTileQ * MT * RTW, o = RTW < kAttnWarps ? 16 * MT * RTW * kRowO * 4 : 0;
+        return q > o ? q : o;
+    }
+    // buffer (queries, then the joined rows), the warps' m and l, row factors, barriers and flags, scan, ring
+    static constexpr int kStats = kAttnWarps * 16 * MT * 8 + 16 * MT * kAttnWarps * 4;
+    static __host__ __device__ int fixed(int RTW) { return (buf_bytes(RTW) + kStats + kAttnStages * 20 + 128 + 15) / 16 * 16; }
+};
+
+template <int D, int MT, bool SPLIT>
+__global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8_attention_kernel(const AttnPlan p) {
+    using L = AttnSmem<D, MT, SPLIT>;
+    constexpr int kNB = D / 32, kND = D / 8;
+    extern __shared__ __align__(128) uint8_t sm[];
+    const AttnArgs& a = p.a;
+    const int RTW = p.g.RTW, NG = kAttnWarps / RTW, RP = p.g.RP, S = p.stages;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int grp = wid / RTW, rt = wid - grp * RTW;
+    uint4* qs = reinterpret_cast<uint4*>(sm);
+    float* buf = reinterpret_cast<float*>(sm);
+    float2* stat = reinterpret_cast<float2*>(sm + L::buf_bytes(RTW));        // [warps][16 MT]: m, l
+    float* qf = reinterpret_cast<float*>(stat + kAttnWarps * 16 * MT);       // [RP] row factors
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uintptr_t>(qf + 16 * MT * kAttnWarps));  // [NG * S]
+    uint64_t* empty = full + kAttnStages;
+    int* flag = reinterpret_cast<int*>(empty + kAttnStages);                          // [NG * S]: the stage holds a record
+    int64_t* scan = reinterpret_cast<int64_t*>(flag + kAttnStages);                   // [8]
+    volatile int* dead = reinterpret_cast<int*>(scan + 8);
+    int* found = reinterpret_cast<int*>(scan + 8) + 1;                       // b
+    int64_t* found_off = scan + 10;
+    uint8_t* ring = sm + L::fixed(RTW) + static_cast<int64_t>(grp) * S * L::kRec;
+    full += grp * S;
+    empty += grp * S;
+    flag += grp * S;
+
+    pdl_trigger();
+    // ---- the call's units and this CTA's range: a thread sums a run of sequences
+    const int B = a.c.n_seqs;
+    const int span = (B + kAttnThreads - 1) / kAttnThreads, b0 = min(B, static_cast<int>(threadIdx.x) * span), b1 = min(B, b0 + span);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        int len, first, n;
+        attn_seq(a, b, len, first, n, blockIdx.x == 0);
+        mine += n;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[wid] = incl;
+    if (threadIdx.x == 0) {
+        *dead = 0;
+        *found = -1;
+        for (int i = 0; i < S * NG; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, RTW);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
+    int64_t total = 0, before = incl - mine;
+    for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < wid) before += scan[w];
+        total += scan[w];
+    }
+    const int64_t U = total * p.segs;
+    int64_t chunk = (U + gridDim.x - 1) / gridDim.x;
+    if (chunk < p.min_chunk) chunk = p.min_chunk;
+    if (blockIdx.x == 0) {  // the plan that the joining kernel reads
+        int64_t at = before;
+        for (int b = b0; b < b1; ++b) {
+            int len, first, n;
+            attn_seq(a, b, len, first, n, false);
+            p.plan[b] = at;
+            at += n;
+        }
+        if (threadIdx.x == 0) {
+            p.plan[B] = total;
+            p.plan[B + 1] = chunk;
+        }
+    }
+    const int64_t u0 = blockIdx.x * chunk, u1 = u0 + chunk < U ? u0 + chunk : U;
+    if (u0 >= u1) return;
+    if (before * p.segs <= u0 && u0 < (before + mine) * p.segs) {
+        int64_t at = before;
+        for (int b = b0; b < b1; ++b) {
+            int len, first, n;
+            attn_seq(a, b, len, first, n, false);
+            if (u0 < (at + n) * p.segs) {
+                *found = b;
+                *found_off = u0 - at * p.segs;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+
+    AttnPiece x;  // the piece being computed
+    x.b = *found;
+    attn_seq(a, x.b, x.len, x.first, x.n, false);
+    {
+        const int64_t off = *found_off;
+        x.seg = static_cast<int>(off / x.n);
+        const int u = static_cast<int>(off - static_cast<int64_t>(x.seg) * x.n);
+        const int64_t rest = u1 - u0;
+        const int take = rest < x.n - u ? static_cast<int>(rest) : x.n - u;
+        x.blk = x.first + u;
+        x.end = x.blk + take;
+        x.left = rest - take;
+    }
+
+    // ---- copies: the group's first warp issues its blocks S ahead of the arithmetic
+    AttnPiece ip = x;
+    int iu = ip.blk + grp, ik = 0, pgi = 32, pg = 0;  // next unit, copies issued, page ids in the lanes
+    bool more = rt == 0;
+    auto issue = [&]() {
+        if (!more) return;
+        while (iu >= ip.end) {
+            if (!attn_next(p, ip)) {
+                more = false;
+                return;
+            }
+            iu = ip.blk + grp;
+            pgi = 32;
+        }
+        if (pgi == 32) {
+            const int u = iu + lane * NG;
+            pg = u < ip.end ? __ldg(a.c.table + ip.b * a.c.table_stride + u / a.c.page_blocks) : -1;
+            pgi = 0;
+        }
+        const int page = __shfl_sync(0xffffffffu, pg, pgi);
+        ++pgi;
+        const int s = ik % S;
+        if (RTW > 1 && ik >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(empty + s, ((ik / S) - 1) & 1))) {
+            if (lane == 0) set_err(a.err, MOE_ERR_TIMEOUT);
+            *dead = 1;
+            more = false;
+            return;
+        }
+        if (lane == 0) {
+            const bool ok = page >= 0 && page < a.c.n_pages;
+            flag[s] = ok;
+            if (ok) {
+                const int h = ip.seg / p.g.RB;
+                const uint8_t* src = a.c.pool + ((static_cast<int64_t>(page) * a.c.n_kv + h) * a.c.page_blocks +
+                                                 iu % a.c.page_blocks) * L::kRec;
+                mbar_arrive_expect_tx(full + s, L::kRec);
+                bulk_g2s(ring + s * L::kRec, src, L::kRec, full + s);
+            } else {
+                set_err(a.err, MOE_ERR_PAGE);
+                mbar_arrive_expect_tx(full + s, 0);
+            }
+        }
+        iu += NG;
+        ++ik;
+    };
+    for (int i = 0; i < S; ++i) issue();
+
+    int ck = 0, landed = 0;  // blocks consumed; copies seen to land
+    for (int piece = 0;; ++piece) {
+        const int kv = x.seg / p.g.RB, rb = x.seg - kv * p.g.RB;
+        // ---- queries: shifted by a power of two into fp16's range, stored as the lanes take them
+        {
+            constexpr int LPR = D <= 128 ? 16 : 32, RPW = 32 / LPR;  // lanes per row, rows of a warp at once
+            const int sub = lane / LPR, pc = lane - sub * LPR;      // the lane's eight dims: 8 pc ..
+            const bool in = pc < kND;
+            for (int r0 = (wid * RPW + sub); r0 < RP; r0 += kAttnWarps * RPW * 2) {
+                float v[2][8];
+                bool ok[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = rb * RP + r0 + i * kAttnWarps * RPW;
+                    ok[i] = in && r0 + i * kAttnWarps * RPW < RP && r < p.R;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+                    if (ok[i]) {
+                        const int t = r / a.G, h = kv * a.G + r - t * a.G;
+                        const int64_t at = x.b * a.qs + t * a.qt + h * a.qh + pc * 8;
+                        if (SPLIT) load8<MOE_F32>(static_cast<const float*>(a.q) + at, a.qvec, v[i]);
+                        else if (p.out_type == MOE_F16) load8<MOE_F16>(static_cast<const __half*>(a.q) + at, a.qvec, v[i]);
+                        else load8<MOE_BF16>(static_cast<const __nv_bfloat16*>(a.q) + at, a.qvec, v[i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rr = r0 + i * kAttnWarps * RPW;
+                    float amax = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float y = fabsf(v[i][e]);
+                        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(y));
+                    }
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) {
+                        const float y = __shfl_xor_sync(0xffffffffu, amax, o);
+                        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(y));
+                    }
+                    // amax * 2^k in [2^13, 2^14)
+                    const bool fine = amax < INFINITY;
+                    int k = fine && amax > 0.0f ? 13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127) : 0;
+                    k = min(k, 120);
+                    const float up = __int_as_float((k + 127) << 23);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y0 = fine ? v[i][2 * e] * up : 0.0f, y1 = fine ? v[i][2 * e + 1] * up : 0.0f;
+                        hi[e] = pack_h2(y0, y1);
+                        if (SPLIT) {
+                            const float2 h2 = unpack_h2(hi[e]);
+                            lo[e] = pack_h2(y0 - h2.x, y1 - h2.y);
+                        }
+                    }
+                    if (rr < RP && in) {
+                        const int tile = rr >> 4, row = rr & 15;
+                        const int at = ((tile * kNB + (pc >> 2)) * 2 + (row >> 3)) * 32 + (row & 7) * 4 + (pc & 3);
+                        qs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if (SPLIT) qs[at + MT * RTW * D * 2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        if (pc == 0) qf[rr] = fine ? a.scale * kLog2e * __int_as_float((127 - k) << 23) : __int_as_float(0x7fffffff);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+
+        float o[MT][kND][4], m[MT][2], l[MT][2], fr[MT][2], vref = 0.0f;
+        int pos[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int i = 0; i < kND; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                m[mt][q] = -INFINITY;
+                l[mt][q] = 0.0f;
+                const int rr = (rt * MT + mt) * 16 + q * 8 + g, r = rb * RP + rr;
+                fr[mt][q] = qf[rr];
+                pos[mt][q] = r < p.R ? x.len - a.T + r / a.G : -1;
+            }
+        }
+        const int before_window = x.len - a.T;
+        for (int u = x.blk + grp; u < x.end; u += NG, ++ck) {
+            const int s = ck % S;
+            bool ok = !__any_sync(0xffffffffu, *dead);  // (the lanes stay together)
+            if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(full + s, (ck / S) & 1))) {
+                if (lane == 0) set_err(a.err, MOE_ERR_TIMEOUT);
+                *dead = 1;
+                ok = false;
+            }
+            if (ok) landed = ck + 1;
+            if (ok && flag[s]) {
+                const uint8_t* rec = ring + s * L::kRec;
+                const float2 sc = *reinterpret_cast<const float2*>(rec);
+                const uint8_t* kp = rec + kKvHead + g * 32 + c * 8;
+                float sa[MT][4][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sa[mt][jj][e] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kNB; ++i) {
+                    uint4 qa[MT], qb[MT], la[MT], lb[MT];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint4* f = qs + (((rt * MT + mt) * kNB + i) * 2) * 32 + lane;
+                        qa[mt] = f[0];
+                        qb[mt] = f[32];
+                        if (SPLIT) {
+                            la[mt] = f[MT * RTW * D * 2];
+                            lb[mt] = f[MT * RTW * D * 2 + 32];
+                        }
+                    }
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(kp + (jj * kNB + i) * 256);
+                        uint32_t k0, k1, k2, k3;
+                        codes_h2(w.x, k0, k1);
+                        codes_h2(w.y, k2, k3);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            mma_16816(sa[mt][jj], qa[mt].x, qb[mt].x, qa[mt].y, qb[mt].y, k0, k1);
+                            mma_16816(sa[mt][jj], qa[mt].z, qb[mt].z, qa[mt].w, qb[mt].w, k2, k3);
+                            if (SPLIT) {
+                                mma_16816(sa[mt][jj], la[mt].x, lb[mt].x, la[mt].y, lb[mt].y, k0, k1);
+                                mma_16816(sa[mt][jj], la[mt].z, lb[mt].z, la[mt].w, lb[mt].w, k2, k3);
+                            }
+                        }
+                    }
+                }
+                // ---- scores; lane (g, c) holds rows g, g + 8 and tokens 8 c + 2 jj + e
+                const int t0 = u * kKvBlock;
+                const bool mask = t0 + kKvBlock > before_window || (a.window > 0 && t0 <= x.len - 1 - a.window);
+                uint32_t see[MT][2];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float f = fr[mt][q] * sc.x;
+#pragma unroll
+                        for (int jj = 0; jj < 4; ++jj) {
+                            sa[mt][jj][2 * q] *= f;
+                            sa[mt][jj][2 * q + 1] *= f;
+                        }
+                        see[mt][q] = 0xffu;
+                    }
+                if (mask) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int ps = pos[mt][q];
+                            uint32_t bits = 0, keep = 0;
+                            if (a.tree && ps >= 0) bits = static_cast<uint32_t>(__ldg(a.tree + static_cast<int64_t>(x.b) * a.T + ps - before_window));
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int j = t0 + 8 * c + i, w = j - before_window;
+                                const bool in = a.tree ? (w < 0 || (w < a.T && (bits >> (w & 31) & 1u))) : j <= ps;
+                                if (in && ps >= 0 && (a.window == 0 || j > ps - a.window)) keep |= 1u << i;
+                            }
+                            see[mt][q] = keep;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (!(keep >> i & 1u)) sa[mt][i >> 1][2 * q + (i & 1)] = -INFINITY;
+                        }
+                }
+                // ---- running maximum; o and l are rescaled only where one of the warp's rows grew
+                float base[MT][2], al[MT][2];
+                bool grew = false;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float bm = fmaxf(sa[mt][0][2 * q], sa[mt][0][2 * q + 1]);
+#pragma unroll
+                        for (int jj = 1; jj < 4; ++jj) bm = fmaxf(bm, fmaxf(sa[mt][jj][2 * q], sa[mt][jj][2 * q + 1]));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+                        const float nm = fmaxf(m[mt][q], bm);
+                        const float bs = nm == -INFINITY ? 0.0f : nm;
+                        grew |= nm > m[mt][q];
+                        al[mt][q] = ex2(m[mt][q] - bs);
+                        m[mt][q] = nm;
+                        base[mt][q] = bs - kAttnShift;
+                    }
+                const float vs = sc.y;
+                float ov = 1.0f;
+                if (vs > vref) {
+                    ov = vref > 0.0f ? __fdiv_rn(vref, vs) : 0.0f;
+                    vref = vs;
+                    grew = true;
+                }
+                const float F = vref > 0.0f ? __fdiv_rn(vs, vref) : vs;
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            l[mt][q] *= al[mt][q];
+                            const float f = al[mt][q] * ov;
+#pragma unroll
+                            for (int i = 0; i < kND; ++i) {
+                                o[mt][i][2 * q] *= f;
+                                o[mt][i][2 * q + 1] *= f;
+                            }
+                        }
+                }
+                // ---- weights: the lane's tokens 8 c + 4 xx + 0..3 feed product step xx
+                uint32_t pa[MT][2][4], pl[MT][2][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int jj = 0; jj < 4; ++jj) {
+                            const float p0 = ex2(sa[mt][jj][2 * q] - base[mt][q]), p1 = ex2(sa[mt][jj][2 * q + 1] - base[mt][q]);
+                            l[mt][q] += p0 + p1;
+                            float w0 = p0 * F, w1 = p1 * F;
+                            if (mask) {  // an unseen token adds nothing, whatever the block's scale is
+                                if (!(see[mt][q] >> (2 * jj) & 1u)) w0 = 0.0f;
+                                if (!(see[mt][q] >> (2 * jj + 1) & 1u)) w1 = 0.0f;
+                            }
+                            const uint32_t h = pack_h2(w0, w1);
+                            pa[mt][jj >> 1][(jj & 1) * 2 + q] = h;
+                            if (SPLIT) {
+                                const float2 h2 = unpack_h2(h);
+                                pl[mt][jj >> 1][(jj & 1) * 2 + q] = pack_h2(w0 - h2.x, w1 - h2.y);
+                            }
+                        }
+                const uint8_t* vp = rec + kKvHead + kKvBlock * D + g * 32 + c * 8;
+#pragma unroll
+                for (int i = 0; i < kND; ++i) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(vp + i * 256);
+                    uint32_t v0, v1, v2, v3;
+                    codes_h2(w.x, v0, v1);
+                    codes_h2(w.y, v2, v3);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma_16816(o[mt][i], pa[mt][0][0], pa[mt][0][1], pa[mt][0][2], pa[mt][0][3], v0, v1);
+                        mma_16816(o[mt][i], pa[mt][1][0], pa[mt][1][1], pa[mt][1][2], pa[mt][1][3], v2, v3);
+                        if (SPLIT) {
+                            mma_16816(o[mt][i], pl[mt][0][0], pl[mt][0][1], pl[mt][0][2], pl[mt][0][3], v0, v1);
+                            mma_16816(o[mt][i], pl[mt][1][0], pl[mt][1][1], pl[mt][1][2], pl[mt][1][3], v2, v3);
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // the stage has been read
+            if (RTW > 1 && lane == 0)
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(empty + s)) : "memory");
+            if (ok) issue();
+        }
+
+        // ---- join the groups, in order, and write the piece's rows: to out, or as a part
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                l[mt][q] += __shfl_xor_sync(0xffffffffu, l[mt][q], 1);
+                l[mt][q] += __shfl_xor_sync(0xffffffffu, l[mt][q], 2);
+                if (c == 0) stat[wid * 16 * MT + mt * 16 + q * 8 + g] = make_float2(m[mt][q], l[mt][q]);
+            }
+        __syncthreads();
+        float cf[MT][2], M[MT][2], Ls[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int at = mt * 16 + q * 8 + g;
+                float mm = -INFINITY, ll = 0.0f;
+                for (int k = 0; k < NG; ++k) mm = fmaxf(mm, stat[(k * RTW + rt) * 16 * MT + at].x);
+                const float bs = mm == -INFINITY ? 0.0f : mm;
+                for (int k = 0; k < NG; ++k) {
+                    const float2 v = stat[(k * RTW + rt) * 16 * MT + at];
+                    ll += v.y * ex2(v.x - bs);
+                }
+                M[mt][q] = mm;
+                Ls[mt][q] = ll;
+                cf[mt][q] = ll == 0.0f ? 0.0f : vref * (ex2(m[mt][q] - bs) / ll);
+            }
+        const bool whole = x.blk == x.first && x.end == x.first + x.n;
+        float* part = p.parts + (2LL * blockIdx.x + (piece ? 1 : 0)) * attn_part_floats(RP, D);
+        if (grp == 0 && c == 0) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int rr = (rt * MT + mt) * 16 + q * 8 + g, r = rb * RP + rr;
+                    if (!whole) {
+                        part[static_cast<int64_t>(RP) * D + rr] = M[mt][q];
+                        part[static_cast<int64_t>(RP) * D + RP + rr] = Ls[mt][q];
+                    } else if (a.lse && r < p.R) {
+                        const int t = r / a.G, h = kv * a.G + r - t * a.G;
+                        a.lse[(static_cast<int64_t>(x.b) * a.T + t) * a.n_heads + h] =
+                            Ls[mt][q] == 0.0f ? -INFINITY : (M[mt][q] - kAttnShift) * kLn2 + logf(Ls[mt][q]);
+                    }
+                }
+        }
+        auto put = [&](int rr, int d, float v0, float v1) {  // two neighbouring dims of a row
+            if (!whole) {
+                *reinterpret_cast<float2*>(part + static_cast<int64_t>(rr) * D + d) = make_float2(v0, v1);
+                return;
+            }
+            const int r = rb * RP + rr;
+            if (r >= p.R) return;
+            const int t = r / a.G, h = kv * a.G + r - t * a.G;
+            const int64_t at = ((static_cast<int64_t>(x.b) * a.T + t) * a.n_heads + h) * D + d;
+            if (SPLIT) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(v0, v1);
+            else if (p.out_type == MOE_F16) *reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + at) = __floats2half2_rn(v0, v1);
+            else *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + at) = __floats2bfloat162_rn(v0, v1);
+        };
+        if (NG == 1) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < kND; ++i)
+                        put((rt * MT + mt) * 16 + q * 8 + g, i * 8 + 2 * c, o[mt][i][2 * q] * cf[mt][q], o[mt][i][2 * q + 1] * cf[mt][q]);
+            __syncthreads();  // the queries have been read by all
+        } else {
+            for (int k = 0; k < NG; ++k) {
+                if (grp == k) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int i = 0; i < kND; ++i) {
+                                float2* d = reinterpret_cast<float2*>(buf + ((rt * MT + mt) * 16 + q * 8 + g) * L::kRowO + i * 8 + 2 * c);
+                                float2 v = make_float2(o[mt][i][2 * q] * cf[mt][q], o[mt][i][2 * q + 1] * cf[mt][q]);
+                                if (k) {
+                                    const float2 w = *d;
+                                    v.x += w.x;
+                                    v.y += w.y;
+                                }
+                                *d = v;
+                            }
+                }
+                __syncthreads();
+            }
+            for (int i = threadIdx.x; i < RP * (D / 2); i += kAttnThreads) {
+                const int rr = i / (D / 2), d = (i - rr * (D / 2)) * 2;
+                const float2 v = *reinterpret_cast<const float2*>(buf + rr * L::kRowO + d);
+                put(rr, d, v.x, v.y);
+            }
+            __syncthreads();
+        }
+        if (!attn_next(p, x)) break;
+    }
+    if (*dead && rt == 0)  // leave no copy of this CTA's in flight
+        for (int k = landed; k < ik; ++k) mbar_wait_bounded(full + k % S, (k / S) & 1);
+}
+
+template <int D, int MT, bool SPLIT>
+cudaError_t launch_attn(AttnPlan p, cudaStream_t st) {
+    using L = AttnSmem<D, MT, SPLIT>;
+    auto kern = kv8_attention_kernel<D, MT, SPLIT>;
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> sms[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+    constexpr int kSmMax = 227 * 1024;
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (n <= 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmMax);
+        if (e != cudaSuccess) return e;
+        sms[dev].store(n, std::memory_order_relaxed);
+    }
+    // CTAs per SM that the registers allow, fewer where the row buffer leaves no room for the ring
+    int occ = MT == 1 && D <= 128 ? 3 : 2;
+    const int NG = kAttnWarps / p.g.RTW, fixed = L::fixed(p.g.RTW);
+    int stages = 0;
+    for (;; --occ) {
+        stages = ((228 * 1024) / occ - 1024 - fixed) / L::kRec / NG;
+        if (stages >= 2 || occ == 1) break;
+    }
+    if (stages < 1) return cudaErrorInvalidConfiguration;
+    if (stages * NG > kAttnStages) stages = kAttnStages / NG;
+    p.stages = stages;
+    p.smem = fixed + stages * NG * L::kRec;
+    p.min_chunk = NG;
+    int grid = n * occ;
+    if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
+    e = launch_kernel(kern, dim3(grid), dim3(kAttnThreads), p.smem, st, false, p);
+    return e;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace moe

@@ -1,0 +1,22 @@
+// kv8_attention_16.cu - the attention kernel for fp16 and bf16 queries.
+#include <atomic>
+
+#include "kv8_attention.cuh"
+
+namespace moe {
+
+cudaError_t launch_attn_16(const AttnPlan& p, cudaStream_t st) {
+    const bool two = p.g.MT == 2;
+    switch (p.a.c.D) {
+    case 32: return two ? launch_attn<32, 2, false>(p, st) : launch_attn<32, 1, false>(p, st);
+    case 64: return two ? launch_attn<64, 2, false>(p, st) : launch_attn<64, 1, false>(p, st);
+    case 96: return two ? launch_attn<96, 2, false>(p, st) : launch_attn<96, 1, false>(p, st);
+    case 128: return two ? launch_attn<128, 2, false>(p, st) : launch_attn<128, 1, false>(p, st);
+    case 160: return launch_attn<160, 1, false>(p, st);
+    case 192: return launch_attn<192, 1, false>(p, st);
+    case 224: return launch_attn<224, 1, false>(p, st);
+    default: return launch_attn<256, 1, false>(p, st);
+    }
+}
+
+}  // namespace moe
