@@ -23,13 +23,13 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
     const int b = static_cast<int>(row / a.n_heads / a.T);
     const int kv = h / a.G, r = t * a.G + h - kv * a.G, rb = r / p.g.RP, rr = r - rb * p.g.RP;
     const int64_t at = p.plan[b], n = p.plan[b + 1] - at, chunk = p.plan[a.c.n_seqs + 1];
-    const int64_t s0 = at * p.segs + (static_cast<int64_t>(kv) * p.g.RB + rb) * n;
+    const int64_t s0 = at * p.segs + (static_cast<int64_t>(kv) * p.g.RB + rb) * n;  // n, s0 with the fixed part
     int i0 = 0, cnt = 0;
     bool head = false;
     if (n > 0) {
-        i0 = static_cast<int>(s0 / chunk);
+        i0 = static_cast<int>((s0 + kAttnSegCost) / chunk);  // the CTA of the first block
         cnt = static_cast<int>((s0 + n - 1) / chunk) - i0 + 1;
-        head = s0 == i0 * chunk;
+        head = s0 <= i0 * chunk;  // that CTA has no block of an earlier segment
         if (cnt == 1) return;
     }
     const int64_t pf = attn_part_floats(p.g.RP, D), ml = static_cast<int64_t>(p.g.RP) * D + rr;

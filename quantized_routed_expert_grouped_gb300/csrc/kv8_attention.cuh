@@ -2,26 +2,30 @@
 //
 // Mathematics. The rows of a key/value head are its queries (token t, head h of its group): R = T *
 // n_heads / n_kv_heads of them share every key and value. For a row, in base 2 (log2 e is in the
-// row's factor), s_j = f * (q . (c_j - 128)) with f = scale * log2 e * k_scale * (the query's own
-// power of two), m = max s_j, l = sum 2^(s_j - m + 15), o = sum 2^(s_j - m + 15) (v_scale / vref)
-// (c_j - 128), out = o * vref / l. m, vref (the largest v_scale so far) and with them l and o are
-// kept running, block by block of 32 tokens. The 2^15 uses fp16's range for the weights from 2^15
-// down to 2^-24, so that a long tail of small ones keeps its sum; v_scale / vref <= 1 joins the
-// weights because blocks differ in scale. Codes and, after a shift by a power of two, 16-bit queries
-// are exact in fp16; an fp32 query and its weights are two fp16 parts each (SPLIT). Sums are fp32.
+// row's factor), s_j = f * (q . (c_j - 128)) with f = |scale| * log2 e * k_scale * (the query's own
+// power of two), l = sum 2^(s_j - m + 11), o = sum 2^(s_j - m + 11) (v_scale / vref) (c_j - 128),
+// out = o * vref / l, with a reference m that is at most 4 below the largest s_j. m, vref (the
+// largest v_scale so far) and with them l and o are kept running, block by block of 32 tokens; o and
+// l are rescaled only when m moves, which after the first blocks is rare. The 2^11 and the slack of
+// 2^4 use fp16's range for the weights from 2^15 down to 2^-24, so that a long tail of small ones
+// keeps its sum; v_scale / vref <= 1 joins the weights because blocks differ in scale. Codes and,
+// after a shift by a power of two, 16-bit queries are exact in fp16; an fp32 query and its weights
+// are two fp16 parts each (SPLIT). Sums are fp32. Key codes enter as fp16 subnormals (two byte
+// permutes per four codes) and the score starts at -128 * sum q, which is of the scores' own size;
+// value codes are centred (two subtractions more): the sum of weights would be far above the result.
 //
 // Layout. A matrix instruction (m16n8k16) takes 16 rows; its other operand is the record itself: a
 // lane's eight bytes of a 256-byte tile are its part of two instructions' keys (eight dims of one
 // token) or values (eight tokens of one dim), and the tokens whose scores a lane receives are the
-// ones whose weights it must supply, so neither scores nor weights leave the registers. Four codes
-// become two half2 with two byte permutes (0x64 above a byte is 1024 + code) and two subtractions.
+// ones whose weights it must supply, so neither scores nor weights leave the registers.
 // The row count is small and the cache is read once, so the work is a stream of records through
 // registers, not a tile product: the matrix instructions that take register operands fit it, while
 // operands staged for tcgen05 would have to be widened to fp16 in shared memory first (twice the
 // bytes written and read there again).
 //
-// Split. The call's blocks, over all sequences, heads and groups of rows, are one list; each CTA
-// takes an equal range of it, and its four warps the range's blocks in turn, each with its own ring
+// Split. The call's blocks, over all sequences, heads and groups of rows, are one list (each
+// (sequence, head, group) starts with kAttnSegCost units for its fixed work); each CTA takes an
+// equal range of it, and its four warps the range's blocks in turn, each with its own ring
 // of shared-memory stages that bulk copies fill (one copy a block: keys, values and scales are
 // one record). A CTA joins its warps' results in warp order. Ranges that end inside a sequence
 // leave a part (rows, m, l) in the workspace, and a second kernel joins the parts in list order:
@@ -29,6 +33,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv8.cuh"
@@ -40,7 +45,10 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnStages = 32;          // ring stages of a CTA, at most
 constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many CTAs
-constexpr float kAttnShift = 15.0f;      // weights are held times 2^15
+// A row's reference m follows its maximum only once that is kAttnSlack (in powers of two) above it;
+// weights are held times 2^kAttnShift, so they stay below 2^15.
+constexpr float kAttnShift = 11.0f, kAttnSlack = 4.0f;
+constexpr int kAttnSegCost = 8;          // blocks that a segment's fixed work (queries, joining) costs
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 
 // Row tiles of a pass over the blocks: MT tiles of 16 rows per warp, RTW warps share a ring.
@@ -56,7 +64,7 @@ inline __host__ __device__ AttnGeom attn_geom(int R, int D) {
     g.RB = (R + g.RP - 1) / g.RP;
     return g;
 }
-// workspace: int64 plan[n_seqs + 2] (units before each sequence; the chunk), then two parts per CTA
+// workspace: int64 plan[n_seqs + 2] (cost before each sequence; the chunk), then two parts per CTA
 inline __host__ __device__ int64_t attn_plan_bytes(int n_seqs) { return (static_cast<int64_t>(n_seqs) + 2 + 1) / 2 * 16; }
 inline __host__ __device__ int64_t attn_part_floats(int RP, int D) { return static_cast<int64_t>(RP) * (D + 2); }
 
@@ -96,6 +104,9 @@ __device__ __forceinline__ void attn_seq(const AttnArgs& a, int b, int& len, int
     n = len > 0 ? ((len - 1) >> 5) + 1 - first : 0;
 }
 
+// What a segment of n blocks counts for in the list.
+__host__ __device__ __forceinline__ int64_t attn_cost(int n) { return n ? n + kAttnSegCost : 0; }
+
 #ifdef __CUDACC__
 
 __device__ __forceinline__ float ex2(float x) {
@@ -111,6 +122,34 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ unsigned long long pk2(float x, float y) {
+    return (static_cast<unsigned long long>(__float_as_uint(y)) << 32) | __float_as_uint(x);
+}
+__device__ __forceinline__ float2 up2(unsigned long long v) {
+    return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// four codes -> two half2 of code * 2^-24 (fp16's subnormals; exact)
+__device__ __forceinline__ void codes_sub(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    lo = prmt(w, 0u, 0x4140u);
+    hi = prmt(w, 0u, 0x4342u);
 }
 
 // four codes -> two half2 of code - 128 (exact)
@@ -132,11 +171,21 @@ __device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(
 // A run of blocks [blk, end) of one segment within the CTA's range.
 struct AttnPiece {
     int b, seg, len, first, n, blk, end;
-    int64_t left;  // units of the CTA's range after this piece
+    int64_t left;  // of the CTA's range after this piece, in units of cost
 };
 
+// The rest of the CTA's range starts `off` into the current segment's kAttnSegCost + n units: its
+// blocks, and what is left after them. (A range that ends within the fixed part has no blocks here.)
+__device__ __forceinline__ void attn_take(AttnPiece& x, int64_t off, int64_t rest) {
+    const int64_t u = off > kAttnSegCost ? off - kAttnSegCost : 0;
+    const int64_t end = off + rest - kAttnSegCost;
+    x.blk = x.first + static_cast<int>(u);
+    x.end = x.first + static_cast<int>(end < u ? u : end < x.n ? end : x.n);
+    x.left = rest - (kAttnSegCost + x.n - off);
+}
+
 __device__ __forceinline__ bool attn_next(const AttnPlan& p, AttnPiece& x) {
-    if (x.left <= 0) return false;
+    if (x.left <= kAttnSegCost) return false;  // no block of the next segment
     if (++x.seg == p.segs) {
         x.seg = 0;
         do {
@@ -144,10 +193,7 @@ __device__ __forceinline__ bool attn_next(const AttnPlan& p, AttnPiece& x) {
             attn_seq(p.a, x.b, x.len, x.first, x.n, false);
         } while (x.n == 0);
     }
-    const int take = x.left < x.n ? static_cast<int>(x.left) : x.n;
-    x.blk = x.first;
-    x.end = x.first + take;
-    x.left -= take;
+    attn_take(x, 0, x.left);
     return true;
 }
 
@@ -160,8 +206,8 @@ struct AttnSmem {
         const int q = kTileQ * MT * RTW, o = RTW < kAttnWarps ? 16 * MT * RTW * kRowO * 4 : 0;
         return q > o ? q : o;
     }
-    // buffer (queries, then the joined rows), the warps' m and l, row factors, barriers and flags, scan, ring
-    static constexpr int kStats = kAttnWarps * 16 * MT * 8 + 16 * MT * kAttnWarps * 4;
+    // buffer (queries, then the joined rows), the warps' m and l, row factors and offsets, barriers and flags, scan, ring
+    static constexpr int kStats = 2 * kAttnWarps * 16 * MT * 8;
     static __host__ __device__ int fixed(int RTW) { return (buf_bytes(RTW) + kStats + kAttnStages * 20 + 128 + 15) / 16 * 16; }
 };
 
@@ -177,7 +223,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
     uint4* qs = reinterpret_cast<uint4*>(sm);
     float* buf = reinterpret_cast<float*>(sm);
     float2* stat = reinterpret_cast<float2*>(sm + L::buf_bytes(RTW));        // [warps][16 MT]: m, l
-    float* qf = reinterpret_cast<float*>(stat + kAttnWarps * 16 * MT);       // [RP] row factors
+    float2* qf = stat + kAttnWarps * 16 * MT;                                // [RP]: a row's factor and offset
     uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uintptr_t>(qf + 16 * MT * kAttnWarps));  // [NG * S]
     uint64_t* empty = full + kAttnStages;
     int* flag = reinterpret_cast<int*>(empty + kAttnStages);                          // [NG * S]: the stage holds a record
@@ -198,7 +244,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
     for (int b = b0; b < b1; ++b) {
         int len, first, n;
         attn_seq(a, b, len, first, n, blockIdx.x == 0);
-        mine += n;
+        mine += attn_cost(n);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -231,7 +277,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
             int len, first, n;
             attn_seq(a, b, len, first, n, false);
             p.plan[b] = at;
-            at += n;
+            at += attn_cost(n);
         }
         if (threadIdx.x == 0) {
             p.plan[B] = total;
@@ -245,12 +291,12 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
         for (int b = b0; b < b1; ++b) {
             int len, first, n;
             attn_seq(a, b, len, first, n, false);
-            if (u0 < (at + n) * p.segs) {
+            if (u0 < (at + attn_cost(n)) * p.segs) {
                 *found = b;
                 *found_off = u0 - at * p.segs;
                 break;
             }
-            at += n;
+            at += attn_cost(n);
         }
     }
     __syncthreads();
@@ -260,18 +306,15 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
     attn_seq(a, x.b, x.len, x.first, x.n, false);
     {
         const int64_t off = *found_off;
-        x.seg = static_cast<int>(off / x.n);
-        const int u = static_cast<int>(off - static_cast<int64_t>(x.seg) * x.n);
-        const int64_t rest = u1 - u0;
-        const int take = rest < x.n - u ? static_cast<int>(rest) : x.n - u;
-        x.blk = x.first + u;
-        x.end = x.blk + take;
-        x.left = rest - take;
+        x.seg = static_cast<int>(off / attn_cost(x.n));
+        attn_take(x, off - static_cast<int64_t>(x.seg) * attn_cost(x.n), u1 - u0);
+        if (x.blk == x.end) return;  // the range ends within a segment's fixed part
     }
 
     // ---- copies: the group's first warp issues its blocks S ahead of the arithmetic
     AttnPiece ip = x;
-    int iu = ip.blk + grp, ik = 0, pgi = 32, pg = 0;  // next unit, copies issued, page ids in the lanes
+    int iu = ip.blk + grp, ik = 0, is = 0, iph = 1, pgi = 32;  // next block, copies issued, stage and its phase
+    int64_t src = -1;                                           // records of the next 32 blocks, in the lanes
     bool more = rt == 0;
     auto issue = [&]() {
         if (!more) return;
@@ -285,38 +328,43 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
         }
         if (pgi == 32) {
             const int u = iu + lane * NG;
-            pg = u < ip.end ? __ldg(a.c.table + ip.b * a.c.table_stride + u / a.c.page_blocks) : -1;
+            src = -1;
+            if (u < ip.end) {
+                const int pi = u / a.c.page_blocks, page = __ldg(a.c.table + ip.b * a.c.table_stride + pi);
+                if (page >= 0 && page < a.c.n_pages)
+                    src = (static_cast<int64_t>(page) * a.c.n_kv + ip.seg / p.g.RB) * a.c.page_blocks + u - pi * a.c.page_blocks;
+            }
             pgi = 0;
         }
-        const int page = __shfl_sync(0xffffffffu, pg, pgi);
+        const int64_t r = __shfl_sync(0xffffffffu, src, pgi);
         ++pgi;
-        const int s = ik % S;
-        if (RTW > 1 && ik >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(empty + s, ((ik / S) - 1) & 1))) {
+        if (RTW > 1 && ik >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(empty + is, iph))) {
             if (lane == 0) set_err(a.err, MOE_ERR_TIMEOUT);
             *dead = 1;
             more = false;
             return;
         }
         if (lane == 0) {
-            const bool ok = page >= 0 && page < a.c.n_pages;
-            flag[s] = ok;
-            if (ok) {
-                const int h = ip.seg / p.g.RB;
-                const uint8_t* src = a.c.pool + ((static_cast<int64_t>(page) * a.c.n_kv + h) * a.c.page_blocks +
-                                                 iu % a.c.page_blocks) * L::kRec;
-                mbar_arrive_expect_tx(full + s, L::kRec);
-                bulk_g2s(ring + s * L::kRec, src, L::kRec, full + s);
+            flag[is] = r >= 0;
+            if (r >= 0) {
+                mbar_arrive_expect_tx(full + is, L::kRec);
+                bulk_g2s(ring + is * L::kRec, a.c.pool + r * L::kRec, L::kRec, full + is);
             } else {
                 set_err(a.err, MOE_ERR_PAGE);
-                mbar_arrive_expect_tx(full + s, 0);
+                mbar_arrive_expect_tx(full + is, 0);
             }
         }
         iu += NG;
         ++ik;
+        if (++is == S) {
+            is = 0;
+            iph ^= 1;
+        }
     };
     for (int i = 0; i < S; ++i) issue();
 
-    int ck = 0, landed = 0;  // blocks consumed; copies seen to land
+    int cs = 0, cph = 0, landed = 0;  // the stage to consume and its phase; copies seen to land
+    bool lost = false;
     for (int piece = 0;; ++piece) {
         const int kv = x.seg / p.g.RB, rb = x.seg - kv * p.g.RB;
         // ---- queries: shifted by a power of two into fp16's range, stored as the lanes take them
@@ -359,31 +407,40 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                     const bool fine = amax < INFINITY;
                     int k = fine && amax > 0.0f ? 13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127) : 0;
                     k = min(k, 120);
-                    const float up = __int_as_float((k + 127) << 23);
+                    const float up = __int_as_float((k + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
+                    float sum = 0.0f;
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float y0 = fine ? v[i][2 * e] * up : 0.0f, y1 = fine ? v[i][2 * e + 1] * up : 0.0f;
                         hi[e] = pack_h2(y0, y1);
+                        const float2 h2 = unpack_h2(hi[e]);
+                        sum += h2.x + h2.y;
                         if (SPLIT) {
-                            const float2 h2 = unpack_h2(hi[e]);
                             lo[e] = pack_h2(y0 - h2.x, y1 - h2.y);
+                            const float2 l2 = unpack_h2(lo[e]);
+                            sum += l2.x + l2.y;
                         }
                     }
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (rr < RP && in) {
                         const int tile = rr >> 4, row = rr & 15;
                         const int at = ((tile * kNB + (pc >> 2)) * 2 + (row >> 3)) * 32 + (row & 7) * 4 + (pc & 3);
                         qs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         if (SPLIT) qs[at + MT * RTW * D * 2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        if (pc == 0) qf[rr] = fine ? a.scale * kLog2e * __int_as_float((127 - k) << 23) : __int_as_float(0x7fffffff);
+                        if (pc == 0)
+                            qf[rr] = make_float2(fine ? fabsf(a.scale) * kLog2e * __int_as_float((127 - k) << 23) * 16777216.0f
+                                                      : __int_as_float(0x7fffffff),
+                                                 sum * (-128.0f / 16777216.0f));
                     }
                 }
             }
         }
         __syncthreads();
 
-        float o[MT][kND][4], m[MT][2], l[MT][2], fr[MT][2], vref = 0.0f;
-        int pos[MT][2];
+        float o[MT][kND][4], m[MT][2], nb[MT][2], fr[MT][2], off[MT][2], vref = 0.0f, vinv = 0.0f;
+        unsigned long long l[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -393,33 +450,36 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 m[mt][q] = -INFINITY;
-                l[mt][q] = 0.0f;
-                const int rr = (rt * MT + mt) * 16 + q * 8 + g, r = rb * RP + rr;
-                fr[mt][q] = qf[rr];
-                pos[mt][q] = r < p.R ? x.len - a.T + r / a.G : -1;
+                nb[mt][q] = 0.0f;
+                l[mt][q] = 0;
+                const float2 f = qf[(rt * MT + mt) * 16 + q * 8 + g];
+                fr[mt][q] = f.x;
+                off[mt][q] = f.y;
             }
         }
         const int before_window = x.len - a.T;
-        for (int u = x.blk + grp; u < x.end; u += NG, ++ck) {
-            const int s = ck % S;
-            bool ok = !__any_sync(0xffffffffu, *dead);  // (the lanes stay together)
-            if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(full + s, (ck / S) & 1))) {
+        for (int u = x.blk + grp; u < x.end; u += NG) {
+            // (the lanes stay together; a wait that gives up ends the CTA's arithmetic)
+            if (!lost && !__all_sync(0xffffffffu, mbar_try_wait(full + cs, cph)) &&
+                (__any_sync(0xffffffffu, *dead) || !__all_sync(0xffffffffu, mbar_wait_retry(full + cs, cph)))) {
                 if (lane == 0) set_err(a.err, MOE_ERR_TIMEOUT);
                 *dead = 1;
-                ok = false;
+                lost = true;
             }
-            if (ok) landed = ck + 1;
-            if (ok && flag[s]) {
-                const uint8_t* rec = ring + s * L::kRec;
+            if (!lost) ++landed;
+            if (!lost && flag[cs]) {
+                const uint8_t* rec = ring + cs * L::kRec;
                 const float2 sc = *reinterpret_cast<const float2*>(rec);
                 const uint8_t* kp = rec + kKvHead + g * 32 + c * 8;
+                // scores, in units of the row's factor times k_scale: the codes enter as code * 2^-24, so the
+                // sum starts at -128 * 2^-24 times the query's sum
                 float sa[MT][4][4];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sa[mt][jj][e] = 0.0f;
+                        for (int e = 0; e < 4; ++e) sa[mt][jj][e] = off[mt][e >> 1];
 #pragma unroll
                 for (int i = 0; i < kNB; ++i) {
                     uint4 qa[MT], qb[MT], la[MT], lb[MT];
@@ -437,8 +497,8 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                     for (int jj = 0; jj < 4; ++jj) {
                         const uint2 w = *reinterpret_cast<const uint2*>(kp + (jj * kNB + i) * 256);
                         uint32_t k0, k1, k2, k3;
-                        codes_h2(w.x, k0, k1);
-                        codes_h2(w.y, k2, k3);
+                        codes_sub(w.x, k0, k1);
+                        codes_sub(w.y, k2, k3);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
                             mma_16816(sa[mt][jj], qa[mt].x, qb[mt].x, qa[mt].y, qb[mt].y, k0, k1);
@@ -450,44 +510,29 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                         }
                     }
                 }
-                // ---- scores; lane (g, c) holds rows g, g + 8 and tokens 8 c + 2 jj + e
+                // lane (g, c) holds rows g, g + 8 and tokens 8 c + 2 jj + e; an unseen one becomes -inf
                 const int t0 = u * kKvBlock;
                 const bool mask = t0 + kKvBlock > before_window || (a.window > 0 && t0 <= x.len - 1 - a.window);
-                uint32_t see[MT][2];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float f = fr[mt][q] * sc.x;
-#pragma unroll
-                        for (int jj = 0; jj < 4; ++jj) {
-                            sa[mt][jj][2 * q] *= f;
-                            sa[mt][jj][2 * q + 1] *= f;
-                        }
-                        see[mt][q] = 0xffu;
-                    }
                 if (mask) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const int ps = pos[mt][q];
-                            uint32_t bits = 0, keep = 0;
-                            if (a.tree && ps >= 0) bits = static_cast<uint32_t>(__ldg(a.tree + static_cast<int64_t>(x.b) * a.T + ps - before_window));
+                            const int r = rb * RP + (rt * MT + mt) * 16 + q * 8 + g;
+                            const int t = r / a.G, ps = r < p.R ? before_window + t : -1;
+                            uint32_t bits = 0;
+                            if (a.tree && ps >= 0) bits = static_cast<uint32_t>(__ldg(a.tree + static_cast<int64_t>(x.b) * a.T + t));
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const int j = t0 + 8 * c + i, w = j - before_window;
                                 const bool in = a.tree ? (w < 0 || (w < a.T && (bits >> (w & 31) & 1u))) : j <= ps;
-                                if (in && ps >= 0 && (a.window == 0 || j > ps - a.window)) keep |= 1u << i;
+                                if (!(in && ps >= 0 && (a.window == 0 || j > ps - a.window)))
+                                    sa[mt][i >> 1][2 * q + (i & 1)] = -INFINITY;
                             }
-                            see[mt][q] = keep;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (!(keep >> i & 1u)) sa[mt][i >> 1][2 * q + (i & 1)] = -INFINITY;
                         }
                 }
-                // ---- running maximum; o and l are rescaled only where one of the warp's rows grew
-                float base[MT][2], al[MT][2];
+                // ---- running reference; o and l are rescaled only where one of the warp's rows outgrew it
+                float f[MT][2], top[MT][2];
                 bool grew = false;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
@@ -496,59 +541,75 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                         float bm = fmaxf(sa[mt][0][2 * q], sa[mt][0][2 * q + 1]);
 #pragma unroll
                         for (int jj = 1; jj < 4; ++jj) bm = fmaxf(bm, fmaxf(sa[mt][jj][2 * q], sa[mt][jj][2 * q + 1]));
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-                        const float nm = fmaxf(m[mt][q], bm);
-                        const float bs = nm == -INFINITY ? 0.0f : nm;
-                        grew |= nm > m[mt][q];
-                        al[mt][q] = ex2(m[mt][q] - bs);
-                        m[mt][q] = nm;
-                        base[mt][q] = bs - kAttnShift;
+                        f[mt][q] = fr[mt][q] * sc.x;
+                        top[mt][q] = bm * f[mt][q];
+                        grew |= top[mt][q] > m[mt][q] + kAttnSlack;
                     }
-                const float vs = sc.y;
-                float ov = 1.0f;
-                if (vs > vref) {
-                    ov = vref > 0.0f ? __fdiv_rn(vref, vs) : 0.0f;
-                    vref = vs;
-                    grew = true;
-                }
-                const float F = vref > 0.0f ? __fdiv_rn(vs, vref) : vs;
-                if (__any_sync(0xffffffffu, grew)) {
+                if (__any_sync(0xffffffffu, grew || sc.y > vref)) {
+                    float ov = 1.0f;
+                    if (sc.y > vref) {
+                        ov = vref > 0.0f ? __fdiv_rn(vref, sc.y) : 0.0f;
+                        vref = sc.y;
+                        vinv = __fdiv_rn(1.0f, vref);
+                    }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            l[mt][q] *= al[mt][q];
-                            const float f = al[mt][q] * ov;
+                            float bm = fmaxf(top[mt][q], __shfl_xor_sync(0xffffffffu, top[mt][q], 1));
+                            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+                            const float nm = fmaxf(m[mt][q], bm);
+                            float al = 1.0f;
+                            if (nm > m[mt][q]) {
+                                al = ex2(m[mt][q] - nm);
+                                m[mt][q] = nm;
+                                nb[mt][q] = kAttnShift - nm;
+                            }
+                            l[mt][q] = mul2(l[mt][q], pk2(al, al));
+                            al *= ov;
 #pragma unroll
                             for (int i = 0; i < kND; ++i) {
-                                o[mt][i][2 * q] *= f;
-                                o[mt][i][2 * q + 1] *= f;
+                                o[mt][i][2 * q] *= al;
+                                o[mt][i][2 * q + 1] *= al;
                             }
                         }
                 }
+                const float F = vref > 0.0f ? sc.y * vinv : sc.y;
                 // ---- weights: the lane's tokens 8 c + 4 xx + 0..3 feed product step xx
                 uint32_t pa[MT][2][4], pl[MT][2][4];
+                auto weights = [&](auto masked) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
+                        for (int q = 0; q < 2; ++q) {
+                            const unsigned long long ff = pk2(f[mt][q], f[mt][q]), bb = pk2(nb[mt][q], nb[mt][q]);
 #pragma unroll
-                        for (int jj = 0; jj < 4; ++jj) {
-                            const float p0 = ex2(sa[mt][jj][2 * q] - base[mt][q]), p1 = ex2(sa[mt][jj][2 * q + 1] - base[mt][q]);
-                            l[mt][q] += p0 + p1;
-                            float w0 = p0 * F, w1 = p1 * F;
-                            if (mask) {  // an unseen token adds nothing, whatever the block's scale is
-                                if (!(see[mt][q] >> (2 * jj) & 1u)) w0 = 0.0f;
-                                if (!(see[mt][q] >> (2 * jj + 1) & 1u)) w1 = 0.0f;
-                            }
-                            const uint32_t h = pack_h2(w0, w1);
-                            pa[mt][jj >> 1][(jj & 1) * 2 + q] = h;
-                            if (SPLIT) {
-                                const float2 h2 = unpack_h2(h);
-                                pl[mt][jj >> 1][(jj & 1) * 2 + q] = pack_h2(w0 - h2.x, w1 - h2.y);
+                            for (int jj = 0; jj < 4; ++jj) {
+                                const float s0 = sa[mt][jj][2 * q], s1 = sa[mt][jj][2 * q + 1];
+                                float2 w = up2(fma2(pk2(s0, s1), ff, bb));
+                                w.x = ex2(w.x);
+                                w.y = ex2(w.y);
+                                if (decltype(masked)::value) {  // an unseen token adds nothing, whatever the scales are
+                                    if (s0 == -INFINITY) w.x = 0.0f;
+                                    if (s1 == -INFINITY) w.y = 0.0f;
+                                }
+                                l[mt][q] = add2(l[mt][q], pk2(w.x, w.y));
+                                w = up2(mul2(pk2(w.x, w.y), pk2(F, F)));
+                                if (decltype(masked)::value) {
+                                    if (s0 == -INFINITY) w.x = 0.0f;
+                                    if (s1 == -INFINITY) w.y = 0.0f;
+                                }
+                                const uint32_t h = pack_h2(w.x, w.y);
+                                pa[mt][jj >> 1][(jj & 1) * 2 + q] = h;
+                                if (SPLIT) {
+                                    const float2 h2 = unpack_h2(h);
+                                    pl[mt][jj >> 1][(jj & 1) * 2 + q] = pack_h2(w.x - h2.x, w.y - h2.y);
+                                }
                             }
                         }
+                };
+                if (mask) weights(std::true_type{});
+                else weights(std::false_type{});
                 const uint8_t* vp = rec + kKvHead + kKvBlock * D + g * 32 + c * 8;
 #pragma unroll
                 for (int i = 0; i < kND; ++i) {
@@ -569,8 +630,12 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
             }
             __syncwarp();  // the stage has been read
             if (RTW > 1 && lane == 0)
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(empty + s)) : "memory");
-            if (ok) issue();
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(empty + cs)) : "memory");
+            if (++cs == S) {
+                cs = 0;
+                cph ^= 1;
+            }
+            if (!lost) issue();
         }
 
         // ---- join the groups, in order, and write the piece's rows: to out, or as a part
@@ -578,9 +643,11 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                l[mt][q] += __shfl_xor_sync(0xffffffffu, l[mt][q], 1);
-                l[mt][q] += __shfl_xor_sync(0xffffffffu, l[mt][q], 2);
-                if (c == 0) stat[wid * 16 * MT + mt * 16 + q * 8 + g] = make_float2(m[mt][q], l[mt][q]);
+                const float2 l2 = up2(l[mt][q]);
+                float ls = l2.x + l2.y;
+                ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+                ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+                if (c == 0) stat[wid * 16 * MT + mt * 16 + q * 8 + g] = make_float2(m[mt][q], ls);
             }
         __syncthreads();
         float cf[MT][2], M[MT][2], Ls[MT][2];
@@ -704,7 +771,7 @@ cudaError_t launch_attn(AttnPlan p, cudaStream_t st) {
     if (stages * NG > kAttnStages) stages = kAttnStages / NG;
     p.stages = stages;
     p.smem = fixed + stages * NG * L::kRec;
-    p.min_chunk = NG;
+    p.min_chunk = kAttnSegCost + NG;
     int grid = n * occ;
     if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
     e = launch_kernel(kern, dim3(grid), dim3(kAttnThreads), p.smem, st, false, p);
