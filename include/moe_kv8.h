@@ -93,9 +93,8 @@ int moe_kv8_read(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int
  * are split in two fp16 parts. A page that cannot be read (MOE_ERR_PAGE) counts as not seen.
  * Limits: 1 <= T <= 32, n_heads a multiple of n_kv_heads. lens may be 0 (nothing seen) and is
  * clamped to the page table (MOE_ERR_PAGE).
- * workspace: moe_kv8_attention_workspace_bytes(...) bytes, 16-byte aligned, zeroed before the first
- * call that uses it; a call leaves it ready for the next one with the same or smaller
- * arguments. Calls that may run at the same time need a workspace each. */
+ * workspace: moe_kv8_attention_workspace_bytes(...) bytes, 16-byte aligned, of any contents; calls
+ * that may run at the same time need one each. */
 typedef struct moe_kv8_attention_call {
     moe_kv8_cache cache;
     const void* q; /* element (b, t, h, d) at b * q_seq_stride + t * q_token_stride + h * q_head_stride + d */

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -334,9 +335,16 @@ def qsa_block_scores(q, keys, key_scale, scores=None, stream=None):
 
 
 # ---------------------------------------------------------------- the attention side (moe_kv8.h)
-# These calls return tensors that they allocate when none are given, so a small call's time is the
-# binding's: it passes plain integers and checks only what the library cannot see (devices, types,
-# shapes and strides of tensors). Everything else is checked by the library.
+# A small call's time is the binding's, so these pass packed structures and plain integers, and
+# check only what the library cannot see (devices, types, shapes and strides of tensors); everything
+# else is checked by the library.
+
+_CACHE = "PqiiiPqii"                             # moe_kv8_cache
+_pack_rows = struct.Struct("@" + _CACHE + "0q").pack, struct.Struct("@PPiqqqqq").pack
+_pack_attn = struct.Struct("@" + _CACHE + "0qPiiiqqqPPifPPPqP").pack
+_pack_norm = struct.Struct("@PPPPPPiiqqqif").pack
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 
 def _elem(t):
     try:
@@ -345,47 +353,64 @@ def _elem(t):
         raise MoeError(f"float32, float16 or bfloat16 expected, got {t.dtype}") from None
 
 
-def _ptr(t):
-    if t is None:
-        return 0
-    if not t.is_cuda:
+def _device(t):
+    dev = t.get_device()
+    if dev < 0:
         raise MoeError("device tensor expected")
+    return dev
+
+
+def _ptr(t, dev):
+    if t.get_device() != dev:
+        raise MoeError(f"a tensor on device {dev} expected")
     return t.data_ptr()
 
 
-def _ints(t, name, numel):
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != numel:
+def _ints(t, name, numel, dev):
+    if t.dtype is not torch.int32 or t.numel() != numel or not t.is_contiguous():
         raise MoeError(f"{name}: a contiguous int32 tensor of {numel} elements expected")
-    return _ptr(t)
+    return _ptr(t, dev)
 
 
-def _err(err):
-    return None if err is None else _ints(err, "err", err.numel())
+def _err(err, dev):
+    return 0 if err is None else _ints(err, "err", 1, dev)
 
 
-def _raw_stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _empty(stream, shape, dtype, device):
+    """A tensor of the caching allocator, of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _on(stream, *tensors):
-    """Tensors of the caching allocator that are used on another stream than their own."""
-    if stream is not None:
+def _launch(f, dev, stream, tensors, *args):
+    """Call f(*args, stream); tensors are marked as used on a stream that is not the current one."""
+    if stream is None:
+        rc = f(*args, _raw_stream(dev))
+    else:
+        rc = f(*args, stream.cuda_stream)
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+    if rc:
+        raise MoeError(f"{rc}: {strerror(rc)}")
 
 
 def _kv8_cache(pool, page_table):
-    if pool.dtype != torch.uint8 or pool.dim() != 4 or not pool.is_contiguous():
+    """The fields of moe_kv8_cache, and the device."""
+    dev = _device(pool)
+    shape, rows = pool.shape, page_table.shape
+    if pool.dtype is not torch.uint8 or len(shape) != 4 or not pool.is_contiguous():
         raise MoeError("pool: contiguous uint8 [pages, kv heads, page tokens / 32, block bytes] expected")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+    if page_table.dtype is not torch.int32 or len(rows) != 2 or (page_table.stride(1) != 1 and rows[1] > 1):
         raise MoeError("page_table: int32 [sequences, pages] with contiguous rows expected")
-    n_pages, hkv, nb, rec = pool.shape
+    n_pages, hkv, nb, rec = shape
     if rec < 16 or (rec - 16) % 64:
         raise MoeError(f"pool: records of {rec} bytes are of no head size")
-    return KV8CacheC(_ptr(pool), n_pages, hkv, (rec - 16) // 64, nb * 32, _ptr(page_table),
-                     page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1], page_table.shape[1],
-                     page_table.shape[0])
+    n, pages = rows
+    return (pool.data_ptr(), n_pages, hkv, (rec - 16) // 64, nb * 32, _ptr(page_table, dev),
+            page_table.stride(0) if n > 1 else pages, pages, n), dev
 
 
 def kv8_block_bytes(head_dim: int) -> int:
@@ -401,22 +426,29 @@ def kv8_pool(n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int = 64
     return torch.zeros((n_pages, n_kv_heads, page_tokens // 32, rec), dtype=torch.uint8, device=device)
 
 
-def _kv8_rows(c, k, v):
-    if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype or k.shape[1] != c.n_kv_heads or \
-            k.shape[2] != c.head_dim or k.stride(2) != 1 or v.stride(2) != 1:
-        raise MoeError(f"k, v: [tokens, {c.n_kv_heads}, {c.head_dim}] of one type, contiguous in the last dimension, expected")
-    return KV8RowsC(_ptr(k), _ptr(v), _elem(k), k.shape[0], k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+def _kv8_move(f, pool, page_table, cu_tokens, start, n_tokens, dtype, k, v, err, stream):
+    c, dev = _kv8_cache(pool, page_table)
+    hkv, D, n = c[2], c[3], c[8]
+    if n_tokens is None:
+        n_tokens = k.shape[0]
+    if k is None:
+        k = _empty(stream, (n_tokens, hkv, D), dtype, pool.device)
+    if v is None:
+        v = _empty(stream, (n_tokens, hkv, D), k.dtype, pool.device)
+    ks, vs = k.stride(), v.stride()
+    if k.shape != (n_tokens, hkv, D) or v.shape != k.shape or v.dtype is not k.dtype or ks[2] != 1 or vs[2] != 1:
+        raise MoeError(f"k, v: [{n_tokens}, {hkv}, {D}] of one type, contiguous in the last dimension, expected")
+    rows = _pack_rows[1](_ptr(k, dev), _ptr(v, dev), _elem(k), n_tokens, ks[0], ks[1], vs[0], vs[1])
+    _launch(f, dev, stream, (k, v, pool, page_table, cu_tokens, start, err), _pack_rows[0](*c), rows,
+            _ints(cu_tokens, "cu_tokens", n + 1, dev), _ints(start, "start", n, dev), _err(err, dev))
+    return k, v
 
 
 def kv8_write(k, v, pool, page_table, cu_tokens, start, err=None, stream=None):
     """Quantise rows k, v [tokens, kv heads, head_dim] into the cache: rows cu_tokens[b] ..
     cu_tokens[b+1] become positions start[b] .. of sequence b, which ends with them. cu_tokens int32
     [sequences + 1], start int32 [sequences], page_table int32 [sequences, pages]; all on the device."""
-    c = _kv8_cache(pool, page_table)
-    r = _kv8_rows(c, k, v)
-    _check(lib().moe_kv8_write(ctypes.byref(c), ctypes.byref(r), _ints(cu_tokens, "cu_tokens", c.n_seqs + 1),
-                               _ints(start, "start", c.n_seqs), _err(err), _raw_stream(stream)))
-    _on(stream, k, v, pool, page_table, cu_tokens, start, err)
+    _kv8_move(lib().moe_kv8_write, pool, page_table, cu_tokens, start, None, None, k, v, err, stream)
 
 
 def kv8_read(pool, page_table, cu_tokens, start, n_tokens, dtype=torch.bfloat16, k=None, v=None, err=None,
@@ -424,29 +456,17 @@ def kv8_read(pool, page_table, cu_tokens, start, n_tokens, dtype=torch.bfloat16,
     """Read positions start[b] .. of each sequence back as rows cu_tokens[b] .. cu_tokens[b+1] of
     k, v [n_tokens, kv heads, head_dim] (allocated as `dtype` when not given). n_tokens is
     cu_tokens' last value. Rows of a sequence or block that is refused (err) are left as they were."""
-    c = _kv8_cache(pool, page_table)
-    shape = (n_tokens, c.n_kv_heads, c.head_dim)
-    if k is None or v is None:
-        with torch.cuda.stream(stream):
-            k = torch.empty(shape, dtype=dtype, device=pool.device) if k is None else k
-            v = torch.empty(shape, dtype=k.dtype, device=pool.device) if v is None else v
-    if k.shape[0] != n_tokens:
-        raise MoeError(f"k, v: {n_tokens} rows expected")
-    r = _kv8_rows(c, k, v)
-    _check(lib().moe_kv8_read(ctypes.byref(c), ctypes.byref(r), _ints(cu_tokens, "cu_tokens", c.n_seqs + 1),
-                              _ints(start, "start", c.n_seqs), _err(err), _raw_stream(stream)))
-    _on(stream, k, v, pool, page_table, cu_tokens, start, err)
-    return k, v
+    return _kv8_move(lib().moe_kv8_read, pool, page_table, cu_tokens, start, n_tokens, dtype, k, v, err, stream)
 
 
 def kv8_attention_workspace(n_seqs: int, T: int, n_heads: int, n_kv_heads: int, head_dim: int,
                             device="cuda") -> torch.Tensor:
-    """A zeroed workspace for kv8_attention calls of these sizes or smaller ones, to be kept between
-    calls (one for each stream that calls run on at the same time)."""
+    """A workspace for kv8_attention calls of these sizes or smaller ones, to be kept between calls
+    (one for each stream that calls run on at the same time)."""
     n = int(lib().moe_kv8_attention_workspace_bytes(n_seqs, T, n_heads, n_kv_heads, head_dim))
     if not n:
         raise MoeError(strerror(-3))
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def kv8_attention(q, pool, page_table, lens, scale=None, window=0, tree=None, workspace=None, out=None, lse=None,
@@ -456,31 +476,30 @@ def kv8_attention(q, pool, page_table, lens, scale=None, window=0, tree=None, wo
     [sequences, T], bit j of tree[b, t] lets query t see window token j (else: causal). Returns out
     [sequences, T, heads, head_dim] of q's type, and with_lse (or a given lse) also the log of the
     softmax sums, fp32 [sequences, T, heads]; a query that sees nothing gives zeros and -inf."""
-    c = _kv8_cache(pool, page_table)
-    if q.dim() != 4 or q.shape[0] != c.n_seqs or q.shape[3] != c.head_dim or q.stride(3) != 1:
-        raise MoeError(f"q: [{c.n_seqs}, T, heads, {c.head_dim}], contiguous in the last dimension, expected")
-    B, T, hq, D = q.shape
-    if workspace is None or out is None or (with_lse and lse is None):
-        with torch.cuda.stream(stream):
-            if workspace is None:
-                workspace = kv8_attention_workspace(B, T, hq, c.n_kv_heads, D, q.device)
-            if out is None:
-                out = torch.empty((B, T, hq, D), dtype=q.dtype, device=q.device)
-            if with_lse and lse is None:
-                lse = torch.empty((B, T, hq), dtype=torch.float32, device=q.device)
-    if out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+    c, dev = _kv8_cache(pool, page_table)
+    shape, qs = q.shape, q.stride()
+    if len(shape) != 4 or shape[0] != c[8] or shape[3] != c[3] or qs[3] != 1:
+        raise MoeError(f"q: [{c[8]}, T, heads, {c[3]}], contiguous in the last dimension, expected")
+    B, T, hq, D = shape
+    if workspace is None:
+        workspace = _empty(stream, (max(16, lib().moe_kv8_attention_workspace_bytes(B, T, hq, c[2], D)),), torch.uint8, q.device)
+    if out is None:
+        out = _empty(stream, shape, q.dtype, q.device)
+    elif out.dtype is not q.dtype or out.shape != shape or not out.is_contiguous():
         raise MoeError("out: contiguous, of q's shape and type, expected")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, T, hq) or not lse.is_contiguous()):
+    if lse is None:
+        if with_lse:
+            lse = _empty(stream, (B, T, hq), torch.float32, q.device)
+    elif lse.dtype is not torch.float32 or lse.shape != (B, T, hq) or not lse.is_contiguous():
         raise MoeError("lse: contiguous float32 [sequences, T, heads] expected")
     if not workspace.is_contiguous():
         raise MoeError("workspace: a contiguous tensor expected")
-    a = KV8AttentionC(c, _ptr(q), _elem(q), T, hq, q.stride(0), q.stride(1), q.stride(2),
-                      _ints(lens, "lens", B), None if tree is None else _ints(tree, "tree", B * T), window,
-                      D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse) or None, _ptr(workspace),
-                      workspace.numel() * workspace.element_size(), _err(err))
-    _check(lib().moe_kv8_attention(ctypes.byref(a), _raw_stream(stream)))
-    _on(stream, q, pool, page_table, lens, tree, out, lse, workspace, err)
-    return (out, lse) if lse is not None else out
+    a = _pack_attn(*c, _ptr(q, dev), _elem(q), T, hq, qs[0], qs[1], qs[2], _ints(lens, "lens", B, dev),
+                   0 if tree is None else _ints(tree, "tree", B * T, dev), window, D ** -0.5 if scale is None else scale,
+                   _ptr(out, dev), 0 if lse is None else _ptr(lse, dev), _ptr(workspace, dev), workspace.nbytes,
+                   _err(err, dev))
+    _launch(lib().moe_kv8_attention, dev, stream, (q, pool, page_table, lens, tree, out, lse, workspace, err), a)
+    return out if lse is None else (out, lse)
 
 
 def add_rms_norm_q8_1(x, weight, residual=None, eps=1e-6, sum_out=None, y=None, xq=None, with_y=False, stream=None):
@@ -488,47 +507,45 @@ def add_rms_norm_q8_1(x, weight, residual=None, eps=1e-6, sum_out=None, y=None, 
     x, residual [rows, cols] of one type, weight [cols]. Returns (sum, y, xq): h in x's type (None
     without a residual, unless sum_out is given; sum_out may be the residual itself), y in x's type
     (with_y or a given y, else None), xq uint8 [rows, cols/32, 36]."""
-    if x.dim() != 2 or x.stride(1) != 1 or weight.shape != x.shape[1:] or not weight.is_contiguous():
+    dev, shape, dtype, device = _device(x), x.shape, x.dtype, x.device
+    if len(shape) != 2 or x.stride(1) != 1 or weight.shape != shape[1:] or not weight.is_contiguous():
         raise MoeError("x: [rows, cols] with contiguous rows, weight: contiguous [cols], expected")
-    rows, cols = x.shape
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or residual.stride(1) != 1):
-        raise MoeError("residual: x's shape and type, with contiguous rows, expected")
-    with_sum = residual is not None and sum_out is None
-    if with_sum or (with_y and y is None) or xq is None:
-        with torch.cuda.stream(stream):
-            if with_sum:
-                sum_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-            if with_y and y is None:
-                y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-            if xq is None:
-                xq = torch.empty((rows, cols // 32, 36), dtype=torch.uint8, device=x.device)
+    rows, cols = shape
+    if residual is not None:
+        if residual.shape != shape or residual.dtype is not dtype or residual.stride(1) != 1:
+            raise MoeError("residual: x's shape and type, with contiguous rows, expected")
+        if sum_out is None:
+            sum_out = _empty(stream, shape, dtype, device)
+    if y is None and with_y:
+        y = _empty(stream, shape, dtype, device)
     for t in (sum_out, y):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or not t.is_contiguous()):
+        if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()):
             raise MoeError("sum_out, y: contiguous, of x's shape and type, expected")
-    if xq.dtype != torch.uint8 or xq.shape != (rows, cols // 32, 36) or not xq.is_contiguous():
+    if xq is None:
+        xq = _empty(stream, (rows, cols // 32, 36), torch.uint8, device)
+    elif xq.dtype is not torch.uint8 or xq.shape != (rows, cols // 32, 36) or not xq.is_contiguous():
         raise MoeError("xq: contiguous uint8 [rows, cols/32, 36] expected")
-    c = NormCallC(_ptr(x), _ptr(residual) or None, _ptr(weight), _ptr(sum_out) or None, _ptr(y) or None,
-                  _ptr(xq) or None, _elem(x), _elem(weight), rows, x.stride(0),
-                  0 if residual is None else residual.stride(0), cols, eps)
     if rows:
-        _check(lib().moe_add_rms_norm_q8_1(ctypes.byref(c), _raw_stream(stream)))
-        _on(stream, x, residual, weight, sum_out, y, xq)
+        c = _pack_norm(x.data_ptr(), 0 if residual is None else _ptr(residual, dev), _ptr(weight, dev),
+                       0 if sum_out is None else _ptr(sum_out, dev), 0 if y is None else _ptr(y, dev), _ptr(xq, dev),
+                       _elem(x), _elem(weight), rows, x.stride(0) if rows > 1 else cols,
+                       0 if residual is None else residual.stride(0) if rows > 1 else cols, cols, eps)
+        _launch(lib().moe_add_rms_norm_q8_1, dev, stream, (x, residual, weight, sum_out, y, xq), c)
     return sum_out, y, xq
 
 
 def dequantize_q8_1(xq, dtype=torch.float32, out=None, stream=None):
     """The values that q8_1 rows [rows, cols/32, 36] stand for, [rows, cols] of `dtype`."""
-    if xq.dtype != torch.uint8 or xq.dim() != 3 or xq.shape[2] != 36 or not xq.is_contiguous():
+    dev, shape = _device(xq), xq.shape
+    if xq.dtype is not torch.uint8 or len(shape) != 3 or shape[2] != 36 or not xq.is_contiguous():
         raise MoeError("xq: contiguous uint8 [rows, cols/32, 36] expected")
-    rows, cols = xq.shape[0], xq.shape[1] * 32
+    rows, cols = shape[0], shape[1] * 32
     if out is None:
-        with torch.cuda.stream(stream):
-            out = torch.empty((rows, cols), dtype=dtype, device=xq.device)
-    if out.shape != (rows, cols) or not out.is_contiguous():
+        out = _empty(stream, (rows, cols), dtype, xq.device)
+    elif out.shape != (rows, cols) or not out.is_contiguous():
         raise MoeError("out: contiguous [rows, cols] expected")
     if rows:
-        _check(lib().moe_dequantize_q8_1(_ptr(xq), rows, cols, _ptr(out), _elem(out), _raw_stream(stream)))
-        _on(stream, xq, out)
+        _launch(lib().moe_dequantize_q8_1, dev, stream, (xq, out), xq.data_ptr(), rows, cols, _ptr(out, dev), _elem(out))
     return out
 
 
