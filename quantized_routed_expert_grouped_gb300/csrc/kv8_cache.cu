@@ -1,4 +1,18 @@
 // kv8_cache.cu - quantising keys and values into the paged 8-bit cache, and reading them back.
+//
+// Write: scale = max |x| / 127 over a block's tokens and dims, code = rint(x * (1 / scale)) + 128; where a
+// block keeps earlier tokens, scale = max(old, new) and their codes become rint((c - 128) * (old / scale)) + 128.
+// Read: (code - 128) * scale. Every step is one fp32 operation, so the results are the same bits for any
+// layout of the work.
+//
+// Both are bound by memory: a value costs its own size and one byte, and a few operations (a product, an
+// addition that rounds and moves the code into the low byte, a byte permute). Write: one CTA per
+// (block, head) holds all of the block's new keys and values in registers between the maximum and the
+// codes, so they are read once, with D / 8 vectors per thread in flight. Read: one warp per (block, head).
+// Keys: a lane's 16-byte (fp32: 32-byte) vector of one token becomes eight consecutive bytes of the
+// record, 256 bytes a warp. Values are stored by dim: a warp takes 16 dims of the block's 32 tokens
+// (lane = token, so that every lane's sector is read whole) and turns its 512 bytes in shared memory; the
+// read turns blocks of eight dims and four tokens in registers.
 #include "internal.h"
 #include "kv8.cuh"
 #include "kv8_api.h"
@@ -16,99 +30,285 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 
+// Eight consecutive elements as they lie in memory.
 template <int TYPE>
+struct Raw8 {
+    static constexpr int kWords = 2 * static_cast<int>(sizeof(typename Elem<TYPE>::T));
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const typename Elem<TYPE>::T* p, bool vec) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        } else if (TYPE == MOE_F32) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                w[i] = __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i) |
+                       static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1)) << 16;
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if (TYPE == MOE_F32) return __uint_as_float(w[e & (kWords - 1)]);
+        const uint32_t x = w[e >> 1];
+        if (TYPE == MOE_BF16) return __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16);
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(e & 1 ? x >> 16 : x & 0xffffu)));
+    }
+    __device__ __forceinline__ float amax(float m) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(get(e)));
+        return m;
+    }
+};
+
+// x * inv rounded to an integer (ties to even) in the low byte of the result, plus 128: |x * inv| <= 127
+// up to two roundings, so adding 1.5 * 2^23 + 128 leaves the integer in the low bits.
+__device__ __forceinline__ uint32_t code_word(float x, float inv) {
+    return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.0f + 128.0f));
+}
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return prmt(prmt(a, b, 0x0040u), prmt(c, d, 0x0040u), 0x5410u);
+}
+// byte i of w, a code, as code - 128
+__device__ __forceinline__ float code_value(uint32_t w, int i) {
+    return __fadd_rn(__uint_as_float(prmt(w, 0x4b000000u, 0x7440u + i)), -8388736.0f);  // 2^23 + 128
+}
+
+struct Scales {
+    float scale, inv, ratio;
+    bool grew;
+};
+__device__ __forceinline__ Scales block_scale(float amax, float old) {
+    Scales s;
+    s.scale = max_nan(old, amax < kKvTiny ? 0.0f : __fdiv_rn(amax, 127.0f));
+    if (!(s.scale <= 3.4028234e38f)) s.scale = __int_as_float(0x7fffffff);
+    const bool some = s.scale > 0.0f;
+    s.inv = some ? __fdiv_rn(1.0f, s.scale) : 0.0f;
+    s.ratio = some ? __fdiv_rn(old, s.scale) : 0.0f;
+    s.grew = s.scale != old;
+    return s;
+}
+// four codes under a larger scale (a block without one holds zeros)
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+    return pack4(code_word(code_value(w, 0), ratio), code_word(code_value(w, 1), ratio), code_word(code_value(w, 2), ratio),
+                 code_word(code_value(w, 3), ratio));
+}
+
+// NB = D / 32.
+template <int TYPE, int NB>
 __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<const typename Elem<TYPE>::T> K,
                                                              KvRows<const typename Elem<TYPE>::T> V,
                                                              int64_t n_tokens, const int32_t* cu, const int32_t* start,
                                                              int32_t* err) {
-    __shared__ float red[4];
-    const int h = blockIdx.y, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const KvSlot s = kv8_slot(blockIdx.x, cu, start, c.n_seqs, n_tokens, err);
+    constexpr int D = NB * 32, kVU = 2 * NB, kVW = (kVU + 3) / 4;  // the values' units of 16 dims, a warp's share
+    __shared__ float red[2][4];
+    __shared__ __align__(16) uint8_t turn[4][512];
+    const int h = blockIdx.x % c.n_kv, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const KvSlot s = kv8_slot(blockIdx.x / c.n_kv, cu, start, c.n_seqs, n_tokens, err);
     if (s.b < 0) return;
     uint8_t* rec = kv8_record(c, s.b, s.blk, h, err);
     if (!rec) return;
-    const int pieces = c.D / 8;
-    for (int w = 0; w < 2; ++w) {  // keys, then values
-        const auto& R = w ? V : K;
-        const auto* base = R.p + s.row * R.ts + h * R.hs;
-        float amax = 0.0f, v[8];
-        for (int i = s.t0 * pieces + threadIdx.x; i < s.t1 * pieces; i += kThreads) {
-            const int t = i / pieces, d = (i - t * pieces) * 8;
-            load8<TYPE>(base + t * R.ts + d, R.vec, v);
-            for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(v[e]));
+    const auto* kb = K.p + s.row * K.ts + h * K.hs;
+    const auto* vb = V.p + s.row * V.ts + h * V.hs;
+    const float2 old2 = s.t0 > 0 ? *reinterpret_cast<const float2*>(rec) : make_float2(0.0f, 0.0f);
+
+    Raw8<TYPE> k[NB], v[kVW][2];
+    auto k_token = [&](int n) {  // of the thread's n-th eight bytes of the keys
+        const int tile = n * 4 + wid, jj = tile / NB, g = lane >> 2;
+        return 8 * (g >> 1) + 2 * jj + (g & 1);
+    };
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const int t = k_token(n), d = ((n * 4 + wid) % NB) * 32 + (lane & 3) * 8;
+        k[n].clear();
+        if (t >= s.t0 && t < s.t1) k[n].load(kb + t * K.ts + d, K.vec);
+    }
+#pragma unroll
+    for (int n = 0; n < kVW; ++n) {
+        const int unit = n * 4 + wid;
+        v[n][0].clear();
+        v[n][1].clear();
+        if (unit < kVU && lane >= s.t0 && lane < s.t1) {
+            v[n][0].load(vb + lane * V.ts + unit * 16, V.vec);
+            v[n][1].load(vb + lane * V.ts + unit * 16 + 8, V.vec);
         }
-        for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (lane == 0) red[wid] = amax;
-        __syncthreads();
-        amax = max_nan(max_nan(red[0], red[1]), max_nan(red[2], red[3]));
-        float* sp = reinterpret_cast<float*>(rec) + w;
-        const float old = s.t0 > 0 ? *sp : 0.0f;
-        __syncthreads();
-        float scale = amax < kKvTiny ? 0.0f : __fdiv_rn(amax, 127.0f);
-        scale = max_nan(old, scale);
-        if (!(scale <= 3.4028234e38f)) scale = __int_as_float(0x7fffffff);
-        const bool some = scale > 0.0f;
-        const float inv = some ? __fdiv_rn(1.0f, scale) : 0.0f, ratio = some ? __fdiv_rn(old, scale) : 0.0f;
-        for (int i = s.t0 * pieces + threadIdx.x; i < s.t1 * pieces; i += kThreads) {
-            const int t = i / pieces, d = (i - t * pieces) * 8;
-            load8<TYPE>(base + t * R.ts + d, R.vec, v);
-            for (int e = 0; e < 8; ++e) {
-                const int q = some ? __float2int_rn(fminf(fmaxf(__fmul_rn(v[e], inv), -127.0f), 127.0f)) : 0;
-                rec[w ? kv8_v_at(c.D, t, d + e) : kv8_k_at(c.D, t, d + e)] = static_cast<uint8_t>(q + 128);
+    }
+    float ak = 0.0f, av = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) ak = k[n].amax(ak);
+#pragma unroll
+    for (int n = 0; n < kVW; ++n) av = v[n][1].amax(v[n][0].amax(av));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        ak = max_nan(ak, __shfl_xor_sync(0xffffffffu, ak, o));
+        av = max_nan(av, __shfl_xor_sync(0xffffffffu, av, o));
+    }
+    if (lane == 0) {
+        red[0][wid] = ak;
+        red[1][wid] = av;
+    }
+    __syncthreads();  // also: every thread has read the old scales
+    ak = max_nan(max_nan(red[0][0], red[0][1]), max_nan(red[0][2], red[0][3]));
+    av = max_nan(max_nan(red[1][0], red[1][1]), max_nan(red[1][2], red[1][3]));
+    const Scales sk = block_scale(ak, old2.x), sv = block_scale(av, old2.y);
+    if (threadIdx.x == 0) *reinterpret_cast<float2*>(rec) = make_float2(sk.scale, sv.scale);
+
+    // a block without a scale (zeros, or not finite) holds codes 128
+    const bool some_k = sk.inv > 0.0f, some_v = sv.inv > 0.0f;
+    uint2* kr = reinterpret_cast<uint2*>(rec + kKvHead);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const int t = k_token(n);
+        uint2* at = kr + (n * 4 + wid) * 32 + lane;
+        if (t >= s.t0 && t < s.t1) {
+            uint2 q = make_uint2(0x80808080u, 0x80808080u);
+            if (some_k) {
+                q.x = pack4(code_word(k[n].get(0), sk.inv), code_word(k[n].get(1), sk.inv), code_word(k[n].get(2), sk.inv),
+                            code_word(k[n].get(3), sk.inv));
+                q.y = pack4(code_word(k[n].get(4), sk.inv), code_word(k[n].get(5), sk.inv), code_word(k[n].get(6), sk.inv),
+                            code_word(k[n].get(7), sk.inv));
+            }
+            *at = q;
+        } else if (t < s.t0 && sk.grew) {
+            uint2 q = *at;
+            q.x = some_k ? rescale4(q.x, sk.ratio) : 0x80808080u;
+            q.y = some_k ? rescale4(q.y, sk.ratio) : 0x80808080u;
+            *at = q;
+        }
+    }
+    uint8_t* vr = rec + kKvHead + kKvBlock * D;
+    if (s.t0 == 0 && s.t1 == 32) {
+#pragma unroll
+        for (int n = 0; n < kVW; ++n) {
+            const int unit = n * 4 + wid;
+            if (unit < kVU) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    turn[wid][e * 32 + lane] = some_v ? static_cast<uint8_t>(code_word(v[n][e >> 3].get(e & 7), sv.inv)) : 128;
+                __syncwarp();
+                reinterpret_cast<uint4*>(vr + unit * 512)[lane] = reinterpret_cast<const uint4*>(turn[wid])[lane];
+                __syncwarp();
             }
         }
-        if (s.t0 > 0 && scale != old)
-            for (int i = threadIdx.x; i < s.t0 * c.D; i += kThreads) {
-                const int t = i / c.D, d = i - t * c.D;
-                uint8_t* p = rec + (w ? kv8_v_at(c.D, t, d) : kv8_k_at(c.D, t, d));
-                const int q = some ? __float2int_rn(__fmul_rn(static_cast<float>(*p - 128), ratio)) : 0;
-                *p = static_cast<uint8_t>(q + 128);
+        return;
+    }
+    // part of a block: single bytes of the new tokens, words of the kept ones where the scale grew
+#pragma unroll
+    for (int n = 0; n < kVW; ++n) {
+        const int unit = n * 4 + wid;
+        if (unit < kVU && lane >= s.t0 && lane < s.t1) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                vr[(unit * 16 + e) * 32 + lane] = some_v ? static_cast<uint8_t>(code_word(v[n][e >> 3].get(e & 7), sv.inv)) : 128;
+        }
+    }
+    if (s.t0 > 0 && sv.grew) {
+        const int words = (s.t0 + 3) / 4;  // of a dim's 32 bytes
+        for (int i = threadIdx.x; i < D * words; i += kThreads) {
+            const int d = i / words, q = i - d * words;
+            uint32_t* at = reinterpret_cast<uint32_t*>(vr + d * 32) + q;
+            const uint32_t w = some_v ? rescale4(*at, sv.ratio) : 0x80808080u;
+            if (4 * q + 4 <= s.t0) {
+                *at = w;
+            } else {  // the word's last bytes belong to new tokens
+                for (int e = 0; 4 * q + e < s.t0; ++e) reinterpret_cast<uint8_t*>(at)[e] = static_cast<uint8_t>(w >> (8 * e));
             }
-        if (threadIdx.x == 0) *sp = scale;
+        }
     }
 }
 
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<typename Elem<TYPE>::T> K,
-                                                            KvRows<typename Elem<TYPE>::T> V, int64_t n_tokens,
+                                                            KvRows<typename Elem<TYPE>::T> V, int64_t n_tokens, int64_t n_work,
                                                             const int32_t* cu, const int32_t* start, int32_t* err) {
-    const int h = blockIdx.y;
-    const KvSlot s = kv8_slot(blockIdx.x, cu, start, c.n_seqs, n_tokens, err);
+    const int lane = threadIdx.x & 31;
+    const int64_t work = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (work >= n_work) return;
+    const int h = static_cast<int>(work % c.n_kv);
+    const KvSlot s = kv8_slot(work / c.n_kv, cu, start, c.n_seqs, n_tokens, err);
     if (s.b < 0) return;
     const uint8_t* rec = kv8_record(c, s.b, s.blk, h, err);
     if (!rec) return;
-    const int pieces = c.D / 8;
-    for (int w = 0; w < 2; ++w) {
-        const auto& R = w ? V : K;
-        auto* base = R.p + s.row * R.ts + h * R.hs;
-        const float scale = reinterpret_cast<const float*>(rec)[w];
-        for (int i = s.t0 * pieces + threadIdx.x; i < s.t1 * pieces; i += kThreads) {
-            const int t = i / pieces, d = (i - t * pieces) * 8;
-            float v[8];
-            for (int e = 0; e < 8; ++e)
-                v[e] = (rec[w ? kv8_v_at(c.D, t, d + e) : kv8_k_at(c.D, t, d + e)] - 128) * scale;
-            store8<TYPE>(base + t * R.ts + d, R.vec, v);
+    auto* kb = K.p + s.row * K.ts + h * K.hs;
+    auto* vb = V.p + s.row * V.ts + h * V.hs;
+    const int NB = c.D / 32;
+    const float2 sc = __ldg(reinterpret_cast<const float2*>(rec));
+    const int g = lane >> 2;
+    const uint2* kr = reinterpret_cast<const uint2*>(rec + kKvHead);
+#pragma unroll 2
+    for (int i = 0; i < NB; ++i) {
+        uint2 q[4];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) q[jj] = __ldg(kr + (jj * NB + i) * 32 + lane);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+            const int t = 8 * (g >> 1) + 2 * jj + (g & 1);
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(code_value(e < 4 ? q[jj].x : q[jj].y, e & 3), sc.x);
+            if (t >= s.t0 && t < s.t1) store8<TYPE>(kb + t * K.ts + i * 32 + (lane & 3) * 8, K.vec, x);
+        }
+    }
+    // lane (dims 8 dg .., tokens 4 tq ..) of 32 dims
+    const int tq = lane & 7, dg = lane >> 3;
+    const uint32_t* vr = reinterpret_cast<const uint32_t*>(rec + kKvHead + kKvBlock * c.D);
+#pragma unroll 2
+    for (int i = 0; i < NB; ++i) {
+        uint32_t q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = __ldg(vr + (i * 32 + dg * 8 + e) * 8 + tq);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = 4 * tq + j;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(code_value(q[e], j), sc.y);
+            if (t >= s.t0 && t < s.t1) store8<TYPE>(vb + t * V.ts + i * 32 + dg * 8, V.vec, x);
         }
     }
 }
 
 template <int TYPE>
 cudaError_t write_t(const KvCache& c, const moe_kv8_rows& r, const int32_t* cu, const int32_t* start, int32_t* err,
-                    bool kvec, bool vvec, dim3 grid, cudaStream_t st) {
+                    bool kvec, bool vvec, unsigned grid, cudaStream_t st) {
     using T = typename Elem<TYPE>::T;
     const KvRows<const T> K{static_cast<const T*>(r.k), r.k_token_stride, r.k_head_stride, kvec};
     const KvRows<const T> V{static_cast<const T*>(r.v), r.v_token_stride, r.v_head_stride, vvec};
-    kv8_write_kernel<TYPE><<<grid, kThreads, 0, st>>>(c, K, V, r.n_tokens, cu, start, err);
+    switch (c.D / 32) {
+#define MOE_KV8_CASE(NB) \
+    case NB: kv8_write_kernel<TYPE, NB><<<grid, kThreads, 0, st>>>(c, K, V, r.n_tokens, cu, start, err); break;
+        MOE_KV8_CASE(1)
+        MOE_KV8_CASE(2)
+        MOE_KV8_CASE(3)
+        MOE_KV8_CASE(4)
+        MOE_KV8_CASE(5)
+        MOE_KV8_CASE(6)
+        MOE_KV8_CASE(7)
+        MOE_KV8_CASE(8)
+#undef MOE_KV8_CASE
+    }
     return cudaGetLastError();
 }
 
 template <int TYPE>
 cudaError_t read_t(const KvCache& c, const moe_kv8_rows& r, const int32_t* cu, const int32_t* start, int32_t* err,
-                   bool kvec, bool vvec, dim3 grid, cudaStream_t st) {
+                   bool kvec, bool vvec, int64_t work, cudaStream_t st) {
     using T = typename Elem<TYPE>::T;
     const KvRows<T> K{static_cast<T*>(r.k), r.k_token_stride, r.k_head_stride, kvec};
     const KvRows<T> V{static_cast<T*>(r.v), r.v_token_stride, r.v_head_stride, vvec};
-    kv8_read_kernel<TYPE><<<grid, kThreads, 0, st>>>(c, K, V, r.n_tokens, cu, start, err);
+    const unsigned grid = static_cast<unsigned>((work + kThreads / 32 - 1) / (kThreads / 32));
+    kv8_read_kernel<TYPE><<<grid, kThreads, 0, st>>>(c, K, V, r.n_tokens, work, cu, start, err);
     return cudaGetLastError();
 }
 
@@ -116,7 +316,7 @@ cudaError_t read_t(const KvCache& c, const moe_kv8_rows& r, const int32_t* cu, c
 
 cudaError_t launch_kv8_write(const KvCache& c, const moe_kv8_rows& r, const int32_t* cu, const int32_t* start,
                              int32_t* err, bool kvec, bool vvec, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>(kv8_slots(r.n_tokens, c.n_seqs)), c.n_kv);
+    const unsigned grid = static_cast<unsigned>(kv8_slots(r.n_tokens, c.n_seqs) * c.n_kv);
     if (r.type == MOE_F32) return write_t<MOE_F32>(c, r, cu, start, err, kvec, vvec, grid, st);
     if (r.type == MOE_F16) return write_t<MOE_F16>(c, r, cu, start, err, kvec, vvec, grid, st);
     return write_t<MOE_BF16>(c, r, cu, start, err, kvec, vvec, grid, st);
@@ -124,10 +324,10 @@ cudaError_t launch_kv8_write(const KvCache& c, const moe_kv8_rows& r, const int3
 
 cudaError_t launch_kv8_read(const KvCache& c, const moe_kv8_rows& r, const int32_t* cu, const int32_t* start,
                             int32_t* err, bool kvec, bool vvec, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>(kv8_slots(r.n_tokens, c.n_seqs)), c.n_kv);
-    if (r.type == MOE_F32) return read_t<MOE_F32>(c, r, cu, start, err, kvec, vvec, grid, st);
-    if (r.type == MOE_F16) return read_t<MOE_F16>(c, r, cu, start, err, kvec, vvec, grid, st);
-    return read_t<MOE_BF16>(c, r, cu, start, err, kvec, vvec, grid, st);
+    const int64_t work = kv8_slots(r.n_tokens, c.n_seqs) * c.n_kv;
+    if (r.type == MOE_F32) return read_t<MOE_F32>(c, r, cu, start, err, kvec, vvec, work, st);
+    if (r.type == MOE_F16) return read_t<MOE_F16>(c, r, cu, start, err, kvec, vvec, work, st);
+    return read_t<MOE_BF16>(c, r, cu, start, err, kvec, vvec, work, st);
 }
 
 }  // namespace moe

@@ -3,10 +3,14 @@
 //
 //   h = x + residual;  y = h * (1 / sqrt(mean(h^2) + eps)) * weight;  xq = q8_1(y)
 //
-// One CTA per row; a thread holds eight consecutive values of up to four chunks in registers, so
-// the row is read once and the outputs may overwrite the inputs. A q8_1 block of 32 values is four
+// One CTA per row; a thread holds eight consecutive values of C chunks in registers, so the row is
+// read once and the outputs may overwrite the inputs. A q8_1 block of 32 values is four
 // neighbouring threads. The sum of squares is fp32: per thread, then over the warp's lanes, then
 // over the warps in order.
+//
+// Bound by memory; what the kernel adds is latency (a row's loads, one barrier, its stores), which
+// other rows' CTAs cover: two chunks a thread keep eight 4096-column rows on an SM. The q8_1 codes are
+// round(y / d) with an IEEE quotient; a product with 1 / d decides all but those within 2^-10 of a tie.
 #include "internal.h"
 #include "kv8.cuh"
 #include "kv8_api.h"
@@ -15,7 +19,13 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxChunks = 4;
+// round-half-away(y / d) for |y| <= 127 d up to rounding, inv = 1 / d (IEEE)
+__device__ __forceinline__ int q8_1_code(float y, float d, float inv) {
+    const float r = __fmul_rn(y, inv);  // within 2^-15 of the quotient
+    const float n = rintf(r);
+    if (fabsf(fabsf(r - n) - 0.5f) > 9.765625e-4f) return static_cast<int>(n);
+    return static_cast<int>(roundf(__fdiv_rn(y, d)));
+}
 
 // the q8_1 block of four neighbouring lanes' values (32 in all): the lane's codes and header word
 __device__ __forceinline__ void quad_q8_1(const float (&y)[8], uint32_t (&code)[2], uint32_t& hdr) {
@@ -31,11 +41,13 @@ __device__ __forceinline__ void quad_q8_1(const float (&y)[8], uint32_t (&code)[
         asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(v));
     }
     const float d = __fdiv_rn(amax, 127.0f);
+    // 1 / d of a subnormal d may overflow: then every quotient is taken by division
+    const float inv = d > 1.1754944e-38f && d < 3.4028234e38f ? __fdiv_rn(1.0f, d) : __int_as_float(0x7fffffff);
     int S = 0;
     code[0] = code[1] = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const int q = d == 0.0f ? 0 : static_cast<int>(roundf(__fdiv_rn(y[e], d)));
+        const int q = d == 0.0f ? 0 : q8_1_code(y[e], d, inv);
         S += q;
         code[e >> 2] |= static_cast<uint32_t>(q & 255) << (8 * (e & 3));
     }
@@ -52,8 +64,8 @@ __device__ __forceinline__ void weight8(const void* w, int w_type, int col, floa
     else load8<MOE_BF16>(static_cast<const __nv_bfloat16*>(w) + col, true, v);
 }
 
-template <int TYPE>
-__global__ void __launch_bounds__(1024) add_rms_norm_q8_1_kernel(moe_norm_call c) {
+template <int TYPE, int C>
+__global__ void __launch_bounds__(1024) add_rms_norm_q8_1_kernel(const moe_norm_call c) {
     using E = Elem<TYPE>;
     using T = typename E::T;
     __shared__ float red[32];
@@ -61,21 +73,26 @@ __global__ void __launch_bounds__(1024) add_rms_norm_q8_1_kernel(moe_norm_call c
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const T* x = static_cast<const T*>(c.x) + row * c.x_stride;
     const T* r = c.residual ? static_cast<const T*>(c.residual) + row * c.residual_stride : nullptr;
-    float h[kMaxChunks][8], ss = 0.0f;
+    float h[C][8], ss = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kMaxChunks; ++k) {
+    for (int k = 0; k < C; ++k) {  // all of the row's loads before the arithmetic
         const int col = (k * blockDim.x + threadIdx.x) * 8;
-        if (col >= c.cols) continue;
-        load8<TYPE>(x + col, true, h[k]);
-        if (r) {
-            float v[8];
-            load8<TYPE>(r + col, true, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[k][e] += v[e];
+        for (int e = 0; e < 8; ++e) h[k][e] = 0.0f;
+        if (col < c.cols) {
+            load8<TYPE>(x + col, true, h[k]);
+            if (r) {
+                float v[8];
+                load8<TYPE>(r + col, true, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[k][e] += v[e];
+            }
         }
+    }
+#pragma unroll
+    for (int k = 0; k < C; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(h[k][e], h[k][e], ss);
-    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (lane == 0) red[wid] = ss;
@@ -84,7 +101,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_q8_1_kernel(moe_norm_call c
     for (int w = 0; w < nw; ++w) ss += red[w];
     const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(c.cols)) + c.eps));
 #pragma unroll
-    for (int k = 0; k < kMaxChunks; ++k) {
+    for (int k = 0; k < C; ++k) {
         // a warp's columns are whole q8_1 blocks, and lanes past the row carry zeros into its shuffles
         const int col = (k * blockDim.x + threadIdx.x) * 8;
         const bool in = col < c.cols;
@@ -128,15 +145,28 @@ __global__ void __launch_bounds__(256) dequantize_q8_1_kernel(const moe_q8_1* __
 
 }  // namespace
 
+namespace {
+
+template <int TYPE>
+cudaError_t norm_t(const moe_norm_call& c, cudaStream_t st) {
+    const int pieces = c.cols / 8;
+    const unsigned grid = static_cast<unsigned>(c.rows);
+    // few rows: as many threads as the row has pieces, for the shortest chain; many: two pieces a thread
+    const int chunks = pieces > 2048 ? 4 : pieces > 1024 || (c.rows > 304 && pieces >= 64) ? 2 : 1;
+    const int threads = ((pieces + chunks - 1) / chunks + 31) / 32 * 32;
+    if (chunks == 1) add_rms_norm_q8_1_kernel<TYPE, 1><<<grid, threads, 0, st>>>(c);
+    else if (chunks == 2) add_rms_norm_q8_1_kernel<TYPE, 2><<<grid, threads, 0, st>>>(c);
+    else add_rms_norm_q8_1_kernel<TYPE, 4><<<grid, threads, 0, st>>>(c);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_add_rms_norm_q8_1(const moe_norm_call& c, cudaStream_t st) {
     if (c.rows == 0) return cudaSuccess;
-    int threads = (c.cols / 8 + 31) / 32 * 32;
-    if (threads > 1024) threads = 1024;
-    const unsigned grid = static_cast<unsigned>(c.rows);
-    if (c.type == MOE_F32) add_rms_norm_q8_1_kernel<MOE_F32><<<grid, threads, 0, st>>>(c);
-    else if (c.type == MOE_F16) add_rms_norm_q8_1_kernel<MOE_F16><<<grid, threads, 0, st>>>(c);
-    else add_rms_norm_q8_1_kernel<MOE_BF16><<<grid, threads, 0, st>>>(c);
-    return cudaGetLastError();
+    if (c.type == MOE_F32) return norm_t<MOE_F32>(c, st);
+    if (c.type == MOE_F16) return norm_t<MOE_F16>(c, st);
+    return norm_t<MOE_BF16>(c, st);
 }
 
 cudaError_t launch_dequantize_q8_1(const moe_q8_1* xq, int64_t n_blocks, void* out, int type, cudaStream_t st) {
