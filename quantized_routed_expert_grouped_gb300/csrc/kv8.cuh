@@ -83,6 +83,58 @@ __device__ __forceinline__ void store8(typename Elem<TYPE>::T* p, bool vec, cons
     }
 }
 
+// max of non-negative values that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Eight consecutive elements as they lie in memory.
+template <int TYPE>
+struct Raw8 {
+    static constexpr int kWords = 2 * static_cast<int>(sizeof(typename Elem<TYPE>::T));
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const typename Elem<TYPE>::T* p, bool vec) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        } else if (TYPE == MOE_F32) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                w[i] = __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i) |
+                       static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1)) << 16;
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if (TYPE == MOE_F32) return __uint_as_float(w[e & (kWords - 1)]);
+        const uint32_t x = w[(e >> 1) & (kWords - 1)];
+        return TYPE == MOE_BF16 ? __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16) : half(e);
+    }
+    __device__ __forceinline__ float half(int e) const {  // of 16-bit words that hold fp16
+        const uint32_t x = w[(e >> 1) & (kWords - 1)];
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(e & 1 ? x >> 16 : x & 0xffffu)));
+    }
+    __device__ __forceinline__ float amax(float m) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(get(e)));
+        return m;
+    }
+};
+
 // Device copy of moe_kv8_cache.
 struct KvCache {
     uint8_t* pool;

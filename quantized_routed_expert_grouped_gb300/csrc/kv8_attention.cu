@@ -34,40 +34,55 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
     }
     const int64_t pf = attn_part_floats(p.g.RP, D), ml = static_cast<int64_t>(p.g.RP) * D + rr;
     auto part = [&](int j) { return p.parts + (2LL * (i0 + j) + (j == 0 && !head ? 1 : 0)) * pf; };
-    float M = -INFINITY, Ls = 0.0f;
-    for (int j = lane; j < cnt; j += 32) M = fmaxf(M, part(j)[ml]);
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float base = M == -INFINITY ? 0.0f : M;
-    for (int j = lane; j < cnt; j += 32) Ls += part(j)[ml + p.g.RP] * ex2(part(j)[ml] - base);
-    for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
-    const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
-    float4 v[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
-    for (int j0 = w; j0 < cnt; j0 += WPR * 4) {
-        float4 y[4][2];
-        float wt[4];
+    constexpr int kRun = 4;
+    float4 y[kRun][2];
+    float ym[kRun], yl[kRun];
+    auto fetch = [&](int j0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kRun; ++k) {
             const int j = j0 + k * WPR;
-            wt[k] = 0.0f;
+            ym[k] = -INFINITY;
+            yl[k] = 0.0f;
             if (j >= cnt) continue;
             const float* q = part(j);
-            wt[k] = q[ml + p.g.RP] * ex2(q[ml] - base) * inv;
+            ym[k] = q[ml];
+            yl[k] = q[ml + p.g.RP];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (i * 128 + lane * 4 < D) y[k][i] = *reinterpret_cast<const float4*>(q + static_cast<int64_t>(rr) * D + i * 128 + lane * 4);
         }
+    };
+    fetch(w);  // with the loads of all parts' m and l below
+    float M = -INFINITY, Ls = 0.0f;
+    for (int j = lane; j < cnt; j += 32) {  // (a lane's running sum, for its running maximum)
+        const float m = part(j)[ml], l = part(j)[ml + p.g.RP], nm = fmaxf(M, m), bs = nm == -INFINITY ? 0.0f : nm;
+        Ls = Ls * ex2(M - bs) + l * ex2(m - bs);
+        M = nm;
+    }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (j0 + k * WPR < cnt) {
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m = __shfl_xor_sync(0xffffffffu, M, o), l = __shfl_xor_sync(0xffffffffu, Ls, o);
+        const float nm = fmaxf(M, m), bs = nm == -INFINITY ? 0.0f : nm;
+        Ls = Ls * ex2(M - bs) + l * ex2(m - bs);
+        M = nm;
+    }
+    const float base = M == -INFINITY ? 0.0f : M, inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
+    float4 v[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+    for (int j0 = w; j0 < cnt; j0 += WPR * kRun) {
+        if (j0 != w) fetch(j0);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (i * 128 + lane * 4 < D) {
-                        v[i].x = fmaf(wt[k], y[k][i].x, v[i].x);
-                        v[i].y = fmaf(wt[k], y[k][i].y, v[i].y);
-                        v[i].z = fmaf(wt[k], y[k][i].z, v[i].z);
-                        v[i].w = fmaf(wt[k], y[k][i].w, v[i].w);
-                    }
-            }
+        for (int k = 0; k < kRun; ++k) {
+            if (j0 + k * WPR >= cnt) continue;
+            const float wt = yl[k] * ex2(ym[k] - base) * inv;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (i * 128 + lane * 4 < D) {
+                    v[i].x = fmaf(wt, y[k][i].x, v[i].x);
+                    v[i].y = fmaf(wt, y[k][i].y, v[i].y);
+                    v[i].z = fmaf(wt, y[k][i].z, v[i].z);
+                    v[i].w = fmaf(wt, y[k][i].w, v[i].w);
+                }
+        }
     }
     if (WPR > 1) {
 #pragma unroll

@@ -43,12 +43,12 @@ namespace moe {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kAttnStages = 32;          // ring stages of a CTA, at most
+constexpr int kAttnStages = 24;          // ring stages of a CTA, at most
 constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many CTAs
 // A row's reference m follows its maximum only once that is kAttnSlack (in powers of two) above it;
 // weights are held times 2^kAttnShift, so they stay below 2^15.
 constexpr float kAttnShift = 11.0f, kAttnSlack = 4.0f;
-constexpr int kAttnSegCost = 8;          // blocks that a segment's fixed work (queries, joining) costs
+constexpr int kAttnSegCost = 16;         // blocks that a segment's fixed work (queries, joining) costs
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 
 // Row tiles of a pass over the blocks: MT tiles of 16 rows per warp, RTW warps share a ring.
@@ -117,7 +117,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -206,8 +206,9 @@ struct AttnSmem {
         const int q = kTileQ * MT * RTW, o = RTW < kAttnWarps ? 16 * MT * RTW * kRowO * 4 : 0;
         return q > o ? q : o;
     }
-    // buffer (queries, then the joined rows), the warps' m and l, row factors and offsets, barriers and flags, scan, ring
-    static constexpr int kStats = 2 * kAttnWarps * 16 * MT * 8;
+    // buffer (queries, then the joined rows), the warps' m and l, row factors and offsets, output rows, the
+    // warps' pieces, barriers and flags, scan, ring
+    static constexpr int kStats = kAttnWarps * 16 * MT * 20 + 2 * kAttnWarps * static_cast<int>(sizeof(AttnPiece));
     static __host__ __device__ int fixed(int RTW) { return (buf_bytes(RTW) + kStats + kAttnStages * 20 + 128 + 15) / 16 * 16; }
 };
 
@@ -224,7 +225,9 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
     float* buf = reinterpret_cast<float*>(sm);
     float2* stat = reinterpret_cast<float2*>(sm + L::buf_bytes(RTW));        // [warps][16 MT]: m, l
     float2* qf = stat + kAttnWarps * 16 * MT;                                // [RP]: a row's factor and offset
-    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uintptr_t>(qf + 16 * MT * kAttnWarps));  // [NG * S]
+    int* orow = reinterpret_cast<int*>(qf + 16 * MT * kAttnWarps);           // [RP]: a row's (token, head) in out, -1: none
+    AttnPiece* pieces = reinterpret_cast<AttnPiece*>(orow + 16 * MT * kAttnWarps) + 2 * wid;  // computed, issued
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<AttnPiece*>(orow + 16 * MT * kAttnWarps) + 2 * kAttnWarps);  // [NG * S]
     uint64_t* empty = full + kAttnStages;
     int* flag = reinterpret_cast<int*>(empty + kAttnStages);                          // [NG * S]: the stage holds a record
     int64_t* scan = reinterpret_cast<int64_t*>(flag + kAttnStages);                   // [8]
@@ -301,38 +304,60 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
     }
     __syncthreads();
 
-    AttnPiece x;  // the piece being computed
-    x.b = *found;
-    attn_seq(a, x.b, x.len, x.first, x.n, false);
     {
+        AttnPiece x;
+        x.b = *found;
+        attn_seq(a, x.b, x.len, x.first, x.n, false);
         const int64_t off = *found_off;
         x.seg = static_cast<int>(off / attn_cost(x.n));
         attn_take(x, off - static_cast<int64_t>(x.seg) * attn_cost(x.n), u1 - u0);
         if (x.blk == x.end) return;  // the range ends within a segment's fixed part
+        if (lane == 0) pieces[0] = pieces[1] = x;
+        __syncwarp();
     }
 
+    // ---- queries of a piece: two rows of a lane are loaded ahead, the others with the conversion
+    constexpr int LPR = D <= 128 ? 16 : 32, RPW = 32 / LPR;  // lanes per row, rows of a warp at once
+    constexpr int kStep = kAttnWarps * RPW;                   // rows of the CTA at once
+    const int qr = wid * RPW + lane / LPR, pc = lane % LPR;   // the lane's first row; its eight dims: 8 pc ..
+    using Q8 = Raw8<SPLIT ? MOE_F32 : MOE_BF16>;
+    auto load_q = [&](Q8& v, int b, int seg, int rr) {
+        const int kv = seg / p.g.RB, r = (seg - kv * p.g.RB) * RP + rr;
+        v.clear();
+        if (pc < kND && rr < RP && r < p.R) {
+            const int t = r / a.G, h = kv * a.G + r - t * a.G;
+            const int64_t at = b * a.qs + t * a.qt + h * a.qh + pc * 8;
+            v.load(static_cast<const typename Elem<SPLIT ? MOE_F32 : MOE_BF16>::T*>(a.q) + at, a.qvec);
+        }
+    };
+    Q8 q0, q1;
+    load_q(q0, pieces[0].b, pieces[0].seg, qr);
+    load_q(q1, pieces[0].b, pieces[0].seg, qr + kStep);
+
     // ---- copies: the group's first warp issues its blocks S ahead of the arithmetic
-    AttnPiece ip = x;
-    int iu = ip.blk + grp, ik = 0, is = 0, iph = 1, pgi = 32;  // next block, copies issued, stage and its phase
+    int iu = pieces[1].blk + grp, iend = pieces[1].end, ik = 0, is = 0, iph = 1, pgi = 32;  // next block, copies issued, stage, phase
     int64_t src = -1;                                           // records of the next 32 blocks, in the lanes
     bool more = rt == 0;
     auto issue = [&]() {
         if (!more) return;
-        while (iu >= ip.end) {
-            if (!attn_next(p, ip)) {
-                more = false;
-                return;
-            }
-            iu = ip.blk + grp;
+        while (iu >= iend) {
+            AttnPiece t = pieces[1];
+            more = attn_next(p, t);
+            if (!more) return;
+            __syncwarp();
+            if (lane == 0) pieces[1] = t;
+            __syncwarp();
+            iu = t.blk + grp;
+            iend = t.end;
             pgi = 32;
         }
         if (pgi == 32) {
             const int u = iu + lane * NG;
             src = -1;
-            if (u < ip.end) {
-                const int pi = u / a.c.page_blocks, page = __ldg(a.c.table + ip.b * a.c.table_stride + pi);
+            if (u < iend) {
+                const int pi = u / a.c.page_blocks, page = __ldg(a.c.table + pieces[1].b * a.c.table_stride + pi);
                 if (page >= 0 && page < a.c.n_pages)
-                    src = (static_cast<int64_t>(page) * a.c.n_kv + ip.seg / p.g.RB) * a.c.page_blocks + u - pi * a.c.page_blocks;
+                    src = (static_cast<int64_t>(page) * a.c.n_kv + pieces[1].seg / p.g.RB) * a.c.page_blocks + u - pi * a.c.page_blocks;
             }
             pgi = 0;
         }
@@ -366,73 +391,62 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
     int cs = 0, cph = 0, landed = 0;  // the stage to consume and its phase; copies seen to land
     bool lost = false;
     for (int piece = 0;; ++piece) {
-        const int kv = x.seg / p.g.RB, rb = x.seg - kv * p.g.RB;
+        const int xb = pieces[0].b, xseg = pieces[0].seg, kv = xseg / p.g.RB, rb = xseg - kv * p.g.RB;
+        const int rows = min(RP, p.R - rb * RP);
         // ---- queries: shifted by a power of two into fp16's range, stored as the lanes take them
-        {
-            constexpr int LPR = D <= 128 ? 16 : 32, RPW = 32 / LPR;  // lanes per row, rows of a warp at once
-            const int sub = lane / LPR, pc = lane - sub * LPR;      // the lane's eight dims: 8 pc ..
-            const bool in = pc < kND;
-            for (int r0 = (wid * RPW + sub); r0 < RP; r0 += kAttnWarps * RPW * 2) {
-                float v[2][8];
-                bool ok[2];
+        for (int r0 = qr; r0 < RP; r0 += 2 * kStep) {
+            if (r0 != qr) {
+                load_q(q0, xb, xseg, r0);
+                load_q(q1, xb, xseg, r0 + kStep);
+            }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = rb * RP + r0 + i * kAttnWarps * RPW;
-                    ok[i] = in && r0 + i * kAttnWarps * RPW < RP && r < p.R;
+            for (int i = 0; i < 2; ++i) {
+                const Q8& v = i ? q1 : q0;
+                const int rr = r0 + i * kStep;
+                float y[8], amax = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-                    if (ok[i]) {
-                        const int t = r / a.G, h = kv * a.G + r - t * a.G;
-                        const int64_t at = x.b * a.qs + t * a.qt + h * a.qh + pc * 8;
-                        if (SPLIT) load8<MOE_F32>(static_cast<const float*>(a.q) + at, a.qvec, v[i]);
-                        else if (p.out_type == MOE_F16) load8<MOE_F16>(static_cast<const __half*>(a.q) + at, a.qvec, v[i]);
-                        else load8<MOE_BF16>(static_cast<const __nv_bfloat16*>(a.q) + at, a.qvec, v[i]);
+                for (int e = 0; e < 8; ++e) {
+                    y[e] = SPLIT || p.out_type == MOE_BF16 ? v.get(e) : v.half(e);
+                    const float z = fabsf(y[e]);
+                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(z));
+                }
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) {
+                    const float z = __shfl_xor_sync(0xffffffffu, amax, o);
+                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(z));
+                }
+                // amax * 2^k in [2^13, 2^14); a negative scale turns the query's sign
+                const bool fine = amax < INFINITY;
+                int k = fine && amax > 0.0f ? 13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127) : 0;
+                k = min(k, 120);
+                const float up = __int_as_float((k + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
+                float sum = 0.0f;
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y0 = fine ? y[2 * e] * up : 0.0f, y1 = fine ? y[2 * e + 1] * up : 0.0f;
+                    hi[e] = pack_h2(y0, y1);
+                    const float2 h2 = unpack_h2(hi[e]);
+                    sum += h2.x + h2.y;
+                    if (SPLIT) {
+                        lo[e] = pack_h2(y0 - h2.x, y1 - h2.y);
+                        const float2 l2 = unpack_h2(lo[e]);
+                        sum += l2.x + l2.y;
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int rr = r0 + i * kAttnWarps * RPW;
-                    float amax = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float y = fabsf(v[i][e]);
-                        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(y));
-                    }
-#pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) {
-                        const float y = __shfl_xor_sync(0xffffffffu, amax, o);
-                        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(y));
-                    }
-                    // amax * 2^k in [2^13, 2^14)
-                    const bool fine = amax < INFINITY;
-                    int k = fine && amax > 0.0f ? 13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127) : 0;
-                    k = min(k, 120);
-                    const float up = __int_as_float((k + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
-                    float sum = 0.0f;
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y0 = fine ? v[i][2 * e] * up : 0.0f, y1 = fine ? v[i][2 * e + 1] * up : 0.0f;
-                        hi[e] = pack_h2(y0, y1);
-                        const float2 h2 = unpack_h2(hi[e]);
-                        sum += h2.x + h2.y;
-                        if (SPLIT) {
-                            lo[e] = pack_h2(y0 - h2.x, y1 - h2.y);
-                            const float2 l2 = unpack_h2(lo[e]);
-                            sum += l2.x + l2.y;
-                        }
-                    }
-#pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (rr < RP && in) {
-                        const int tile = rr >> 4, row = rr & 15;
-                        const int at = ((tile * kNB + (pc >> 2)) * 2 + (row >> 3)) * 32 + (row & 7) * 4 + (pc & 3);
-                        qs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        if (SPLIT) qs[at + MT * RTW * D * 2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        if (pc == 0)
-                            qf[rr] = make_float2(fine ? fabsf(a.scale) * kLog2e * __int_as_float((127 - k) << 23) * 16777216.0f
-                                                      : __int_as_float(0x7fffffff),
-                                                 sum * (-128.0f / 16777216.0f));
+                for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (rr < RP && pc < kND) {
+                    const int tile = rr >> 4, row = rr & 15;
+                    const int at = ((tile * kNB + (pc >> 2)) * 2 + (row >> 3)) * 32 + (row & 7) * 4 + (pc & 3);
+                    qs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if (SPLIT) qs[at + MT * RTW * D * 2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (pc == 0) {
+                        qf[rr] = make_float2(fine ? fabsf(a.scale) * kLog2e * __int_as_float((127 - k) << 23) * 16777216.0f
+                                                  : __int_as_float(0x7fffffff),
+                                             sum * (-128.0f / 16777216.0f));
+                        const int r = rb * RP + rr, t = r / a.G;
+                        orow[rr] = r < p.R ? t * a.n_heads + kv * a.G + r - t * a.G : -1;
                     }
                 }
             }
@@ -457,8 +471,9 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                 off[mt][q] = f.y;
             }
         }
-        const int before_window = x.len - a.T;
-        for (int u = x.blk + grp; u < x.end; u += NG) {
+        const int xend = pieces[0].end, before_window = pieces[0].len - a.T;
+        const int behind = a.window > 0 ? pieces[0].len - 1 - a.window : -1;  // the last query does not see this far back
+        for (int u = pieces[0].blk + grp; u < xend; u += NG) {
             // (the lanes stay together; a wait that gives up ends the CTA's arithmetic)
             if (!lost && !__all_sync(0xffffffffu, mbar_try_wait(full + cs, cph)) &&
                 (__any_sync(0xffffffffu, *dead) || !__all_sync(0xffffffffu, mbar_wait_retry(full + cs, cph)))) {
@@ -493,26 +508,40 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                             lb[mt] = f[MT * RTW * D * 2 + 32];
                         }
                     }
+                    uint32_t kk[4][4];
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj) {
                         const uint2 w = *reinterpret_cast<const uint2*>(kp + (jj * kNB + i) * 256);
-                        uint32_t k0, k1, k2, k3;
-                        codes_sub(w.x, k0, k1);
-                        codes_sub(w.y, k2, k3);
+                        codes_sub(w.x, kk[jj][0], kk[jj][1]);
+                        codes_sub(w.y, kk[jj][2], kk[jj][3]);
+                    }
+                    // sums of different tokens in turn, so that no product waits for the one before it
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            mma_16816(sa[mt][jj], qa[mt].x, qb[mt].x, qa[mt].y, qb[mt].y, k0, k1);
-                            mma_16816(sa[mt][jj], qa[mt].z, qb[mt].z, qa[mt].w, qb[mt].w, k2, k3);
-                            if (SPLIT) {
-                                mma_16816(sa[mt][jj], la[mt].x, lb[mt].x, la[mt].y, lb[mt].y, k0, k1);
-                                mma_16816(sa[mt][jj], la[mt].z, lb[mt].z, la[mt].w, lb[mt].w, k2, k3);
-                            }
-                        }
+                    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            mma_16816(sa[mt][jj], qa[mt].x, qb[mt].x, qa[mt].y, qb[mt].y, kk[jj][0], kk[jj][1]);
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            mma_16816(sa[mt][jj], qa[mt].z, qb[mt].z, qa[mt].w, qb[mt].w, kk[jj][2], kk[jj][3]);
+                    if (SPLIT) {
+#pragma unroll
+                        for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+                                mma_16816(sa[mt][jj], la[mt].x, lb[mt].x, la[mt].y, lb[mt].y, kk[jj][0], kk[jj][1]);
+#pragma unroll
+                        for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+                                mma_16816(sa[mt][jj], la[mt].z, lb[mt].z, la[mt].w, lb[mt].w, kk[jj][2], kk[jj][3]);
                     }
                 }
                 // lane (g, c) holds rows g, g + 8 and tokens 8 c + 2 jj + e; an unseen one becomes -inf
                 const int t0 = u * kKvBlock;
-                const bool mask = t0 + kKvBlock > before_window || (a.window > 0 && t0 <= x.len - 1 - a.window);
+                const bool mask = t0 + kKvBlock > before_window || t0 <= behind;
                 if (mask) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
@@ -521,7 +550,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                             const int r = rb * RP + (rt * MT + mt) * 16 + q * 8 + g;
                             const int t = r / a.G, ps = r < p.R ? before_window + t : -1;
                             uint32_t bits = 0;
-                            if (a.tree && ps >= 0) bits = static_cast<uint32_t>(__ldg(a.tree + static_cast<int64_t>(x.b) * a.T + t));
+                            if (a.tree && ps >= 0) bits = static_cast<uint32_t>(__ldg(a.tree + static_cast<int64_t>(xb) * a.T + t));
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const int j = t0 + 8 * c + i, w = j - before_window;
@@ -611,20 +640,31 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                 if (mask) weights(std::true_type{});
                 else weights(std::false_type{});
                 const uint8_t* vp = rec + kKvHead + kKvBlock * D + g * 32 + c * 8;
+                constexpr int kRun = 4;  // dims' sums in turn, as above (kND is a multiple of 4)
 #pragma unroll
-                for (int i = 0; i < kND; ++i) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(vp + i * 256);
-                    uint32_t v0, v1, v2, v3;
-                    codes_h2(w.x, v0, v1);
-                    codes_h2(w.y, v2, v3);
+                for (int i0 = 0; i0 < kND; i0 += kRun) {
+                    uint32_t v[kRun][4];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma_16816(o[mt][i], pa[mt][0][0], pa[mt][0][1], pa[mt][0][2], pa[mt][0][3], v0, v1);
-                        mma_16816(o[mt][i], pa[mt][1][0], pa[mt][1][1], pa[mt][1][2], pa[mt][1][3], v2, v3);
-                        if (SPLIT) {
-                            mma_16816(o[mt][i], pl[mt][0][0], pl[mt][0][1], pl[mt][0][2], pl[mt][0][3], v0, v1);
-                            mma_16816(o[mt][i], pl[mt][1][0], pl[mt][1][1], pl[mt][1][2], pl[mt][1][3], v2, v3);
-                        }
+                    for (int i = 0; i < kRun; ++i) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(vp + (i0 + i) * 256);
+                        codes_h2(w.x, v[i][0], v[i][1]);
+                        codes_h2(w.y, v[i][2], v[i][3]);
+                    }
+#pragma unroll
+                    for (int xx = 0; xx < 2; ++xx)
+#pragma unroll
+                        for (int i = 0; i < kRun; ++i)
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+                                mma_16816(o[mt][i0 + i], pa[mt][xx][0], pa[mt][xx][1], pa[mt][xx][2], pa[mt][xx][3], v[i][2 * xx], v[i][2 * xx + 1]);
+                    if (SPLIT) {
+#pragma unroll
+                        for (int xx = 0; xx < 2; ++xx)
+#pragma unroll
+                            for (int i = 0; i < kRun; ++i)
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt)
+                                    mma_16816(o[mt][i0 + i], pl[mt][xx][0], pl[mt][xx][1], pl[mt][xx][2], pl[mt][xx][3], v[i][2 * xx], v[i][2 * xx + 1]);
                     }
                 }
             }
@@ -667,56 +707,77 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                 Ls[mt][q] = ll;
                 cf[mt][q] = ll == 0.0f ? 0.0f : vref * (ex2(m[mt][q] - bs) / ll);
             }
-        const bool whole = x.blk == x.first && x.end == x.first + x.n;
+        const AttnPiece* xp = pieces;
+        const bool whole = xp->blk == xp->first && xp->end == xp->first + xp->n;
         float* part = p.parts + (2LL * blockIdx.x + (piece ? 1 : 0)) * attn_part_floats(RP, D);
+        const int64_t orow0 = static_cast<int64_t>(xb) * a.T * a.n_heads;
+        // the next piece's first queries are on their way during the joining
+        AttnPiece nx = pieces[0];
+        const bool again = attn_next(p, nx);
+        __syncwarp();
+        if (lane == 0) pieces[0] = nx;
+        __syncwarp();
+        if (again) {
+            load_q(q0, nx.b, nx.seg, qr);
+            load_q(q1, nx.b, nx.seg, qr + kStep);
+        }
         if (grp == 0 && c == 0) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const int rr = (rt * MT + mt) * 16 + q * 8 + g, r = rb * RP + rr;
+                    const int rr = (rt * MT + mt) * 16 + q * 8 + g;
+                    if (rr >= rows) continue;
                     if (!whole) {
                         part[static_cast<int64_t>(RP) * D + rr] = M[mt][q];
                         part[static_cast<int64_t>(RP) * D + RP + rr] = Ls[mt][q];
-                    } else if (a.lse && r < p.R) {
-                        const int t = r / a.G, h = kv * a.G + r - t * a.G;
-                        a.lse[(static_cast<int64_t>(x.b) * a.T + t) * a.n_heads + h] =
-                            Ls[mt][q] == 0.0f ? -INFINITY : (M[mt][q] - kAttnShift) * kLn2 + logf(Ls[mt][q]);
+                    } else if (a.lse) {
+                        a.lse[orow0 + orow[rr]] = Ls[mt][q] == 0.0f ? -INFINITY : (M[mt][q] - kAttnShift) * kLn2 + logf(Ls[mt][q]);
                     }
                 }
         }
-        auto put = [&](int rr, int d, float v0, float v1) {  // two neighbouring dims of a row
+        auto put = [&](int rr, int d, float4 v) {  // four neighbouring dims of a row
             if (!whole) {
-                *reinterpret_cast<float2*>(part + static_cast<int64_t>(rr) * D + d) = make_float2(v0, v1);
+                *reinterpret_cast<float4*>(part + static_cast<int64_t>(rr) * D + d) = v;
                 return;
             }
-            const int r = rb * RP + rr;
-            if (r >= p.R) return;
-            const int t = r / a.G, h = kv * a.G + r - t * a.G;
-            const int64_t at = ((static_cast<int64_t>(x.b) * a.T + t) * a.n_heads + h) * D + d;
-            if (SPLIT) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(v0, v1);
-            else if (p.out_type == MOE_F16) *reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + at) = __floats2half2_rn(v0, v1);
-            else *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + at) = __floats2bfloat162_rn(v0, v1);
+            const int64_t at = (orow0 + orow[rr]) * D + d;
+            if (SPLIT) {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+            } else if (p.out_type == MOE_F16) {
+                *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + at) = make_uint2(pack_h2(v.x, v.y), pack_h2(v.z, v.w));
+            } else {
+                const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x, v.y), y1 = __floats2bfloat162_rn(v.z, v.w);
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+            }
         };
         if (NG == 1) {
+            // one warp holds the row: neighbouring lanes swap halves, so that each has four dims of a row
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int i = 0; i < kND; ++i)
-                        put((rt * MT + mt) * 16 + q * 8 + g, i * 8 + 2 * c, o[mt][i][2 * q] * cf[mt][q], o[mt][i][2 * q + 1] * cf[mt][q]);
-            __syncthreads();  // the queries have been read by all
+                for (int i = 0; i < kND; ++i) {
+                    const float x0 = o[mt][i][0] * cf[mt][0], x1 = o[mt][i][1] * cf[mt][0];
+                    const float y0 = o[mt][i][2] * cf[mt][1], y1 = o[mt][i][3] * cf[mt][1];
+                    const bool odd = c & 1;
+                    const float s0 = __shfl_xor_sync(0xffffffffu, odd ? x0 : y0, 1), s1 = __shfl_xor_sync(0xffffffffu, odd ? x1 : y1, 1);
+                    const int rr = (rt * MT + mt) * 16 + (odd ? 8 : 0) + g;
+                    if (rr < rows) put(rr, i * 8 + (c & 2) * 2, odd ? make_float4(s0, s1, y0, y1) : make_float4(x0, x1, s0, s1));
+                }
+            __syncthreads();  // the queries and rows have been read by all
         } else {
             for (int k = 0; k < NG; ++k) {
                 if (grp == k) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                        for (int q = 0; q < 2; ++q)
+                        for (int q = 0; q < 2; ++q) {
+                            const int r8 = (rt * MT + mt) * 16 + q * 8;
+                            if (r8 >= rows) continue;
 #pragma unroll
                             for (int i = 0; i < kND; ++i) {
-                                float2* d = reinterpret_cast<float2*>(buf + ((rt * MT + mt) * 16 + q * 8 + g) * L::kRowO + i * 8 + 2 * c);
+                                float2* d = reinterpret_cast<float2*>(buf + (r8 + g) * L::kRowO + i * 8 + 2 * c);
                                 float2 v = make_float2(o[mt][i][2 * q] * cf[mt][q], o[mt][i][2 * q + 1] * cf[mt][q]);
                                 if (k) {
                                     const float2 w = *d;
@@ -725,17 +786,17 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                                 }
                                 *d = v;
                             }
+                        }
                 }
                 __syncthreads();
             }
-            for (int i = threadIdx.x; i < RP * (D / 2); i += kAttnThreads) {
-                const int rr = i / (D / 2), d = (i - rr * (D / 2)) * 2;
-                const float2 v = *reinterpret_cast<const float2*>(buf + rr * L::kRowO + d);
-                put(rr, d, v.x, v.y);
+            for (int i = threadIdx.x; i < rows * (D / 4); i += kAttnThreads) {
+                const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4;
+                put(rr, d, *reinterpret_cast<const float4*>(buf + rr * L::kRowO + d));
             }
             __syncthreads();
         }
-        if (!attn_next(p, x)) break;
+        if (!again) break;
     }
     if (*dead && rt == 0)  // leave no copy of this CTA's in flight
         for (int k = landed; k < ik; ++k) mbar_wait_bounded(full + k % S, (k / S) & 1);
