@@ -115,14 +115,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// d = a b + c, a: the four words that a lane holds of 16 rows by 16
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint4 a, uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint4 a, uint32_t b0, uint32_t b1) { mma_16816(d, a, b0, b1, d); }
 
 __device__ __forceinline__ unsigned long long pk2(float x, float y) {
     return (static_cast<unsigned long long>(__float_as_uint(y)) << 32) | __float_as_uint(x);
@@ -167,6 +167,8 @@ __device__ __forceinline__ uint32_t pack_h2(float x, float y) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+
+__device__ __forceinline__ uint32_t& word(uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // A run of blocks [blk, end) of one segment within the CTA's range.
 struct AttnPiece {
@@ -335,11 +337,11 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
     load_q(q1, pieces[0].b, pieces[0].seg, qr + kStep);
 
     // ---- copies: the group's first warp issues its blocks S ahead of the arithmetic
-    int iu = pieces[1].blk + grp, iend = pieces[1].end, ik = 0, is = 0, iph = 1, pgi = 32;  // next block, copies issued, stage, phase
-    int64_t src = -1;                                           // records of the next 32 blocks, in the lanes
+    int iu = pieces[1].blk + grp, iend = pieces[1].end;       // the next blocks to look up, and the piece's end
+    int ik = 0, is = 0, iph = 1, at = 0, ready = 0;            // copies issued, stage, phase; blocks looked up
+    const uint8_t* src = nullptr;                              // records of up to 32 blocks, one a lane; nullptr: unreadable
     bool more = rt == 0;
-    auto issue = [&]() {
-        if (!more) return;
+    auto look_up = [&]() {
         while (iu >= iend) {
             AttnPiece t = pieces[1];
             more = attn_next(p, t);
@@ -349,37 +351,37 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
             __syncwarp();
             iu = t.blk + grp;
             iend = t.end;
-            pgi = 32;
         }
-        if (pgi == 32) {
-            const int u = iu + lane * NG;
-            src = -1;
-            if (u < iend) {
-                const int pi = u / a.c.page_blocks, page = __ldg(a.c.table + pieces[1].b * a.c.table_stride + pi);
-                if (page >= 0 && page < a.c.n_pages)
-                    src = (static_cast<int64_t>(page) * a.c.n_kv + pieces[1].seg / p.g.RB) * a.c.page_blocks + u - pi * a.c.page_blocks;
-            }
-            pgi = 0;
+        const int u = iu + lane * NG;
+        src = nullptr;
+        if (u < iend) {
+            const int pi = u / a.c.page_blocks, page = __ldg(a.c.table + pieces[1].b * a.c.table_stride + pi);
+            if (page >= 0 && page < a.c.n_pages)
+                src = a.c.pool + ((static_cast<int64_t>(page) * a.c.n_kv + pieces[1].seg / p.g.RB) * a.c.page_blocks + u - pi * a.c.page_blocks) * L::kRec;
         }
-        const int64_t r = __shfl_sync(0xffffffffu, src, pgi);
-        ++pgi;
-        if (RTW > 1 && ik >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(empty + is, iph))) {
+        at = 0;
+        ready = min(32, (iend - iu + NG - 1) / NG);
+        iu += 32 * NG;
+    };
+    auto issue = [&]() {
+        if (at == ready) {
+            if (more) look_up();
+            if (!more) return;
+        }
+        if (RTW > 1 && !__all_sync(0xffffffffu, mbar_wait_bounded(empty + is, iph))) {
             if (lane == 0) set_err(a.err, MOE_ERR_TIMEOUT);
             *dead = 1;
             more = false;
+            ready = at;
             return;
         }
-        if (lane == 0) {
-            flag[is] = r >= 0;
-            if (r >= 0) {
-                mbar_arrive_expect_tx(full + is, L::kRec);
-                bulk_g2s(ring + is * L::kRec, a.c.pool + r * L::kRec, L::kRec, full + is);
-            } else {
-                set_err(a.err, MOE_ERR_PAGE);
-                mbar_arrive_expect_tx(full + is, 0);
-            }
+        if (lane == at) {
+            flag[is] = src != nullptr;
+            mbar_arrive_expect_tx(full + is, src ? L::kRec : 0);
+            if (src) bulk_g2s(ring + is * L::kRec, src, L::kRec, full + is);
+            else set_err(a.err, MOE_ERR_PAGE);
         }
-        iu += NG;
+        ++at;
         ++ik;
         if (++is == S) {
             is = 0;
@@ -437,10 +439,14 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
 #pragma unroll
                 for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (rr < RP && pc < kND) {
+                    // a lane's operand of a step: (row g, dims 0-1), (row g + 8, 0-1), (g, 2-3), (g + 8, 2-3) of its four
                     const int tile = rr >> 4, row = rr & 15;
-                    const int at = ((tile * kNB + (pc >> 2)) * 2 + (row >> 3)) * 32 + (row & 7) * 4 + (pc & 3);
-                    qs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if (SPLIT) qs[at + MT * RTW * D * 2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    uint32_t* at = reinterpret_cast<uint32_t*>(qs + ((tile * kNB + (pc >> 2)) * 2) * 32 + (row & 7) * 4 + (pc & 3)) + (row >> 3);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        at[(e >> 1) * 128 + (e & 1) * 2] = hi[e];
+                        if (SPLIT) at[(e >> 1) * 128 + (e & 1) * 2 + MT * RTW * D * 8] = lo[e];
+                    }
                     if (pc == 0) {
                         qf[rr] = make_float2(fine ? fabsf(a.scale) * kLog2e * __int_as_float((127 - k) << 23) * 16777216.0f
                                                   : __int_as_float(0x7fffffff),
@@ -453,7 +459,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
         }
         __syncthreads();
 
-        float o[MT][kND][4], m[MT][2], nb[MT][2], fr[MT][2], off[MT][2], vref = 0.0f, vinv = 0.0f;
+        float o[MT][kND][4], m[MT][2], nb[MT][2], fr[MT][2], off[MT][4], vref = 0.0f, vinv = 0.0f;
         unsigned long long l[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                 l[mt][q] = 0;
                 const float2 f = qf[(rt * MT + mt) * 16 + q * 8 + g];
                 fr[mt][q] = f.x;
-                off[mt][q] = f.y;
+                off[mt][2 * q] = off[mt][2 * q + 1] = f.y;
             }
         }
         const int xend = pieces[0].end, before_window = pieces[0].len - a.T;
@@ -489,12 +495,6 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                 // scores, in units of the row's factor times k_scale: the codes enter as code * 2^-24, so the
                 // sum starts at -128 * 2^-24 times the query's sum
                 float sa[MT][4][4];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sa[mt][jj][e] = off[mt][e >> 1];
 #pragma unroll
                 for (int i = 0; i < kNB; ++i) {
                     uint4 qa[MT], qb[MT], la[MT], lb[MT];
@@ -520,23 +520,26 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
-                            mma_16816(sa[mt][jj], qa[mt].x, qb[mt].x, qa[mt].y, qb[mt].y, kk[jj][0], kk[jj][1]);
+                            {
+                                if (i == 0) mma_16816(sa[mt][jj], qa[mt], kk[jj][0], kk[jj][1], off[mt]);
+                                else mma_16816(sa[mt][jj], qa[mt], kk[jj][0], kk[jj][1]);
+                            }
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
-                            mma_16816(sa[mt][jj], qa[mt].z, qb[mt].z, qa[mt].w, qb[mt].w, kk[jj][2], kk[jj][3]);
+                            mma_16816(sa[mt][jj], qb[mt], kk[jj][2], kk[jj][3]);
                     if (SPLIT) {
 #pragma unroll
                         for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt)
-                                mma_16816(sa[mt][jj], la[mt].x, lb[mt].x, la[mt].y, lb[mt].y, kk[jj][0], kk[jj][1]);
+                                mma_16816(sa[mt][jj], la[mt], kk[jj][0], kk[jj][1]);
 #pragma unroll
                         for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt)
-                                mma_16816(sa[mt][jj], la[mt].z, lb[mt].z, la[mt].w, lb[mt].w, kk[jj][2], kk[jj][3]);
+                                mma_16816(sa[mt][jj], lb[mt], kk[jj][2], kk[jj][3]);
                     }
                 }
                 // lane (g, c) holds rows g, g + 8 and tokens 8 c + 2 jj + e; an unseen one becomes -inf
@@ -605,7 +608,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                 }
                 const float F = vref > 0.0f ? sc.y * vinv : sc.y;
                 // ---- weights: the lane's tokens 8 c + 4 xx + 0..3 feed product step xx
-                uint32_t pa[MT][2][4], pl[MT][2][4];
+                uint4 pa[MT][2], pl[MT][2];
                 auto weights = [&](auto masked) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
@@ -629,10 +632,10 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                                     if (s1 == -INFINITY) w.y = 0.0f;
                                 }
                                 const uint32_t h = pack_h2(w.x, w.y);
-                                pa[mt][jj >> 1][(jj & 1) * 2 + q] = h;
+                                word(pa[mt][jj >> 1], (jj & 1) * 2 + q) = h;
                                 if (SPLIT) {
                                     const float2 h2 = unpack_h2(h);
-                                    pl[mt][jj >> 1][(jj & 1) * 2 + q] = pack_h2(w.x - h2.x, w.y - h2.y);
+                                    word(pl[mt][jj >> 1], (jj & 1) * 2 + q) = pack_h2(w.x - h2.x, w.y - h2.y);
                                 }
                             }
                         }
@@ -656,7 +659,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                         for (int i = 0; i < kRun; ++i)
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt)
-                                mma_16816(o[mt][i0 + i], pa[mt][xx][0], pa[mt][xx][1], pa[mt][xx][2], pa[mt][xx][3], v[i][2 * xx], v[i][2 * xx + 1]);
+                                mma_16816(o[mt][i0 + i], pa[mt][xx], v[i][2 * xx], v[i][2 * xx + 1]);
                     if (SPLIT) {
 #pragma unroll
                         for (int xx = 0; xx < 2; ++xx)
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
                             for (int i = 0; i < kRun; ++i)
 #pragma unroll
                                 for (int mt = 0; mt < MT; ++mt)
-                                    mma_16816(o[mt][i0 + i], pl[mt][xx][0], pl[mt][xx][1], pl[mt][xx][2], pl[mt][xx][3], v[i][2 * xx], v[i][2 * xx + 1]);
+                                    mma_16816(o[mt][i0 + i], pl[mt][xx], v[i][2 * xx], v[i][2 * xx + 1]);
                     }
                 }
             }
