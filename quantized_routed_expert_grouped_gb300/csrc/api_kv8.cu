@@ -110,6 +110,7 @@ int moe_kv8_attention(const moe_kv8_attention_call* call, cudaStream_t stream) {
     a.lse = call->lse;
     a.workspace = call->workspace;
     a.err = call->err;
+    if (!attn_list_fits(a)) return MOE_E_CAP;
     return status(launch_kv8_attention(a, call->type, stream));
 }
 

@@ -25,6 +25,7 @@ struct AttnArgs {
     void* workspace;
     int32_t* err;
 };
+bool attn_list_fits(const AttnArgs& a);
 int64_t attn_workspace_bytes(int n_seqs, int T, int n_heads, int n_kv, int D);
 cudaError_t launch_kv8_attention(const AttnArgs& a, int type, cudaStream_t st);
 

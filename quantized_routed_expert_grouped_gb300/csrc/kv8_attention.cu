@@ -16,20 +16,24 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
     pdl_wait();
     const AttnArgs& a = p.a;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, sub = wid / WPR, w = wid - sub * WPR, D = a.c.D;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub;
-    const int64_t rows = static_cast<int64_t>(a.c.n_seqs) * a.T * a.n_heads;
+    const int row = blockIdx.x * kRows + sub, rows = a.c.n_seqs * a.T * a.n_heads;
     if (row >= rows) return;  // WPR == 1 where more than one row shares the CTA
-    const int h = static_cast<int>(row % a.n_heads), t = static_cast<int>(row / a.n_heads % a.T);
-    const int b = static_cast<int>(row / a.n_heads / a.T);
+    const int bt = row / a.n_heads, h = row - bt * a.n_heads, b = bt / a.T, t = bt - b * a.T;
     const int kv = h / a.G, r = t * a.G + h - kv * a.G, rb = r / p.g.RP, rr = r - rb * p.g.RP;
-    const int64_t at = p.plan[b], n = p.plan[b + 1] - at, chunk = p.plan[a.c.n_seqs + 1];
-    const int64_t s0 = at * p.segs + (static_cast<int64_t>(kv) * p.g.RB + rb) * n;  // n, s0 with the fixed part
+    const int at = p.plan[b], n = p.plan[b + 1] - at, chunk = p.plan[a.c.n_seqs + 1];
+    const int s0 = at * p.segs + (kv * p.g.RB + rb) * n;  // in the list
     int i0 = 0, cnt = 0;
     bool head = false;
     if (n > 0) {
-        i0 = static_cast<int>((s0 + kAttnSegCost) / chunk);  // the CTA of the first block
-        cnt = static_cast<int>((s0 + n - 1) / chunk) - i0 + 1;
-        head = s0 <= i0 * chunk;  // that CTA has no block of an earlier segment
+        if (chunk) {
+            i0 = (s0 + kAttnSegCost) / chunk;  // the CTA of the first block
+            cnt = (s0 + n - 1) / chunk - i0 + 1;
+            head = s0 <= static_cast<int64_t>(i0) * chunk;  // that CTA has no block of an earlier segment
+        } else {  // a CTA per part
+            i0 = s0;
+            cnt = n;
+            head = true;
+        }
         if (cnt == 1) return;
     }
     const int64_t pf = attn_part_floats(p.g.RP, D), ml = static_cast<int64_t>(p.g.RP) * D + rr;
@@ -106,13 +110,13 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
         const int d = i * 128 + lane * 4;
         if (d >= D) continue;
         if (p.out_type == MOE_F32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + d) = v[i];
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + static_cast<int64_t>(row) * D + d) = v[i];
         } else if (p.out_type == MOE_F16) {
-            __half2* q = reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + row * D + d);
+            __half2* q = reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + static_cast<int64_t>(row) * D + d);
             q[0] = __floats2half2_rn(v[i].x, v[i].y);
             q[1] = __floats2half2_rn(v[i].z, v[i].w);
         } else {
-            __nv_bfloat162* q = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d);
+            __nv_bfloat162* q = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<int64_t>(row) * D + d);
             q[0] = __floats2bfloat162_rn(v[i].x, v[i].y);
             q[1] = __floats2bfloat162_rn(v[i].z, v[i].w);
         }
@@ -125,6 +129,13 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
 int64_t attn_workspace_bytes(int n_seqs, int T, int n_heads, int n_kv, int D) {
     const AttnGeom g = attn_geom(T * (n_heads / n_kv), D);
     return attn_plan_bytes(n_seqs) + 2LL * kAttnMaxCtas * attn_part_floats(g.RP, D) * 4;
+}
+
+// The list of blocks, with the segments' fixed parts, is counted in 32 bits.
+bool attn_list_fits(const AttnArgs& a) {
+    const AttnGeom g = attn_geom(a.T * a.G, a.c.D);
+    const double most = 1.0 * a.c.n_seqs * a.c.n_kv * g.RB * (1.0 * a.c.max_pages * a.c.page_blocks + kAttnSegCost);
+    return most < 2147483647.0 - 2 * kAttnMaxCtas;
 }
 
 cudaError_t launch_attn_combine(const AttnPlan& p, cudaStream_t st) {
@@ -142,7 +153,7 @@ cudaError_t launch_kv8_attention(const AttnArgs& a, int type, cudaStream_t st) {
     p.g = attn_geom(p.R, a.c.D);
     p.segs = a.c.n_kv * p.g.RB;
     p.out_type = type;
-    p.plan = static_cast<int64_t*>(a.workspace);
+    p.plan = static_cast<int*>(a.workspace);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + attn_plan_bytes(a.c.n_seqs));
     const cudaError_t e = type == MOE_F32 ? launch_attn_f32(p, st) : launch_attn_16(p, st);
     return e == cudaSuccess ? launch_attn_combine(p, st) : e;

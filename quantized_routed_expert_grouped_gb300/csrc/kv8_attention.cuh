@@ -23,9 +23,9 @@
 // operands staged for tcgen05 would have to be widened to fp16 in shared memory first (twice the
 // bytes written and read there again).
 //
-// Split. The call's blocks, over all sequences, heads and groups of rows, are one list (each
-// (sequence, head, group) starts with kAttnSegCost units for its fixed work); each CTA takes an
-// equal range of it, and its four warps the range's blocks in turn, each with its own ring
+// Split. The call's blocks, over all sequences, heads and groups of rows, are one list. Few segments
+// (sequence, head, group) are cut into even parts, a CTA each; many into equal ranges of the list, in
+// which a segment starts with kAttnSegCost units for its fixed work. A CTA's four warps take its blocks in turn, each with its own ring
 // of shared-memory stages that bulk copies fill (one copy a block: keys, values and scales are
 // one record). A CTA joins its warps' results in warp order. Ranges that end inside a sequence
 // leave a part (rows, m, l) in the workspace, and a second kernel joins the parts in list order:
@@ -48,6 +48,7 @@ constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many C
 // A row's reference m follows its maximum only once that is kAttnSlack (in powers of two) above it;
 // weights are held times 2^kAttnShift, so they stay below 2^15.
 constexpr float kAttnShift = 11.0f, kAttnSlack = 4.0f;
+constexpr int kAttnMinPart = 8;          // blocks of a part, at least (but for a segment's remainder)
 constexpr int kAttnSegCost = 16;         // blocks that a segment's fixed work (queries, joining) costs
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 
@@ -64,8 +65,9 @@ inline __host__ __device__ AttnGeom attn_geom(int R, int D) {
     g.RB = (R + g.RP - 1) / g.RP;
     return g;
 }
-// workspace: int64 plan[n_seqs + 2] (cost before each sequence; the chunk), then two parts per CTA
-inline __host__ __device__ int64_t attn_plan_bytes(int n_seqs) { return (static_cast<int64_t>(n_seqs) + 2 + 1) / 2 * 16; }
+// workspace: int32 plan[n_seqs + 2] (what comes before each sequence in the list; the chunk, 0: a CTA
+// per part), then two parts per CTA
+inline __host__ __device__ int64_t attn_plan_bytes(int n_seqs) { return (static_cast<int64_t>(n_seqs) + 2 + 3) / 4 * 16; }
 inline __host__ __device__ int64_t attn_part_floats(int RP, int D) { return static_cast<int64_t>(RP) * (D + 2); }
 
 struct AttnPlan {
@@ -74,9 +76,8 @@ struct AttnPlan {
     int R, segs;     // rows of a key/value head; segments (head, pass) of a sequence
     int out_type;
     int stages;      // ring stages per group of RTW warps
-    int min_chunk;
     int smem;
-    int64_t* plan;
+    int* plan;
     float* parts;
 };
 
@@ -104,8 +105,28 @@ __device__ __forceinline__ void attn_seq(const AttnArgs& a, int b, int& len, int
     n = len > 0 ? ((len - 1) >> 5) + 1 - first : 0;
 }
 
-// What a segment of n blocks counts for in the list.
-__host__ __device__ __forceinline__ int64_t attn_cost(int n) { return n ? n + kAttnSegCost : 0; }
+// How the list is cut. By parts (tb > 0): a segment of n blocks takes ceil(n / tb) CTAs, which share it
+// evenly. By cost: a segment counts for kAttnSegCost + n, and the CTAs take equal ranges.
+struct AttnCut {
+    int tb, chunk;  // of the list per CTA; 1 by parts
+    __host__ __device__ __forceinline__ int cost(int n) const { return !n ? 0 : tb ? (n + tb - 1) / tb : n + kAttnSegCost; }
+};
+// blocks: of all segments; segs: segments that have any.
+// (The host keeps the whole list, at its longest, below 2^31.)
+__device__ __forceinline__ AttnCut attn_cut(int blocks, int segs, int ctas) {
+    AttnCut c;
+    c.tb = 0;
+    c.chunk = (blocks + segs * kAttnSegCost + ctas - 1) / ctas;
+    if (segs < ctas) {
+        int tb = (blocks + (ctas - segs) - 1) / (ctas - segs);  // then the parts are at most `ctas`
+        if (tb < kAttnMinPart) tb = kAttnMinPart;
+        if (tb <= c.chunk || tb <= kAttnMinPart) {
+            c.tb = tb;
+            c.chunk = 1;
+        }
+    }
+    return c;
+}
 
 #ifdef __CUDACC__
 
@@ -173,19 +194,17 @@ __device__ __forceinline__ uint32_t& word(uint4& v, int i) { return i == 0 ? v.x
 // A run of blocks [blk, end) of one segment within the CTA's range.
 struct AttnPiece {
     int b, seg, len, first, n, blk, end;
-    int64_t left;  // of the CTA's range after this piece, in units of cost
+    int left;  // of the CTA's range after this piece, in units of cost
 };
 
 // The rest of the CTA's range starts `off` into the current segment's kAttnSegCost + n units: its
 // blocks, and what is left after them. (A range that ends within the fixed part has no blocks here.)
-__device__ __forceinline__ void attn_take(AttnPiece& x, int64_t off, int64_t rest) {
-    const int64_t u = off > kAttnSegCost ? off - kAttnSegCost : 0;
-    const int64_t end = off + rest - kAttnSegCost;
-    x.blk = x.first + static_cast<int>(u);
-    x.end = x.first + static_cast<int>(end < u ? u : end < x.n ? end : x.n);
+__device__ __forceinline__ void attn_take(AttnPiece& x, int off, int rest) {
+    const int u = off > kAttnSegCost ? off - kAttnSegCost : 0, end = off + rest - kAttnSegCost;
+    x.blk = x.first + u;
+    x.end = x.first + (end < u ? u : end < x.n ? end : x.n);
     x.left = rest - (kAttnSegCost + x.n - off);
 }
-
 __device__ __forceinline__ bool attn_next(const AttnPlan& p, AttnPiece& x) {
     if (x.left <= kAttnSegCost) return false;  // no block of the next segment
     if (++x.seg == p.segs) {
@@ -209,13 +228,13 @@ struct AttnSmem {
         return q > o ? q : o;
     }
     // buffer (queries, then the joined rows), the warps' m and l, row factors and offsets, output rows, the
-    // warps' pieces, barriers and flags, scan, ring
+    // warps' pieces, barriers and flags, ring
     static constexpr int kStats = kAttnWarps * 16 * MT * 20 + 2 * kAttnWarps * static_cast<int>(sizeof(AttnPiece));
-    static __host__ __device__ int fixed(int RTW) { return (buf_bytes(RTW) + kStats + kAttnStages * 20 + 128 + 15) / 16 * 16; }
+    static __host__ __device__ int fixed(int RTW) { return (buf_bytes(RTW) + kStats + kAttnStages * 20 + 16 + 15) / 16 * 16; }
 };
 
 template <int D, int MT, bool SPLIT>
-__global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8_attention_kernel(const AttnPlan p) {
+__global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 3 : 2) kv8_attention_kernel(const AttnPlan p) {
     using L = AttnSmem<D, MT, SPLIT>;
     constexpr int kNB = D / 32, kND = D / 8;
     extern __shared__ __align__(128) uint8_t sm[];
@@ -232,93 +251,100 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
     uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<AttnPiece*>(orow + 16 * MT * kAttnWarps) + 2 * kAttnWarps);  // [NG * S]
     uint64_t* empty = full + kAttnStages;
     int* flag = reinterpret_cast<int*>(empty + kAttnStages);                          // [NG * S]: the stage holds a record
-    int64_t* scan = reinterpret_cast<int64_t*>(flag + kAttnStages);                   // [8]
-    volatile int* dead = reinterpret_cast<int*>(scan + 8);
-    int* found = reinterpret_cast<int*>(scan + 8) + 1;                       // b
-    int64_t* found_off = scan + 10;
+    volatile int* dead = flag + kAttnStages;                                 // a wait gave up
     uint8_t* ring = sm + L::fixed(RTW) + static_cast<int64_t>(grp) * S * L::kRec;
     full += grp * S;
     empty += grp * S;
     flag += grp * S;
 
     pdl_trigger();
-    // ---- the call's units and this CTA's range: a thread sums a run of sequences
-    const int B = a.c.n_seqs;
-    const int span = (B + kAttnThreads - 1) / kAttnThreads, b0 = min(B, static_cast<int>(threadIdx.x) * span), b1 = min(B, b0 + span);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        int len, first, n;
-        attn_seq(a, b, len, first, n, blockIdx.x == 0);
-        mine += attn_cost(n);
+    if (rt == 0) {
+        if (lane == 0) {
+            for (int i = 0; i < S; ++i) {
+                mbar_init(full + i, 1);
+                mbar_init(empty + i, RTW);
+            }
+            if (wid == 0) *dead = 0;
+            fence_barrier_init();
+        }
+        __syncwarp();
     }
-    int64_t incl = mine;
+    // ---- the list and this CTA's range: each warp sums the sequences for itself, a lane a run of them
+    const int B = a.c.n_seqs, span = (B + 31) / 32, b0 = min(B, lane * span), b1 = min(B, b0 + span);
+    AttnPiece x;
+    int blocks = 0, some = 0;
+    x.n = 0;
+    for (int b = b0; b < b1; ++b) {
+        attn_seq(a, b, x.len, x.first, x.n, blockIdx.x == 0 && wid == 0);
+        blocks += x.n;
+        some += x.n > 0;
+    }
+    const AttnCut cut = attn_cut(static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(blocks))) * p.segs,
+                                 static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(some))) * p.segs, gridDim.x);
+    int mine = 0;
+    if (span == 1) {  // the lane's one sequence is in x
+        mine = cut.cost(x.n);
+    } else {
+        for (int b = b0; b < b1; ++b) {
+            attn_seq(a, b, x.len, x.first, x.n, false);
+            mine += cut.cost(x.n);
+        }
+    }
+    int before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
     }
-    if (lane == 31) scan[wid] = incl;
-    if (threadIdx.x == 0) {
-        *dead = 0;
-        *found = -1;
-        for (int i = 0; i < S * NG; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, RTW);
-        }
-        fence_barrier_init();
-    }
-    __syncthreads();
-    int64_t total = 0, before = incl - mine;
-    for (int w = 0; w < kAttnWarps; ++w) {
-        if (w < wid) before += scan[w];
-        total += scan[w];
-    }
-    const int64_t U = total * p.segs;
-    int64_t chunk = (U + gridDim.x - 1) / gridDim.x;
-    if (chunk < p.min_chunk) chunk = p.min_chunk;
-    if (blockIdx.x == 0) {  // the plan that the joining kernel reads
-        int64_t at = before;
+    const int U = __shfl_sync(0xffffffffu, before, 31) * p.segs;
+    before -= mine;
+    if (blockIdx.x == 0 && wid == 0) {  // the plan that the joining kernel reads
+        int sum = before;
         for (int b = b0; b < b1; ++b) {
             int len, first, n;
             attn_seq(a, b, len, first, n, false);
-            p.plan[b] = at;
-            at += attn_cost(n);
+            p.plan[b] = sum;
+            sum += cut.cost(n);
         }
-        if (threadIdx.x == 0) {
-            p.plan[B] = total;
-            p.plan[B + 1] = chunk;
-        }
-    }
-    const int64_t u0 = blockIdx.x * chunk, u1 = u0 + chunk < U ? u0 + chunk : U;
-    if (u0 >= u1) return;
-    if (before * p.segs <= u0 && u0 < (before + mine) * p.segs) {
-        int64_t at = before;
-        for (int b = b0; b < b1; ++b) {
-            int len, first, n;
-            attn_seq(a, b, len, first, n, false);
-            if (u0 < (at + attn_cost(n)) * p.segs) {
-                *found = b;
-                *found_off = u0 - at * p.segs;
-                break;
-            }
-            at += attn_cost(n);
+        if (lane == 0) {
+            p.plan[B] = U / p.segs;
+            p.plan[B + 1] = cut.tb ? 0 : cut.chunk;
         }
     }
-    __syncthreads();
-
+    const int64_t from = static_cast<int64_t>(blockIdx.x) * cut.chunk;
+    if (from >= U) return;
+    const int u0 = static_cast<int>(from), u1 = u0 < U - cut.chunk ? u0 + cut.chunk : U;
     {
-        AttnPiece x;
-        x.b = *found;
-        attn_seq(a, x.b, x.len, x.first, x.n, false);
-        const int64_t off = *found_off;
-        x.seg = static_cast<int>(off / attn_cost(x.n));
-        attn_take(x, off - static_cast<int64_t>(x.seg) * attn_cost(x.n), u1 - u0);
-        if (x.blk == x.end) return;  // the range ends within a segment's fixed part
+        const int who = __ffs(__ballot_sync(0xffffffffu, before * p.segs <= u0 && u0 < (before + mine) * p.segs)) - 1;
+        int sum = __shfl_sync(0xffffffffu, before, who);
+        x.b = who * span;
+        if (span == 1) {
+            x.len = __shfl_sync(0xffffffffu, x.len, who);
+            x.first = __shfl_sync(0xffffffffu, x.first, who);
+            x.n = __shfl_sync(0xffffffffu, x.n, who);
+        } else {
+            for (;; ++x.b) {
+                attn_seq(a, x.b, x.len, x.first, x.n, false);
+                if (u0 < (sum + cut.cost(x.n)) * p.segs) break;
+                sum += cut.cost(x.n);
+            }
+        }
+        const int off = u0 - sum * p.segs, k = cut.cost(x.n), seg = off / k, j = off - seg * k;
+        x.seg = seg;
+        if (cut.tb) {  // the first n % k parts have a block more
+            const int each = x.n / k, more = x.n - each * k;
+            x.blk = x.first + j * each + min(j, more);
+            x.end = x.blk + each + (j < more);
+            x.left = 0;
+        } else {
+            attn_take(x, j, u1 - u0);
+            if (x.blk == x.end) return;  // the range ends within a segment's fixed part
+        }
         if (lane == 0) pieces[0] = pieces[1] = x;
         __syncwarp();
     }
 
-    // ---- queries of a piece: two rows of a lane are loaded ahead, the others with the conversion
+    // ---- queries of a piece: kAhead rows of a lane are loaded ahead, the others with the conversion
     constexpr int LPR = D <= 128 ? 16 : 32, RPW = 32 / LPR;  // lanes per row, rows of a warp at once
     constexpr int kStep = kAttnWarps * RPW;                   // rows of the CTA at once
     const int qr = wid * RPW + lane / LPR, pc = lane % LPR;   // the lane's first row; its eight dims: 8 pc ..
@@ -332,9 +358,13 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
             v.load(static_cast<const typename Elem<SPLIT ? MOE_F32 : MOE_BF16>::T*>(a.q) + at, a.qvec);
         }
     };
-    Q8 q0, q1;
-    load_q(q0, pieces[0].b, pieces[0].seg, qr);
-    load_q(q1, pieces[0].b, pieces[0].seg, qr + kStep);
+    constexpr int kAhead = 2;
+    Q8 qa8[kAhead];
+    auto load_qs = [&](int b, int seg, int r0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load_q(qa8[i], b, seg, r0 + i * kStep);
+    };
+    load_qs(x.b, x.seg, qr);
 
     // ---- copies: the group's first warp issues its blocks S ahead of the arithmetic
     int iu = pieces[1].blk + grp, iend = pieces[1].end;       // the next blocks to look up, and the piece's end
@@ -396,14 +426,11 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
         const int xb = pieces[0].b, xseg = pieces[0].seg, kv = xseg / p.g.RB, rb = xseg - kv * p.g.RB;
         const int rows = min(RP, p.R - rb * RP);
         // ---- queries: shifted by a power of two into fp16's range, stored as the lanes take them
-        for (int r0 = qr; r0 < RP; r0 += 2 * kStep) {
-            if (r0 != qr) {
-                load_q(q0, xb, xseg, r0);
-                load_q(q1, xb, xseg, r0 + kStep);
-            }
+        for (int r0 = qr; r0 < RP; r0 += kAhead * kStep) {
+            if (r0 != qr) load_qs(xb, xseg, r0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const Q8& v = i ? q1 : q0;
+            for (int i = 0; i < kAhead; ++i) {
+                const Q8& v = qa8[i];
                 const int rr = r0 + i * kStep;
                 float y[8], amax = 0.0f;
 #pragma unroll
@@ -720,10 +747,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 ? 3 : 2) kv8
         __syncwarp();
         if (lane == 0) pieces[0] = nx;
         __syncwarp();
-        if (again) {
-            load_q(q0, nx.b, nx.seg, qr);
-            load_q(q1, nx.b, nx.seg, qr + kStep);
-        }
+        if (again) load_qs(nx.b, nx.seg, qr);
         if (grp == 0 && c == 0) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -824,7 +848,7 @@ cudaError_t launch_attn(AttnPlan p, cudaStream_t st) {
         sms[dev].store(n, std::memory_order_relaxed);
     }
     // CTAs per SM that the registers allow, fewer where the row buffer leaves no room for the ring
-    int occ = MT == 1 && D <= 128 ? 3 : 2;
+    int occ = MT == 1 && D <= 128 && !SPLIT ? 3 : 2;
     const int NG = kAttnWarps / p.g.RTW, fixed = L::fixed(p.g.RTW);
     int stages = 0;
     for (;; --occ) {
@@ -835,7 +859,6 @@ cudaError_t launch_attn(AttnPlan p, cudaStream_t st) {
     if (stages * NG > kAttnStages) stages = kAttnStages / NG;
     p.stages = stages;
     p.smem = fixed + stages * NG * L::kRec;
-    p.min_chunk = kAttnSegCost + NG;
     int grid = n * occ;
     if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
     e = launch_kernel(kern, dim3(grid), dim3(kAttnThreads), p.smem, st, false, p);

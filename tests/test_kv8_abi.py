@@ -71,6 +71,7 @@ def test_attention_refusals(m):
     for p in ("q", "lens", "out", "workspace"):
         assert call(**{p: None}) == NULL, p
     assert call(type=7) == TYPE
+    assert call(cache(m, max_pages=1 << 29, table_stride=1 << 29)) == CAP  # more blocks than 32 bits count
     for kw in (dict(T=0), dict(T=33), dict(n_heads=0), dict(n_heads=9), dict(window=-1)):
         assert call(**kw) == SHAPE, kw
     assert call(q=17) == ALIGN and call(out=24) == ALIGN and call(workspace=20) == ALIGN
