@@ -40,7 +40,7 @@ int cache_rows(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int32
     if (!valid_elem(rows->type)) return MOE_E_TYPE;
     if (rows->n_tokens < 0 || rows->n_tokens > 0x7fffffff) return MOE_E_SHAPE;
     // one CTA per (block, head)
-    if (kv8_slots(rows->n_tokens, cache->n_seqs) * cache->n_kv_heads > 0x7fffffff) return MOE_E_CAP;
+    if (kv8_slots(rows->n_tokens, cache->n_seqs) * cache->n_kv_heads > 0x3fffffff) return MOE_E_CAP;
     if (rows->n_tokens > 0 && (!rows->k || !rows->v)) return MOE_E_NULL;
     const int eb = elem_bytes(rows->type);
     rc = check_rows(rows->k, rows->k_token_stride, rows->k_head_stride, eb, kvec);

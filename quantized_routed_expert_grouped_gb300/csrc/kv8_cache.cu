@@ -5,14 +5,14 @@
 // Read: (code - 128) * scale. Every step is one fp32 operation, so the results are the same bits for any
 // layout of the work.
 //
-// Both are bound by memory: a value costs its own size and one byte, and a few operations (a product, an
+// Both are bound by memory; a value costs its own size and one byte, and a few operations (a product, an
 // addition that rounds and moves the code into the low byte, a byte permute). Write: one CTA per
 // (block, head) holds all of the block's new keys and values in registers between the maximum and the
-// codes, so they are read once, with D / 8 vectors per thread in flight. Read: one warp per (block, head).
-// Keys: a lane's 16-byte (fp32: 32-byte) vector of one token becomes eight consecutive bytes of the
-// record, 256 bytes a warp. Values are stored by dim: a warp takes 16 dims of the block's 32 tokens
-// (lane = token, so that every lane's sector is read whole) and turns its 512 bytes in shared memory; the
-// read turns blocks of eight dims and four tokens in registers.
+// codes, so they are read once, with D / 16 vectors per thread in flight. Read: one warp per (block, head)
+// and keys or values. A warp takes eight tokens by 32 dims, 64 or 128 bytes of each row: of the keys
+// that is a tile of the record, 256 bytes; the values are stored by dim, so the write turns them in shared
+// memory (rows of 36 bytes: no two lanes of a store share a bank), and the read turns blocks of eight
+// dims and four tokens in registers.
 #include "internal.h"
 #include "kv8.cuh"
 #include "kv8_api.h"
@@ -62,44 +62,38 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<c
                                                              KvRows<const typename Elem<TYPE>::T> V,
                                                              int64_t n_tokens, const int32_t* cu, const int32_t* start,
                                                              int32_t* err) {
-    constexpr int D = NB * 32, kVU = 2 * NB, kVW = (kVU + 3) / 4;  // the values' units of 16 dims, a warp's share
+    constexpr int D = NB * 32, kTurn = 36;  // bytes of a dim's 32 tokens in shared memory, padded
     __shared__ float red[2][4];
-    __shared__ __align__(16) uint8_t turn[4][512];
+    __shared__ __align__(16) uint8_t turn[D * kTurn];
     const int h = blockIdx.x % c.n_kv, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const KvSlot s = kv8_slot(blockIdx.x / c.n_kv, cu, start, c.n_seqs, n_tokens, err);
     if (s.b < 0) return;
     uint8_t* rec = kv8_record(c, s.b, s.blk, h, err);
     if (!rec) return;
-    const auto* kb = K.p + s.row * K.ts + h * K.hs;
-    const auto* vb = V.p + s.row * V.ts + h * V.hs;
+    const auto* kb = K.p + s.row * K.ts + h * K.hs + (lane & 3) * 8;
+    const auto* vb = V.p + s.row * V.ts + h * V.hs + (lane & 3) * 8;
     const float2 old2 = s.t0 > 0 ? *reinterpret_cast<const float2*>(rec) : make_float2(0.0f, 0.0f);
 
-    Raw8<TYPE> k[NB], v[kVW][2];
+    Raw8<TYPE> k[NB], v[NB];
     auto k_token = [&](int n) {  // of the thread's n-th eight bytes of the keys
-        const int tile = n * 4 + wid, jj = tile / NB, g = lane >> 2;
+        const int jj = (n * 4 + wid) / NB, g = lane >> 2;
         return 8 * (g >> 1) + 2 * jj + (g & 1);
     };
+    const int vt = wid * 8 + (lane >> 2);  // the token of its values, dims 32 n + 8 (lane & 3) ..
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-        const int t = k_token(n), d = ((n * 4 + wid) % NB) * 32 + (lane & 3) * 8;
+        const int t = k_token(n);
         k[n].clear();
-        if (t >= s.t0 && t < s.t1) k[n].load(kb + t * K.ts + d, K.vec);
-    }
-#pragma unroll
-    for (int n = 0; n < kVW; ++n) {
-        const int unit = n * 4 + wid;
-        v[n][0].clear();
-        v[n][1].clear();
-        if (unit < kVU && lane >= s.t0 && lane < s.t1) {
-            v[n][0].load(vb + lane * V.ts + unit * 16, V.vec);
-            v[n][1].load(vb + lane * V.ts + unit * 16 + 8, V.vec);
-        }
+        v[n].clear();
+        if (t >= s.t0 && t < s.t1) k[n].load(kb + t * K.ts + ((n * 4 + wid) % NB) * 32, K.vec);
+        if (vt >= s.t0 && vt < s.t1) v[n].load(vb + vt * V.ts + n * 32, V.vec);
     }
     float ak = 0.0f, av = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) ak = k[n].amax(ak);
-#pragma unroll
-    for (int n = 0; n < kVW; ++n) av = v[n][1].amax(v[n][0].amax(av));
+    for (int n = 0; n < NB; ++n) {
+        ak = k[n].amax(ak);
+        av = v[n].amax(av);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         ak = max_nan(ak, __shfl_xor_sync(0xffffffffu, ak, o));
@@ -118,64 +112,67 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<c
     // a block without a scale (zeros, or not finite) holds codes 128
     const bool some_k = sk.inv > 0.0f, some_v = sv.inv > 0.0f;
     uint2* kr = reinterpret_cast<uint2*>(rec + kKvHead);
+    uint8_t* vr = rec + kKvHead + kKvBlock * D;
+    if (s.t0 > 0 && sk.grew) {  // kept tokens under the larger scale
+        uint2 q[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            if (k_token(n) < s.t0) q[n] = kr[(n * 4 + wid) * 32 + lane];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            if (k_token(n) < s.t0)
+                kr[(n * 4 + wid) * 32 + lane] = some_k ? make_uint2(rescale4(q[n].x, sk.ratio), rescale4(q[n].y, sk.ratio))
+                                                       : make_uint2(0x80808080u, 0x80808080u);
+    }
+    if (s.t0 > 0 && sv.grew) {
+        const int words = (s.t0 + 3) / 4;  // of a dim's 32 bytes: D words / 128 <= 2 NB a thread
+        uint32_t q[2 * NB];
+#pragma unroll
+        for (int n = 0; n < 2 * NB; ++n) {
+            const int i = n * kThreads + threadIdx.x, d = i / words;
+            if (d < D) q[n] = *(reinterpret_cast<const uint32_t*>(vr + d * 32) + i - d * words);
+        }
+#pragma unroll
+        for (int n = 0; n < 2 * NB; ++n) {
+            const int i = n * kThreads + threadIdx.x, d = i / words, x = i - d * words;
+            if (d >= D) continue;
+            uint32_t* at = reinterpret_cast<uint32_t*>(vr + d * 32) + x;
+            const uint32_t w = some_v ? rescale4(q[n], sv.ratio) : 0x80808080u;
+            if (4 * x + 4 <= s.t0) {
+                *at = w;
+            } else {  // the word's last bytes belong to new tokens
+                for (int e = 0; 4 * x + e < s.t0; ++e) reinterpret_cast<uint8_t*>(at)[e] = static_cast<uint8_t>(w >> (8 * e));
+            }
+        }
+    }
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         const int t = k_token(n);
-        uint2* at = kr + (n * 4 + wid) * 32 + lane;
-        if (t >= s.t0 && t < s.t1) {
-            uint2 q = make_uint2(0x80808080u, 0x80808080u);
-            if (some_k) {
-                q.x = pack4(code_word(k[n].get(0), sk.inv), code_word(k[n].get(1), sk.inv), code_word(k[n].get(2), sk.inv),
-                            code_word(k[n].get(3), sk.inv));
-                q.y = pack4(code_word(k[n].get(4), sk.inv), code_word(k[n].get(5), sk.inv), code_word(k[n].get(6), sk.inv),
-                            code_word(k[n].get(7), sk.inv));
-            }
-            *at = q;
-        } else if (t < s.t0 && sk.grew) {
-            uint2 q = *at;
-            q.x = some_k ? rescale4(q.x, sk.ratio) : 0x80808080u;
-            q.y = some_k ? rescale4(q.y, sk.ratio) : 0x80808080u;
-            *at = q;
+        if (t < s.t0 || t >= s.t1) continue;
+        uint2 q = make_uint2(0x80808080u, 0x80808080u);
+        if (some_k) {
+            q.x = pack4(code_word(k[n].get(0), sk.inv), code_word(k[n].get(1), sk.inv), code_word(k[n].get(2), sk.inv),
+                        code_word(k[n].get(3), sk.inv));
+            q.y = pack4(code_word(k[n].get(4), sk.inv), code_word(k[n].get(5), sk.inv), code_word(k[n].get(6), sk.inv),
+                        code_word(k[n].get(7), sk.inv));
         }
+        kr[(n * 4 + wid) * 32 + lane] = q;
     }
-    uint8_t* vr = rec + kKvHead + kKvBlock * D;
-    if (s.t0 == 0 && s.t1 == 32) {
+    const bool whole = s.t0 == 0 && s.t1 == 32;
+    if (vt >= s.t0 && vt < s.t1) {  // part of a block: single bytes
+        uint8_t* at = (whole ? turn : vr) + vt;
+        const int step = whole ? kTurn : 32;
 #pragma unroll
-        for (int n = 0; n < kVW; ++n) {
-            const int unit = n * 4 + wid;
-            if (unit < kVU) {
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    turn[wid][e * 32 + lane] = some_v ? static_cast<uint8_t>(code_word(v[n][e >> 3].get(e & 7), sv.inv)) : 128;
-                __syncwarp();
-                reinterpret_cast<uint4*>(vr + unit * 512)[lane] = reinterpret_cast<const uint4*>(turn[wid])[lane];
-                __syncwarp();
-            }
-        }
-        return;
+            for (int e = 0; e < 8; ++e)
+                at[(n * 32 + (lane & 3) * 8 + e) * step] = some_v ? static_cast<uint8_t>(code_word(v[n].get(e), sv.inv)) : 128;
     }
-    // part of a block: single bytes of the new tokens, words of the kept ones where the scale grew
-#pragma unroll
-    for (int n = 0; n < kVW; ++n) {
-        const int unit = n * 4 + wid;
-        if (unit < kVU && lane >= s.t0 && lane < s.t1) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                vr[(unit * 16 + e) * 32 + lane] = some_v ? static_cast<uint8_t>(code_word(v[n][e >> 3].get(e & 7), sv.inv)) : 128;
-        }
-    }
-    if (s.t0 > 0 && sv.grew) {
-        const int words = (s.t0 + 3) / 4;  // of a dim's 32 bytes
-        for (int i = threadIdx.x; i < D * words; i += kThreads) {
-            const int d = i / words, q = i - d * words;
-            uint32_t* at = reinterpret_cast<uint32_t*>(vr + d * 32) + q;
-            const uint32_t w = some_v ? rescale4(*at, sv.ratio) : 0x80808080u;
-            if (4 * q + 4 <= s.t0) {
-                *at = w;
-            } else {  // the word's last bytes belong to new tokens
-                for (int e = 0; 4 * q + e < s.t0; ++e) reinterpret_cast<uint8_t*>(at)[e] = static_cast<uint8_t>(w >> (8 * e));
-            }
-        }
+    if (!whole) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < D * 2; i += kThreads) {  // 16 tokens of a dim
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(turn + (i >> 1) * kTurn + (i & 1) * 16);
+        reinterpret_cast<uint4*>(vr)[i] = make_uint4(at[0], at[1], at[2], at[3]);
     }
 }
 
@@ -184,8 +181,10 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
                                                             KvRows<typename Elem<TYPE>::T> V, int64_t n_tokens, int64_t n_work,
                                                             const int32_t* cu, const int32_t* start, int32_t* err) {
     const int lane = threadIdx.x & 31;
-    const int64_t work = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    int64_t work = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     if (work >= n_work) return;
+    const bool values = work & 1;
+    work >>= 1;
     const int h = static_cast<int>(work % c.n_kv);
     const KvSlot s = kv8_slot(work / c.n_kv, cu, start, c.n_seqs, n_tokens, err);
     if (s.b < 0) return;
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
     const int g = lane >> 2;
     const uint2* kr = reinterpret_cast<const uint2*>(rec + kKvHead);
 #pragma unroll 2
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < NB && !values; ++i) {
         uint2 q[4];
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) q[jj] = __ldg(kr + (jj * NB + i) * 32 + lane);
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
     const int tq = lane & 7, dg = lane >> 3;
     const uint32_t* vr = reinterpret_cast<const uint32_t*>(rec + kKvHead + kKvBlock * c.D);
 #pragma unroll 2
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < NB && values; ++i) {
         uint32_t q[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = __ldg(vr + (i * 32 + dg * 8 + e) * 8 + tq);
@@ -275,7 +274,7 @@ cudaError_t launch_kv8_write(const KvCache& c, const moe_kv8_rows& r, const int3
 
 cudaError_t launch_kv8_read(const KvCache& c, const moe_kv8_rows& r, const int32_t* cu, const int32_t* start,
                             int32_t* err, bool kvec, bool vvec, cudaStream_t st) {
-    const int64_t work = kv8_slots(r.n_tokens, c.n_seqs) * c.n_kv;
+    const int64_t work = kv8_slots(r.n_tokens, c.n_seqs) * c.n_kv * 2;
     if (r.type == MOE_F32) return read_t<MOE_F32>(c, r, cu, start, err, kvec, vvec, work, st);
     if (r.type == MOE_F16) return read_t<MOE_F16>(c, r, cu, start, err, kvec, vvec, work, st);
     return read_t<MOE_BF16>(c, r, cu, start, err, kvec, vvec, work, st);
