@@ -128,12 +128,55 @@ struct Raw8 {
         const uint32_t x = w[(e >> 1) & (kWords - 1)];
         return __half2float(__ushort_as_half(static_cast<unsigned short>(e & 1 ? x >> 16 : x & 0xffffu)));
     }
-    __device__ __forceinline__ float amax(float m) const {
+    // The running maximum of magnitudes, as bits (a NaN is above all): of one value, or of two 16-bit halves.
+    __device__ __forceinline__ uint32_t amax(uint32_t m) const {
+        if constexpr (TYPE == MOE_F32) {
+            float f = __uint_as_float(m);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(get(e)));
-        return m;
+            for (int i = 0; i < kWords; ++i) f = max_nan(f, fabsf(__uint_as_float(w[i])));
+            return __float_as_uint(f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            return m;
+        }
+    }
+    static __device__ __forceinline__ uint32_t float_bits(uint32_t m) {  // of amax(), as fp32
+        if (TYPE == MOE_F32) return m;
+        const uint32_t h = max(m >> 16, m & 0xffffu);
+        return TYPE == MOE_BF16 ? h << 16 : __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
     }
 };
+
+// Packed fp32 pairs.
+__device__ __forceinline__ unsigned long long pk2(float x, float y) {
+    return (static_cast<unsigned long long>(__float_as_uint(y)) << 32) | __float_as_uint(x);
+}
+__device__ __forceinline__ float2 up2(unsigned long long v) {
+    return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t lo2(unsigned long long v) { return static_cast<uint32_t>(v); }
+__device__ __forceinline__ uint32_t hi2(unsigned long long v) { return static_cast<uint32_t>(v >> 32); }
+
+// the low bytes of four words
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return prmt(prmt(a, b, 0x0040u), prmt(c, d, 0x0040u), 0x5410u);
+}
 
 // Device copy of moe_kv8_cache.
 struct KvCache {

@@ -145,28 +145,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint4 a, uint32_t b0, u
 }
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint4 a, uint32_t b0, uint32_t b1) { mma_16816(d, a, b0, b1, d); }
 
-__device__ __forceinline__ unsigned long long pk2(float x, float y) {
-    return (static_cast<unsigned long long>(__float_as_uint(y)) << 32) | __float_as_uint(x);
-}
-__device__ __forceinline__ float2 up2(unsigned long long v) {
-    return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // four codes -> two half2 of code * 2^-24 (fp16's subnormals; exact)
 __device__ __forceinline__ void codes_sub(uint32_t w, uint32_t& lo, uint32_t& hi) {
     lo = prmt(w, 0u, 0x4140u);

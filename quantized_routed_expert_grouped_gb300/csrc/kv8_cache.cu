@@ -13,6 +13,8 @@
 // that is a tile of the record, 256 bytes; the values are stored by dim, so the write turns them in shared
 // memory (rows of 36 bytes: no two lanes of a store share a bank), and the read turns blocks of eight
 // dims and four tokens in registers.
+#include <type_traits>
+
 #include "internal.h"
 #include "kv8.cuh"
 #include "kv8_api.h"
@@ -28,8 +30,9 @@ constexpr int kThreads = 128;
 __device__ __forceinline__ uint32_t code_word(float x, float inv) {
     return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.0f + 128.0f));
 }
-__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    return prmt(prmt(a, b, 0x0040u), prmt(c, d, 0x0040u), 0x5410u);
+__device__ __forceinline__ unsigned long long code_words(float x, float y, float inv) {
+    // (single products: the assembler joins a packed product and a packed addition into one rounding)
+    return add2(pk2(__fmul_rn(x, inv), __fmul_rn(y, inv)), pk2(12582912.0f + 128.0f, 12582912.0f + 128.0f));
 }
 // byte i of w, a code, as code - 128
 __device__ __forceinline__ float code_value(uint32_t w, int i) {
@@ -63,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<c
                                                              int64_t n_tokens, const int32_t* cu, const int32_t* start,
                                                              int32_t* err) {
     constexpr int D = NB * 32, kTurn = 36;  // bytes of a dim's 32 tokens in shared memory, padded
-    __shared__ float red[2][4];
+    __shared__ uint32_t red[2][4];
     __shared__ __align__(16) uint8_t turn[D * kTurn];
     const int h = blockIdx.x % c.n_kv, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const KvSlot s = kv8_slot(blockIdx.x / c.n_kv, cu, start, c.n_seqs, n_tokens, err);
@@ -88,25 +91,22 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<c
         if (t >= s.t0 && t < s.t1) k[n].load(kb + t * K.ts + ((n * 4 + wid) % NB) * 32, K.vec);
         if (vt >= s.t0 && vt < s.t1) v[n].load(vb + vt * V.ts + n * 32, V.vec);
     }
-    float ak = 0.0f, av = 0.0f;
+    uint32_t ak = 0, av = 0;  // magnitudes order as their bits do
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         ak = k[n].amax(ak);
         av = v[n].amax(av);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        ak = max_nan(ak, __shfl_xor_sync(0xffffffffu, ak, o));
-        av = max_nan(av, __shfl_xor_sync(0xffffffffu, av, o));
-    }
+    ak = __reduce_max_sync(0xffffffffu, Raw8<TYPE>::float_bits(ak));
+    av = __reduce_max_sync(0xffffffffu, Raw8<TYPE>::float_bits(av));
     if (lane == 0) {
         red[0][wid] = ak;
         red[1][wid] = av;
     }
     __syncthreads();  // also: every thread has read the old scales
-    ak = max_nan(max_nan(red[0][0], red[0][1]), max_nan(red[0][2], red[0][3]));
-    av = max_nan(max_nan(red[1][0], red[1][1]), max_nan(red[1][2], red[1][3]));
-    const Scales sk = block_scale(ak, old2.x), sv = block_scale(av, old2.y);
+    ak = max(max(red[0][0], red[0][1]), max(red[0][2], red[0][3]));
+    av = max(max(red[1][0], red[1][1]), max(red[1][2], red[1][3]));
+    const Scales sk = block_scale(__uint_as_float(ak), old2.x), sv = block_scale(__uint_as_float(av), old2.y);
     if (threadIdx.x == 0) *reinterpret_cast<float2*>(rec) = make_float2(sk.scale, sv.scale);
 
     // a block without a scale (zeros, or not finite) holds codes 128
@@ -151,22 +151,28 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<c
         if (t < s.t0 || t >= s.t1) continue;
         uint2 q = make_uint2(0x80808080u, 0x80808080u);
         if (some_k) {
-            q.x = pack4(code_word(k[n].get(0), sk.inv), code_word(k[n].get(1), sk.inv), code_word(k[n].get(2), sk.inv),
-                        code_word(k[n].get(3), sk.inv));
-            q.y = pack4(code_word(k[n].get(4), sk.inv), code_word(k[n].get(5), sk.inv), code_word(k[n].get(6), sk.inv),
-                        code_word(k[n].get(7), sk.inv));
+            unsigned long long x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = code_words(k[n].get(2 * e), k[n].get(2 * e + 1), sk.inv);
+            q.x = pack4(lo2(x[0]), hi2(x[0]), lo2(x[1]), hi2(x[1]));
+            q.y = pack4(lo2(x[2]), hi2(x[2]), lo2(x[3]), hi2(x[3]));
         }
         kr[(n * 4 + wid) * 32 + lane] = q;
     }
     const bool whole = s.t0 == 0 && s.t1 == 32;
-    if (vt >= s.t0 && vt < s.t1) {  // part of a block: single bytes
-        uint8_t* at = (whole ? turn : vr) + vt;
-        const int step = whole ? kTurn : 32;
+    if (vt >= s.t0 && vt < s.t1) {
+        auto put = [&](uint8_t* at, auto step) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                at[(n * 32 + (lane & 3) * 8 + e) * step] = some_v ? static_cast<uint8_t>(code_word(v[n].get(e), sv.inv)) : 128;
+                for (int e = 0; e < 4; ++e) {
+                    const unsigned long long x = some_v ? code_words(v[n].get(2 * e), v[n].get(2 * e + 1), sv.inv) : (128ull << 32 | 128);
+                    at[(n * 32 + 2 * e) * step.value] = static_cast<uint8_t>(lo2(x));
+                    at[(n * 32 + 2 * e + 1) * step.value] = static_cast<uint8_t>(hi2(x));
+                }
+        };
+        if (whole) put(turn + (lane & 3) * 8 * kTurn + vt, std::integral_constant<int, kTurn>{});
+        else put(vr + (lane & 3) * 8 * 32 + vt, std::integral_constant<int, 32>{});  // part of a block: single bytes
     }
     if (!whole) return;
     __syncthreads();

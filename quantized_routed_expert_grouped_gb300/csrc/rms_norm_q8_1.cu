@@ -8,9 +8,9 @@
 // neighbouring threads. The sum of squares is fp32: per thread, then over the warp's lanes, then
 // over the warps in order.
 //
-// Bound by memory; what the kernel adds is latency (a row's loads, one barrier, its stores), which
-// other rows' CTAs cover: two chunks a thread keep eight 4096-column rows on an SM. The q8_1 codes are
-// round(y / d) with an IEEE quotient; a product with 1 / d decides all but those within 2^-10 of a tie.
+// Bound by memory where there are many rows; what the kernel adds is latency (a row's loads, one barrier,
+// its stores), which other rows' CTAs cover, and the arithmetic, kept to a dozen instructions a value by
+// packed pairs and by codes that are divided out only next to a tie.
 #include "internal.h"
 #include "kv8.cuh"
 #include "kv8_api.h"
@@ -19,45 +19,50 @@ namespace moe {
 
 namespace {
 
-// round-half-away(y / d) for |y| <= 127 d up to rounding, inv = 1 / d (IEEE)
-__device__ __forceinline__ int q8_1_code(float y, float d, float inv) {
-    const float r = __fmul_rn(y, inv);  // within 2^-15 of the quotient
-    const float n = rintf(r);
-    if (fabsf(fabsf(r - n) - 0.5f) > 9.765625e-4f) return static_cast<int>(n);
-    return static_cast<int>(roundf(__fdiv_rn(y, d)));
-}
-
 // the q8_1 block of four neighbouring lanes' values (32 in all): the lane's codes and header word
 __device__ __forceinline__ void quad_q8_1(const float (&y)[8], uint32_t (&code)[2], uint32_t& hdr) {
     float amax = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float v = fabsf(y[e]);
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(v));
-    }
+    for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(y[e]));
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        const float v = __shfl_xor_sync(0xffffffffu, amax, o);
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(v));
-    }
+    for (int o = 1; o < 4; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float d = __fdiv_rn(amax, 127.0f);
-    // 1 / d of a subnormal d may overflow: then every quotient is taken by division
-    const float inv = d > 1.1754944e-38f && d < 3.4028234e38f ? __fdiv_rn(1.0f, d) : __int_as_float(0x7fffffff);
-    int S = 0;
-    code[0] = code[1] = 0;
+    // Candidates: y * (1 / d) is within 2^-15 of the quotient, and adding 1.5 * 2^23 rounds it to an
+    // integer, in the low bits. Where one lies that near a tie (or 1 / d is not a normal number), the
+    // lane's codes are taken from the quotients.
+    const float inv = d > 1.1754944e-38f && d < 3.4028234e38f ? __fdiv_rn(1.0f, d) : 0.0f;
+    const unsigned long long vv = pk2(inv, inv), up = pk2(12582912.0f, 12582912.0f), down = pk2(-12582912.0f, -12582912.0f);
+    unsigned long long x[4], sum = 0;
+    float far = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int q = d == 0.0f ? 0 : q8_1_code(y[e], d, inv);
-        S += q;
-        code[e >> 2] |= static_cast<uint32_t>(q & 255) << (8 * (e & 3));
+    for (int e = 0; e < 4; ++e) {
+        const unsigned long long r = mul2(pk2(y[2 * e], y[2 * e + 1]), vv);
+        x[e] = add2(r, up);
+        const unsigned long long n = add2(x[e], down);
+        const float2 rr = up2(r), nn = up2(n);
+        far = fmaxf(far, fmaxf(fabsf(rr.x - nn.x), fabsf(rr.y - nn.y)));
+        sum = add2(sum, n);
+    }
+    const float2 s2 = up2(sum);
+    float S = s2.x + s2.y;
+    code[0] = pack4(lo2(x[0]), hi2(x[0]), lo2(x[1]), hi2(x[1]));
+    code[1] = pack4(lo2(x[2]), hi2(x[2]), lo2(x[3]), hi2(x[3]));
+    if (!(far < 0.5f - 3.0517578125e-5f) || inv == 0.0f) {
+        int sum_i = 0;
+        code[0] = code[1] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int q = d == 0.0f ? 0 : static_cast<int>(roundf(__fdiv_rn(y[e], d)));
+            sum_i += q;
+            code[e >> 2] |= static_cast<uint32_t>(q & 255) << (8 * (e & 3));
+        }
+        S = static_cast<float>(sum_i);
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-    hdr = __half_as_ushort(__float2half_rn(d)) |
-          static_cast<uint32_t>(__half_as_ushort(__float2half_rn(__fmul_rn(d, static_cast<float>(S))))) << 16;
+    hdr = __half_as_ushort(__float2half_rn(d)) | static_cast<uint32_t>(__half_as_ushort(__float2half_rn(__fmul_rn(d, S)))) << 16;
 }
 
-template <int TYPE>
 __device__ __forceinline__ void weight8(const void* w, int w_type, int col, float (&v)[8]) {
     if (w_type == MOE_F32) load8<MOE_F32>(static_cast<const float*>(w) + col, true, v);
     else if (w_type == MOE_F16) load8<MOE_F16>(static_cast<const __half*>(w) + col, true, v);
@@ -65,7 +70,7 @@ __device__ __forceinline__ void weight8(const void* w, int w_type, int col, floa
 }
 
 template <int TYPE, int C>
-__global__ void __launch_bounds__(1024) add_rms_norm_q8_1_kernel(const moe_norm_call c) {
+__global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_norm_q8_1_kernel(const moe_norm_call c) {
     using E = Elem<TYPE>;
     using T = typename E::T;
     __shared__ float red[32];
@@ -73,26 +78,27 @@ __global__ void __launch_bounds__(1024) add_rms_norm_q8_1_kernel(const moe_norm_
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const T* x = static_cast<const T*>(c.x) + row * c.x_stride;
     const T* r = c.residual ? static_cast<const T*>(c.residual) + row * c.residual_stride : nullptr;
-    float h[C][8], ss = 0.0f;
+    Raw8<TYPE> rx[C], rr[C];
 #pragma unroll
     for (int k = 0; k < C; ++k) {  // all of the row's loads before the arithmetic
         const int col = (k * blockDim.x + threadIdx.x) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[k][e] = 0.0f;
+        rx[k].clear();
+        rr[k].clear();
         if (col < c.cols) {
-            load8<TYPE>(x + col, true, h[k]);
-            if (r) {
-                float v[8];
-                load8<TYPE>(r + col, true, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[k][e] += v[e];
-            }
+            rx[k].load(x + col, true);
+            if (r) rr[k].load(r + col, true);
         }
     }
+    unsigned long long h[C][4], s2 = 0;
 #pragma unroll
     for (int k = 0; k < C; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(h[k][e], h[k][e], ss);
+        for (int e = 0; e < 4; ++e) {
+            h[k][e] = add2(pk2(rx[k].get(2 * e), rx[k].get(2 * e + 1)), pk2(rr[k].get(2 * e), rr[k].get(2 * e + 1)));
+            s2 = fma2(h[k][e], h[k][e], s2);
+        }
+    const float2 ss2 = up2(s2);
+    float ss = ss2.x + ss2.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (lane == 0) red[wid] = ss;
@@ -108,10 +114,22 @@ __global__ void __launch_bounds__(1024) add_rms_norm_q8_1_kernel(const moe_norm_
         if (!__any_sync(0xffffffffu, in)) continue;
         float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (in) {
-            if (c.sum) store8<TYPE>(static_cast<T*>(c.sum) + row * c.cols + col, true, h[k]);
-            weight8<TYPE>(c.weight, c.w_type, col, y);
+            if (c.sum) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = h[k][e] * inv * y[e];
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = up2(h[k][e]);
+                    y[2 * e] = v.x;
+                    y[2 * e + 1] = v.y;
+                }
+                store8<TYPE>(static_cast<T*>(c.sum) + row * c.cols + col, true, y);
+            }
+            weight8(c.weight, c.w_type, col, y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = up2(mul2(mul2(h[k][e], pk2(inv, inv)), pk2(y[2 * e], y[2 * e + 1])));
+                y[2 * e] = v.x;
+                y[2 * e + 1] = v.y;
+            }
             if (c.y) store8<TYPE>(static_cast<T*>(c.y) + row * c.cols + col, true, y);
         }
         if (c.xq) {
@@ -152,7 +170,7 @@ cudaError_t norm_t(const moe_norm_call& c, cudaStream_t st) {
     const int pieces = c.cols / 8;
     const unsigned grid = static_cast<unsigned>(c.rows);
     // few rows: as many threads as the row has pieces, for the shortest chain; many: two pieces a thread
-    const int chunks = pieces > 2048 ? 4 : pieces > 1024 || (c.rows > 304 && pieces >= 64) ? 2 : 1;
+    const int chunks = pieces > 1024 ? 4 : c.rows > 304 && pieces >= 64 ? 2 : 1;
     const int threads = ((pieces + chunks - 1) / chunks + 31) / 32 * 32;
     if (chunks == 1) add_rms_norm_q8_1_kernel<TYPE, 1><<<grid, threads, 0, st>>>(c);
     else if (chunks == 2) add_rms_norm_q8_1_kernel<TYPE, 2><<<grid, threads, 0, st>>>(c);
