@@ -3,16 +3,16 @@
 // Mathematics. The rows of a key/value head are its queries (token t, head h of its group): R = T *
 // n_heads / n_kv_heads of them share every key and value. For a row, in base 2 (log2 e is in the
 // row's factor), s_j = f * (q . (c_j - 128)) with f = |scale| * log2 e * k_scale * (the query's own
-// power of two), l = sum 2^(s_j - m + 11), o = sum 2^(s_j - m + 11) (v_scale / vref) (c_j - 128),
-// out = o * vref / l, with a reference m that is at most 4 below the largest s_j. m, vref (the
-// largest v_scale so far) and with them l and o are kept running, block by block of 32 tokens; o and
-// l are rescaled only when m moves, which after the first blocks is rare. The 2^11 and the slack of
-// 2^4 use fp16's range for the weights from 2^15 down to 2^-24, so that a long tail of small ones
-// keeps its sum; v_scale / vref <= 1 joins the weights because blocks differ in scale. Codes and,
-// after a shift by a power of two, 16-bit queries are exact in fp16; an fp32 query and its weights
-// are two fp16 parts each (SPLIT). Sums are fp32. Key codes enter as fp16 subnormals (two byte
-// permutes per four codes) and the score starts at -128 * sum q, which is of the scores' own size;
-// value codes are centred (two subtractions more): the sum of weights would be far above the result.
+// power of two). A block's v_scale is r * 2^e, 1 <= r < 2. Kept running, block by block:
+//   p_j = 2^(s_j - m + 11),  l = sum p_j,  o = sum p_j 2^(e + d) r (c_j - 128),  out = o 2^-d / l,
+// with d = m - n - 1, m at most 4 below the largest s_j and n at most 4 below the largest s_j + e, both
+// whole numbers (so that their differences are exact): what is held in fp16, p_j 2^(e + d) r < 2^15, is large where a token's share of the output is, whatever its
+// block's scale. o and l are rescaled only when m or n moves, which after the first blocks is rare. fp16's
+// range below 2^10, down to 2^-24, keeps a long tail of small weights. Codes and, after a shift by a
+// power of two, 16-bit queries are exact in fp16; an fp32 query and its weights are two fp16 parts
+// each (SPLIT). Sums are fp32. Key codes enter as fp16 subnormals (two byte permutes per four codes) and
+// the score starts at -128 * sum q, which is of the scores' own size; value codes are centred (two
+// subtractions more): the sum of weights would be far above the result.
 //
 // Layout. A matrix instruction (m16n8k16) takes 16 rows; its other operand is the record itself: a
 // lane's eight bytes of a 256-byte tile are its part of two instructions' keys (eight dims of one
@@ -45,8 +45,8 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnStages = 24;          // ring stages of a CTA, at most
 constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many CTAs
-// A row's reference m follows its maximum only once that is kAttnSlack (in powers of two) above it;
-// weights are held times 2^kAttnShift, so they stay below 2^15.
+// A row's references m and n move to their maxima only once those are kAttnSlack (in powers of two)
+// above; l is held times 2^kAttnShift, the weights of the values times 2^(kAttnShift - 1).
 constexpr float kAttnShift = 11.0f, kAttnSlack = 4.0f;
 constexpr int kAttnMinPart = 8;          // blocks of a part, at least (but for a segment's remainder)
 constexpr int kAttnSegCost = 16;         // blocks that a segment's fixed work (queries, joining) costs
@@ -405,11 +405,27 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
         const int rows = min(RP, p.R - rb * RP);
         // ---- queries: shifted by a power of two into fp16's range, stored as the lanes take them
         for (int r0 = qr; r0 < RP; r0 += kAhead * kStep) {
-            if (r0 != qr) load_qs(xb, xseg, r0);
+            Q8 now[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) now[i] = qa8[i];
+            if (r0 + kAhead * kStep < RP) load_qs(xb, xseg, r0 + kAhead * kStep);  // (the next rows are on their way)
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const Q8& v = qa8[i];
+                const Q8& v = now[i];
                 const int rr = r0 + i * kStep;
+                if (rr - lane / LPR >= rows) {  // none of the warp's rows has a query
+                    if (rr < RP && pc < kND) {
+                        const int tile = rr >> 4, row = rr & 15;
+                        uint32_t* to = reinterpret_cast<uint32_t*>(qs + ((tile * kNB + (pc >> 2)) * 2) * 32 + (row & 7) * 4 + (pc & 3)) + (row >> 3);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            to[(e >> 1) * 128 + (e & 1) * 2] = 0;
+                            if (SPLIT) to[(e >> 1) * 128 + (e & 1) * 2 + MT * RTW * D * 8] = 0;
+                        }
+                        if (pc == 0) qf[rr] = make_float2(0.0f, 0.0f);
+                    }
+                    continue;
+                }
                 float y[8], amax = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
         }
         __syncthreads();
 
-        float o[MT][kND][4], m[MT][2], nb[MT][2], fr[MT][2], off[MT][4], vref = 0.0f, vinv = 0.0f;
+        float o[MT][kND][4], m[MT][2], dd[MT][2], fr[MT][2], off[MT][4];
         unsigned long long l[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -475,7 +491,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 m[mt][q] = -INFINITY;
-                nb[mt][q] = 0.0f;
+                dd[mt][q] = INFINITY;  // n = m - d - 1
                 l[mt][q] = 0;
                 const float2 f = qf[(rt * MT + mt) * 16 + q * 8 + g];
                 fr[mt][q] = f.x;
@@ -496,6 +512,10 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
             if (!lost && flag[cs]) {
                 const uint8_t* rec = ring + cs * L::kRec;
                 const float2 sc = *reinterpret_cast<const float2*>(rec);
+                // v_scale = r * 2^e; a block of zeros (or below fp32's normal range) adds to l alone
+                const bool some = sc.y >= 1.17549435e-38f && sc.y < INFINITY;
+                const float e = some ? static_cast<float>(static_cast<int>(__float_as_uint(sc.y) >> 23) - 127) : -INFINITY;
+                const float r = some ? __uint_as_float((__float_as_uint(sc.y) & 0x007fffffu) | 0x3f800000u) : sc.y < INFINITY ? 0.0f : NAN;
                 const uint8_t* kp = rec + kKvHead + g * 32 + c * 8;
                 // scores, in units of the row's factor times k_scale: the codes enter as code * 2^-24, so the
                 // sum starts at -128 * 2^-24 times the query's sum
@@ -555,8 +575,8 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const int r = rb * RP + (rt * MT + mt) * 16 + q * 8 + g;
-                            const int t = r / a.G, ps = r < p.R ? before_window + t : -1;
+                            const int row = rb * RP + (rt * MT + mt) * 16 + q * 8 + g;
+                            const int t = row / a.G, ps = row < p.R ? before_window + t : -1;
                             uint32_t bits = 0;
                             if (a.tree && ps >= 0) bits = static_cast<uint32_t>(__ldg(a.tree + static_cast<int64_t>(xb) * a.T + t));
 #pragma unroll
@@ -580,38 +600,28 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                         for (int jj = 1; jj < 4; ++jj) bm = fmaxf(bm, fmaxf(sa[mt][jj][2 * q], sa[mt][jj][2 * q + 1]));
                         f[mt][q] = fr[mt][q] * sc.x;
                         top[mt][q] = bm * f[mt][q];
-                        grew |= top[mt][q] > m[mt][q] + kAttnSlack;
+                        grew |= top[mt][q] > m[mt][q] + kAttnSlack || top[mt][q] + e > m[mt][q] - dd[mt][q] + (kAttnSlack - 1.0f);
                     }
-                if (__any_sync(0xffffffffu, grew || sc.y > vref)) {
-                    float ov = 1.0f;
-                    if (sc.y > vref) {
-                        ov = vref > 0.0f ? __fdiv_rn(vref, sc.y) : 0.0f;
-                        vref = sc.y;
-                        vinv = __fdiv_rn(1.0f, vref);
-                    }
+                if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             float bm = fmaxf(top[mt][q], __shfl_xor_sync(0xffffffffu, top[mt][q], 1));
                             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-                            const float nm = fmaxf(m[mt][q], bm);
-                            float al = 1.0f;
-                            if (nm > m[mt][q]) {
-                                al = ex2(m[mt][q] - nm);
-                                m[mt][q] = nm;
-                                nb[mt][q] = kAttnShift - nm;
-                            }
+                            bm = ceilf(bm);
+                            const float m0 = m[mt][q], n0 = m0 - dd[mt][q] - 1.0f, m1 = fmaxf(m0, bm), n1 = fmaxf(n0, bm + e);
+                            const float al = m1 > m0 ? ex2(m0 - m1) : 1.0f, ol = n1 > n0 ? ex2(n0 - n1) : 1.0f;
+                            m[mt][q] = m1;
+                            if (n1 > -INFINITY) dd[mt][q] = m1 - n1 - 1.0f;
                             l[mt][q] = mul2(l[mt][q], pk2(al, al));
-                            al *= ov;
 #pragma unroll
                             for (int i = 0; i < kND; ++i) {
-                                o[mt][i][2 * q] *= al;
-                                o[mt][i][2 * q + 1] *= al;
+                                o[mt][i][2 * q] *= ol;
+                                o[mt][i][2 * q + 1] *= ol;
                             }
                         }
                 }
-                const float F = vref > 0.0f ? sc.y * vinv : sc.y;
                 // ---- weights: the lane's tokens 8 c + 4 xx + 0..3 feed product step xx
                 uint4 pa[MT][2], pl[MT][2];
                 auto weights = [&](auto masked) {
@@ -619,7 +629,8 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const unsigned long long ff = pk2(f[mt][q], f[mt][q]), bb = pk2(nb[mt][q], nb[mt][q]);
+                            const float fac = some ? r * ex2(e + dd[mt][q]) : r;
+                            const unsigned long long ff = pk2(f[mt][q], f[mt][q]), bb = pk2(kAttnShift - m[mt][q], kAttnShift - m[mt][q]);
 #pragma unroll
                             for (int jj = 0; jj < 4; ++jj) {
                                 const float s0 = sa[mt][jj][2 * q], s1 = sa[mt][jj][2 * q + 1];
@@ -631,7 +642,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                                     if (s1 == -INFINITY) w.y = 0.0f;
                                 }
                                 l[mt][q] = add2(l[mt][q], pk2(w.x, w.y));
-                                w = up2(mul2(pk2(w.x, w.y), pk2(F, F)));
+                                w = up2(mul2(pk2(w.x, w.y), pk2(fac, fac)));
                                 if (decltype(masked)::value) {
                                     if (s0 == -INFINITY) w.x = 0.0f;
                                     if (s1 == -INFINITY) w.y = 0.0f;
@@ -713,7 +724,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                 }
                 M[mt][q] = mm;
                 Ls[mt][q] = ll;
-                cf[mt][q] = ll == 0.0f ? 0.0f : vref * (ex2(m[mt][q] - bs) / ll);
+                cf[mt][q] = ll == 0.0f ? 0.0f : ex2(m[mt][q] - bs - dd[mt][q]) / ll;
             }
         const AttnPiece* xp = pieces;
         const bool whole = xp->blk == xp->first && xp->end == xp->first + xp->n;
