@@ -10,6 +10,13 @@
 
 namespace moe {
 
+// These kernels may start before the one they follow has ended (they wait for it before they touch
+// memory), so what they read is not constant over their lifetime: plain loads, not the read-only path.
+template <typename T>
+__device__ __forceinline__ T gload(const T* p) {
+    return *p;
+}
+
 constexpr int kKvBlock = 32;                  // tokens of a record
 constexpr int kKvHead = 16;                   // record header: f32 k_scale, f32 v_scale, 8 unused
 constexpr float kKvTiny = 7.888609052210118e-31f;  // 2^-100: a block below it is stored as zeros
@@ -54,7 +61,7 @@ __device__ __forceinline__ void load8(const typename Elem<TYPE>::T* p, bool vec,
     } u;
     if (vec) {
 #pragma unroll
-        for (int i = 0; i < kB / 16; ++i) u.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        for (int i = 0; i < kB / 16; ++i) u.w[i] = gload(reinterpret_cast<const uint4*>(p) + i);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) u.e[i] = p[i];
@@ -99,7 +106,7 @@ struct Raw8 {
         if (vec) {
 #pragma unroll
             for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                const uint4 v = gload(reinterpret_cast<const uint4*>(p) + i);
                 w[4 * i] = v.x;
                 w[4 * i + 1] = v.y;
                 w[4 * i + 2] = v.z;
@@ -107,12 +114,12 @@ struct Raw8 {
             }
         } else if (TYPE == MOE_F32) {
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+            for (int i = 0; i < kWords; ++i) w[i] = gload(reinterpret_cast<const uint32_t*>(p) + i);
         } else {
 #pragma unroll
             for (int i = 0; i < kWords; ++i)
-                w[i] = __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i) |
-                       static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1)) << 16;
+                w[i] = gload(reinterpret_cast<const uint16_t*>(p) + 2 * i) |
+                       static_cast<uint32_t>(gload(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1)) << 16;
         }
     }
     __device__ __forceinline__ void clear() {
@@ -191,7 +198,7 @@ struct KvCache {
 __device__ __forceinline__ uint8_t* kv8_record(const KvCache& c, int b, int j, int h, int32_t* err) {
     const int pi = j / c.page_blocks, pb = j - pi * c.page_blocks;
     if (pi < c.max_pages) {
-        const int32_t pg = __ldg(c.table + b * c.table_stride + pi);
+        const int32_t pg = gload(c.table + b * c.table_stride + pi);
         if (pg >= 0 && pg < c.n_pages)
             return c.pool + ((static_cast<int64_t>(pg) * c.n_kv + h) * c.page_blocks + pb) * c.rec;
     }
@@ -214,7 +221,7 @@ struct KvSlot {
 
 // Find slot `s`. All threads of a warp call it with the same s; the sequence is found by a 32-way
 // search over its lanes (one round of loads per factor of 32 in n_seqs).
-__device__ __forceinline__ KvSlot kv8_slot(int64_t s, const int32_t* __restrict__ cu, const int32_t* __restrict__ start,
+__device__ __forceinline__ KvSlot kv8_slot(int64_t s, const int32_t* cu, const int32_t* start,
                                            int n_seqs, int64_t n_tokens, int32_t* err) {
     KvSlot r;
     r.b = -1;
@@ -225,13 +232,13 @@ __device__ __forceinline__ KvSlot kv8_slot(int64_t s, const int32_t* __restrict_
     while (n > 1) {
         const int step = (n + 31) / 32;
         const int i = lo + lane * step;
-        const bool ok = lane * step < n && (static_cast<int64_t>(__ldg(cu + i)) >> 5) + 2LL * i <= s;
+        const bool ok = lane * step < n && (static_cast<int64_t>(gload(cu + i)) >> 5) + 2LL * i <= s;
         const unsigned m = __ballot_sync(0xffffffffu, ok);
         const int k = m ? 31 - __clz(m) : 0;
         n = min(step, n - k * step);
         lo += k * step;
     }
-    const int64_t c0 = __ldg(cu + lo), c1 = __ldg(cu + lo + 1), p0 = __ldg(start + lo);
+    const int64_t c0 = gload(cu + lo), c1 = gload(cu + lo + 1), p0 = gload(start + lo);
     if (c0 < 0 || c1 < c0 || c1 > n_tokens || p0 < 0 || p0 + (c1 - c0) > 0x7fffffff) {
         set_err(err, MOE_ERR_LEN);
         return r;

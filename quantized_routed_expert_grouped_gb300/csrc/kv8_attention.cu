@@ -14,6 +14,7 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
     constexpr int kRows = 8 / WPR;
     __shared__ float acc[WPR > 1 ? 8 : 1][256];
     pdl_wait();
+    pdl_trigger();
     const AttnArgs& a = p.a;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, sub = wid / WPR, w = wid - sub * WPR, D = a.c.D;
     const int row = blockIdx.x * kRows + sub, rows = a.c.n_seqs * a.T * a.n_heads;
@@ -140,6 +141,18 @@ bool attn_list_fits(const AttnArgs& a) {
 
 cudaError_t launch_attn_combine(const AttnPlan& p, cudaStream_t st) {
     const int64_t rows = static_cast<int64_t>(p.a.c.n_seqs) * p.a.T * p.a.n_heads;
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kv8_combine_kernel<8>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kv8_combine_kernel<1>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_relaxed);
+    }
     // few rows have many parts each
     if (rows <= 1024)
         return launch_kernel(kv8_combine_kernel<8>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, true, p);

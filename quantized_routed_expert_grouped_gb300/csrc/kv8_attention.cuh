@@ -87,7 +87,7 @@ cudaError_t launch_attn_combine(const AttnPlan& p, cudaStream_t st);
 
 // Blocks that a sequence's queries can see: n blocks from `first`.
 __device__ __forceinline__ void attn_seq(const AttnArgs& a, int b, int& len, int& first, int& n, bool report) {
-    len = __ldg(a.lens + b);
+    len = gload(a.lens + b);
     const int64_t cap = static_cast<int64_t>(a.c.max_pages) * a.c.page_blocks * kKvBlock;
     if (len < 0) {
         if (report) set_err(a.err, MOE_ERR_LEN);
@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
     empty += grp * S;
     flag += grp * S;
 
-    pdl_trigger();
     if (rt == 0) {
         if (lane == 0) {
             for (int i = 0; i < S; ++i) {
@@ -247,6 +246,8 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
         }
         __syncwarp();
     }
+    pdl_wait();
+    pdl_trigger();  // (the joining kernel waits for this one's end in turn)
     // ---- the list and this CTA's range: each warp sums the sequences for itself, a lane a run of them
     const int B = a.c.n_seqs, span = (B + 31) / 32, b0 = min(B, lane * span), b1 = min(B, b0 + span);
     AttnPiece x;
@@ -345,31 +346,29 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
     load_qs(x.b, x.seg, qr);
 
     // ---- copies: the group's first warp issues its blocks S ahead of the arithmetic
-    int iu = pieces[1].blk + grp, iend = pieces[1].end;       // the next blocks to look up, and the piece's end
-    int ik = 0, is = 0, iph = 1, at = 0, ready = 0;            // copies issued, stage, phase; blocks looked up
-    const uint8_t* src = nullptr;                              // records of up to 32 blocks, one a lane; nullptr: unreadable
+    // (pieces[1].blk: the next block to look up)
+    int is = 0, iph = 1, at = 0, ready = 0;  // stage, its phase before; blocks looked up
+    const uint8_t* src = nullptr;            // records of up to 32 blocks, one a lane; nullptr: unreadable
     bool more = rt == 0;
     auto look_up = [&]() {
-        while (iu >= iend) {
-            AttnPiece t = pieces[1];
+        AttnPiece t = pieces[1];
+        while (t.blk + grp >= t.end) {
             more = attn_next(p, t);
             if (!more) return;
-            __syncwarp();
-            if (lane == 0) pieces[1] = t;
-            __syncwarp();
-            iu = t.blk + grp;
-            iend = t.end;
         }
-        const int u = iu + lane * NG;
+        const int u = t.blk + grp + lane * NG;
         src = nullptr;
-        if (u < iend) {
-            const int pi = u / a.c.page_blocks, page = __ldg(a.c.table + pieces[1].b * a.c.table_stride + pi);
+        if (u < t.end) {
+            const int pi = u / a.c.page_blocks, page = gload(a.c.table + t.b * a.c.table_stride + pi);
             if (page >= 0 && page < a.c.n_pages)
-                src = a.c.pool + ((static_cast<int64_t>(page) * a.c.n_kv + pieces[1].seg / p.g.RB) * a.c.page_blocks + u - pi * a.c.page_blocks) * L::kRec;
+                src = a.c.pool + ((static_cast<int64_t>(page) * a.c.n_kv + t.seg / p.g.RB) * a.c.page_blocks + u - pi * a.c.page_blocks) * L::kRec;
         }
         at = 0;
-        ready = min(32, (iend - iu + NG - 1) / NG);
-        iu += 32 * NG;
+        ready = min(32, (t.end - t.blk - grp + NG - 1) / NG);
+        t.blk += 32 * NG;
+        __syncwarp();
+        if (lane == 0) pieces[1] = t;
+        __syncwarp();
     };
     auto issue = [&]() {
         if (at == ready) {
@@ -390,7 +389,6 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
             else set_err(a.err, MOE_ERR_PAGE);
         }
         ++at;
-        ++ik;
         if (++is == S) {
             is = 0;
             iph ^= 1;
@@ -398,12 +396,13 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
     };
     for (int i = 0; i < S; ++i) issue();
 
-    int cs = 0, cph = 0, landed = 0;  // the stage to consume and its phase; copies seen to land
+    int cs = 0, cph = 0;  // the stage to consume and its phase
     bool lost = false;
     for (int piece = 0;; ++piece) {
+        // ---- queries: shifted by a power of two into fp16's range, stored as the lanes take them
+        {
         const int xb = pieces[0].b, xseg = pieces[0].seg, kv = xseg / p.g.RB, rb = xseg - kv * p.g.RB;
         const int rows = min(RP, p.R - rb * RP);
-        // ---- queries: shifted by a power of two into fp16's range, stored as the lanes take them
         for (int r0 = qr; r0 < RP; r0 += kAhead * kStep) {
             Q8 now[kAhead];
 #pragma unroll
@@ -478,6 +477,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                 }
             }
         }
+        }
         __syncthreads();
 
         float o[MT][kND][4], m[MT][2], dd[MT][2], fr[MT][2], off[MT][4];
@@ -508,7 +508,6 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                 *dead = 1;
                 lost = true;
             }
-            if (!lost) ++landed;
             if (!lost && flag[cs]) {
                 const uint8_t* rec = ring + cs * L::kRec;
                 const float2 sc = *reinterpret_cast<const float2*>(rec);
@@ -575,10 +574,10 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const int row = rb * RP + (rt * MT + mt) * 16 + q * 8 + g;
+                            const int row = pieces[0].seg % p.g.RB * RP + (rt * MT + mt) * 16 + q * 8 + g;
                             const int t = row / a.G, ps = row < p.R ? before_window + t : -1;
                             uint32_t bits = 0;
-                            if (a.tree && ps >= 0) bits = static_cast<uint32_t>(__ldg(a.tree + static_cast<int64_t>(xb) * a.T + t));
+                            if (a.tree && ps >= 0) bits = static_cast<uint32_t>(gload(a.tree + static_cast<int64_t>(pieces[0].b) * a.T + t));
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const int j = t0 + 8 * c + i, w = j - before_window;
@@ -600,7 +599,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                         for (int jj = 1; jj < 4; ++jj) bm = fmaxf(bm, fmaxf(sa[mt][jj][2 * q], sa[mt][jj][2 * q + 1]));
                         f[mt][q] = fr[mt][q] * sc.x;
                         top[mt][q] = bm * f[mt][q];
-                        grew |= top[mt][q] > m[mt][q] + kAttnSlack || top[mt][q] + e > m[mt][q] - dd[mt][q] + (kAttnSlack - 1.0f);
+                        grew |= top[mt][q] - m[mt][q] > fminf(kAttnSlack, kAttnSlack - 1.0f - (e + dd[mt][q]));
                     }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -726,10 +725,11 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                 Ls[mt][q] = ll;
                 cf[mt][q] = ll == 0.0f ? 0.0f : ex2(m[mt][q] - bs - dd[mt][q]) / ll;
             }
-        const AttnPiece* xp = pieces;
+        const AttnPiece* xp = pieces;  // (read again: nothing of it is held during the loop)
+        const int rows = min(RP, p.R - xp->seg % p.g.RB * RP);
         const bool whole = xp->blk == xp->first && xp->end == xp->first + xp->n;
         float* part = p.parts + (2LL * blockIdx.x + (piece ? 1 : 0)) * attn_part_floats(RP, D);
-        const int64_t orow0 = static_cast<int64_t>(xb) * a.T * a.n_heads;
+        const int64_t orow0 = static_cast<int64_t>(xp->b) * a.T * a.n_heads;
         // the next piece's first queries are on their way during the joining
         AttnPiece nx = pieces[0];
         const bool again = attn_next(p, nx);
@@ -814,8 +814,8 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
         }
         if (!again) break;
     }
-    if (*dead && rt == 0)  // leave no copy of this CTA's in flight
-        for (int k = landed; k < ik; ++k) mbar_wait_bounded(full + k % S, (k / S) & 1);
+    if (*dead && rt == 0)  // leave no copy of this CTA's in flight: a stage's last one is of this round or the one before
+        for (int k = 0; k < S; ++k) mbar_wait_bounded(full + k, k < is ? iph ^ 1 : iph);
 }
 
 template <int D, int MT, bool SPLIT>
@@ -833,6 +833,8 @@ cudaError_t launch_attn(AttnPlan p, cudaStream_t st) {
     if (n <= 0) {
         e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmMax);
+        // (as the joining kernel: an SM that has to change its split waits until it is empty)
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
         sms[dev].store(n, std::memory_order_relaxed);
     }
@@ -850,7 +852,7 @@ cudaError_t launch_attn(AttnPlan p, cudaStream_t st) {
     p.smem = fixed + stages * NG * L::kRec;
     int grid = n * occ;
     if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
-    e = launch_kernel(kern, dim3(grid), dim3(kAttnThreads), p.smem, st, false, p);
+    e = launch_kernel(kern, dim3(grid), dim3(kAttnThreads), p.smem, st, true, p);
     return e;
 }
 

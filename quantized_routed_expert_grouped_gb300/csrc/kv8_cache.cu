@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<c
     __shared__ uint32_t red[2][4];
     __shared__ __align__(16) uint8_t turn[D * kTurn];
     const int h = blockIdx.x % c.n_kv, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_trigger();
     const KvSlot s = kv8_slot(blockIdx.x / c.n_kv, cu, start, c.n_seqs, n_tokens, err);
     if (s.b < 0) return;
     uint8_t* rec = kv8_record(c, s.b, s.blk, h, err);
@@ -189,6 +191,8 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
     const int lane = threadIdx.x & 31;
     int64_t work = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     if (work >= n_work) return;
+    pdl_wait();
+    pdl_trigger();
     const bool values = work & 1;
     work >>= 1;
     const int h = static_cast<int>(work % c.n_kv);
@@ -199,14 +203,14 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
     auto* kb = K.p + s.row * K.ts + h * K.hs;
     auto* vb = V.p + s.row * V.ts + h * V.hs;
     const int NB = c.D / 32;
-    const float2 sc = __ldg(reinterpret_cast<const float2*>(rec));
+    const float2 sc = gload(reinterpret_cast<const float2*>(rec));
     const int g = lane >> 2;
     const uint2* kr = reinterpret_cast<const uint2*>(rec + kKvHead);
 #pragma unroll 2
     for (int i = 0; i < NB && !values; ++i) {
         uint2 q[4];
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj) q[jj] = __ldg(kr + (jj * NB + i) * 32 + lane);
+        for (int jj = 0; jj < 4; ++jj) q[jj] = gload(kr + (jj * NB + i) * 32 + lane);
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             const int t = 8 * (g >> 1) + 2 * jj + (g & 1);
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
     for (int i = 0; i < NB && values; ++i) {
         uint32_t q[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = __ldg(vr + (i * 32 + dg * 8 + e) * 8 + tq);
+        for (int e = 0; e < 8; ++e) q[e] = gload(vr + (i * 32 + dg * 8 + e) * 8 + tq);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int t = 4 * tq + j;
@@ -243,7 +247,7 @@ cudaError_t write_t(const KvCache& c, const moe_kv8_rows& r, const int32_t* cu, 
     const KvRows<const T> V{static_cast<const T*>(r.v), r.v_token_stride, r.v_head_stride, vvec};
     switch (c.D / 32) {
 #define MOE_KV8_CASE(NB) \
-    case NB: kv8_write_kernel<TYPE, NB><<<grid, kThreads, 0, st>>>(c, K, V, r.n_tokens, cu, start, err); break;
+    case NB: return launch_kernel(kv8_write_kernel<TYPE, NB>, dim3(grid), dim3(kThreads), 0, st, true, c, K, V, r.n_tokens, cu, start, err);
         MOE_KV8_CASE(1)
         MOE_KV8_CASE(2)
         MOE_KV8_CASE(3)
@@ -254,7 +258,7 @@ cudaError_t write_t(const KvCache& c, const moe_kv8_rows& r, const int32_t* cu, 
         MOE_KV8_CASE(8)
 #undef MOE_KV8_CASE
     }
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 template <int TYPE>
@@ -264,8 +268,7 @@ cudaError_t read_t(const KvCache& c, const moe_kv8_rows& r, const int32_t* cu, c
     const KvRows<T> K{static_cast<T*>(r.k), r.k_token_stride, r.k_head_stride, kvec};
     const KvRows<T> V{static_cast<T*>(r.v), r.v_token_stride, r.v_head_stride, vvec};
     const unsigned grid = static_cast<unsigned>((work + kThreads / 32 - 1) / (kThreads / 32));
-    kv8_read_kernel<TYPE><<<grid, kThreads, 0, st>>>(c, K, V, r.n_tokens, work, cu, start, err);
-    return cudaGetLastError();
+    return launch_kernel(kv8_read_kernel<TYPE>, dim3(grid), dim3(kThreads), 0, st, true, c, K, V, r.n_tokens, work, cu, start, err);
 }
 
 }  // namespace

@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_n
     using E = Elem<TYPE>;
     using T = typename E::T;
     __shared__ float red[32];
+    pdl_wait();
+    pdl_trigger();
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const T* x = static_cast<const T*>(c.x) + row * c.x_stride;
@@ -147,14 +149,16 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_n
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(256) dequantize_q8_1_kernel(const moe_q8_1* __restrict__ xq, int64_t n_blocks,
-                                                              typename Elem<TYPE>::T* __restrict__ out) {
+__global__ void __launch_bounds__(256) dequantize_q8_1_kernel(const moe_q8_1* xq, int64_t n_blocks,
+                                                              typename Elem<TYPE>::T* out) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= n_blocks * 4) return;
+    pdl_wait();
+    pdl_trigger();
     const uint32_t* blk = reinterpret_cast<const uint32_t*>(xq + (i >> 2));
     const int part = static_cast<int>(i & 3);
-    const float d = h2f_bits(__ldg(blk));
-    const uint32_t w[2] = {__ldg(blk + 1 + 2 * part), __ldg(blk + 2 + 2 * part)};
+    const float d = h2f_bits(gload(blk));
+    const uint32_t w[2] = {gload(blk + 1 + 2 * part), gload(blk + 2 + 2 * part)};
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = d * static_cast<float>(static_cast<int8_t>(w[e >> 2] >> (8 * (e & 3))));
@@ -172,10 +176,9 @@ cudaError_t norm_t(const moe_norm_call& c, cudaStream_t st) {
     // few rows: as many threads as the row has pieces, for the shortest chain; many: two pieces a thread
     const int chunks = pieces > 1024 ? 4 : c.rows > 304 && pieces >= 64 ? 2 : 1;
     const int threads = ((pieces + chunks - 1) / chunks + 31) / 32 * 32;
-    if (chunks == 1) add_rms_norm_q8_1_kernel<TYPE, 1><<<grid, threads, 0, st>>>(c);
-    else if (chunks == 2) add_rms_norm_q8_1_kernel<TYPE, 2><<<grid, threads, 0, st>>>(c);
-    else add_rms_norm_q8_1_kernel<TYPE, 4><<<grid, threads, 0, st>>>(c);
-    return cudaGetLastError();
+    if (chunks == 1) return launch_kernel(add_rms_norm_q8_1_kernel<TYPE, 1>, dim3(grid), dim3(threads), 0, st, true, c);
+    if (chunks == 2) return launch_kernel(add_rms_norm_q8_1_kernel<TYPE, 2>, dim3(grid), dim3(threads), 0, st, true, c);
+    return launch_kernel(add_rms_norm_q8_1_kernel<TYPE, 4>, dim3(grid), dim3(threads), 0, st, true, c);
 }
 
 }  // namespace
@@ -190,12 +193,12 @@ cudaError_t launch_add_rms_norm_q8_1(const moe_norm_call& c, cudaStream_t st) {
 cudaError_t launch_dequantize_q8_1(const moe_q8_1* xq, int64_t n_blocks, void* out, int type, cudaStream_t st) {
     if (n_blocks == 0) return cudaSuccess;
     const unsigned grid = static_cast<unsigned>((n_blocks * 4 + 255) / 256);
-    if (type == MOE_F32) dequantize_q8_1_kernel<MOE_F32><<<grid, 256, 0, st>>>(xq, n_blocks, static_cast<float*>(out));
-    else if (type == MOE_F16)
-        dequantize_q8_1_kernel<MOE_F16><<<grid, 256, 0, st>>>(xq, n_blocks, static_cast<__half*>(out));
-    else
-        dequantize_q8_1_kernel<MOE_BF16><<<grid, 256, 0, st>>>(xq, n_blocks, static_cast<__nv_bfloat16*>(out));
-    return cudaGetLastError();
+    if (type == MOE_F32)
+        return launch_kernel(dequantize_q8_1_kernel<MOE_F32>, dim3(grid), dim3(256), 0, st, true, xq, n_blocks, static_cast<float*>(out));
+    if (type == MOE_F16)
+        return launch_kernel(dequantize_q8_1_kernel<MOE_F16>, dim3(grid), dim3(256), 0, st, true, xq, n_blocks, static_cast<__half*>(out));
+    return launch_kernel(dequantize_q8_1_kernel<MOE_BF16>, dim3(grid), dim3(256), 0, st, true, xq, n_blocks,
+                         static_cast<__nv_bfloat16*>(out));
 }
 
 }  // namespace moe
