@@ -1,5 +1,7 @@
 // kv8_attention.cu - planning the attention call, and the kernel that joins the parts of sequences
 // that several CTAs worked on.
+#include <algorithm>
+
 #include "kv8_attention.cuh"
 
 namespace moe {
@@ -128,13 +130,16 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
 }  // namespace
 
 int64_t attn_workspace_bytes(int n_seqs, int T, int n_heads, int n_kv, int D) {
-    const AttnGeom g = attn_geom(T * (n_heads / n_kv), D);
-    return attn_plan_bytes(n_seqs) + 2LL * kAttnMaxCtas * attn_part_floats(g.RP, D) * 4;
+    // (as much as any smaller head_dim asks for, so that a workspace serves smaller calls too)
+    const int R = T * (n_heads / n_kv);
+    int64_t floats = attn_part_floats(attn_geom(R, D, false).RP, D);
+    if (D > 128) floats = std::max(floats, attn_part_floats(attn_geom(R, 128, false).RP, 128));
+    return attn_plan_bytes(n_seqs) + 2LL * kAttnMaxCtas * floats * 4;
 }
 
 // The list of blocks, with the segments' fixed parts, is counted in 32 bits.
 bool attn_list_fits(const AttnArgs& a) {
-    const AttnGeom g = attn_geom(a.T * a.G, a.c.D);
+    const AttnGeom g = attn_geom(a.T * a.G, a.c.D, false);
     const double most = 1.0 * a.c.n_seqs * a.c.n_kv * g.RB * (1.0 * a.c.max_pages * a.c.page_blocks + kAttnSegCost);
     return most < 2147483647.0 - 2 * kAttnMaxCtas;
 }
@@ -163,12 +168,12 @@ cudaError_t launch_kv8_attention(const AttnArgs& a, int type, cudaStream_t st) {
     AttnPlan p{};
     p.a = a;
     p.R = a.T * a.G;
-    p.g = attn_geom(p.R, a.c.D);
+    p.g = attn_geom(p.R, a.c.D, type == MOE_F32);
     p.segs = a.c.n_kv * p.g.RB;
     p.out_type = type;
     p.plan = static_cast<int*>(a.workspace);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + attn_plan_bytes(a.c.n_seqs));
-    const cudaError_t e = type == MOE_F32 ? launch_attn_f32(p, st) : launch_attn_16(p, st);
+    const cudaError_t e = type == MOE_F32 ? launch_attn_f32(p, st) : type == MOE_F16 ? launch_attn_f16(p, st) : launch_attn_bf16(p, st);
     return e == cudaSuccess ? launch_attn_combine(p, st) : e;
 }
 

@@ -10,7 +10,7 @@
 // block's scale. o and l are rescaled only when m or n moves, which after the first blocks is rare. fp16's
 // range below 2^10, down to 2^-24, keeps a long tail of small weights. Codes and, after a shift by a
 // power of two, 16-bit queries are exact in fp16; an fp32 query and its weights are two fp16 parts
-// each (SPLIT). Sums are fp32. Key codes enter as fp16 subnormals (two byte permutes per four codes) and
+// each. Sums are fp32. Key codes enter as fp16 subnormals (two byte permutes per four codes) and
 // the score starts at -128 * sum q, which is of the scores' own size; value codes are centred (two
 // subtractions more): the sum of weights would be far above the result.
 //
@@ -43,6 +43,9 @@ namespace moe {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
+// fp16 parts: one of a query and of a weight; of a weight two, for fp16 outputs, whose error one part's rounding
+// would raise by 1.4 (with two row tiles a warp the products bound the kernel, and one part it is); of both two, for fp32.
+constexpr int kAttnPlain = 0, kAttnWeights = 1, kAttnSplit = 2;
 constexpr int kAttnStages = 24;          // ring stages of a CTA, at most
 constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many CTAs
 // A row's references m and n move to their maxima only once those are kAttnSlack (in powers of two)
@@ -52,15 +55,18 @@ constexpr int kAttnMinPart = 8;          // blocks of a part, at least (but for 
 constexpr int kAttnSegCost = 16;         // blocks that a segment's fixed work (queries, joining) costs
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 
-// Row tiles of a pass over the blocks: MT tiles of 16 rows per warp, RTW warps share a ring.
+// Row tiles of a pass over the blocks: MT tiles of 16 rows per warp; two warps share a ring where there are
+// more rows. Further rows are further passes, which find the blocks in L2: four warps on a ring left one
+// CTA with 128 rows of queries to convert, 20 us for a short sequence. Two fp16 parts and two tiles a warp do
+// not fit its registers: 32 fp32 rows are a tile for each of two warps (32 x 32k tokens: 115 instead of 134 us).
 struct AttnGeom {
     int MT, RTW, RP, RB;  // RP = 16 MT RTW rows a pass, RB passes
 };
-inline __host__ __device__ AttnGeom attn_geom(int R, int D) {
+inline __host__ __device__ AttnGeom attn_geom(int R, int D, bool split) {
     AttnGeom g;
-    g.MT = D <= 128 && R > 16 ? 2 : 1;
+    g.MT = D <= 128 && R > (split ? 32 : 16) ? 2 : 1;
     const int tiles = (R + 16 * g.MT - 1) / (16 * g.MT);
-    g.RTW = tiles >= 3 ? 4 : tiles;
+    g.RTW = tiles >= 2 ? 2 : 1;
     g.RP = 16 * g.MT * g.RTW;
     g.RB = (R + g.RP - 1) / g.RP;
     return g;
@@ -82,7 +88,8 @@ struct AttnPlan {
 };
 
 cudaError_t launch_attn_f32(const AttnPlan& p, cudaStream_t st);
-cudaError_t launch_attn_16(const AttnPlan& p, cudaStream_t st);
+cudaError_t launch_attn_f16(const AttnPlan& p, cudaStream_t st);
+cudaError_t launch_attn_bf16(const AttnPlan& p, cudaStream_t st);
 cudaError_t launch_attn_combine(const AttnPlan& p, cudaStream_t st);
 
 // Blocks that a sequence's queries can see: n blocks from `first`.
@@ -196,13 +203,14 @@ __device__ __forceinline__ bool attn_next(const AttnPlan& p, AttnPiece& x) {
     return true;
 }
 
-template <int D, int MT, bool SPLIT>
+template <int D, int MT, int PREC>
 struct AttnSmem {
+    static constexpr bool SPLIT = PREC == kAttnSplit;
     static constexpr int kRec = kv8_record_bytes(D);
     static constexpr int kTileQ = D * 32 * (SPLIT ? 2 : 1);  // fragments of 16 rows
     static constexpr int kRowO = D + 8;                      // floats of a row in the joining buffer
     static __host__ __device__ int buf_bytes(int RTW) {
-        const int q = kTileQ * MT * RTW, o = RTW < kAttnWarps ? 16 * MT * RTW * kRowO * 4 : 0;
+        const int q = kTileQ * MT * RTW, o = 16 * MT * RTW * kRowO * 4;
         return q > o ? q : o;
     }
     // buffer (queries, then the joined rows), the warps' m and l, row factors and offsets, output rows, the
@@ -211,9 +219,10 @@ struct AttnSmem {
     static __host__ __device__ int fixed(int RTW) { return (buf_bytes(RTW) + kStats + kAttnStages * 20 + 16 + 15) / 16 * 16; }
 };
 
-template <int D, int MT, bool SPLIT>
-__global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 3 : 2) kv8_attention_kernel(const AttnPlan p) {
-    using L = AttnSmem<D, MT, SPLIT>;
+template <int D, int MT, int PREC>
+__global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC != kAttnSplit ? 3 : 2) kv8_attention_kernel(const AttnPlan p) {
+    using L = AttnSmem<D, MT, PREC>;
+    constexpr bool SPLIT = PREC == kAttnSplit, W2 = PREC != kAttnPlain;  // two parts of a query; of a weight
     constexpr int kNB = D / 32, kND = D / 8;
     extern __shared__ __align__(128) uint8_t sm[];
     const AttnArgs& a = p.a;
@@ -648,7 +657,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                                 }
                                 const uint32_t h = pack_h2(w.x, w.y);
                                 word(pa[mt][jj >> 1], (jj & 1) * 2 + q) = h;
-                                if (SPLIT) {
+                                if (W2) {
                                     const float2 h2 = unpack_h2(h);
                                     word(pl[mt][jj >> 1], (jj & 1) * 2 + q) = pack_h2(w.x - h2.x, w.y - h2.y);
                                 }
@@ -675,7 +684,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt)
                                 mma_16816(o[mt][i0 + i], pa[mt][xx], v[i][2 * xx], v[i][2 * xx + 1]);
-                    if (SPLIT) {
+                    if (W2) {
 #pragma unroll
                         for (int xx = 0; xx < 2; ++xx)
 #pragma unroll
@@ -768,21 +777,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
                     make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
             }
         };
-        if (NG == 1) {
-            // one warp holds the row: neighbouring lanes swap halves, so that each has four dims of a row
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int i = 0; i < kND; ++i) {
-                    const float x0 = o[mt][i][0] * cf[mt][0], x1 = o[mt][i][1] * cf[mt][0];
-                    const float y0 = o[mt][i][2] * cf[mt][1], y1 = o[mt][i][3] * cf[mt][1];
-                    const bool odd = c & 1;
-                    const float s0 = __shfl_xor_sync(0xffffffffu, odd ? x0 : y0, 1), s1 = __shfl_xor_sync(0xffffffffu, odd ? x1 : y1, 1);
-                    const int rr = (rt * MT + mt) * 16 + (odd ? 8 : 0) + g;
-                    if (rr < rows) put(rr, i * 8 + (c & 2) * 2, odd ? make_float4(s0, s1, y0, y1) : make_float4(x0, x1, s0, s1));
-                }
-            __syncthreads();  // the queries and rows have been read by all
-        } else {
+        {
             for (int k = 0; k < NG; ++k) {
                 if (grp == k) {
 #pragma unroll
@@ -818,10 +813,10 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && !SPLIT ? 
         for (int k = 0; k < S; ++k) mbar_wait_bounded(full + k, k < is ? iph ^ 1 : iph);
 }
 
-template <int D, int MT, bool SPLIT>
+template <int D, int MT, int PREC>
 cudaError_t launch_attn(AttnPlan p, cudaStream_t st) {
-    using L = AttnSmem<D, MT, SPLIT>;
-    auto kern = kv8_attention_kernel<D, MT, SPLIT>;
+    using L = AttnSmem<D, MT, PREC>;
+    auto kern = kv8_attention_kernel<D, MT, PREC>;
     constexpr int kMaxDev = 64;
     static std::atomic<int> sms[kMaxDev];
     int dev = 0;
@@ -839,7 +834,7 @@ cudaError_t launch_attn(AttnPlan p, cudaStream_t st) {
         sms[dev].store(n, std::memory_order_relaxed);
     }
     // CTAs per SM that the registers allow, fewer where the row buffer leaves no room for the ring
-    int occ = MT == 1 && D <= 128 && !SPLIT ? 3 : 2;
+    int occ = MT == 1 && D <= 128 && PREC != kAttnSplit ? 3 : 2;
     const int NG = kAttnWarps / p.g.RTW, fixed = L::fixed(p.g.RTW);
     int stages = 0;
     for (;; --occ) {

@@ -1,6 +1,4 @@
-// kv8_attention_f32.cu - the attention kernel for fp32 queries (two fp16 parts).
-#include <atomic>
-
+// kv8_attention_f32.cu - the attention kernel for fp32 queries.
 #include "kv8_attention.cuh"
 
 namespace moe {
@@ -8,14 +6,14 @@ namespace moe {
 cudaError_t launch_attn_f32(const AttnPlan& p, cudaStream_t st) {
     const bool two = p.g.MT == 2;
     switch (p.a.c.D) {
-    case 32: return two ? launch_attn<32, 2, true>(p, st) : launch_attn<32, 1, true>(p, st);
-    case 64: return two ? launch_attn<64, 2, true>(p, st) : launch_attn<64, 1, true>(p, st);
-    case 96: return two ? launch_attn<96, 2, true>(p, st) : launch_attn<96, 1, true>(p, st);
-    case 128: return two ? launch_attn<128, 2, true>(p, st) : launch_attn<128, 1, true>(p, st);
-    case 160: return launch_attn<160, 1, true>(p, st);
-    case 192: return launch_attn<192, 1, true>(p, st);
-    case 224: return launch_attn<224, 1, true>(p, st);
-    default: return launch_attn<256, 1, true>(p, st);
+    case 32: return two ? launch_attn<32, 2, kAttnSplit>(p, st) : launch_attn<32, 1, kAttnSplit>(p, st);
+    case 64: return two ? launch_attn<64, 2, kAttnSplit>(p, st) : launch_attn<64, 1, kAttnSplit>(p, st);
+    case 96: return two ? launch_attn<96, 2, kAttnSplit>(p, st) : launch_attn<96, 1, kAttnSplit>(p, st);
+    case 128: return two ? launch_attn<128, 2, kAttnSplit>(p, st) : launch_attn<128, 1, kAttnSplit>(p, st);
+    case 160: return launch_attn<160, 1, kAttnSplit>(p, st);
+    case 192: return launch_attn<192, 1, kAttnSplit>(p, st);
+    case 224: return launch_attn<224, 1, kAttnSplit>(p, st);
+    default: return launch_attn<256, 1, kAttnSplit>(p, st);
     }
 }
 
