@@ -92,8 +92,8 @@ int moe_kv8_read(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int
  * fp16 with a shift that keeps 2^-39 of the largest, sums in fp32; fp32 queries and their weights
  * are split in two fp16 parts. A page that cannot be read (MOE_ERR_PAGE) counts as not seen.
  * Limits: 1 <= T <= 32, n_heads a multiple of n_kv_heads; n_seqs * T * n_heads, and n_seqs *
- * n_kv_heads * max_pages * page_tokens / 32 (times the passes over the rows of a key/value head, 64
- * or, above head_dim 128, 32 rows each), below 2^31 (MOE_E_CAP). lens may be 0 (nothing seen) and is
+ * n_kv_heads * max_pages * page_tokens / 32 (times the passes over the rows of a key/value head, 32
+ * rows each), below 2^31 (MOE_E_CAP). lens may be 0 (nothing seen) and is
  * clamped to the page table (MOE_ERR_PAGE).
  * workspace: moe_kv8_attention_workspace_bytes(...) bytes, 16-byte aligned, of any contents; calls
  * that may run at the same time need one each. */

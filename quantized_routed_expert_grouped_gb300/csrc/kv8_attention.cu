@@ -131,16 +131,14 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
 
 int64_t attn_workspace_bytes(int n_seqs, int T, int n_heads, int n_kv, int D) {
     // (as much as any smaller head_dim asks for, so that a workspace serves smaller calls too)
-    const int R = T * (n_heads / n_kv);
-    int64_t floats = attn_part_floats(attn_geom(R, D, false).RP, D);
-    if (D > 128) floats = std::max(floats, attn_part_floats(attn_geom(R, 128, false).RP, 128));
+    const int R = T * (n_heads / n_kv), one = attn_geom(R, false).RP, two = attn_geom(R, true).RP;
+    const int64_t floats = std::max(attn_part_floats(one, D), attn_part_floats(two, std::min(D, 128)));
     return attn_plan_bytes(n_seqs) + 2LL * kAttnMaxCtas * floats * 4;
 }
 
 // The list of blocks, with the segments' fixed parts, is counted in 32 bits.
 bool attn_list_fits(const AttnArgs& a) {
-    const AttnGeom g = attn_geom(a.T * a.G, a.c.D, false);
-    const double most = 1.0 * a.c.n_seqs * a.c.n_kv * g.RB * (1.0 * a.c.max_pages * a.c.page_blocks + kAttnSegCost);
+    const double most = 1.0 * a.c.n_seqs * a.c.n_kv * attn_geom(a.T * a.G, false).RB * (1.0 * a.c.max_pages * a.c.page_blocks + kAttnSegCost);
     return most < 2147483647.0 - 2 * kAttnMaxCtas;
 }
 
@@ -168,7 +166,9 @@ cudaError_t launch_kv8_attention(const AttnArgs& a, int type, cudaStream_t st) {
     AttnPlan p{};
     p.a = a;
     p.R = a.T * a.G;
-    p.g = attn_geom(p.R, a.c.D, type == MOE_F32);
+    const int64_t blocks = static_cast<int64_t>(a.c.n_seqs) * a.c.n_kv * a.c.max_pages * a.c.page_blocks;
+    p.g = attn_geom(p.R, type != MOE_F32 && a.c.D <= 128 && p.R > 16 && blocks >= kAttnLong);
+    p.prec = type == MOE_F32 ? kAttnSplit : type == MOE_F16 && (p.R <= 16 || blocks < kAttnShort) ? kAttnWeights : kAttnPlain;
     p.segs = a.c.n_kv * p.g.RB;
     p.out_type = type;
     p.plan = static_cast<int*>(a.workspace);

@@ -44,7 +44,7 @@ namespace moe {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 // fp16 parts: one of a query and of a weight; of a weight two, for fp16 outputs, whose error one part's rounding
-// would raise by 1.4 (with two row tiles a warp the products bound the kernel, and one part it is); of both two, for fp32.
+// would raise by 1.4 (but see kAttnShort); of both two, for fp32.
 constexpr int kAttnPlain = 0, kAttnWeights = 1, kAttnSplit = 2;
 constexpr int kAttnStages = 24;          // ring stages of a CTA, at most
 constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many CTAs
@@ -57,20 +57,27 @@ constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 
 // Row tiles of a pass over the blocks: MT tiles of 16 rows per warp; two warps share a ring where there are
 // more rows. Further rows are further passes, which find the blocks in L2: four warps on a ring left one
-// CTA with 128 rows of queries to convert, 20 us for a short sequence. Two fp16 parts and two tiles a warp do
-// not fit its registers: 32 fp32 rows are a tile for each of two warps (32 x 32k tokens: 115 instead of 134 us).
+// CTA with 128 rows of queries to convert, 20 us for a short sequence.
 struct AttnGeom {
     int MT, RTW, RP, RB;  // RP = 16 MT RTW rows a pass, RB passes
 };
-inline __host__ __device__ AttnGeom attn_geom(int R, int D, bool split) {
+inline AttnGeom attn_geom(int R, bool two) {
     AttnGeom g;
-    g.MT = D <= 128 && R > (split ? 32 : 16) ? 2 : 1;
-    const int tiles = (R + 16 * g.MT - 1) / (16 * g.MT);
-    g.RTW = tiles >= 2 ? 2 : 1;
+    g.MT = two ? 2 : 1;
+    g.RTW = R > 16 * g.MT ? 2 : 1;
     g.RP = 16 * g.MT * g.RTW;
     g.RB = (R + g.RP - 1) / g.RP;
     return g;
 }
+// Two tiles a warp widen a block's codes once for 32 rows, and leave registers for eight warps an SM instead of
+// twelve: better where the work is long (32 windows of 4 over 8k to 32k tokens: 252 against 285 us), not where it
+// is short (4 over 3k: 24.5 against 22.8), about even at kAttnLong blocks of the page table. Not for fp32
+// (two fp16 parts: 64 rows of 16k tokens 138 against 114 us) or wide heads, whose sums fill the registers.
+constexpr int64_t kAttnLong = 24576;
+// With more than 16 fp16 rows, weights of two parts take as much again as one part where the products bound the
+// kernel: up to so many blocks latency does.
+constexpr int64_t kAttnShort = 4096;
+
 // workspace: int32 plan[n_seqs + 2] (what comes before each sequence in the list; the chunk, 0: a CTA
 // per part), then two parts per CTA
 inline __host__ __device__ int64_t attn_plan_bytes(int n_seqs) { return (static_cast<int64_t>(n_seqs) + 2 + 3) / 4 * 16; }
@@ -80,7 +87,7 @@ struct AttnPlan {
     AttnArgs a;
     AttnGeom g;
     int R, segs;     // rows of a key/value head; segments (head, pass) of a sequence
-    int out_type;
+    int out_type, prec;
     int stages;      // ring stages per group of RTW warps
     int smem;
     int* plan;
@@ -220,7 +227,7 @@ struct AttnSmem {
 };
 
 template <int D, int MT, int PREC>
-__global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC != kAttnSplit ? 3 : 2) kv8_attention_kernel(const AttnPlan p) {
+__global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == kAttnPlain ? 3 : 2) kv8_attention_kernel(const AttnPlan p) {
     using L = AttnSmem<D, MT, PREC>;
     constexpr bool SPLIT = PREC == kAttnSplit, W2 = PREC != kAttnPlain;  // two parts of a query; of a weight
     constexpr int kNB = D / 32, kND = D / 8;
@@ -834,7 +841,7 @@ cudaError_t launch_attn(AttnPlan p, cudaStream_t st) {
         sms[dev].store(n, std::memory_order_relaxed);
     }
     // CTAs per SM that the registers allow, fewer where the row buffer leaves no room for the ring
-    int occ = MT == 1 && D <= 128 && PREC != kAttnSplit ? 3 : 2;
+    int occ = MT == 1 && D <= 128 && PREC == kAttnPlain ? 3 : 2;
     const int NG = kAttnWarps / p.g.RTW, fixed = L::fixed(p.g.RTW);
     int stages = 0;
     for (;; --occ) {

@@ -1,4 +1,4 @@
-// kv8_attention_bf16.cu - the attention kernel for bf16 queries.
+// kv8_attention_bf16.cu - the attention kernel for bf16 queries, and fp16 ones with weights in one part.
 #include "kv8_attention.cuh"
 
 namespace moe {
