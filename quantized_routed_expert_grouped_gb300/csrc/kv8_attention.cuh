@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
     int is = 0, iph = 1, at = 0, ready = 0;  // stage, its phase before; blocks looked up
     const uint8_t* src = nullptr;            // records of up to 32 blocks, one a lane; nullptr: unreadable
     bool more = rt == 0;
+    const uint64_t once = l2_evict_first();
     auto look_up = [&]() {
         AttnPiece t = pieces[1];
         while (t.blk + grp >= t.end) {
@@ -401,7 +402,9 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
         if (lane == at) {
             flag[is] = src != nullptr;
             mbar_arrive_expect_tx(full + is, src ? L::kRec : 0);
-            if (src) bulk_g2s(ring + is * L::kRec, src, L::kRec, full + is);
+            // (read once, unless further passes over the rows follow: 94 instead of 98 us over a million tokens)
+            if (src && p.g.RB == 1) bulk_g2s_hint(ring + is * L::kRec, src, L::kRec, full + is, once);
+            else if (src) bulk_g2s(ring + is * L::kRec, src, L::kRec, full + is);
             else set_err(a.err, MOE_ERR_PAGE);
         }
         ++at;
