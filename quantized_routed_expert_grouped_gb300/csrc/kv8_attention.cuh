@@ -51,7 +51,7 @@ constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many C
 // A row's references m and n move to their maxima only once those are kAttnSlack (in powers of two)
 // above; l is held times 2^kAttnShift, the weights of the values times 2^(kAttnShift - 1).
 constexpr float kAttnShift = 11.0f, kAttnSlack = 4.0f;
-constexpr int kAttnMinPart = 8;          // blocks of a part, at least (but for a segment's remainder)
+constexpr int kAttnWhole = 48;           // blocks of a segment that is left whole
 constexpr int kAttnSegCost = 16;         // blocks that a segment's fixed work (queries, joining) costs
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 
@@ -125,19 +125,20 @@ struct AttnCut {
     int tb, chunk;  // of the list per CTA; 1 by parts
     __host__ __device__ __forceinline__ int cost(int n) const { return !n ? 0 : tb ? (n + tb - 1) / tb : n + kAttnSegCost; }
 };
-// blocks: of all segments; segs: segments that have any.
+// blocks: of all segments; segs: segments that have any; longest: blocks of the longest.
 // (The host keeps the whole list, at its longest, below 2^31.)
-__device__ __forceinline__ AttnCut attn_cut(int blocks, int segs, int ctas) {
+__device__ __forceinline__ AttnCut attn_cut(int blocks, int segs, int longest, int ctas) {
     AttnCut c;
     c.tb = 0;
     c.chunk = (blocks + segs * kAttnSegCost + ctas - 1) / ctas;
     if (segs < ctas) {
-        int tb = (blocks + (ctas - segs) - 1) / (ctas - segs);  // then the parts are at most `ctas`
-        if (tb < kAttnMinPart) tb = kAttnMinPart;
-        if (tb <= c.chunk || tb <= kAttnMinPart) {
-            c.tb = tb;
-            c.chunk = 1;
-        }
+        // a part has a block for each warp at least, or two where there are more parts than the joining reads at once
+        const int least = min(max(longest / 32, kAttnWarps), 2 * kAttnWarps);
+        const int tb = max((blocks + (ctas - segs) - 1) / (ctas - segs), least);  // then the parts are at most `ctas`
+        if (tb <= c.chunk || tb <= least) c.tb = tb;
+        // short segments are not worth cutting: a part costs as much as so many blocks
+        else if (longest <= kAttnWhole) c.tb = longest;
+        if (c.tb) c.chunk = 1;
     }
     return c;
 }
@@ -267,15 +268,17 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
     // ---- the list and this CTA's range: each warp sums the sequences for itself, a lane a run of them
     const int B = a.c.n_seqs, span = (B + 31) / 32, b0 = min(B, lane * span), b1 = min(B, b0 + span);
     AttnPiece x;
-    int blocks = 0, some = 0;
+    int blocks = 0, some = 0, longest = 0;
     x.n = 0;
     for (int b = b0; b < b1; ++b) {
         attn_seq(a, b, x.len, x.first, x.n, blockIdx.x == 0 && wid == 0);
         blocks += x.n;
         some += x.n > 0;
+        longest = max(longest, x.n);
     }
     const AttnCut cut = attn_cut(static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(blocks))) * p.segs,
-                                 static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(some))) * p.segs, gridDim.x);
+                                 static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(some))) * p.segs,
+                                 __reduce_max_sync(0xffffffffu, longest), gridDim.x);
     int mine = 0;
     if (span == 1) {  // the lane's one sequence is in x
         mine = cut.cost(x.n);
