@@ -43,13 +43,13 @@ struct Scales {
     float scale, inv, ratio;
     bool grew;
 };
-__device__ __forceinline__ Scales block_scale(float amax, float old) {
+__device__ __forceinline__ Scales block_scale(float amax, float old, bool kept) {
     Scales s;
     s.scale = max_nan(old, amax < kKvTiny ? 0.0f : __fdiv_rn(amax, 127.0f));
     if (!(s.scale <= 3.4028234e38f)) s.scale = __int_as_float(0x7fffffff);
     const bool some = s.scale > 0.0f;
     s.inv = some ? __fdiv_rn(1.0f, s.scale) : 0.0f;
-    s.ratio = some ? __fdiv_rn(old, s.scale) : 0.0f;
+    s.ratio = some && kept ? __fdiv_rn(old, s.scale) : 0.0f;
     s.grew = s.scale != old;
     return s;
 }
@@ -60,8 +60,12 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 }
 
 // NB = D / 32.
+// CTAs per SM: the more, the more rows in flight and the shorter the last wave (prompts of 25k tokens, 8 heads of
+// 128: 34 us at eight, 37 at the six that the compiler's own choice of registers leaves).
+constexpr int write_ctas(int type, int nb) { return type != MOE_F32 && nb <= 4 ? 8 : type != MOE_F32 || nb <= 4 ? 5 : 3; }
+
 template <int TYPE, int NB>
-__global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<const typename Elem<TYPE>::T> K,
+__global__ void __launch_bounds__(kThreads, write_ctas(TYPE, NB)) kv8_write_kernel(KvCache c, KvRows<const typename Elem<TYPE>::T> K,
                                                              KvRows<const typename Elem<TYPE>::T> V,
                                                              int64_t n_tokens, const int32_t* cu, const int32_t* start,
                                                              int32_t* err) {
@@ -75,23 +79,23 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<c
     if (s.b < 0) return;
     uint8_t* rec = kv8_record(c, s.b, s.blk, h, err);
     if (!rec) return;
-    const auto* kb = K.p + s.row * K.ts + h * K.hs + (lane & 3) * 8;
-    const auto* vb = V.p + s.row * V.ts + h * V.hs + (lane & 3) * 8;
+    auto* kb = K.p + s.row * K.ts + h * K.hs + (lane & 3) * 8;
+    auto* vb = V.p + s.row * V.ts + h * V.hs + (lane & 3) * 8;
     const float2 old2 = s.t0 > 0 ? *reinterpret_cast<const float2*>(rec) : make_float2(0.0f, 0.0f);
 
+    // A lane's values are of one token: of the keys, the warp's group of the record; of the values, eight
+    // tokens a warp. Dims 32 n + 8 (lane & 3) ..
+    const int g = lane >> 2, kt = 8 * (g >> 1) + 2 * wid + (g & 1), vt = wid * 8 + g;
+    const bool kin = kt >= s.t0 && kt < s.t1, vin = vt >= s.t0 && vt < s.t1;
     Raw8<TYPE> k[NB], v[NB];
-    auto k_token = [&](int n) {  // of the thread's n-th eight bytes of the keys
-        const int jj = (n * 4 + wid) / NB, g = lane >> 2;
-        return 8 * (g >> 1) + 2 * jj + (g & 1);
-    };
-    const int vt = wid * 8 + (lane >> 2);  // the token of its values, dims 32 n + 8 (lane & 3) ..
+    kb += kt * K.ts;
+    vb += vt * V.ts;
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-        const int t = k_token(n);
         k[n].clear();
         v[n].clear();
-        if (t >= s.t0 && t < s.t1) k[n].load(kb + t * K.ts + ((n * 4 + wid) % NB) * 32, K.vec);
-        if (vt >= s.t0 && vt < s.t1) v[n].load(vb + vt * V.ts + n * 32, V.vec);
+        if (kin) k[n].load(kb + n * 32, K.vec);
+        if (vin) v[n].load(vb + n * 32, V.vec);
     }
     uint32_t ak = 0, av = 0;  // magnitudes order as their bits do
 #pragma unroll
@@ -108,23 +112,20 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<c
     __syncthreads();  // also: every thread has read the old scales
     ak = max(max(red[0][0], red[0][1]), max(red[0][2], red[0][3]));
     av = max(max(red[1][0], red[1][1]), max(red[1][2], red[1][3]));
-    const Scales sk = block_scale(__uint_as_float(ak), old2.x), sv = block_scale(__uint_as_float(av), old2.y);
+    const Scales sk = block_scale(__uint_as_float(ak), old2.x, s.t0 > 0), sv = block_scale(__uint_as_float(av), old2.y, s.t0 > 0);
     if (threadIdx.x == 0) *reinterpret_cast<float2*>(rec) = make_float2(sk.scale, sv.scale);
 
     // a block without a scale (zeros, or not finite) holds codes 128
     const bool some_k = sk.inv > 0.0f, some_v = sv.inv > 0.0f;
-    uint2* kr = reinterpret_cast<uint2*>(rec + kKvHead);
+    uint2* kr = reinterpret_cast<uint2*>(rec + kKvHead) + wid * NB * 32 + lane;
     uint8_t* vr = rec + kKvHead + kKvBlock * D;
-    if (s.t0 > 0 && sk.grew) {  // kept tokens under the larger scale
+    if (kt < s.t0 && sk.grew) {  // kept tokens under the larger scale
         uint2 q[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
-            if (k_token(n) < s.t0) q[n] = kr[(n * 4 + wid) * 32 + lane];
+        for (int n = 0; n < NB; ++n) q[n] = kr[n * 32];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
-            if (k_token(n) < s.t0)
-                kr[(n * 4 + wid) * 32 + lane] = some_k ? make_uint2(rescale4(q[n].x, sk.ratio), rescale4(q[n].y, sk.ratio))
-                                                       : make_uint2(0x80808080u, 0x80808080u);
+            kr[n * 32] = some_k ? make_uint2(rescale4(q[n].x, sk.ratio), rescale4(q[n].y, sk.ratio)) : make_uint2(0x80808080u, 0x80808080u);
     }
     if (s.t0 > 0 && sv.grew) {
         const int words = (s.t0 + 3) / 4;  // of a dim's 32 bytes: D words / 128 <= 2 NB a thread
@@ -147,22 +148,22 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(KvCache c, KvRows<c
             }
         }
     }
+    if (kin) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        const int t = k_token(n);
-        if (t < s.t0 || t >= s.t1) continue;
-        uint2 q = make_uint2(0x80808080u, 0x80808080u);
-        if (some_k) {
-            unsigned long long x[4];
+        for (int n = 0; n < NB; ++n) {
+            uint2 q = make_uint2(0x80808080u, 0x80808080u);
+            if (some_k) {
+                unsigned long long x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = code_words(k[n].get(2 * e), k[n].get(2 * e + 1), sk.inv);
-            q.x = pack4(lo2(x[0]), hi2(x[0]), lo2(x[1]), hi2(x[1]));
-            q.y = pack4(lo2(x[2]), hi2(x[2]), lo2(x[3]), hi2(x[3]));
+                for (int e = 0; e < 4; ++e) x[e] = code_words(k[n].get(2 * e), k[n].get(2 * e + 1), sk.inv);
+                q.x = pack4(lo2(x[0]), hi2(x[0]), lo2(x[1]), hi2(x[1]));
+                q.y = pack4(lo2(x[2]), hi2(x[2]), lo2(x[3]), hi2(x[3]));
+            }
+            kr[n * 32] = q;
         }
-        kr[(n * 4 + wid) * 32 + lane] = q;
     }
     const bool whole = s.t0 == 0 && s.t1 == 32;
-    if (vt >= s.t0 && vt < s.t1) {
+    if (vin) {
         auto put = [&](uint8_t* at, auto step) {
 #pragma unroll
             for (int n = 0; n < NB; ++n)
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
     const float2 sc = gload(reinterpret_cast<const float2*>(rec));
     const int g = lane >> 2;
     const uint2* kr = reinterpret_cast<const uint2*>(rec + kKvHead);
-#pragma unroll 2
+#pragma unroll 1
     for (int i = 0; i < NB && !values; ++i) {
         uint2 q[4];
 #pragma unroll
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
     // lane (dims 8 dg .., tokens 4 tq ..) of 32 dims
     const int tq = lane & 7, dg = lane >> 3;
     const uint32_t* vr = reinterpret_cast<const uint32_t*>(rec + kKvHead + kKvBlock * c.D);
-#pragma unroll 2
+#pragma unroll 1
     for (int i = 0; i < NB && values; ++i) {
         uint32_t q[8];
 #pragma unroll
