@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
             q[1] = __floats2bfloat162_rn(v[i].z, v[i].w);
         }
     }
-    if (a.lse && lane == 0) a.lse[row] = Ls == 0.0f ? -INFINITY : (M - kAttnShift) * kLn2 + logf(Ls);
+    if (a.lse && lane == 0) a.lse[row] = Ls == 0.0f ? -INFINITY : M * kLn2 + logf(Ls);
 }
 
 }  // namespace

@@ -4,15 +4,17 @@
 // n_heads / n_kv_heads of them share every key and value. For a row, in base 2 (log2 e is in the
 // row's factor), s_j = f * (q . (c_j - 128)) with f = |scale| * log2 e * k_scale * (the query's own
 // power of two). A block's v_scale is r * 2^e, 1 <= r < 2. Kept running, block by block:
-//   p_j = 2^(s_j - m + 11),  l = sum p_j,  o = sum p_j 2^(e + d) r (c_j - 128),  out = o 2^-d / l,
-// with d = m - n - 1, m at most 4 below the largest s_j and n at most 4 below the largest s_j + e, both
-// whole numbers (so that their differences are exact): what is held in fp16, p_j 2^(e + d) r < 2^15, is large where a token's share of the output is, whatever its
-// block's scale. o and l are rescaled only when m or n moves, which after the first blocks is rare. fp16's
-// range below 2^10, down to 2^-24, keeps a long tail of small weights. Codes and, after a shift by a
-// power of two, 16-bit queries are exact in fp16; an fp32 query and its weights are two fp16 parts
-// each. Sums are fp32. Key codes enter as fp16 subnormals (two byte permutes per four codes) and
-// the score starts at -128 * sum q, which is of the scores' own size; value codes are centred (two
-// subtractions more): the sum of weights would be far above the result.
+//   p_j = 2^(s_j - m),  l = sum p_j,  o = sum p_j 2^(e + d) r (c_j - 128),  out = o 2^-d / l,
+// with d = m - n + 10, m at most 4 below the largest s_j and n at most 4 below the largest s_j + e, both
+// whole numbers (so that their differences are exact): what is held in fp16, p_j 2^(e + d) r < 2^15, is
+// large where a token's share of the output is, whatever its block's scale. o and l are rescaled only
+// when m or n moves, which after the first blocks is rare. fp16's range below 2^10, down to 2^-24, keeps a
+// long tail of small weights. Codes and, after a shift by a power of two, 16-bit queries are exact in
+// fp16; an fp32 query and its weights are two fp16 parts each. Sums are fp32. For 16-bit queries the key
+// codes enter as fp16 subnormals (two byte permutes per four codes) and the score starts at -128 * sum q,
+// which is of the scores' own size: what that costs in rounding is far below theirs. For fp32 ones, and
+// the value codes always (the sum of weights would be far above the result), they are centred, with two
+// subtractions more.
 //
 // Layout. A matrix instruction (m16n8k16) takes 16 rows; its other operand is the record itself: a
 // lane's eight bytes of a 256-byte tile are its part of two instructions' keys (eight dims of one
@@ -49,8 +51,8 @@ constexpr int kAttnPlain = 0, kAttnWeights = 1, kAttnSplit = 2;
 constexpr int kAttnStages = 24;          // ring stages of a CTA, at most
 constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many CTAs
 // A row's references m and n move to their maxima only once those are kAttnSlack (in powers of two)
-// above; l is held times 2^kAttnShift, the weights of the values times 2^(kAttnShift - 1).
-constexpr float kAttnShift = 11.0f, kAttnSlack = 4.0f;
+// above; the weights of the values are held times 2^kAttnShift.
+constexpr float kAttnShift = 10.0f, kAttnSlack = 4.0f;
 constexpr int kAttnWhole = 48;           // blocks of a segment that is left whole
 constexpr int kAttnSegCost = 16;         // blocks that a segment's fixed work (queries, joining) costs
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
@@ -490,9 +492,9 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                         if (SPLIT) at[(e >> 1) * 128 + (e & 1) * 2 + MT * RTW * D * 8] = lo[e];
                     }
                     if (pc == 0) {
-                        qf[rr] = make_float2(fine ? fabsf(a.scale) * kLog2e * __int_as_float((127 - k) << 23) * 16777216.0f
+                        qf[rr] = make_float2(fine ? fabsf(a.scale) * kLog2e * __int_as_float((127 - k) << 23) * (SPLIT ? 1.0f : 16777216.0f)
                                                   : __int_as_float(0x7fffffff),
-                                             sum * (-128.0f / 16777216.0f));
+                                             SPLIT ? 0.0f : sum * (-128.0f / 16777216.0f));
                         const int r = rb * RP + rr, t = r / a.G;
                         orow[rr] = r < p.R ? t * a.n_heads + kv * a.G + r - t * a.G : -1;
                     }
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 m[mt][q] = -INFINITY;
-                dd[mt][q] = INFINITY;  // n = m - d - 1
+                dd[mt][q] = INFINITY;  // n = m - d + 10
                 l[mt][q] = 0;
                 const float2 f = qf[(rt * MT + mt) * 16 + q * 8 + g];
                 fr[mt][q] = f.x;
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                 const float e = some ? static_cast<float>(static_cast<int>(__float_as_uint(sc.y) >> 23) - 127) : -INFINITY;
                 const float r = some ? __uint_as_float((__float_as_uint(sc.y) & 0x007fffffu) | 0x3f800000u) : sc.y < INFINITY ? 0.0f : NAN;
                 const uint8_t* kp = rec + kKvHead + g * 32 + c * 8;
-                // scores, in units of the row's factor times k_scale: the codes enter as code * 2^-24, so the
+                // scores, in units of the row's factor times k_scale: where the codes enter as code * 2^-24, the
                 // sum starts at -128 * 2^-24 times the query's sum
                 float sa[MT][4][4];
 #pragma unroll
@@ -558,8 +560,13 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj) {
                         const uint2 w = *reinterpret_cast<const uint2*>(kp + (jj * kNB + i) * 256);
-                        codes_sub(w.x, kk[jj][0], kk[jj][1]);
-                        codes_sub(w.y, kk[jj][2], kk[jj][3]);
+                        if (SPLIT) {
+                            codes_h2(w.x, kk[jj][0], kk[jj][1]);
+                            codes_h2(w.y, kk[jj][2], kk[jj][3]);
+                        } else {
+                            codes_sub(w.x, kk[jj][0], kk[jj][1]);
+                            codes_sub(w.y, kk[jj][2], kk[jj][3]);
+                        }
                     }
                     // sums of different tokens in turn, so that no product waits for the one before it
 #pragma unroll
@@ -621,7 +628,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                         for (int jj = 1; jj < 4; ++jj) bm = fmaxf(bm, fmaxf(sa[mt][jj][2 * q], sa[mt][jj][2 * q + 1]));
                         f[mt][q] = fr[mt][q] * sc.x;
                         top[mt][q] = bm * f[mt][q];
-                        grew |= top[mt][q] - m[mt][q] > fminf(kAttnSlack, kAttnSlack - 1.0f - (e + dd[mt][q]));
+                        grew |= top[mt][q] - m[mt][q] > fminf(kAttnSlack, kAttnSlack + kAttnShift - (e + dd[mt][q]));
                     }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -631,10 +638,10 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                             float bm = fmaxf(top[mt][q], __shfl_xor_sync(0xffffffffu, top[mt][q], 1));
                             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
                             bm = ceilf(bm);
-                            const float m0 = m[mt][q], n0 = m0 - dd[mt][q] - 1.0f, m1 = fmaxf(m0, bm), n1 = fmaxf(n0, bm + e);
+                            const float m0 = m[mt][q], n0 = m0 - dd[mt][q] + kAttnShift, m1 = fmaxf(m0, bm), n1 = fmaxf(n0, bm + e);
                             const float al = m1 > m0 ? ex2(m0 - m1) : 1.0f, ol = n1 > n0 ? ex2(n0 - n1) : 1.0f;
                             m[mt][q] = m1;
-                            if (n1 > -INFINITY) dd[mt][q] = m1 - n1 - 1.0f;
+                            if (n1 > -INFINITY) dd[mt][q] = m1 - n1 + kAttnShift;
                             l[mt][q] = mul2(l[mt][q], pk2(al, al));
 #pragma unroll
                             for (int i = 0; i < kND; ++i) {
@@ -651,7 +658,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const float fac = some ? r * ex2(e + dd[mt][q]) : r;
-                            const unsigned long long ff = pk2(f[mt][q], f[mt][q]), bb = pk2(kAttnShift - m[mt][q], kAttnShift - m[mt][q]);
+                            const unsigned long long ff = pk2(f[mt][q], f[mt][q]), bb = pk2(-m[mt][q], -m[mt][q]);
 #pragma unroll
                             for (int jj = 0; jj < 4; ++jj) {
                                 const float s0 = sa[mt][jj][2 * q], s1 = sa[mt][jj][2 * q + 1];
@@ -770,7 +777,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                         part[static_cast<int64_t>(RP) * D + rr] = M[mt][q];
                         part[static_cast<int64_t>(RP) * D + RP + rr] = Ls[mt][q];
                     } else if (a.lse) {
-                        a.lse[orow0 + orow[rr]] = Ls[mt][q] == 0.0f ? -INFINITY : (M[mt][q] - kAttnShift) * kLn2 + logf(Ls[mt][q]);
+                        a.lse[orow0 + orow[rr]] = Ls[mt][q] == 0.0f ? -INFINITY : M[mt][q] * kLn2 + logf(Ls[mt][q]);
                     }
                 }
         }
