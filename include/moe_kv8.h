@@ -88,13 +88,16 @@ int moe_kv8_read(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int
  * out[b][t][h] = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m), s_j = scale * q[b][t][h] . k_j, over the
  * positions seen, with the key/value head h / (n_heads / n_kv_heads); a query that sees nothing
  * gives zeros. lse[b][t][h] = log sum_j e^(s_j) (-inf where nothing is seen).
- * q, out have type `type`; products of 16-bit queries with the codes are exact, weights are held in
- * fp16 with a shift that keeps 2^-39 of the largest, sums in fp32; fp32 queries and their weights
- * are split in two fp16 parts. A page that cannot be read (MOE_ERR_PAGE) counts as not seen.
+ * q, out have type `type`. Products of 16-bit queries with the codes are exact; weights are held in
+ * fp16, the largest near 2^10, so that weights down to 2^-34 of it count; sums are fp32. A weight is
+ * one fp16 number for bf16, two (its rounding and the rest) for fp32, and for fp16 two where a
+ * key/value head has up to 16 rows (T * n_heads / n_kv_heads) or the page tables up to 4096 blocks in
+ * all, one otherwise. fp32 queries are two fp16 numbers each. A page that cannot be read
+ * (MOE_ERR_PAGE) counts as not seen.
  * Limits: 1 <= T <= 32, n_heads a multiple of n_kv_heads; n_seqs * T * n_heads, and n_seqs *
  * n_kv_heads * max_pages * page_tokens / 32 (times the passes over the rows of a key/value head, 32
- * rows each), below 2^31 (MOE_E_CAP). lens may be 0 (nothing seen) and is
- * clamped to the page table (MOE_ERR_PAGE).
+ * rows each), below 2^31 (MOE_E_CAP). lens may be 0 (nothing seen) and is clamped to the page table
+ * (MOE_ERR_PAGE).
  * workspace: moe_kv8_attention_workspace_bytes(...) bytes, 16-byte aligned, of any contents; calls
  * that may run at the same time need one each. */
 typedef struct moe_kv8_attention_call {

@@ -11,6 +11,10 @@ namespace {
 // WPR warps take one output row's parts in turn; a part is (row / l, m, l), its weight l 2^(m - M) / L.
 // Rows of a segment that one CTA held whole are in out already; a sequence without blocks gives
 // zeros here.
+// Bound by latency (2.5 MB of parts and a chain of two loads: 2 to 4 us behind the attention kernel).
+// The loads of a run of parts are in flight together with those of every part's m and l; several
+// warps a row where the rows are few. Joining in the CTA that ends last instead, in one kernel, took
+// longer (its fence and counter are paid by every CTA).
 template <int WPR>
 __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
     constexpr int kRows = 8 / WPR;

@@ -27,11 +27,21 @@
 //
 // Split. The call's blocks, over all sequences, heads and groups of rows, are one list. Few segments
 // (sequence, head, group) are cut into even parts, a CTA each; many into equal ranges of the list, in
-// which a segment starts with kAttnSegCost units for its fixed work. A CTA's four warps take its blocks in turn, each with its own ring
-// of shared-memory stages that bulk copies fill (one copy a block: keys, values and scales are
-// one record). A CTA joins its warps' results in warp order. Ranges that end inside a sequence
-// leave a part (rows, m, l) in the workspace, and a second kernel joins the parts in list order:
-// the result does not depend on timing.
+// which a segment starts with kAttnSegCost units for its fixed work and a short one is left whole. A
+// CTA's four warps take its blocks in turn, each with its own ring of shared-memory stages that bulk
+// copies fill (one copy a block: keys, values and scales are one record). A CTA joins its warps'
+// results in warp order. Ranges that end inside a sequence leave a part (rows, m, l) in the workspace,
+// and a second kernel joins the parts in list order: the result does not depend on timing.
+//
+// What bounds it (GB300; the rate is of the records alone, of 6787 GB/s that a copy reaches):
+//   1 sequence of 1,048,579 tokens, one head of 256 dims, 16 rows, bf16: 94.5 us, 5.7 TB/s: memory, and
+//     ~12 us of launches, queries, first copies and joining;
+//   64 sequences of 0 to 16k tokens, 8 heads of 128, 4 rows, bf16: 48.7 us, 5.0 TB/s: the same;
+//   1 of 131,077 tokens, 4 heads of 128, 16 rows, fp32: 41.5 us, 3.2 TB/s: issue and latency of the two
+//     parts' products at eight warps an SM, and the same fixed part;
+//   32 windows of 4 over 8k to 33k tokens, 8 heads of 128, 32 rows, fp16: 247 us, 4.8 TB/s: the matrix
+//     instructions and the widening of codes, at eight warps an SM (pipe 48 %, issue 40 %);
+//   one token at 777 positions: 10.3 us, all latency.
 #pragma once
 
 #include <atomic>

@@ -13,6 +13,10 @@
 // that is a tile of the record, 256 bytes; the values are stored by dim, so the write turns them in shared
 // memory (rows of 36 bytes: no two lanes of a store share a bank), and the read turns blocks of eight
 // dims and four tokens in registers.
+// Measured (GB300, of 6787 GB/s that a copy reaches; bf16, 8 heads of 128): writing 26k tokens of seven
+// prompts, 33 us for 105 MB of rows and 53 MB of records (4.8 TB/s; the instructions fill 67 % of the
+// issue slots), reading them back 31 us. Reading 87k tokens of five prefixes: 86 us for 179 MB and 355 MB
+// (6.2 TB/s, memory). Small calls (64 windows of 4 tokens) take 6 us each, launch and latency.
 #include <type_traits>
 
 #include "internal.h"
