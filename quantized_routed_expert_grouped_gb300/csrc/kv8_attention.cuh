@@ -34,14 +34,14 @@
 // and a second kernel joins the parts in list order: the result does not depend on timing.
 //
 // What bounds it (GB300; the rate is of the records alone, of 6787 GB/s that a copy reaches):
-//   1 sequence of 1,048,579 tokens, one head of 256 dims, 16 rows, bf16: 94.5 us, 5.7 TB/s: memory, and
-//     ~12 us of launches, queries, first copies and joining;
-//   64 sequences of 0 to 16k tokens, 8 heads of 128, 4 rows, bf16: 48.7 us, 5.0 TB/s: the same;
-//   1 of 131,077 tokens, 4 heads of 128, 16 rows, fp32: 41.5 us, 3.2 TB/s: issue and latency of the two
+//   1 sequence of 1,048,579 tokens, one head of 256 dims, 16 rows, bf16: 90 us, 5.9 TB/s: memory, and
+//     ~9 us of launches, queries, first copies and joining;
+//   64 sequences of 0 to 16k tokens, 8 heads of 128, 4 rows, bf16: 48.2 us, 5.0 TB/s: the same;
+//   1 of 131,077 tokens, 4 heads of 128, 16 rows, fp32: 38.8 us, 3.5 TB/s: issue and latency of the two
 //     parts' products at eight warps an SM, and the same fixed part;
-//   32 windows of 4 over 8k to 33k tokens, 8 heads of 128, 32 rows, fp16: 247 us, 4.8 TB/s: the matrix
+//   32 windows of 4 over 8k to 33k tokens, 8 heads of 128, 32 rows, fp16: 244 us, 4.8 TB/s: the matrix
 //     instructions and the widening of codes, at eight warps an SM (pipe 48 %, issue 40 %);
-//   one token at 777 positions: 10.3 us, all latency.
+//   one token at 777 positions: 9.9 us, all latency.
 #pragma once
 
 #include <atomic>
