@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_n
                     y[2 * e] = v.x;
                     y[2 * e + 1] = v.y;
                 }
-                store8<TYPE>(static_cast<T*>(c.sum) + row * c.cols + col, true, y);
+                store8_pair<TYPE, 1>(static_cast<T*>(c.sum) + row * c.cols + col, true, y);
             }
             weight8(c.weight, c.w_type, col, y);
 #pragma unroll
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_n
                 y[2 * e] = v.x;
                 y[2 * e + 1] = v.y;
             }
-            if (c.y) store8<TYPE>(static_cast<T*>(c.y) + row * c.cols + col, true, y);
+            if (c.y) store8_pair<TYPE, 1>(static_cast<T*>(c.y) + row * c.cols + col, true, y);
         }
         if (c.xq) {
             uint32_t code[2], hdr;
@@ -151,21 +151,36 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_n
     }
 }
 
-template <int TYPE>
+// N pieces of eight values a thread, all loaded first: with one the loads in flight do not cover memory's
+// latency where there are many rows.
+template <int TYPE, int N>
 __global__ void __launch_bounds__(256) dequantize_q8_1_kernel(const moe_q8_1* xq, int64_t n_blocks,
                                                               typename Elem<TYPE>::T* out) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= n_blocks * 4) return;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * N) + threadIdx.x, n = n_blocks * 4;
     pdl_wait();
     pdl_trigger();
-    const uint32_t* blk = reinterpret_cast<const uint32_t*>(xq + (i >> 2));
-    const int part = static_cast<int>(i & 3);
-    const float d = h2f_bits(gload(blk));
-    const uint32_t w[2] = {gload(blk + 1 + 2 * part), gload(blk + 2 + 2 * part)};
-    float v[8];
+    uint32_t hdr[N], w[N][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = d * static_cast<float>(static_cast<int8_t>(w[e >> 2] >> (8 * (e & 3))));
-    store8<TYPE>(out + i * 8, true, v);
+    for (int k = 0; k < N; ++k) {
+        const int64_t i = i0 + k * 256;
+        if (i >= n) continue;
+        const uint32_t* blk = reinterpret_cast<const uint32_t*>(xq + (i >> 2));
+        const int part = static_cast<int>(i & 3);
+        hdr[k] = gload(blk);
+        w[k][0] = gload(blk + 1 + 2 * part);
+        w[k][1] = gload(blk + 2 + 2 * part);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int64_t i = i0 + k * 256;
+        if (i >= n) continue;
+        const float d = h2f_bits(hdr[k]);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // code + 128 in the low bits of 2^23
+            v[e] = d * __fadd_rn(__uint_as_float(prmt(w[k][e >> 2] ^ 0x80808080u, 0x4b000000u, 0x7440u + (e & 3))), -8388736.0f);
+        store8_pair<TYPE, 1>(out + i * 8, true, v);
+    }
 }
 
 }  // namespace
@@ -184,6 +199,17 @@ cudaError_t norm_t(const moe_norm_call& c, cudaStream_t st) {
     return launch_kernel(add_rms_norm_q8_1_kernel<TYPE, 4>, dim3(grid), dim3(threads), 0, st, true, c);
 }
 
+template <int TYPE>
+cudaError_t dequantize_t(const moe_q8_1* xq, int64_t n_blocks, typename Elem<TYPE>::T* out, cudaStream_t st) {
+    constexpr int kMany = 2;
+    const int64_t pieces = n_blocks * 4;
+    if (pieces <= 304 * 2048)  // at most two rounds of the device's threads
+        return launch_kernel(dequantize_q8_1_kernel<TYPE, 1>, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, st, true, xq, n_blocks, out);
+    constexpr int kCta = 256 * kMany;
+    return launch_kernel(dequantize_q8_1_kernel<TYPE, kMany>, dim3(static_cast<unsigned>((pieces + kCta - 1) / kCta)), dim3(256), 0, st, true, xq,
+                         n_blocks, out);
+}
+
 }  // namespace
 
 cudaError_t launch_add_rms_norm_q8_1(const moe_norm_call& c, cudaStream_t st) {
@@ -195,13 +221,9 @@ cudaError_t launch_add_rms_norm_q8_1(const moe_norm_call& c, cudaStream_t st) {
 
 cudaError_t launch_dequantize_q8_1(const moe_q8_1* xq, int64_t n_blocks, void* out, int type, cudaStream_t st) {
     if (n_blocks == 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>((n_blocks * 4 + 255) / 256);
-    if (type == MOE_F32)
-        return launch_kernel(dequantize_q8_1_kernel<MOE_F32>, dim3(grid), dim3(256), 0, st, true, xq, n_blocks, static_cast<float*>(out));
-    if (type == MOE_F16)
-        return launch_kernel(dequantize_q8_1_kernel<MOE_F16>, dim3(grid), dim3(256), 0, st, true, xq, n_blocks, static_cast<__half*>(out));
-    return launch_kernel(dequantize_q8_1_kernel<MOE_BF16>, dim3(grid), dim3(256), 0, st, true, xq, n_blocks,
-                         static_cast<__nv_bfloat16*>(out));
+    if (type == MOE_F32) return dequantize_t<MOE_F32>(xq, n_blocks, static_cast<float*>(out), st);
+    if (type == MOE_F16) return dequantize_t<MOE_F16>(xq, n_blocks, static_cast<__half*>(out), st);
+    return dequantize_t<MOE_BF16>(xq, n_blocks, static_cast<__nv_bfloat16*>(out), st);
 }
 
 }  // namespace moe
