@@ -73,7 +73,7 @@ __device__ __forceinline__ void weight8(const void* w, int w_type, int col, floa
 }
 
 template <int TYPE, int C>
-__global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_norm_q8_1_kernel(const moe_norm_call c) {
+__global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? (TYPE == MOE_F32 ? 2 : 4) : 1) add_rms_norm_q8_1_kernel(const moe_norm_call c) {
     using E = Elem<TYPE>;
     using T = typename E::T;
     __shared__ float red[32];
@@ -110,6 +110,10 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_n
     __syncthreads();  // also: every thread's reads of the row lie before the writes below
     ss = 0.0f;
     for (int w = 0; w < nw; ++w) ss += red[w];
+    auto put8 = [&](T* to, const float (&v)[8]) {
+        if (C > 1) store8_pair<TYPE, 1>(to, true, v);
+        else store8<TYPE>(to, true, v);  // (few rows: the exchange would add to the chain)
+    };
     const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(c.cols)) + c.eps));
 #pragma unroll
     for (int k = 0; k < C; ++k) {
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_n
                     y[2 * e] = v.x;
                     y[2 * e + 1] = v.y;
                 }
-                store8_pair<TYPE, 1>(static_cast<T*>(c.sum) + row * c.cols + col, true, y);
+                put8(static_cast<T*>(c.sum) + row * c.cols + col, y);
             }
             weight8(c.weight, c.w_type, col, y);
 #pragma unroll
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024, C == 2 ? 4 : 1) add_rms_n
                 y[2 * e] = v.x;
                 y[2 * e + 1] = v.y;
             }
-            if (c.y) store8_pair<TYPE, 1>(static_cast<T*>(c.y) + row * c.cols + col, true, y);
+            if (c.y) put8(static_cast<T*>(c.y) + row * c.cols + col, y);
         }
         if (c.xq) {
             uint32_t code[2], hdr;
