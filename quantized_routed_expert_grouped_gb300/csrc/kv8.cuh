@@ -90,26 +90,25 @@ __device__ __forceinline__ void store8(typename Elem<TYPE>::T* p, bool vec, cons
     }
 }
 
-// store8 where lanes l and l ^ X (the one without bit X first) store neighbouring eights of one row, both or
-// neither. In fp32 a lane's two vectors lie 32 bytes from the next lane's, so that each store would fill
+// store8, where `on`, by a whole warp in which lanes l and l ^ X (the one without bit X first) store neighbouring
+// eights of one row, both or neither. In fp32 a lane's two vectors lie 32 bytes from the next lane's, so that each store would fill
 // half of every sector; the lanes exchange halves first, and each store fills whole ones.
 template <int TYPE, int X>
-__device__ __forceinline__ void store8_pair(typename Elem<TYPE>::T* p, bool vec, const float (&v)[8]) {
+__device__ __forceinline__ void store8_pair(typename Elem<TYPE>::T* p, bool vec, const float (&v)[8], bool on) {
     if constexpr (TYPE == MOE_F32) {
         if (vec) {
-            const int lane = threadIdx.x & 31;
-            const unsigned pair = 1u << lane | 1u << (lane ^ X);
-            const bool second = lane & X;
+            const bool second = threadIdx.x & X;
             float r[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = __shfl_xor_sync(pair, second ? v[i] : v[4 + i], X);
+            for (int i = 0; i < 4; ++i) r[i] = __shfl_xor_sync(0xffffffffu, second ? v[i] : v[4 + i], X);
+            if (!on) return;
             float* at = second ? p - 4 : p;
             *reinterpret_cast<float4*>(at) = second ? make_float4(r[0], r[1], r[2], r[3]) : make_float4(v[0], v[1], v[2], v[3]);
             *reinterpret_cast<float4*>(at + 8) = second ? make_float4(v[4], v[5], v[6], v[7]) : make_float4(r[0], r[1], r[2], r[3]);
             return;
         }
     }
-    store8<TYPE>(p, vec, v);
+    if (on) store8<TYPE>(p, vec, v);
 }
 
 // max of non-negative values that keeps a NaN

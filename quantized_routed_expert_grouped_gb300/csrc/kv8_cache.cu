@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(code_value(e < 4 ? q[jj].x : q[jj].y, e & 3), sc.x);
-            if (t >= s.t0 && t < s.t1) store8_pair<TYPE, 1>(kb + t * K.ts + i * 32 + (lane & 3) * 8, K.vec, x);
+            store8_pair<TYPE, 1>(kb + t * K.ts + i * 32 + (lane & 3) * 8, K.vec, x, t >= s.t0 && t < s.t1);
         }
     }
     // lane (dims 8 dg .., tokens 4 tq ..) of 32 dims
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(KvCache c, KvRows<ty
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(code_value(q[e], j), sc.y);
-            if (t >= s.t0 && t < s.t1) store8_pair<TYPE, 8>(vb + t * V.ts + i * 32 + dg * 8, V.vec, x);
+            store8_pair<TYPE, 8>(vb + t * V.ts + i * 32 + dg * 8, V.vec, x, t >= s.t0 && t < s.t1);
         }
     }
 }

@@ -110,9 +110,9 @@ __global__ void __launch_bounds__(1024, C == 2 && TYPE != MOE_F32 ? 2 : 1) add_r
     __syncthreads();  // also: every thread's reads of the row lie before the writes below
     ss = 0.0f;
     for (int w = 0; w < nw; ++w) ss += red[w];
-    auto put8 = [&](T* to, const float (&v)[8]) {
-        if (C > 1) store8_pair<TYPE, 1>(to, true, v);
-        else store8<TYPE>(to, true, v);  // (few rows: the exchange would add to the chain)
+    auto put8 = [&](T* to, const float (&v)[8], bool on) {
+        if (C > 1) store8_pair<TYPE, 1>(to, true, v, on);
+        else if (on) store8<TYPE>(to, true, v);  // (few rows: the exchange would add to the chain)
     };
     const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(c.cols)) + c.eps));
 #pragma unroll
@@ -122,16 +122,16 @@ __global__ void __launch_bounds__(1024, C == 2 && TYPE != MOE_F32 ? 2 : 1) add_r
         const bool in = col < c.cols;
         if (!__any_sync(0xffffffffu, in)) continue;
         float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (in) {
-            if (c.sum) {
+        if (c.sum) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 v = up2(h[k][e]);
-                    y[2 * e] = v.x;
-                    y[2 * e + 1] = v.y;
-                }
-                put8(static_cast<T*>(c.sum) + row * c.cols + col, y);
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = up2(h[k][e]);
+                y[2 * e] = v.x;
+                y[2 * e + 1] = v.y;
             }
+            put8(static_cast<T*>(c.sum) + row * c.cols + col, y, in);
+        }
+        if (in) {
             weight8(c.weight, c.w_type, col, y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(1024, C == 2 && TYPE != MOE_F32 ? 2 : 1) add_r
                 y[2 * e] = v.x;
                 y[2 * e + 1] = v.y;
             }
-            if (c.y) put8(static_cast<T*>(c.y) + row * c.cols + col, y);
         }
+        if (c.y) put8(static_cast<T*>(c.y) + row * c.cols + col, y, in);
         if (c.xq) {
             uint32_t code[2], hdr;
             quad_q8_1(y, code, hdr);
@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(256) dequantize_q8_1_kernel(const moe_q8_1* xq
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const int64_t i = i0 + k * 256;
+        hdr[k] = w[k][0] = w[k][1] = 0;
         if (i >= n) continue;
         const uint32_t* blk = reinterpret_cast<const uint32_t*>(xq + (i >> 2));
         const int part = static_cast<int>(i & 3);
@@ -177,13 +178,12 @@ __global__ void __launch_bounds__(256) dequantize_q8_1_kernel(const moe_q8_1* xq
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const int64_t i = i0 + k * 256;
-        if (i >= n) continue;
         const float d = h2f_bits(hdr[k]);
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)  // code + 128 in the low bits of 2^23
             v[e] = d * __fadd_rn(__uint_as_float(prmt(w[k][e >> 2] ^ 0x80808080u, 0x4b000000u, 0x7440u + (e & 3))), -8388736.0f);
-        store8_pair<TYPE, 1>(out + i * 8, true, v);
+        store8_pair<TYPE, 1>(out + i * 8, true, v, i < n);
     }
 }
 
