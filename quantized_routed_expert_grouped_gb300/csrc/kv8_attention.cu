@@ -43,11 +43,20 @@ __device__ __forceinline__ void join_ml(float& M, float& Ls, float m, float l) {
     Ls = Ls * ex2(M - bs) + l * ex2(m - bs);
     M = nm;
 }
+// The power 2^(m - M) by which a part counts, as a factor of its weight and one of its rows: fp32 may not hold it as one,
+// while the rows' values are as far above the other parts'. (To the sum of the weights such a part adds nothing.)
+__device__ __forceinline__ float2 part_power(float m, float M) {
+    constexpr float kLeast = -120.0f;
+    return make_float2(ex2(fmaxf(m - M, kLeast)), ex2(fminf(m - M - kLeast, 0.0f)));
+}
 __device__ __forceinline__ void axpy4(float w, const float4& y, float4& v) {
     v.x = fmaf(w, y.x, v.x);
     v.y = fmaf(w, y.y, v.y);
     v.z = fmaf(w, y.z, v.z);
     v.w = fmaf(w, y.w, v.w);
+}
+__device__ __forceinline__ void axpy4(float2 w, const float4& y, float4& v) {
+    axpy4(w.x, make_float4(y.x * w.y, y.y * w.y, y.z * w.y, y.w * w.y), v);
 }
 __device__ __forceinline__ void put_out(const AttnPlan& p, int row, int d, const float4& v) {
     const int64_t at = static_cast<int64_t>(row) * p.a.c.D + d;
@@ -76,7 +85,8 @@ constexpr int kManyParts = 32;
 constexpr int kSlice = 64, kSubs = 256 / (kSlice / 4), kAtOnce = 8;
 static_assert(kAttnMaxCtas <= 512, "two parts a thread");
 __global__ void __launch_bounds__(256) kv8_combine_parts_kernel(const AttnPlan p) {
-    __shared__ float wt[512], wm[8];
+    __shared__ float2 wt[512];
+    __shared__ float wm[8];
     __shared__ float4 acc[8][kSlice / 4 + 1];
     pdl_wait();
     pdl_trigger();
@@ -112,7 +122,10 @@ __global__ void __launch_bounds__(256) kv8_combine_parts_kernel(const AttnPlan p
     const float base = M == -INFINITY ? 0.0f : M;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (i == 0 || x.cnt > 256) wt[tid + i * 256] = l[i] * ex2(m[i] - base);
+        if (i == 0 || x.cnt > 256) {
+            const float2 w = part_power(m[i], base);
+            wt[tid + i * 256] = make_float2(l[i] * w.x, w.y);
+        }
     __syncthreads();
     float4 v = make_float4(0, 0, 0, 0);
     float L = 0.0f;
@@ -121,8 +134,8 @@ __global__ void __launch_bounds__(256) kv8_combine_parts_kernel(const AttnPlan p
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k)
             if (j0 + k * kSubs < x.cnt) {
-                const float w = wt[j0 + k * kSubs];
-                L += w;
+                const float2 w = wt[j0 + k * kSubs];
+                L += w.x;
                 if (d < D) axpy4(w, y[k], v);
             }
     }
@@ -194,7 +207,8 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const AttnPlan p) {
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
             if (j0 + k * WPR >= x.cnt) continue;
-            const float wt = yl[k] * ex2(ym[k] - base) * inv;
+            float2 wt = part_power(ym[k], base);
+            wt.x *= yl[k] * inv;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (i * 128 + lane * 4 < D) axpy4(wt, y[k][i], v[i]);

@@ -8,7 +8,9 @@
 // with d = m - n + 10, m at most 4 below the largest s_j and n at most 4 below the largest s_j + e, both
 // whole numbers (so that their differences are exact): what is held in fp16, p_j 2^(e + d) r < 2^15, is
 // large where a token's share of the output is, whatever its block's scale. o and l are rescaled only
-// when m or n moves, which after the first blocks is rare. fp16's range below 2^10, down to 2^-24, keeps a
+// when m or n moves, which after the first blocks is rare. Where e + d is above kAttnFar (a value scale far
+// above those that the output came from so far, with scores as far below), p_j is held times a power of two, so that
+// neither it nor 2^(e + d) leaves fp32's range. fp16's range below 2^10, down to 2^-24, keeps a
 // long tail of small weights. Codes and, after a shift by a power of two, 16-bit queries are exact in
 // fp16; an fp32 query and its weights are two fp16 parts each. Sums are fp32. For 16-bit queries the key
 // codes enter as fp16 subnormals (two byte permutes per four codes) and the score starts at -128 * sum q,
@@ -63,6 +65,9 @@ constexpr int kAttnMaxCtas = 456;        // parts are kept for at most so many C
 // A row's references m and n move to their maxima only once those are kAttnSlack (in powers of two)
 // above; the weights of the values are held times 2^kAttnShift.
 constexpr float kAttnShift = 10.0f, kAttnSlack = 4.0f;
+// The largest power of two by which a weight is multiplied on its way into a value's weight. (Above it the weight
+// itself may be below fp32's range, and the factor above it: blocks whose value scales lie that far apart.)
+constexpr float kAttnFar = 100.0f;
 constexpr int kAttnWhole = 48;           // blocks of a segment that is left whole
 constexpr int kAttnSegCost = 16;         // blocks that a segment's fixed work (queries, joining) costs
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                 }
                 // ---- running reference; o and l are rescaled only where one of the warp's rows outgrew it
                 float f[MT][2], top[MT][2];
-                bool grew = false;
+                bool grew = false, far = false;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -638,7 +643,8 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                         for (int jj = 1; jj < 4; ++jj) bm = fmaxf(bm, fmaxf(sa[mt][jj][2 * q], sa[mt][jj][2 * q + 1]));
                         f[mt][q] = fr[mt][q] * sc.x;
                         top[mt][q] = bm * f[mt][q];
-                        grew |= top[mt][q] - m[mt][q] > fminf(kAttnSlack, kAttnSlack + kAttnShift - (e + dd[mt][q]));
+                        const float room = fminf(kAttnSlack, kAttnSlack + kAttnShift - (e + dd[mt][q]));
+                        grew |= top[mt][q] - m[mt][q] > room || room < kAttnSlack + kAttnShift - kAttnFar;
                     }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -658,30 +664,37 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                                 o[mt][i][2 * q] *= ol;
                                 o[mt][i][2 * q + 1] *= ol;
                             }
+                            far |= e + dd[mt][q] > kAttnFar;
                         }
+                    far = __any_sync(0xffffffffu, far);
                 }
                 // ---- weights: the lane's tokens 8 c + 4 xx + 0..3 feed product step xx
                 uint4 pa[MT][2], pl[MT][2];
-                auto weights = [&](auto masked) {
+                auto weights = [&](auto special) {  // masked tokens, or a block's scale far above the others'
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const float fac = some ? r * ex2(e + dd[mt][q]) : r;
-                            const unsigned long long ff = pk2(f[mt][q], f[mt][q]), bb = pk2(-m[mt][q], -m[mt][q]);
+                            // p is held times 2^lift
+                            const float lift = decltype(special)::value ? fmaxf(e + dd[mt][q] - kAttnFar, 0.0f) : 0.0f;
+                            const float fac = some ? r * ex2(decltype(special)::value ? fminf(e + dd[mt][q], kAttnFar) : e + dd[mt][q]) : r;
+                            const float bias = decltype(special)::value ? lift - m[mt][q] : -m[mt][q], drop = ex2(-lift);
+                            const unsigned long long ff = pk2(f[mt][q], f[mt][q]), bb = pk2(bias, bias);
 #pragma unroll
                             for (int jj = 0; jj < 4; ++jj) {
                                 const float s0 = sa[mt][jj][2 * q], s1 = sa[mt][jj][2 * q + 1];
                                 float2 w = up2(fma2(pk2(s0, s1), ff, bb));
                                 w.x = ex2(w.x);
                                 w.y = ex2(w.y);
-                                if (decltype(masked)::value) {  // an unseen token adds nothing, whatever the scales are
+                                if (decltype(special)::value) {  // an unseen token adds nothing, whatever the scales are
                                     if (s0 == -INFINITY) w.x = 0.0f;
                                     if (s1 == -INFINITY) w.y = 0.0f;
+                                    l[mt][q] = fma2(pk2(w.x, w.y), pk2(drop, drop), l[mt][q]);
+                                } else {
+                                    l[mt][q] = add2(l[mt][q], pk2(w.x, w.y));
                                 }
-                                l[mt][q] = add2(l[mt][q], pk2(w.x, w.y));
                                 w = up2(mul2(pk2(w.x, w.y), pk2(fac, fac)));
-                                if (decltype(masked)::value) {
+                                if (decltype(special)::value) {
                                     if (s0 == -INFINITY) w.x = 0.0f;
                                     if (s1 == -INFINITY) w.y = 0.0f;
                                 }
@@ -694,7 +707,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                             }
                         }
                 };
-                if (mask) weights(std::true_type{});
+                if (mask || far) weights(std::true_type{});
                 else weights(std::false_type{});
                 const uint8_t* vp = rec + kKvHead + kKvBlock * D + g * 32 + c * 8;
                 constexpr int kRun = 4;  // dims' sums in turn, as above (kND is a multiple of 4)

@@ -1,0 +1,95 @@
+"""moe_kv8_attention at the ends of its ranges, against the formula in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import kv8_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import quantized_routed_expert_grouped_gb300 as mod
+    mod.lib()
+    return mod
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def scaled_blocks(rng, scores, powers, D, hkv):
+    """A cache of one sequence whose block j's tokens all score scores[j] (in powers of two, 0 or below, for a query
+    of one in dim 0) and whose values have the scale 2^powers[j] times 1 to 2; a page a block."""
+    n = len(scores)
+    ref = R.Cache(R.random_pool(rng, n, hkv, D, 32), np.arange(n, dtype=np.int32)[None])
+    for j, (s, e) in enumerate(zip(scores, powers)):
+        rec = ref.block(0, j)
+        rec[:, 16:16 + 32 * D] = 128
+        rec[:, ref.at[0][:, 0]] = 28  # -100
+        rec[:, :4] = np.full((hkv, 1), -s * np.log(2) / 100, np.float32).view(np.uint8)
+        rec[:, 4:8] = (2.0 ** e * rng.uniform(1, 1.9, (hkv, 1))).astype(np.float32).view(np.uint8)
+    return ref
+
+
+def blocks_of(what):
+    if what == "seen":    # as found: infinity in the first, NaN in the second where one warp met both
+        return [[(0, -90), (-120, 30)], [(0, -100), (-150, 20)], [(-150, 20), (0, -100)], [(0, -7), (-126, 119)], [(-30, 119), (0, -90)]]
+    if what == "past":    # the weight itself is far below fp32's range, its share of the output is not
+        return [[(0, -100), (-205, 105)], [(-205, 105), (0, -100)], [(0, -60), (-170, 110)], [(-190, 95), (-10, -85)]]
+    return []
+
+
+@pytest.mark.parametrize("dtype", list(R.TYPES))
+@pytest.mark.parametrize("rows", [1, 20])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("what", ["seen", "past", "drawn"])
+def test_scales_far_apart(m, what, many, rows, dtype):
+    """Blocks whose value scales lie up to 2^210 apart, with scores that make up for it, in every order. Sequences
+    of up to 12 blocks: many of them, so that a warp takes several blocks of one, or one alone, in parts.
+
+    Tolerance, as in test_gpu_kv8_attention.py but for each token's share: (2 ds + 2^-11 for 16-bit outputs, + 2^-17) of
+    sum p |v| / sum p, and what fp16 does not hold of a weight, 2^-34 of the largest p * scale, at codes up to 127 and a scale of
+    up to 1.9 times its power of two. ds = 2^-19 of the score, plus 2^-20."""
+    rng = np.random.default_rng(["seen", "past", "drawn"].index(what))
+    D, hkv = 32, 8
+    cases = blocks_of(what)
+    if what == "drawn":
+        cases = [[(-(e + 105) + rng.uniform(-5, 0), e) for e in rng.integers(-105, 112, 3)] for _ in range(6)]
+        cases = [[(min(s, 0.0), int(e)) for s, e in c] for c in cases]
+    if dtype == "f16":    # what its range holds of the outputs: the block of the largest score has values near 1
+        cases = [[(s, e + up) for s, e in c] for c in cases for up in [-max(c)[1] - 4] if max(e for _, e in c) + up < 120]
+        cases.append([(0, -3), (-118, 117)])
+    lens, T, G = ([317] * 57 if many else [317]), rows, 1
+    for c in cases:
+        kinds = [c[int(rng.integers(len(c)))] for _ in range(10)]
+        kinds[:len(c)] = c
+        ref = scaled_blocks(rng, [s for s, _ in kinds], [e for _, e in kinds], D, hkv)
+        q = torch.zeros((len(lens), T, hkv * G, D), dtype=R.TYPES[dtype], device="cuda")
+        q[..., 0] = 1
+        pool, table = dev(ref.pool), dev(np.repeat(ref.table, len(lens), 0))
+        got, lse = m.kv8_attention(q, pool, table, ints(lens), scale=1.0, with_lse=True)
+        got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+        k, v = (x.astype(np.float64) for x in ref.read(0, 0, 317))
+        s = k[:, :, 0].T  # [heads, tokens]: the query is one in dim 0
+        power = np.repeat([e for _, e in kinds], 32)[:317]
+        for t in range(T):
+            n = 317 - T + t + 1
+            p = np.exp(s[:, :n] - s[:, :n].max(1, keepdims=True))
+            total = p.sum(1, keepdims=True)
+            out = np.einsum("hn,nhd->hd", p, v[:n]) / total
+            size = np.einsum("hn,nhd->hd", p * (2 * (2.0 ** -19 * np.abs(s[:, :n]) + 2.0 ** -20) + (0 if dtype == "f32" else 2.0 ** -11) + 2.0 ** -17),
+                             np.abs(v[:n])) / total
+            lost = n * 2.0 ** -34 * 254 * (p * 2.0 ** power[:n]).max(1, keepdims=True) / total
+            least = 2.0 ** -25 if dtype == "f16" else 2.0 ** -134
+            tol = size + lost + 2 * R.HALF_ULP[dtype] * np.abs(out) + least
+            fits = np.abs(out) + tol < float(torch.finfo(R.TYPES[dtype]).max)
+            assert fits.all()
+            assert (np.abs(got[:, t] - out) <= tol).all(), (c, t)
+            want = s[:, :n].max(1) + np.log(total[:, 0])
+            assert (np.abs(lse[:, t] - want) <= 2.0 ** -17 * (1 + np.abs(want))).all()
