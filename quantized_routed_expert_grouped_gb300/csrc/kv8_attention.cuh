@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                 }
                 // lane (g, c) holds rows g, g + 8 and tokens 8 c + 2 jj + e; an unseen one becomes -inf
                 const int t0 = u * kKvBlock;
-                const bool mask = t0 + kKvBlock > before_window || t0 <= behind;
+                const bool mask = t0 > before_window - kKvBlock || t0 <= behind;  // (the last block ends at up to 2^31)
                 if (mask) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)

@@ -93,3 +93,37 @@ def test_scales_far_apart(m, what, many, rows, dtype):
             assert (np.abs(got[:, t] - out) <= tol).all(), (c, t)
             want = s[:, :n].max(1) + np.log(total[:, 0])
             assert (np.abs(lse[:, t] - want) <= 2.0 ** -17 * (1 + np.abs(want))).all()
+
+
+@pytest.mark.parametrize("T,tree", [(1, False), (3, False), (3, True)])
+def test_last_positions(m, T, tree):
+    """Lengths up to 2^31 - 1, over two pages of 2^20 tokens that the table names by turns."""
+    rng = np.random.default_rng(30)
+    D, page = 32, 1 << 20
+    pool = m.kv8_pool(2, 1, D, page)
+    part = R.random_pool(rng, 2, 1, D, 128)
+    pool[:, :, -4:] = dev(part)      # the ends of the pages are the only blocks that a short window reaches
+    ref = R.Cache(part, np.array([[0, 1]], np.int32))
+    table = ints([0, 1] * 1024).view(1, 2048)
+    q = torch.randn((1, T, 3, D), device="cuda")
+    bits = ints([[1, 3, 5]]) if tree else None
+    for n in [(1 << 31) - 1, (1 << 31) - 30, (1 << 31) - 33]:
+        # of the window's last 128 positions: those of page 1's last four blocks
+        end = 256 - ((1 << 31) - n)
+        for window in (1, 40, 90):
+            got = m.kv8_attention(q, pool, table, ints([n]), window=window, tree=bits)
+            want, _, reach, size = R.attention(q.double().cpu().numpy(), ref, [end], D ** -0.5, window, None if bits is None else bits.cpu().numpy())
+            tol = reach * (2 * (2.0 ** -19 * size + 2.0 ** -20)[..., None] + 2.0 ** -17) + 2.0 ** -23 * np.abs(want) + 2.0 ** -26
+            assert (np.abs(got.double().cpu().numpy() - want) <= tol).all(), (n, window)
+    # and written there
+    start, n = (1 << 31) - 49, 48
+    x = torch.randn((2, n, 1, D), device="cuda")
+    err = ints([0])
+    m.kv8_write(x[0], x[1], pool, table, ints([0, n]), ints([start]), err=err)
+    k, v = m.kv8_read(pool, table, ints([0, n]), ints([start]), n, dtype=torch.float32, err=err)
+    assert int(err) == 0
+    old = ref.block(0, 6).copy()
+    ref.write(0, 256 - 49, [a.cpu().numpy() for a in x])
+    want = ref.read(0, 256 - 49, 255)
+    assert np.array_equal(k.cpu().numpy(), want[0]) and np.array_equal(v.cpu().numpy(), want[1])
+    assert not np.array_equal(old, ref.block(0, 6))
