@@ -129,3 +129,28 @@ def test_no_rows(m):
     x = torch.empty((0, 64), device="cuda")
     total, y, xq = m.add_rms_norm_q8_1(x, torch.ones(64, device="cuda"), residual=x, with_y=True)
     assert total.shape == (0, 64) and xq.shape == (0, 2, 36) and m.dequantize_q8_1(xq).shape == (0, 64)
+
+
+# more than 304 rows of 512 columns or more, and rows of 8,224 to 16,384 columns: two pieces a thread
+@pytest.mark.parametrize("dtype", list(R.TYPES))
+@pytest.mark.parametrize("shape", [(400, 512), (305, 4096), (321, 7200), (3, 8224), (2, 16384), (310, 16352)])
+def test_two_pieces_a_thread(m, shape, dtype):
+    test_norm(m, shape, dtype)
+    rows, cols = shape
+    x, r, w = make(rows + cols, rows, cols, dtype, dtype)
+    want, y0, xq0 = m.add_rms_norm_q8_1(x, w, residual=r, with_y=True)
+    x2, r2 = x.clone(), r.clone()
+    _, _, xq = m.add_rms_norm_q8_1(x2, w, residual=r2, sum_out=r2, y=x2)
+    assert torch.equal(r2, want) and torch.equal(x2, y0) and torch.equal(xq, xq0)
+
+
+@pytest.mark.parametrize("dtype", list(R.TYPES))
+@pytest.mark.parametrize("rows,cols", [(1217, 4096), (155, 32160), (622593, 32)])
+def test_dequantize_many(m, rows, cols, dtype):
+    """More than 622,592 pieces of eight values: two a thread, the last CTA's not all there."""
+    y = torch.randn((rows, cols), generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    xq = m.quantize_q8_1(y)
+    got = m.dequantize_q8_1(xq, dtype=R.TYPES[dtype])
+    d = xq[..., 0:2].contiguous().view(torch.float16).float()
+    want = (d * xq[..., 4:].view(torch.int8).float()).to(R.TYPES[dtype])
+    assert torch.equal(got, want.view(rows, cols))
