@@ -344,6 +344,7 @@ _pack_rows = struct.Struct("@" + _CACHE + "0q").pack, struct.Struct("@PPiqqqqq")
 _pack_attn = struct.Struct("@" + _CACHE + "0qPiiiqqqPPifPPPqP").pack
 _pack_norm = struct.Struct("@PPPPPPiiqqqif").pack
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _elem(t):
@@ -385,7 +386,10 @@ def _empty(stream, shape, dtype, device):
 
 
 def _launch(f, dev, stream, tensors, *args):
-    """Call f(*args, stream); tensors are marked as used on a stream that is not the current one."""
+    """Call f(*args, stream) on device dev, which has to be the current one (the library launches there); tensors
+    are marked as used on a stream that is not the current one."""
+    if dev != _current_device() or (stream is not None and stream.device_index != dev):
+        raise MoeError(f"tensors on device {dev}: the current device, and the stream's, expected")
     if stream is None:
         rc = f(*args, _raw_stream(dev))
     else:

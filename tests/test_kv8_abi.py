@@ -123,3 +123,26 @@ def test_binding_refusals(m):
     for f in bad:
         with pytest.raises(m.MoeError):
             f()
+
+
+def test_binding_device(m, monkeypatch):
+    """The library launches on the current device: tensors, or a stream, of another one are refused before the call."""
+    class Stream:
+        cuda_stream = 0
+
+        def __init__(self, device):
+            self.device_index = device
+    calls = []
+
+    def f(*args):
+        calls.append(args)
+        return 0
+    monkeypatch.setattr(m, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(m, "_raw_stream", lambda dev: 7)
+    for dev, stream in ((1, None), (1, Stream(1)), (0, Stream(1))):
+        with pytest.raises(m.MoeError):
+            m._launch(f, dev, stream, (), 3)
+    assert not calls
+    m._launch(f, 0, None, (), 3)
+    m._launch(f, 0, Stream(0), (), 3)
+    assert calls == [(3, 7), (3, 0)]
