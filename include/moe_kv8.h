@@ -71,7 +71,8 @@ int64_t moe_kv8_block_bytes(int head_dim);
  * not share a block that is written. Alignment: rows 16-byte aligned with strides that keep it are
  * read in vectors, others by element. Errors: MOE_E_NULL, MOE_E_TYPE, MOE_E_SHAPE (head_dim,
  * page_tokens, negative n_tokens), MOE_E_CAP (n_pages, n_seqs, max_pages, n_kv_heads),
- * MOE_E_ALIGN (the pool, or rows off their element's boundary), MOE_E_CUDA. */
+ * MOE_E_ALIGN (the pool, rows off their element's boundary, or page_table, cu_tokens, start or err
+ * off 4 bytes), MOE_E_CUDA. */
 int moe_kv8_write(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int32_t* cu_tokens,
                   const int32_t* start, int32_t* err, cudaStream_t stream);
 
@@ -99,7 +100,8 @@ int moe_kv8_read(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int
  * rows each), below 2^31 (MOE_E_CAP). lens may be 0 (nothing seen) and is clamped to the page table
  * (MOE_ERR_PAGE).
  * workspace: moe_kv8_attention_workspace_bytes(...) bytes, 16-byte aligned, of any contents; calls
- * that may run at the same time need one each. */
+ * that may run at the same time need one each. out is 16-byte aligned, q on its element's boundary,
+ * lens, tree, lse and err on 4 bytes (MOE_E_ALIGN). */
 typedef struct moe_kv8_attention_call {
     moe_kv8_cache cache;
     const void* q; /* element (b, t, h, d) at b * q_seq_stride + t * q_token_stride + h * q_head_stride + d */

@@ -10,6 +10,9 @@ namespace {
 bool valid_elem(int t) { return t == MOE_F32 || t == MOE_F16 || t == MOE_BF16; }
 int elem_bytes(int t) { return t == MOE_F32 ? 4 : 2; }
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+// int32 and fp32 arrays (a null one is aligned)
+template <typename... P>
+bool off4(const P*... p) { return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) != 0; }
 int status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_E_CUDA; }
 
 int check_cache(const moe_kv8_cache& c, KvCache& k) {
@@ -19,7 +22,7 @@ int check_cache(const moe_kv8_cache& c, KvCache& k) {
         c.n_seqs <= 0 || c.n_seqs > (1 << 20) || c.table_stride < c.max_pages)
         return MOE_E_CAP;
     // positions are 32-bit: no table past 2^31 - 1 of them is addressable
-    if (off16(c.pool) || (reinterpret_cast<uintptr_t>(c.page_table) & 3u)) return MOE_E_ALIGN;
+    if (off16(c.pool) || off4(c.page_table)) return MOE_E_ALIGN;
     k = KvCache{static_cast<uint8_t*>(c.pool), c.page_table, c.table_stride, c.n_pages, c.n_kv_heads, c.head_dim,
                 c.page_tokens / kKvBlock, c.max_pages, c.n_seqs, kv8_record_bytes(c.head_dim)};
     return MOE_OK;
@@ -33,7 +36,7 @@ int check_rows(const void* p, int64_t ts, int64_t hs, int eb, bool& vec) {
 }
 
 int cache_rows(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int32_t* cu, const int32_t* start,
-               KvCache& k, bool& kvec, bool& vvec) {
+               const int32_t* err, KvCache& k, bool& kvec, bool& vvec) {
     if (!cache || !rows || !cu || !start) return MOE_E_NULL;
     int rc = check_cache(*cache, k);
     if (rc) return rc;
@@ -42,6 +45,7 @@ int cache_rows(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int32
     // one CTA per (block, head)
     if (kv8_slots(rows->n_tokens, cache->n_seqs) * cache->n_kv_heads > 0x3fffffff) return MOE_E_CAP;
     if (rows->n_tokens > 0 && (!rows->k || !rows->v)) return MOE_E_NULL;
+    if (off4(cu, start, err)) return MOE_E_ALIGN;
     const int eb = elem_bytes(rows->type);
     rc = check_rows(rows->k, rows->k_token_stride, rows->k_head_stride, eb, kvec);
     return rc ? rc : check_rows(rows->v, rows->v_token_stride, rows->v_head_stride, eb, vvec);
@@ -59,7 +63,7 @@ int moe_kv8_write(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const in
                   int32_t* err, cudaStream_t stream) {
     KvCache k;
     bool kvec, vvec;
-    const int rc = cache_rows(cache, rows, cu_tokens, start, k, kvec, vvec);
+    const int rc = cache_rows(cache, rows, cu_tokens, start, err, k, kvec, vvec);
     if (rc || rows->n_tokens == 0) return rc;
     return status(launch_kv8_write(k, *rows, cu_tokens, start, err, kvec, vvec, stream));
 }
@@ -68,7 +72,7 @@ int moe_kv8_read(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int
                  int32_t* err, cudaStream_t stream) {
     KvCache k;
     bool kvec, vvec;
-    const int rc = cache_rows(cache, rows, cu_tokens, start, k, kvec, vvec);
+    const int rc = cache_rows(cache, rows, cu_tokens, start, err, k, kvec, vvec);
     if (rc || rows->n_tokens == 0) return rc;
     return status(launch_kv8_read(k, *rows, cu_tokens, start, err, kvec, vvec, stream));
 }
@@ -91,7 +95,9 @@ int moe_kv8_attention(const moe_kv8_attention_call* call, cudaStream_t stream) {
         return MOE_E_SHAPE;
     if (static_cast<int64_t>(a.c.n_seqs) * call->T * call->n_heads > 0x7fffffff) return MOE_E_CAP;
     const int eb = elem_bytes(call->type);
-    if (reinterpret_cast<uintptr_t>(call->q) % eb || off16(call->out) || off16(call->workspace)) return MOE_E_ALIGN;
+    if (reinterpret_cast<uintptr_t>(call->q) % eb || off16(call->out) || off16(call->workspace) ||
+        off4(call->lens, call->tree, call->lse, call->err))
+        return MOE_E_ALIGN;
     if (call->workspace_bytes < moe_kv8_attention_workspace_bytes(a.c.n_seqs, call->T, call->n_heads, a.c.n_kv, a.c.D))
         return MOE_E_SCRATCH;
     a.q = call->q;
@@ -122,7 +128,7 @@ int moe_add_rms_norm_q8_1(const moe_norm_call* c, cudaStream_t stream) {
         return MOE_E_SHAPE;
     const int eb = elem_bytes(c->type);
     if (off16(c->x) || off16(c->residual) || off16(c->weight) || off16(c->sum) || off16(c->y) ||
-        (reinterpret_cast<uintptr_t>(c->xq) & 3u) || c->x_stride * eb % 16 ||
+        off4(c->xq) || c->x_stride * eb % 16 ||
         (c->residual && c->residual_stride * eb % 16))
         return MOE_E_ALIGN;
     return status(launch_add_rms_norm_q8_1(*c, stream));
@@ -133,7 +139,7 @@ int moe_dequantize_q8_1(const moe_q8_1* xq, int64_t rows, int64_t cols, void* ou
     if (!valid_elem(type)) return MOE_E_TYPE;
     if (rows < 0 || cols <= 0 || cols % 32 || rows > 0x7fffffff || cols > 0x7fffffff || rows * (cols / 32) > 0x7fffffff)
         return MOE_E_SHAPE;
-    if ((reinterpret_cast<uintptr_t>(xq) & 3u) || off16(out)) return MOE_E_ALIGN;
+    if (off4(xq) || off16(out)) return MOE_E_ALIGN;
     return status(launch_dequantize_q8_1(xq, rows * (cols / 32), out, type, stream));
 }
 

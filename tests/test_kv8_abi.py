@@ -146,3 +146,17 @@ def test_binding_device(m, monkeypatch):
     m._launch(f, 0, None, (), 3)
     m._launch(f, 0, Stream(0), (), 3)
     assert calls == [(3, 7), (3, 0)]
+
+
+def test_arrays_off_their_boundary(m):
+    """int32 and fp32 arrays off 4 bytes are refused before a kernel would read them."""
+    import ctypes
+    L, ref = m.lib(), ctypes.byref
+    rows = m.KV8RowsC(k=16, v=16, type=0, n_tokens=8, k_token_stride=256, k_head_stride=128, v_token_stride=256, v_head_stride=128)
+    for f in (L.moe_kv8_write, L.moe_kv8_read):
+        for cu, start, err in ((18, 16, 16), (16, 17, 16), (16, 16, 22)):
+            assert f(ref(cache(m)), ref(rows), cu, start, err, None) == ALIGN
+    call = dict(cache=cache(m), q=16, type=2, T=4, n_heads=8, q_seq_stride=4096, q_token_stride=1024, q_head_stride=128, lens=16, tree=16,
+                scale=1.0, out=16, lse=16, err=16, workspace=16, workspace_bytes=L.moe_kv8_attention_workspace_bytes(2, 4, 8, 2, 128))
+    for name in ("lens", "tree", "lse", "err"):
+        assert L.moe_kv8_attention(ref(m.KV8AttentionC(**{**call, name: 18})), None) == ALIGN, name
