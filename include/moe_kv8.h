@@ -85,7 +85,12 @@ int moe_kv8_read(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int
  * values already). Sequence b holds lens[b] positions; query t sits at position p = lens[b] - T + t
  * and sees position j when 0 <= j < lens[b], p >= 0 and
  *   - without tree: j <= p;  with tree: j < lens[b] - T, or bit j - (lens[b] - T) of tree[b][t] is set;
- *   - window == 0 or j > p - window.
+ *   - window == 0 or j > p - window (a window of 2^31 - 64 or more counts as 0, no limit).
+ * In a tree, positions in a path are not those in the window: with depth, the distance that `window`
+ * limits is counted from lens[b] - T + depth[b][t] to j, or to lens[b] - T + depth[b][i] for window
+ * token i = j - (lens[b] - T). (depth: a token's number of ancestors in the window, at most its index t;
+ * one outside [0, t] counts as the nearer end. Each query then sees what it would if its path were
+ * decoded token by token.)
  * out[b][t][h] = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m), s_j = scale * q[b][t][h] . k_j, over the
  * positions seen, with the key/value head h / (n_heads / n_kv_heads); a query that sees nothing
  * gives zeros. lse[b][t][h] = log sum_j e^(s_j) (-inf where nothing is seen).
@@ -101,7 +106,7 @@ int moe_kv8_read(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int
  * (MOE_ERR_PAGE).
  * workspace: moe_kv8_attention_workspace_bytes(...) bytes, 16-byte aligned, of any contents; calls
  * that may run at the same time need one each. out is 16-byte aligned, q on its element's boundary,
- * lens, tree, lse and err on 4 bytes (MOE_E_ALIGN). */
+ * lens, tree, depth, lse and err on 4 bytes (MOE_E_ALIGN). */
 typedef struct moe_kv8_attention_call {
     moe_kv8_cache cache;
     const void* q; /* element (b, t, h, d) at b * q_seq_stride + t * q_token_stride + h * q_head_stride + d */
@@ -116,6 +121,7 @@ typedef struct moe_kv8_attention_call {
     void* workspace;
     int64_t workspace_bytes;
     int32_t* err; /* optional */
+    const int32_t* depth; /* [n_seqs][T], or NULL; only with tree (MOE_E_SHAPE) */
 } moe_kv8_attention_call;
 
 int64_t moe_kv8_attention_workspace_bytes(int n_seqs, int T, int n_heads, int n_kv_heads, int head_dim);

@@ -94,7 +94,7 @@ class KV8AttentionC(ctypes.Structure):
         ("cache", KV8CacheC), ("q", _P), ("type", ctypes.c_int32), ("T", ctypes.c_int32),
         ("n_heads", ctypes.c_int32), ("q_seq_stride", _I64), ("q_token_stride", _I64), ("q_head_stride", _I64),
         ("lens", _P), ("tree", _P), ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("out", _P),
-        ("lse", _P), ("workspace", _P), ("workspace_bytes", _I64), ("err", _P),
+        ("lse", _P), ("workspace", _P), ("workspace_bytes", _I64), ("err", _P), ("depth", _P),
     ]
 
 
@@ -341,7 +341,7 @@ def qsa_block_scores(q, keys, key_scale, scores=None, stream=None):
 
 _CACHE = "PqiiiPqii"                             # moe_kv8_cache
 _pack_rows = struct.Struct("@" + _CACHE + "0q").pack, struct.Struct("@PPiqqqqq").pack
-_pack_attn = struct.Struct("@" + _CACHE + "0qPiiiqqqPPifPPPqP").pack
+_pack_attn = struct.Struct("@" + _CACHE + "0qPiiiqqqPPifPPPqPP").pack
 _pack_norm = struct.Struct("@PPPPPPiiqqqif").pack
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
@@ -474,10 +474,12 @@ def kv8_attention_workspace(n_seqs: int, T: int, n_heads: int, n_kv_heads: int, 
 
 
 def kv8_attention(q, pool, page_table, lens, scale=None, window=0, tree=None, workspace=None, out=None, lse=None,
-                  with_lse=False, err=None, stream=None):
+                  with_lse=False, err=None, stream=None, depth=None):
     """Attention of q [sequences, T, heads, head_dim] (the last T of lens[b] cached positions; T <= 32)
     over the cache. window: a query sees that many positions up to its own (0: all); tree: int32
-    [sequences, T], bit j of tree[b, t] lets query t see window token j (else: causal). Returns out
+    [sequences, T], bit j of tree[b, t] lets query t see window token j (else: causal); depth: int32
+    [sequences, T], a token's number of ancestors in the tree, from which `window` is then counted (else: from
+    its index in the window, which in a path with fewer ancestors hides the oldest tokens). Returns out
     [sequences, T, heads, head_dim] of q's type, and with_lse (or a given lse) also the log of the
     softmax sums, fp32 [sequences, T, heads]; a query that sees nothing gives zeros and -inf."""
     c, dev = _kv8_cache(pool, page_table)
@@ -501,8 +503,8 @@ def kv8_attention(q, pool, page_table, lens, scale=None, window=0, tree=None, wo
     a = _pack_attn(*c, _ptr(q, dev), _elem(q), T, hq, qs[0], qs[1], qs[2], _ints(lens, "lens", B, dev),
                    0 if tree is None else _ints(tree, "tree", B * T, dev), window, D ** -0.5 if scale is None else scale,
                    _ptr(out, dev), 0 if lse is None else _ptr(lse, dev), _ptr(workspace, dev), workspace.nbytes,
-                   _err(err, dev))
-    _launch(lib().moe_kv8_attention, dev, stream, (q, pool, page_table, lens, tree, out, lse, workspace, err), a)
+                   _err(err, dev), 0 if depth is None else _ints(depth, "depth", B * T, dev))
+    _launch(lib().moe_kv8_attention, dev, stream, (q, pool, page_table, lens, tree, depth, out, lse, workspace, err), a)
     return out if lse is None else (out, lse)
 
 

@@ -91,12 +91,13 @@ int moe_kv8_attention(const moe_kv8_attention_call* call, cudaStream_t stream) {
     if (rc) return rc;
     if (!call->q || !call->lens || !call->out || !call->workspace) return MOE_E_NULL;
     if (!valid_elem(call->type)) return MOE_E_TYPE;
-    if (call->T < 1 || call->T > 32 || call->n_heads <= 0 || call->n_heads % a.c.n_kv || call->window < 0)
+    if (call->T < 1 || call->T > 32 || call->n_heads <= 0 || call->n_heads % a.c.n_kv || call->window < 0 ||
+        (call->depth && !call->tree))
         return MOE_E_SHAPE;
     if (static_cast<int64_t>(a.c.n_seqs) * call->T * call->n_heads > 0x7fffffff) return MOE_E_CAP;
     const int eb = elem_bytes(call->type);
     if (reinterpret_cast<uintptr_t>(call->q) % eb || off16(call->out) || off16(call->workspace) ||
-        off4(call->lens, call->tree, call->lse, call->err))
+        off4(call->lens, call->tree, call->depth, call->lse, call->err))
         return MOE_E_ALIGN;
     if (call->workspace_bytes < moe_kv8_attention_workspace_bytes(a.c.n_seqs, call->T, call->n_heads, a.c.n_kv, a.c.D))
         return MOE_E_SCRATCH;
@@ -110,7 +111,8 @@ int moe_kv8_attention(const moe_kv8_attention_call* call, cudaStream_t stream) {
     a.G = call->n_heads / a.c.n_kv;
     a.lens = call->lens;
     a.tree = call->tree;
-    a.window = call->window;
+    a.window = call->window < kKvNoWindow ? call->window : 0;
+    a.depth = a.window > 0 ? call->depth : nullptr;
     a.scale = call->scale;
     a.out = call->out;
     a.lse = call->lse;

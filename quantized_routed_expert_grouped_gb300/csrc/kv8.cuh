@@ -18,6 +18,7 @@ __device__ __forceinline__ T gload(const T* p) {
 }
 
 constexpr int kKvBlock = 32;                  // tokens of a record
+constexpr int kKvNoWindow = 0x7fffffff - 63;  // a window of as many positions is none (and a position less it fits in 32 bits)
 constexpr int kKvHead = 16;                   // record header: f32 k_scale, f32 v_scale, 8 unused
 constexpr float kKvTiny = 7.888609052210118e-31f;  // 2^-100: a block below it is stored as zeros
 

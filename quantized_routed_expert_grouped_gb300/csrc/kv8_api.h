@@ -18,6 +18,7 @@ struct AttnArgs {
     int T, n_heads, G;
     const int32_t* lens;
     const int32_t* tree;
+    const int32_t* depth;  // nullptr where it has no effect
     int window;
     float scale;
     void* out;

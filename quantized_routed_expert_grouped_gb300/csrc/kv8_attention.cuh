@@ -136,6 +136,9 @@ __device__ __forceinline__ void attn_seq(const AttnArgs& a, int b, int& len, int
     n = len > 0 ? ((len - 1) >> 5) + 1 - first : 0;
 }
 
+// The depth of window token t of the sequence whose tokens are bt ..: at most its index.
+__device__ __forceinline__ int attn_depth(const AttnArgs& a, int64_t bt, int t) { return min(max(gload(a.depth + bt + t), 0), t); }
+
 // How the list is cut. By parts (tb > 0): a segment of n blocks takes ceil(n / tb) CTAs, which share it
 // evenly. By cost: a segment counts for kAttnSegCost + n, and the CTAs take equal ranges.
 struct AttnCut {
@@ -621,12 +624,24 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                             const int row = pieces[0].seg % p.g.RB * RP + (rt * MT + mt) * 16 + q * 8 + g;
                             const int t = row / a.G, ps = row < p.R ? before_window + t : -1;
                             uint32_t bits = 0;
-                            if (a.tree && ps >= 0) bits = static_cast<uint32_t>(gload(a.tree + static_cast<int64_t>(pieces[0].b) * a.T + t));
+                            int from = a.window > 0 ? max(ps - a.window, -1) : -1;  // positions up to it are out of sight
+                            if (a.tree && ps >= 0) {
+                                const int64_t bt = static_cast<int64_t>(pieces[0].b) * a.T;
+                                bits = static_cast<uint32_t>(gload(a.tree + bt + t));
+                                if (a.depth) {
+                                    const int d = attn_depth(a, bt, t);
+                                    from = max(before_window + d - a.window, -1);
+#pragma unroll 1
+                                    for (int w = 0; w < a.T; ++w)
+                                        if (d - attn_depth(a, bt, w) >= a.window) bits &= ~(1u << w);
+                                }
+                            }
+                            if (ps < 0) from = 0x7fffffff;
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const int j = t0 + 8 * c + i, w = j - before_window;
                                 const bool in = a.tree ? (w < 0 || (w < a.T && (bits >> (w & 31) & 1u))) : j <= ps;
-                                if (!(in && ps >= 0 && (a.window == 0 || j > ps - a.window)))
+                                if (!(in && j > from))
                                     sa[mt][i >> 1][2 * q + (i & 1)] = -INFINITY;
                             }
                         }

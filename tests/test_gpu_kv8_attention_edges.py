@@ -127,3 +127,61 @@ def test_last_positions(m, T, tree):
     want = ref.read(0, 256 - 49, 255)
     assert np.array_equal(k.cpu().numpy(), want[0]) and np.array_equal(v.cpu().numpy(), want[1])
     assert not np.array_equal(old, ref.block(0, 6))
+
+
+@pytest.mark.parametrize("dtype", list(R.TYPES))
+@pytest.mark.parametrize("T,window", [(2, 1), (8, 3), (8, 40), (13, 33), (32, 5), (32, 64), (9, 0), (9, 1000)])
+def test_tree_depths(m, T, window, dtype):
+    """With depths, each draft token sees under a sliding window what decoding its path token by token would: the last
+    `window` tokens of context, ancestors and itself. Tolerance as in test_gpu_kv8_attention.py."""
+    rng = np.random.default_rng(40 + T + window)
+    lens, hq, hkv, D = [T, T + 1, 70, 200, T + 31], 6, 2, 64
+    table, n_pages = R.page_table(rng, lens, 32)
+    ref = R.Cache(R.random_pool(rng, n_pages, hkv, D, 32), table)
+    q = torch.from_numpy(rng.standard_normal((len(lens), T, hq, D)).astype(np.float32)).to(R.TYPES[dtype])
+    paths, bits, depth = [], [], []
+    for _ in lens:
+        path = [[0]]
+        for t in range(1, T):  # a child of an earlier token, or another first token
+            parent = int(rng.integers(-1, t))
+            path.append((path[parent] if parent >= 0 else []) + [t])
+        paths.append(path)
+        bits.append([sum(1 << w for w in p) - (1 << 32 if 31 in p else 0) for p in path])
+        depth.append([len(p) - 1 for p in path])
+    err = ints([0])
+    got = m.kv8_attention(q.cuda(), dev(ref.pool), dev(table), ints(lens), window=window, tree=ints(bits), depth=ints(depth), err=err)
+    got, q = got.double().cpu().numpy(), q.double().numpy()
+    assert int(err) == 0
+    for b, n in enumerate(lens):
+        k, v = (x.astype(np.float64) for x in ref.read(b, 0, n))
+        for t, path in enumerate(paths[b]):
+            see = (list(range(n - T)) + [n - T + w for w in path])[-window:]
+            for h in range(hq):
+                kk, vv = k[see, h // 3], v[see, h // 3]
+                s = kk @ q[b, t, h] * D ** -0.5
+                e = np.exp(s - s.max())
+                out, ds = e @ vv / e.sum(), 2.0 ** -19 * (np.abs(kk) @ np.abs(q[b, t, h])).max() * D ** -0.5 + 2.0 ** -20
+                tol = np.abs(vv).max() * (2 * ds + (0 if dtype == "f32" else 2.0 ** -11) + 2.0 ** -17) + 2 * R.HALF_ULP[dtype] * np.abs(out) + 2.0 ** -26
+                assert (np.abs(got[b, t, h] - out) <= tol).all(), (b, t, h)
+
+
+def test_tree_depths_refused(m):
+    rng = np.random.default_rng(50)
+    ref = R.Cache(R.random_pool(rng, 3, 1, 64, 64), np.array([[0, 1]], np.int32))
+    q, pool, table, lens = torch.randn((1, 3, 2, 64), device="cuda"), dev(ref.pool), dev(ref.table), ints([100])
+    tree = ints([[1, 3, 5]])
+    with pytest.raises(m.MoeError):
+        m.kv8_attention(q, pool, table, lens, window=9, depth=ints([[0, 1, 1]]))
+    with pytest.raises(m.MoeError):
+        m.kv8_attention(q, pool, table, lens, window=9, tree=tree, depth=ints([0, 1]))
+    # a depth that no token has at its index counts as the nearest
+    got = m.kv8_attention(q, pool, table, lens, window=2, tree=tree, depth=ints([[5, -1, 3]]))
+    assert torch.equal(got, m.kv8_attention(q, pool, table, lens, window=2, tree=tree, depth=ints([[0, 0, 2]])))
+    # every token a child of the one before: the window's own positions
+    tree = ints([[1, 3, 7]])
+    got = m.kv8_attention(q, pool, table, lens, window=2, tree=tree, depth=ints([[0, 1, 2]]))
+    assert torch.equal(got, m.kv8_attention(q, pool, table, lens, window=2, tree=tree))
+    # and with the widest window there is, in a sequence shorter than the queries
+    for n in (2, 100):
+        got = m.kv8_attention(q, pool, table, ints([n]), window=(1 << 31) - 1, tree=tree, depth=ints([[0, 1, 1]]))
+        assert torch.equal(got, m.kv8_attention(q, pool, table, ints([n]), tree=tree))

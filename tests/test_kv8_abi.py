@@ -160,3 +160,11 @@ def test_arrays_off_their_boundary(m):
                 scale=1.0, out=16, lse=16, err=16, workspace=16, workspace_bytes=L.moe_kv8_attention_workspace_bytes(2, 4, 8, 2, 128))
     for name in ("lens", "tree", "lse", "err"):
         assert L.moe_kv8_attention(ref(m.KV8AttentionC(**{**call, name: 18})), None) == ALIGN, name
+
+
+def test_depth_refusals(m):
+    import ctypes
+    call = dict(cache=cache(m), q=16, type=2, T=4, n_heads=8, q_seq_stride=4096, q_token_stride=1024, q_head_stride=128, lens=16, tree=16,
+                depth=16, window=5, scale=1.0, out=16, workspace=16, workspace_bytes=m.lib().moe_kv8_attention_workspace_bytes(2, 4, 8, 2, 128))
+    f = lambda **kw: m.lib().moe_kv8_attention(ctypes.byref(m.KV8AttentionC(**{**call, **kw})), None)  # noqa: E731
+    assert f(tree=None) == SHAPE and f(tree=None, window=0) == SHAPE and f(depth=18) == ALIGN
