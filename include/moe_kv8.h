@@ -122,6 +122,8 @@ typedef struct moe_kv8_attention_call {
     int64_t workspace_bytes;
     int32_t* err; /* optional */
     const int32_t* depth; /* [n_seqs][T], or NULL; only with tree (MOE_E_SHAPE) */
+    int32_t flags;        /* 0, or MOE_F_TEST_EXPIRE: a test hook, the copies' barriers never complete (MOE_ERR_TIMEOUT
+                           * after about a second per ring stage, at most 13; out and lse then hold anything) */
 } moe_kv8_attention_call;
 
 int64_t moe_kv8_attention_workspace_bytes(int n_seqs, int T, int n_heads, int n_kv_heads, int head_dim);

@@ -95,6 +95,7 @@ class KV8AttentionC(ctypes.Structure):
         ("n_heads", ctypes.c_int32), ("q_seq_stride", _I64), ("q_token_stride", _I64), ("q_head_stride", _I64),
         ("lens", _P), ("tree", _P), ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("out", _P),
         ("lse", _P), ("workspace", _P), ("workspace_bytes", _I64), ("err", _P), ("depth", _P),
+        ("flags", ctypes.c_int32),
     ]
 
 
@@ -341,7 +342,7 @@ def qsa_block_scores(q, keys, key_scale, scores=None, stream=None):
 
 _CACHE = "PqiiiPqii"                             # moe_kv8_cache
 _pack_rows = struct.Struct("@" + _CACHE + "0q").pack, struct.Struct("@PPiqqqqq").pack
-_pack_attn = struct.Struct("@" + _CACHE + "0qPiiiqqqPPifPPPqPP").pack
+_pack_attn = struct.Struct("@" + _CACHE + "0qPiiiqqqPPifPPPqPPi0q").pack
 _pack_norm = struct.Struct("@PPPPPPiiqqqif").pack
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
@@ -503,7 +504,7 @@ def kv8_attention(q, pool, page_table, lens, scale=None, window=0, tree=None, wo
     a = _pack_attn(*c, _ptr(q, dev), _elem(q), T, hq, qs[0], qs[1], qs[2], _ints(lens, "lens", B, dev),
                    0 if tree is None else _ints(tree, "tree", B * T, dev), window, D ** -0.5 if scale is None else scale,
                    _ptr(out, dev), 0 if lse is None else _ptr(lse, dev), _ptr(workspace, dev), workspace.nbytes,
-                   _err(err, dev), 0 if depth is None else _ints(depth, "depth", B * T, dev))
+                   _err(err, dev), 0 if depth is None else _ints(depth, "depth", B * T, dev), 0)
     _launch(lib().moe_kv8_attention, dev, stream, (q, pool, page_table, lens, tree, depth, out, lse, workspace, err), a)
     return out if lse is None else (out, lse)
 

@@ -118,6 +118,7 @@ int moe_kv8_attention(const moe_kv8_attention_call* call, cudaStream_t stream) {
     a.lse = call->lse;
     a.workspace = call->workspace;
     a.err = call->err;
+    a.test_expire = (call->flags & MOE_F_TEST_EXPIRE) != 0;
     if (!attn_list_fits(a)) return MOE_E_CAP;
     return status(launch_kv8_attention(a, call->type, stream));
 }

@@ -25,6 +25,7 @@ struct AttnArgs {
     float* lse;
     void* workspace;
     int32_t* err;
+    int test_expire;  // test hook: 1: each stage waits for an arrival that never comes
 };
 bool attn_list_fits(const AttnArgs& a);
 int64_t attn_workspace_bytes(int n_seqs, int T, int n_heads, int n_kv, int D);

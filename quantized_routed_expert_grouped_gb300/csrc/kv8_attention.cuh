@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
     if (rt == 0) {
         if (lane == 0) {
             for (int i = 0; i < S; ++i) {
-                mbar_init(full + i, 1);
+                mbar_init(full + i, 1 + a.test_expire);
                 mbar_init(empty + i, RTW);
             }
             if (wid == 0) *dead = 0;

@@ -185,3 +185,31 @@ def test_tree_depths_refused(m):
     for n in (2, 100):
         got = m.kv8_attention(q, pool, table, ints([n]), window=(1 << 31) - 1, tree=tree, depth=ints([[0, 1, 1]]))
         assert torch.equal(got, m.kv8_attention(q, pool, table, ints([n]), tree=tree))
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+def test_copy_that_does_not_arrive(m, rows):
+    """The abort path: no stage's barrier completes. Every wait gives up, the call ends with MOE_ERR_TIMEOUT, and the
+    next call, on the same workspace, is right."""
+    import ctypes
+    rng = np.random.default_rng(60)
+    lens, D = [400, 90], 256
+    table, n_pages = R.page_table(rng, lens, 64)
+    ref = R.Cache(R.random_pool(rng, n_pages, 1, D, 64), table)
+    pool, table, lens = dev(ref.pool), dev(table), ints(lens)
+    q = torch.randn((2, rows, 1, D), device="cuda")
+    want = m.kv8_attention(q, pool, table, lens)
+    out, ws, err = torch.zeros_like(q), m.kv8_attention_workspace(2, rows, 1, 1, D), ints([0])
+    cache = m.KV8CacheC(pool=pool.data_ptr(), n_pages=n_pages, n_kv_heads=1, head_dim=D, page_tokens=64, page_table=table.data_ptr(),
+                        table_stride=table.shape[1], max_pages=table.shape[1], n_seqs=2)
+    call = m.KV8AttentionC(cache=cache, q=q.data_ptr(), type=0, T=rows, n_heads=1, q_seq_stride=rows * D, q_token_stride=D, q_head_stride=D,
+                           lens=lens.data_ptr(), scale=D ** -0.5, out=out.data_ptr(), workspace=ws.data_ptr(), workspace_bytes=ws.numel(),
+                           err=err.data_ptr(), flags=m.F_TEST_EXPIRE)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert m.lib().moe_kv8_attention(ctypes.byref(call), stream) == 0
+    torch.cuda.synchronize()
+    assert int(err) == 64
+    err.zero_()
+    call.flags = 0
+    assert m.lib().moe_kv8_attention(ctypes.byref(call), stream) == 0
+    assert torch.equal(out, want) and int(err) == 0
