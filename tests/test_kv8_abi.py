@@ -168,3 +168,26 @@ def test_depth_refusals(m):
                 depth=16, window=5, scale=1.0, out=16, workspace=16, workspace_bytes=m.lib().moe_kv8_attention_workspace_bytes(2, 4, 8, 2, 128))
     f = lambda **kw: m.lib().moe_kv8_attention(ctypes.byref(m.KV8AttentionC(**{**call, **kw})), None)  # noqa: E731
     assert f(tree=None) == SHAPE and f(tree=None, window=0) == SHAPE and f(depth=18) == ALIGN
+
+
+def test_two_descriptions_agree(m):
+    """The binding packs the calls' structures by format; the ctypes structures say the same, field by field."""
+    import ctypes
+    import struct
+    kinds = {ctypes.c_void_p: "P", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f"}
+
+    def flat(s, base=0):
+        for name, t in s._fields_:
+            at = base + getattr(s, name).offset
+            if isinstance(t, type) and issubclass(t, ctypes.Structure):
+                yield from flat(t, at)
+            else:
+                yield at, kinds[t]
+
+    for s, pack in ((m.KV8CacheC, m._pack_rows[0]), (m.KV8RowsC, m._pack_rows[1]), (m.KV8AttentionC, m._pack_attn), (m.NormCallC, m._pack_norm)):
+        fields = list(flat(s))
+        values = [i + 1 for i in range(len(fields))]
+        packed = pack(*values)
+        assert ctypes.sizeof(s) - 8 < len(packed) <= ctypes.sizeof(s)
+        for (at, kind), v in zip(fields, values):
+            assert struct.unpack_from("@" + kind, packed, at)[0] == v
