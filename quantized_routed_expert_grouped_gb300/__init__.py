@@ -443,6 +443,8 @@ def _kv8_move(f, pool, page_table, cu_tokens, start, n_tokens, dtype, k, v, err,
     ks, vs = k.stride(), v.stride()
     if k.shape != (n_tokens, hkv, D) or v.shape != k.shape or v.dtype is not k.dtype or ks[2] != 1 or vs[2] != 1:
         raise MoeError(f"k, v: [{n_tokens}, {hkv}, {D}] of one type, contiguous in the last dimension, expected")
+    if n == 0 and n_tokens == 0:  # no sequences (the library takes one at least)
+        return k, v
     rows = _pack_rows[1](_ptr(k, dev), _ptr(v, dev), _elem(k), n_tokens, ks[0], ks[1], vs[0], vs[1])
     _launch(f, dev, stream, (k, v, pool, page_table, cu_tokens, start, err), _pack_rows[0](*c), rows,
             _ints(cu_tokens, "cu_tokens", n + 1, dev), _ints(start, "start", n, dev), _err(err, dev))
@@ -501,6 +503,8 @@ def kv8_attention(q, pool, page_table, lens, scale=None, window=0, tree=None, wo
         raise MoeError("lse: contiguous float32 [sequences, T, heads] expected")
     if not workspace.is_contiguous():
         raise MoeError("workspace: a contiguous tensor expected")
+    if B == 0:  # no sequences (the library takes one at least)
+        return out if lse is None else (out, lse)
     a = _pack_attn(*c, _ptr(q, dev), _elem(q), T, hq, qs[0], qs[1], qs[2], _ints(lens, "lens", B, dev),
                    0 if tree is None else _ints(tree, "tree", B * T, dev), window, D ** -0.5 if scale is None else scale,
                    _ptr(out, dev), 0 if lse is None else _ptr(lse, dev), _ptr(workspace, dev), workspace.nbytes,

@@ -191,3 +191,21 @@ def test_two_descriptions_agree(m):
         assert ctypes.sizeof(s) - 8 < len(packed) <= ctypes.sizeof(s)
         for (at, kind), v in zip(fields, values):
             assert struct.unpack_from("@" + kind, packed, at)[0] == v
+
+
+def test_no_sequences(m, monkeypatch):
+    """An empty batch is nothing to do: no call of the library, empty results."""
+    monkeypatch.setattr(m, "_device", lambda t: 0)
+    monkeypatch.setattr(m, "_ptr", lambda t, dev: t.data_ptr())
+    monkeypatch.setattr(m, "_current_device", lambda: 0)
+    monkeypatch.setattr(m, "_raw_stream", lambda dev: 0)
+    pool, table = m.kv8_pool(2, 2, 64, 32, device="cpu"), torch.zeros((0, 3), dtype=torch.int32)
+    zero, none = torch.zeros(1, dtype=torch.int32), torch.zeros(0, dtype=torch.int32)
+    x = torch.zeros((0, 2, 64))
+    m.kv8_write(x, x, pool, table, zero, none)
+    k, v = m.kv8_read(pool, table, zero, none, 0)
+    assert k.shape == v.shape == (0, 2, 64) and k.dtype is torch.bfloat16
+    out, lse = m.kv8_attention(torch.zeros((0, 4, 6, 64)), pool, table, none, with_lse=True)
+    assert out.shape == (0, 4, 6, 64) and lse.shape == (0, 4, 6)
+    with pytest.raises(m.MoeError):  # rows of no sequence
+        m.kv8_write(torch.zeros((1, 2, 64)), torch.zeros((1, 2, 64)), pool, table, zero, none)
