@@ -378,6 +378,14 @@ def _err(err, dev):
     return 0 if err is None else _ints(err, "err", 1, dev)
 
 
+def _pack(pack, *values):
+    """A structure's bytes; what its fields do not hold is an argument error."""
+    try:
+        return pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise MoeError(f"an argument is out of its type's range: {e}") from None
+
+
 def _empty(stream, shape, dtype, device):
     """A tensor of the caching allocator, of the stream that will write it."""
     if stream is None:
@@ -445,8 +453,8 @@ def _kv8_move(f, pool, page_table, cu_tokens, start, n_tokens, dtype, k, v, err,
         raise MoeError(f"k, v: [{n_tokens}, {hkv}, {D}] of one type, contiguous in the last dimension, expected")
     if n == 0 and n_tokens == 0:  # no sequences (the library takes one at least)
         return k, v
-    rows = _pack_rows[1](_ptr(k, dev), _ptr(v, dev), _elem(k), n_tokens, ks[0], ks[1], vs[0], vs[1])
-    _launch(f, dev, stream, (k, v, pool, page_table, cu_tokens, start, err), _pack_rows[0](*c), rows,
+    rows = _pack(_pack_rows[1], _ptr(k, dev), _ptr(v, dev), _elem(k), n_tokens, ks[0], ks[1], vs[0], vs[1])
+    _launch(f, dev, stream, (k, v, pool, page_table, cu_tokens, start, err), _pack(_pack_rows[0], *c), rows,
             _ints(cu_tokens, "cu_tokens", n + 1, dev), _ints(start, "start", n, dev), _err(err, dev))
     return k, v
 
@@ -505,7 +513,7 @@ def kv8_attention(q, pool, page_table, lens, scale=None, window=0, tree=None, wo
         raise MoeError("workspace: a contiguous tensor expected")
     if B == 0:  # no sequences (the library takes one at least)
         return out if lse is None else (out, lse)
-    a = _pack_attn(*c, _ptr(q, dev), _elem(q), T, hq, qs[0], qs[1], qs[2], _ints(lens, "lens", B, dev),
+    a = _pack(_pack_attn, *c, _ptr(q, dev), _elem(q), T, hq, qs[0], qs[1], qs[2], _ints(lens, "lens", B, dev),
                    0 if tree is None else _ints(tree, "tree", B * T, dev), window, D ** -0.5 if scale is None else scale,
                    _ptr(out, dev), 0 if lse is None else _ptr(lse, dev), _ptr(workspace, dev), workspace.nbytes,
                    _err(err, dev), 0 if depth is None else _ints(depth, "depth", B * T, dev), 0)
@@ -537,7 +545,7 @@ def add_rms_norm_q8_1(x, weight, residual=None, eps=1e-6, sum_out=None, y=None, 
     elif xq.dtype is not torch.uint8 or xq.shape != (rows, cols // 32, 36) or not xq.is_contiguous():
         raise MoeError("xq: contiguous uint8 [rows, cols/32, 36] expected")
     if rows:
-        c = _pack_norm(x.data_ptr(), 0 if residual is None else _ptr(residual, dev), _ptr(weight, dev),
+        c = _pack(_pack_norm, x.data_ptr(), 0 if residual is None else _ptr(residual, dev), _ptr(weight, dev),
                        0 if sum_out is None else _ptr(sum_out, dev), 0 if y is None else _ptr(y, dev), _ptr(xq, dev),
                        _elem(x), _elem(weight), rows, x.stride(0) if rows > 1 else cols,
                        0 if residual is None else residual.stride(0) if rows > 1 else cols, cols, eps)

@@ -209,3 +209,17 @@ def test_no_sequences(m, monkeypatch):
     assert out.shape == (0, 4, 6, 64) and lse.shape == (0, 4, 6)
     with pytest.raises(m.MoeError):  # rows of no sequence
         m.kv8_write(torch.zeros((1, 2, 64)), torch.zeros((1, 2, 64)), pool, table, zero, none)
+
+
+def test_numbers_out_of_range(m, monkeypatch):
+    """Numbers that a field of the call does not hold raise the package's error."""
+    monkeypatch.setattr(m, "_device", lambda t: 0)
+    monkeypatch.setattr(m, "_ptr", lambda t, dev: t.data_ptr())
+    monkeypatch.setattr(m, "_launch", lambda *a: pytest.fail("launched"))
+    pool, table = m.kv8_pool(2, 2, 64, 32, device="cpu"), torch.zeros((1, 2), dtype=torch.int32)
+    one = torch.zeros(1, dtype=torch.int32)
+    q, x = torch.zeros((1, 1, 4, 64)), torch.zeros((2, 64))
+    for f in (lambda: m.kv8_attention(q, pool, table, one, window=1 << 31), lambda: m.kv8_attention(q, pool, table, one, window=2.5),
+              lambda: m.kv8_attention(q, pool, table, one, scale=10 ** 400), lambda: m.add_rms_norm_q8_1(x, torch.zeros(64), eps="1e-6")):
+        with pytest.raises(m.MoeError):
+            f()
