@@ -213,3 +213,28 @@ def test_copy_that_does_not_arrive(m, rows):
     call.flags = 0
     assert m.lib().moe_kv8_attention(ctypes.byref(call), stream) == 0
     assert torch.equal(out, want) and int(err) == 0
+
+
+@pytest.mark.parametrize("dtype,queries,keys", [("bf16", 104, -104), ("f32", 104, -104), ("f32", -95, 95), ("bf16", -95, 95), ("f16", 104, -104), ("f16", -95, 95),
+                                                ("f32", -110, 112), ("bf16", 115, -105)])
+def test_query_ranges(m, dtype, queries, keys):
+    """scale * max |q| at the ends of its range, with keys that bring the scores back to size (16-bit queries of fp16 by
+    the scale alone). Tolerance as in test_gpu_kv8_attention.py."""
+    rng = np.random.default_rng(70)
+    lens, T, D = [700, 33], 3, 64
+    table, n_pages = R.page_table(rng, lens, 32)
+    pool = R.random_pool(rng, n_pages, 2, D, 32)
+    s = pool[..., :4].copy().view(np.float32) * np.float32(2.0 ** keys)
+    pool[..., :4] = s.view(np.uint8)
+    ref = R.Cache(pool, table)
+    q = rng.standard_normal((2, T, 4, D)).astype(np.float32)
+    q /= np.abs(q).max(-1, keepdims=True)  # at most one
+    part = 0 if dtype == "f16" else queries + 8 if queries > 0 else queries - 5  # of the power, in the queries; the rest in the scale
+    q = torch.from_numpy(q * np.float32(2.0 ** part)).to(R.TYPES[dtype])
+    scale = 2.0 ** (queries - part)
+    got, lse = m.kv8_attention(q.cuda(), dev(ref.pool), dev(table), ints(lens), scale=scale, with_lse=True)
+    out, want, reach, size = R.attention(q.double().numpy(), ref, lens, scale)
+    ds = 2.0 ** -19 * size + 2.0 ** -20
+    tol = reach * (2 * ds[..., None] + (0 if dtype == "f32" else 2.0 ** -11) + 2.0 ** -17) + 2 * R.HALF_ULP[dtype] * np.abs(out) + 2.0 ** -26
+    assert (np.abs(got.double().cpu().numpy() - out) <= tol).all()
+    assert (np.abs(lse.double().cpu().numpy() - want) <= ds + 2.0 ** -18 * (1 + np.abs(want))).all()
