@@ -12,7 +12,9 @@
 // above those that the output came from so far, with scores as far below), p_j is held times a power of two, so that
 // neither it nor 2^(e + d) leaves fp32's range. fp16's range below 2^10, down to 2^-24, keeps a
 // long tail of small weights. Codes and, after a shift by a power of two, 16-bit queries are exact in
-// fp16; an fp32 query and its weights are two fp16 parts each. Sums are fp32. For 16-bit queries the key
+// fp16; an fp32 query and its weights are two fp16 parts each. Sums are fp32; the matrix instructions
+// truncate theirs, which shortens an output by up to 6e-6 of itself where a warp sums over some hundred blocks (in fp32; 16-bit
+// outputs round by far more). For 16-bit queries the key
 // codes enter as fp16 subnormals (two byte permutes per four codes) and the score starts at -128 * sum q,
 // which is of the scores' own size: what that costs in rounding is far below theirs. For fp32 ones, and
 // the value codes always (the sum of weights would be far above the result), they are centred, with two
@@ -36,14 +38,16 @@
 // and a second kernel joins the parts in list order: the result does not depend on timing.
 //
 // What bounds it (GB300; the rate is of the records alone, of 6787 GB/s that a copy reaches):
-//   1 sequence of 1,048,579 tokens, one head of 256 dims, 16 rows, bf16: 90 us, 5.9 TB/s: memory, and
+//   1 sequence of 1,048,579 tokens, one head of 256 dims, 16 rows, bf16: 91 us, 5.9 TB/s: memory, and
 //     ~9 us of launches, queries, first copies and joining;
 //   64 sequences of 0 to 16k tokens, 8 heads of 128, 4 rows, bf16: 48.2 us, 5.0 TB/s: the same;
-//   1 of 131,077 tokens, 4 heads of 128, 16 rows, fp32: 38.8 us, 3.5 TB/s: issue and latency of the two
+//   1 of 131,077 tokens, 4 heads of 128, 16 rows, fp32: 38.6 us, 3.5 TB/s: issue and latency of the two
 //     parts' products at eight warps an SM, and the same fixed part;
 //   32 windows of 4 over 8k to 33k tokens, 8 heads of 128, 32 rows, fp16: 244 us, 4.8 TB/s: the matrix
 //     instructions and the widening of codes, at eight warps an SM (pipe 48 %, issue 40 %);
 //   one token at 777 positions: 9.9 us, all latency.
+// Heads of 160 to 256 dims spill 36 to 164 bytes in the forms of two parts (fp32, fp16 weights); no other
+// form spills. The sums of 32 rows at 128 dims leave the compiler three registers: small changes of the masks cost up to 4 % there.
 #pragma once
 
 #include <atomic>
@@ -88,7 +92,7 @@ inline AttnGeom attn_geom(int R, bool two) {
 }
 // Two tiles a warp widen a block's codes once for 32 rows, and leave registers for eight warps an SM instead of
 // twelve: better where the work is long (32 windows of 4 over 8k to 32k tokens: 252 against 285 us), not where it
-// is short (4 over 3k: 24.5 against 22.8), about even at kAttnLong blocks of the page table. Not for fp32
+// is short (4 over 3k: 22.3 against 22.1), about even at kAttnLong blocks of the page table. Not for fp32
 // (two fp16 parts: 64 rows of 16k tokens 138 against 114 us) or wide heads, whose sums fill the registers.
 constexpr int64_t kAttnLong = 24576;
 // With more than 16 fp16 rows, weights of two parts take as much again as one part where the products bound the
@@ -247,8 +251,15 @@ struct AttnSmem {
     static __host__ __device__ int fixed(int RTW) { return (buf_bytes(RTW) + kStats + kAttnStages * 20 + 16 + 15) / 16 * 16; }
 };
 
+// Registers of a thread: for three CTAs an SM, or two; with 192 the joining kernel's CTAs find room beside two
+// (100k tokens, 16 rows of 64 dims, fp16: 17.5 us, with 195 registers 21.3). Given as a limit, not as CTAs an SM: the compiler then
+// keeps wide heads' loop as fast as at two CTAs (256 dims, fp16: 34 us, else 39).
+constexpr int attn_regs(int D, int MT, int PREC) {
+    return MT == 1 && D <= 128 && PREC == kAttnPlain ? 168 : D == 64 && PREC == kAttnWeights ? 192 : 255;
+}
+
 template <int D, int MT, int PREC>
-__global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == kAttnPlain ? 3 : 2) kv8_attention_kernel(const AttnPlan p) {
+__global__ void __maxnreg__(attn_regs(D, MT, PREC)) kv8_attention_kernel(const AttnPlan p) {
     using L = AttnSmem<D, MT, PREC>;
     constexpr bool SPLIT = PREC == kAttnSplit, W2 = PREC != kAttnPlain;  // two parts of a query; of a weight
     constexpr int kNB = D / 32, kND = D / 8;
@@ -613,21 +624,22 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                                 mma_16816(sa[mt][jj], lb[mt], kk[jj][2], kk[jj][3]);
                     }
                 }
-                // lane (g, c) holds rows g, g + 8 and tokens 8 c + 2 jj + e; an unseen one becomes -inf
+                // lane (g, c) holds rows g, g + 8 and tokens 8 c + 2 jj + e; an unseen one becomes -inf. (special: such tokens,
+                // or a value scale far above those before it)
                 const int t0 = u * kKvBlock;
-                const bool mask = t0 > before_window - kKvBlock || t0 <= behind;  // (the last block ends at up to 2^31)
-                if (mask) {
+                bool special = t0 > before_window - kKvBlock || t0 <= behind;  // (the last block ends at up to 2^31)
+                if (special) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const int row = pieces[0].seg % p.g.RB * RP + (rt * MT + mt) * 16 + q * 8 + g;
-                            const int t = row / a.G, ps = row < p.R ? before_window + t : -1;
-                            uint32_t bits = 0;
+                            const int t = row / a.G, ps = row < p.R ? before_window + t : -1, j0 = t0 + 8 * c;
                             int from = a.window > 0 ? max(ps - a.window, -1) : -1;  // positions up to it are out of sight
+                            uint32_t see;                                            // bit i: the query sees position j0 + i
                             if (a.tree && ps >= 0) {
                                 const int64_t bt = static_cast<int64_t>(pieces[0].b) * a.T;
-                                bits = static_cast<uint32_t>(gload(a.tree + bt + t));
+                                uint32_t bits = static_cast<uint32_t>(gload(a.tree + bt + t)) & (0xffffffffu >> (32 - a.T));
                                 if (a.depth) {
                                     const int d = attn_depth(a, bt, t);
                                     from = max(before_window + d - a.window, -1);
@@ -635,20 +647,20 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                                     for (int w = 0; w < a.T; ++w)
                                         if (d - attn_depth(a, bt, w) >= a.window) bits &= ~(1u << w);
                                 }
+                                const int w = j0 - before_window;  // what lies before the window is seen
+                                see = w >= 0 ? (w < 32 ? bits >> w : 0) : w > -8 ? (bits << -w) | ((1u << -w) - 1) : 0xffu;
+                            } else {
+                                see = ps >= j0 ? 0xffu >> max(7 - (ps - j0), 0) : 0;
                             }
-                            if (ps < 0) from = 0x7fffffff;
+                            see &= 0xffu << min(max(from + 1 - j0, 0), 8);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int j = t0 + 8 * c + i, w = j - before_window;
-                                const bool in = a.tree ? (w < 0 || (w < a.T && (bits >> (w & 31) & 1u))) : j <= ps;
-                                if (!(in && j > from))
-                                    sa[mt][i >> 1][2 * q + (i & 1)] = -INFINITY;
-                            }
+                            for (int i = 0; i < 8; ++i)
+                                if (!(see >> i & 1)) sa[mt][i >> 1][2 * q + (i & 1)] = -INFINITY;
                         }
                 }
                 // ---- running reference; o and l are rescaled only where one of the warp's rows outgrew it
                 float f[MT][2], top[MT][2];
-                bool grew = false, far = false;
+                bool grew = false;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -662,6 +674,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                         grew |= top[mt][q] - m[mt][q] > room || room < kAttnSlack + kAttnShift - kAttnFar;
                     }
                 if (__any_sync(0xffffffffu, grew)) {
+                    bool far = false;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -681,7 +694,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                             }
                             far |= e + dd[mt][q] > kAttnFar;
                         }
-                    far = __any_sync(0xffffffffu, far);
+                    special |= static_cast<bool>(__any_sync(0xffffffffu, far));
                 }
                 // ---- weights: the lane's tokens 8 c + 4 xx + 0..3 feed product step xx
                 uint4 pa[MT][2], pl[MT][2];
@@ -722,7 +735,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 && D <= 128 && PREC == k
                             }
                         }
                 };
-                if (mask || far) weights(std::true_type{});
+                if (special) weights(std::true_type{});
                 else weights(std::false_type{});
                 const uint8_t* vp = rec + kKvHead + kKvBlock * D + g * 32 + c * 8;
                 constexpr int kRun = 4;  // dims' sums in turn, as above (kND is a multiple of 4)
