@@ -99,7 +99,8 @@ int moe_kv8_read(const moe_kv8_cache* cache, const moe_kv8_rows* rows, const int
  * positions seen, with the key/value head h / (n_heads / n_kv_heads); a query that sees nothing
  * gives zeros. lse[b][t][h] = log sum_j e^(s_j) (-inf where nothing is seen).
  * q, out have type `type`. Products of 16-bit queries with the codes are exact; weights are held in
- * fp16, the largest near 2^10, so that weights down to 2^-34 of it count; sums are fp32. A weight is
+ * fp16, the largest near 2^10, so that weights down to 2^-34 of it count; sums are fp32 (the matrix
+ * instructions' truncate: an output over a long context comes out short by up to 6e-6 of itself). A weight is
  * one fp16 number for bf16, two (its rounding and the rest) for fp32, and for fp16 two where a
  * key/value head has up to 16 rows (T * n_heads / n_kv_heads) or the page tables up to 4096 blocks in
  * all, one otherwise. fp32 queries are two fp16 numbers each. Scores are products of a factor per row with a

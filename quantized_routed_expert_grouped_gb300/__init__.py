@@ -476,8 +476,9 @@ def kv8_read(pool, page_table, cu_tokens, start, n_tokens, dtype=torch.bfloat16,
 
 def kv8_attention_workspace(n_seqs: int, T: int, n_heads: int, n_kv_heads: int, head_dim: int,
                             device="cuda") -> torch.Tensor:
-    """A workspace for kv8_attention calls of these sizes or smaller ones, to be kept between calls
-    (one for each stream that calls run on at the same time)."""
+    """A workspace for kv8_attention calls of these sizes, or of fewer sequences, dims, and rows of a key/value
+    head (T * n_heads / n_kv_heads), to be kept between calls (one for each stream that calls run on at the
+    same time)."""
     n = int(lib().moe_kv8_attention_workspace_bytes(n_seqs, T, n_heads, n_kv_heads, head_dim))
     if not n:
         raise MoeError(strerror(-3))

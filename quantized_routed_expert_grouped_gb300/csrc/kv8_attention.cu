@@ -80,7 +80,7 @@ __device__ __forceinline__ void put_out(const AttnPlan& p, int row, int d, const
 // A segment that may have more than kManyParts parts (it has at most a block a warp, and an even share of the CTAs
 // where lengths are even): a CTA for 64 dims of a row. Every part's m and l are loaded at once, a thread each (two past
 // 256), and the rows of 128 parts at once, sixteen threads each, before the first wait. 131k tokens of 4 heads: 31.8 us
-// for the call against 34.6 with the kernel below, a million tokens of one 90.9 against 94.5; 777 tokens 10.9 against 10.2.
+// for the call against 34.6 with the kernel below, a million tokens of one 90.9 against 94.5; 777 tokens 10.4 against 9.8.
 constexpr int kManyParts = 32;
 constexpr int kSlice = 64, kSubs = 256 / (kSlice / 4), kAtOnce = 8;
 static_assert(kAttnMaxCtas <= 512, "two parts a thread");

@@ -40,8 +40,8 @@
 // What bounds it (GB300; the rate is of the records alone, of 6787 GB/s that a copy reaches):
 //   1 sequence of 1,048,579 tokens, one head of 256 dims, 16 rows, bf16: 91 us, 5.9 TB/s: memory, and
 //     ~9 us of launches, queries, first copies and joining;
-//   64 sequences of 0 to 16k tokens, 8 heads of 128, 4 rows, bf16: 48.2 us, 5.0 TB/s: the same;
-//   1 of 131,077 tokens, 4 heads of 128, 16 rows, fp32: 38.6 us, 3.5 TB/s: issue and latency of the two
+//   64 sequences of 0 to 16k tokens, 8 heads of 128, 4 rows, bf16: 47.9 us, 5.1 TB/s: the same;
+//   1 of 131,077 tokens, 4 heads of 128, 16 rows, fp32: 38.5 us, 3.5 TB/s: issue and latency of the two
 //     parts' products at eight warps an SM, and the same fixed part;
 //   32 windows of 4 over 8k to 33k tokens, 8 heads of 128, 32 rows, fp16: 244 us, 4.8 TB/s: the matrix
 //     instructions and the widening of codes, at eight warps an SM (pipe 48 %, issue 40 %);
@@ -92,7 +92,7 @@ inline AttnGeom attn_geom(int R, bool two) {
 }
 // Two tiles a warp widen a block's codes once for 32 rows, and leave registers for eight warps an SM instead of
 // twelve: better where the work is long (32 windows of 4 over 8k to 32k tokens: 252 against 285 us), not where it
-// is short (4 over 3k: 22.3 against 22.1), about even at kAttnLong blocks of the page table. Not for fp32
+// is short (4 over 3k: 22.1 both), about even at kAttnLong blocks of the page table. Not for fp32
 // (two fp16 parts: 64 rows of 16k tokens 138 against 114 us) or wide heads, whose sums fill the registers.
 constexpr int64_t kAttnLong = 24576;
 // With more than 16 fp16 rows, weights of two parts take as much again as one part where the products bound the

@@ -15,7 +15,7 @@
 // dims and four tokens in registers.
 // Measured (GB300, of 6787 GB/s that a copy reaches; bf16, 8 heads of 128): writing 26k tokens of seven
 // prompts, 33 us for 105 MB of rows and 53 MB of records (4.8 TB/s; the instructions fill 67 % of the
-// issue slots), reading them back 31 us. Reading 87k tokens of five prefixes: 86 us for 179 MB and 355 MB
+// issue slots; from fp32 rows 43 us for 209 MB and 53 MB, 6.1 TB/s), reading them back 31 us (into fp32 48 us). Reading 87k tokens of five prefixes: 86 us for 179 MB and 355 MB
 // (6.2 TB/s, memory); 100k tokens into fp32 162 us (6.3 TB/s; 201 with stores that fill half sectors). Small calls (64 windows of 4 tokens) take 6 us each, launch and latency.
 #include <type_traits>
 

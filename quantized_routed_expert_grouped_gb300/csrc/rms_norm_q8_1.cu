@@ -12,8 +12,9 @@
 // its stores), which other rows' CTAs cover, and the arithmetic, kept to a dozen instructions a value by
 // packed pairs and by codes that are divided out only next to a tie.
 // Measured (GB300, of 6787 GB/s that a copy reaches): 8191 rows of 4096, bf16, with the residual, the sum,
-// y and q8_1 rows: 47 us for 134 MB read and 172 MB written (6.4 TB/s, issue slots 72 % full), fp32 85 us for 575 MB
-// (6.8 TB/s; in fp32 half as many CTAs an SM, as at 32 registers the row spilled: 118 us); reading the q8_1 rows
+// y and q8_1 rows: 47 us for 134 MB read and 172 MB written (6.4 TB/s, issue slots 74 % full), fp32 85 us for 575 MB
+// (6.8 TB/s; in fp32 half as many CTAs an SM, as at 32 registers the row spilled: 118 us; 16-bit rows at 32 spill 24 bytes, fp32 ones of more than 16,384 columns
+// 200); reading the q8_1 rows
 // back 14 us for 38 MB and 67 MB (much of it still in L2 at the end). Four rows: 1 to 3 us each.
 #include "internal.h"
 #include "kv8.cuh"
