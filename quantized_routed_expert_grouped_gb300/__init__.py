@@ -1,6 +1,6 @@
 """Grouped routed-expert decode for the verify window, GB300-native (sm_103a).
 
-A thin ctypes binding over the C ABI in ``include/moe_grouped.h`` (library
+A thin ctypes binding over the C ABI in ``include/moe_grouped.h``, ``moe_kv8.h`` and ``moe_decode.h`` (library
 ``_build/libmoe_grouped.so``, built by ``build.py``). The functions here only marshal
 arguments: torch tensors supply device memory and the current CUDA stream; every step runs in
 the library's kernels. There is no CPU fallback: a missing library raises.
@@ -10,6 +10,8 @@ q8_1 rows are uint8 tensors of shape [rows, cols/32, 36].
 from __future__ import annotations
 
 import ctypes
+import fractions
+import math
 import os
 import struct
 
@@ -22,7 +24,7 @@ __all__ = [
     "LayerCall", "layer_sync_ints", "router_topk", "combine", "F_SYNC_PAIR", "F_SYNC_ODD", "F_TEST_EXPIRE",
     "qsa_block_scores", "grouped_fused_sync_ints", "stage_blobs",
     "kv8_block_bytes", "kv8_pool", "kv8_write", "kv8_read", "kv8_attention", "kv8_attention_workspace",
-    "add_rms_norm_q8_1", "dequantize_q8_1",
+    "add_rms_norm_q8_1", "dequantize_q8_1", "Rope", "head_norm_rope", "kv8_append", "token_logprobs",
 ]
 
 Q8_0, Q4B, NL4, CB2, CB3, CB3X, CB2X = 1, 2, 3, 4, 5, 6, 7
@@ -107,6 +109,39 @@ class NormCallC(ctypes.Structure):
     ]
 
 
+class RopeC(ctypes.Structure):
+    _fields_ = [("turns", _P), ("rot", ctypes.c_int32), ("start", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float)]
+
+
+class HeadsC(ctypes.Structure):
+    _fields_ = [
+        ("x", _P), ("out", _P), ("weight", _P), ("x_token_stride", _I64), ("x_head_stride", _I64),
+        ("out_token_stride", _I64), ("out_head_stride", _I64), ("n_heads", ctypes.c_int32),
+    ]
+
+
+class HeadNormCallC(ctypes.Structure):
+    _fields_ = [
+        ("q", HeadsC), ("k", HeadsC), ("rope", RopeC), ("positions", _P), ("n_tokens", _I64),
+        ("type", ctypes.c_int32), ("w_type", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("eps", ctypes.c_float),
+    ]
+
+
+class KV8AppendC(ctypes.Structure):
+    _fields_ = [
+        ("cache", KV8CacheC), ("rows", KV8RowsC), ("q", HeadsC), ("rope", RopeC), ("k_weight", _P), ("cu_tokens", _P),
+        ("start", _P), ("positions", _P), ("w_type", ctypes.c_int32), ("eps", ctypes.c_float), ("err", _P),
+    ]
+
+
+class LogprobsCallC(ctypes.Structure):
+    _fields_ = [
+        ("logits", _P), ("row_stride", _I64), ("type", ctypes.c_int32), ("rows", ctypes.c_int32), ("vocab", ctypes.c_int32),
+        ("n_ids", ctypes.c_int32), ("top", ctypes.c_int32), ("scale", ctypes.c_float), ("ids", _P), ("logprobs", _P),
+        ("top_logprobs", _P), ("top_ids", _P), ("entropy", _P), ("lse", _P),
+    ]
+
+
 _ELEM = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
@@ -150,11 +185,15 @@ def lib():
         L.moe_kv8_attention.argtypes = [_P, _P]
         L.moe_add_rms_norm_q8_1.argtypes = [_P, _P]
         L.moe_dequantize_q8_1.argtypes = [_P, _I64, _I64, _P, _I, _P]
+        L.moe_head_norm_rope.argtypes = [_P, _P]
+        L.moe_kv8_append.argtypes = [_P, _P]
+        L.moe_token_logprobs.argtypes = [_P, _P]
         for f in ("moe_quantize_q8_1", "moe_route_group", "moe_grouped_gu", "moe_swiglu_q8_1",
                   "moe_grouped_down", "moe_expert_grouped", "moe_expert_grouped_static", "moe_test_block_isum",
                   "moe_transcode_cb", "moe_expert_layer", "moe_router_topk", "moe_combine",
                   "moe_qsa_block_scores", "moe_expert_grouped_fused", "moe_stage_blobs", "moe_kv8_write",
-                  "moe_kv8_read", "moe_kv8_attention", "moe_add_rms_norm_q8_1", "moe_dequantize_q8_1"):
+                  "moe_kv8_read", "moe_kv8_attention", "moe_add_rms_norm_q8_1", "moe_dequantize_q8_1",
+                  "moe_head_norm_rope", "moe_kv8_append", "moe_token_logprobs"):
             getattr(L, f).restype = _I
         _LIB = L
     return _LIB
@@ -567,6 +606,185 @@ def dequantize_q8_1(xq, dtype=torch.float32, out=None, stream=None):
     if rows:
         _launch(lib().moe_dequantize_q8_1, dev, stream, (xq, out), xq.data_ptr(), rows, cols, _ptr(out, dev), _elem(out))
     return out
+
+
+# ---------------------------------------------------------------- around the attention side (moe_decode.h)
+
+_ROWS, _HEADS, _ROPE = "PPiqqqqq", "PPPqqqqi0q", "Piiif"
+_pack_heads = struct.Struct("@" + _HEADS * 2 + _ROPE + "Pqiiif").pack
+_pack_append = struct.Struct("@" + _CACHE + "0q" + _ROWS + _HEADS + _ROPE + "PPPPifP").pack
+_pack_logprobs = struct.Struct("@PqiiiiifPPPPPP").pack
+_NO_HEADS, _NO_ROPE = (0,) * 8, (0, 0, 0, 0, 0.0)
+_TWO_PI = 2 * fractions.Fraction("3.14159265358979323846264338327950288419716939937510")
+
+
+class Rope:
+    """A rotation of heads by position, kept between calls: dims start .. start + rot of a head are rot / 2 pairs, dims
+    (start + i, start + i + rot / 2), or interleaved (start + 2 i, start + 2 i + 1), and pair i turns by position * f_i.
+    rot is a multiple of 16, start of 8. f_i = theta^(-2 i / rot), or inv_freq[i] where given (say, frequencies that
+    were rounded to fp32). scaling: None, or for long contexts
+      {"kind": "linear", "scale": s}: all divided by s;
+      {"kind": "yarn", "scale": s, "original": o, "fast": 32, "slow": 1}: pairs that turn less than `slow` times over the
+        original length o are divided by s, those that turn more than `fast` times are kept, with a line in i between (whose
+        ends are moved outward to whole pairs); the rotated dims are multiplied by 0.1 log s + 1;
+      {"kind": "bands", "scale": s, "original": o, "low": 1, "high": 4}: the same by low and high, with a line in the number
+        of turns, and without a factor.
+    factor (of the rotated dims) overrides the scaling's. Angles are exact to 1e-7 at any 32-bit position."""
+
+    def __init__(self, rot, theta=10000.0, start=0, interleaved=False, scaling=None, inv_freq=None, factor=None, device="cuda"):
+        if rot <= 0 or rot % 16 or start < 0 or start % 8:
+            raise MoeError("rot: a multiple of 16, start: a multiple of 8, expected")
+        if inv_freq is None:
+            if not (theta > 0 and math.isfinite(theta)):
+                raise MoeError("theta: a positive number expected")
+            f = [float(theta) ** (-2 * i / rot) for i in range(rot // 2)]
+        else:
+            f = [float(x) for x in inv_freq]
+        if len(f) != rot // 2 or not all(math.isfinite(x) for x in f):
+            raise MoeError(f"inv_freq: {rot // 2} finite numbers expected")
+        f, scaled = self._scaled(f, rot, theta, dict(scaling or {"kind": "none"}))
+        self.inv_freq, self.factor = f, scaled if factor is None else float(factor)
+        self.rot, self.start, self.interleaved = rot, start, bool(interleaved)
+        # fractions of a turn a position, in 64 bits (as int64 tensors hold them)
+        turns = [round(fractions.Fraction(x) / _TWO_PI * 2 ** 64) % 2 ** 64 for x in f]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+        self._device = self.turns.get_device()
+        self._fields = (self.turns.data_ptr(), rot, start, int(self.interleaved), self.factor)
+
+    @staticmethod
+    def _scaled(f, rot, theta, p):
+        kind, s = p.pop("kind", None), p.pop("scale", 1.0)
+        known = {"none": {}, "linear": {}, "yarn": {"original": None, "fast": 32.0, "slow": 1.0}, "bands": {"original": None, "low": 1.0, "high": 4.0}}
+        if kind not in known or not (s > 0 and math.isfinite(s)) or set(p) - set(known[kind]):
+            raise MoeError(f"scaling: unknown kind or fields, or no positive scale: {kind!r}, {sorted(p)}")
+        p = {**known[kind], **p}
+        if kind in ("none", "linear"):
+            return [x / s for x in f], 1.0
+        if not all(x is not None and x > 0 for x in p.values()):
+            raise MoeError(f"scaling: {kind} takes positive {', '.join(p)}")
+        turns = [p["original"] * x / (2 * math.pi) for x in f]
+        if kind == "bands":
+            if p["high"] <= p["low"]:
+                raise MoeError("scaling: high above low expected")
+            keep = [min(max((t - p["low"]) / (p["high"] - p["low"]), 0.0), 1.0) for t in turns]
+            factor = 1.0
+        else:
+            if theta <= 1:
+                raise MoeError("scaling: yarn takes a theta above 1")
+            at = [rot * math.log(p["original"] / (2 * math.pi * p[r])) / (2 * math.log(theta)) for r in ("fast", "slow")]
+            lo, hi = max(math.floor(at[0]), 0), math.ceil(at[1])
+            keep = [1 - (min(max((i - lo) / (hi - lo), 0.0), 1.0) if hi > lo else float(i > lo)) for i in range(rot // 2)]
+            factor = 0.1 * math.log(s) + 1
+        return [x * k + x / s * (1 - k) for x, k in zip(f, keep)], factor
+
+
+def _rope(rope, dev, D):
+    if rope is None:
+        return _NO_ROPE
+    if rope._device != dev:
+        raise MoeError(f"rope: on device {dev} expected")
+    if rope.start + rope.rot > D:
+        raise MoeError(f"rope: dims {rope.start} .. {rope.start + rope.rot} of heads of {D}")
+    return rope._fields
+
+
+def _heads(x, weight, out, N, D, like, dev, stream, name):
+    """The fields of moe_heads, and the rows that they are written to."""
+    shape, xs = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != N or shape[2] != D or (N and xs[2] != 1) or x.dtype is not like.dtype:
+        raise MoeError(f"{name}: [{N}, heads, {D}] of {like.dtype}, contiguous in the last dimension, expected")
+    if out is None:
+        out = _empty(stream, shape, x.dtype, x.device)
+        os = (shape[1] * D, D)
+    else:
+        os = out.stride()
+        if out.shape != shape or out.dtype is not x.dtype or (N and os[2] != 1):
+            raise MoeError(f"{name}_out: {name}'s shape and type, contiguous in the last dimension, expected")
+    if weight is not None and (weight.shape != (D,) or not weight.is_contiguous()):
+        raise MoeError(f"{name}_weight: contiguous [{D}] expected")
+    return (_ptr(x, dev), _ptr(out, dev), 0 if weight is None else _ptr(weight, dev), xs[0], xs[1], os[0], os[1], shape[1]), out
+
+
+def _w_type(a, b):
+    if a is None or b is None:
+        return 0 if a is b else _elem(b if a is None else a)
+    if a.dtype is not b.dtype:
+        raise MoeError("q_weight and k_weight: one type expected")
+    return _elem(a)
+
+
+def head_norm_rope(q, positions, rope=None, k=None, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Norm of each head (where it has a weight [head_dim]) and rotation by position (where there is a Rope) of rows q, and
+    k, [tokens, heads, head_dim], in one pass; positions int32 [tokens] (None without a rotation), negative ones turn back. Returns (q_out,
+    k_out), k_out None without k; q_out may be q itself, k_out k. head_dim: a multiple of 16 up to 256."""
+    dev = _device(q)
+    if len(q.shape) != 3:
+        raise MoeError("q: [tokens, heads, head_dim] expected")
+    N, _, D = q.shape
+    if rope is not None and positions is None:
+        raise MoeError("positions: expected with a rotation")
+    a, q_out = _heads(q, q_weight, q_out, N, D, q, dev, stream, "q")
+    b, k_out = (_NO_HEADS, None) if k is None else _heads(k, k_weight, k_out, N, D, q, dev, stream, "k")
+    c = _pack(_pack_heads, *a, *b, *_rope(rope, dev, D), 0 if positions is None else _ints(positions, "positions", N, dev), N, _elem(q),
+              _w_type(q_weight, None if k is None else k_weight), D, eps)
+    _launch(lib().moe_head_norm_rope, dev, stream, (q, k, q_weight, k_weight, positions, q_out, k_out, None if rope is None else rope.turns), c)
+    return q_out, k_out
+
+
+def kv8_append(k, v, pool, page_table, cu_tokens, start, rope=None, q=None, q_weight=None, k_weight=None, eps=1e-6, positions=None,
+               q_out=None, err=None, stream=None):
+    """kv8_write of keys that are normed (k_weight [head_dim]) and rotated on the way, and the queries of the same tokens, q
+    [tokens, heads, head_dim], normed and rotated beside them: one launch from the projection's rows to what kv8_attention
+    takes. positions int32 [tokens]: what each row turns by (a draft token by its depth in a tree), None: its
+    position in the cache. Returns q_out (None without q); q_out may be q itself. Rows of q_out of a sequence that is refused (err) are left as
+    they were."""
+    c, dev = _kv8_cache(pool, page_table)
+    hkv, D, n = c[2], c[3], c[8]
+    N, ks, vs = k.shape[0], k.stride(), v.stride()
+    if k.shape != (N, hkv, D) or v.shape != k.shape or v.dtype is not k.dtype or (N and (ks[2] != 1 or vs[2] != 1)):
+        raise MoeError(f"k, v: [tokens, {hkv}, {D}] of one type, contiguous in the last dimension, expected")
+    if k_weight is not None and (k_weight.shape != (D,) or not k_weight.is_contiguous()):
+        raise MoeError(f"k_weight: contiguous [{D}] expected")
+    a, q_out = (_NO_HEADS, None) if q is None else _heads(q, q_weight, q_out, N, D, k, dev, stream, "q")
+    if n == 0 and N == 0:  # no sequences (the library takes one at least)
+        return q_out
+    x = _pack(_pack_append, *c, _ptr(k, dev), _ptr(v, dev), _elem(k), N, ks[0], ks[1], vs[0], vs[1], *a, *_rope(rope, dev, D),
+              0 if k_weight is None else _ptr(k_weight, dev), _ints(cu_tokens, "cu_tokens", n + 1, dev), _ints(start, "start", n, dev),
+              0 if positions is None else _ints(positions, "positions", N, dev), _w_type(None if q is None else q_weight, k_weight), eps, _err(err, dev))
+    _launch(lib().moe_kv8_append, dev, stream, (k, v, q, q_out, q_weight, k_weight, pool, page_table, cu_tokens, start, positions, err,
+                                                None if rope is None else rope.turns), x)
+    return q_out
+
+
+def token_logprobs(logits, ids=None, top=0, scale=1.0, stream=None):
+    """Of rows of logits [rows, vocab], with p = softmax(scale * logits): log p of the given tokens, ids int32 [rows, n] (-inf for
+    an id outside the vocabulary, such as -1 for none); the `top` (up to 32) most likely tokens' log p and ids, equal logits in order of
+    their ids; the entropy; and the log-sum-exp. Returns (logprobs fp32 [rows, n], top_logprobs fp32 [rows, top], top_ids
+    int32 [rows, top], entropy fp32 [rows], lse fp32 [rows]), None for what was not asked for."""
+    dev = _device(logits)
+    shape = logits.shape
+    if len(shape) != 2 or (logits.stride(1) != 1 and shape[1] > 1):
+        raise MoeError("logits: [rows, vocab] with contiguous rows expected")
+    if not 0 <= top <= 32:
+        raise MoeError("top: 0 to 32 expected")
+    R, V = shape
+    n = 0
+    if ids is not None:
+        if ids.shape[:1] != (R,) or len(ids.shape) != 2:
+            raise MoeError(f"ids: [{R}, n] expected")
+        n = ids.shape[1]
+    # one allocation for what is fp32: entropy, lse, logprobs, top
+    f = _empty(stream, (R * (2 + n + top),), torch.float32, logits.device)
+    entropy, lse = f[:R], f[R:2 * R]
+    logprobs = None if ids is None else f[2 * R:(2 + n) * R].view(R, n)
+    top_ids = _empty(stream, (R, top), torch.int32, logits.device) if top else None
+    top_lp = f[(2 + n) * R:].view(R, top) if top else None
+    if R:
+        at = f.data_ptr()
+        c = _pack(_pack_logprobs, _ptr(logits, dev), logits.stride(0) if R > 1 else V, _elem(logits), R, V, n, top, scale, 0 if not n else _ints(ids, "ids", R * n, dev),
+                  at + 8 * R, at + 4 * R * (2 + n), 0 if top_ids is None else top_ids.data_ptr(), at, at + 4 * R)
+        _launch(lib().moe_token_logprobs, dev, stream, (logits, ids, f, top_ids), c)
+    return logprobs, top_lp, top_ids, entropy, lse
 
 
 def expert_grouped(*args, stream=None, **kw):

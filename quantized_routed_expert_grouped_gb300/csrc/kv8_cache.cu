@@ -17,51 +17,16 @@
 // prompts, 33 us for 105 MB of rows and 53 MB of records (4.8 TB/s; the instructions fill 67 % of the
 // issue slots; from fp32 rows 43 us for 209 MB and 53 MB, 6.1 TB/s), reading them back 31 us (into fp32 48 us). Reading 87k tokens of five prefixes: 86 us for 179 MB and 355 MB
 // (6.2 TB/s, memory); 100k tokens into fp32 162 us (6.3 TB/s; 201 with stores that fill half sectors). Small calls (64 windows of 4 tokens) take 6 us each, launch and latency.
-#include <type_traits>
-
 #include "internal.h"
 #include "kv8.cuh"
 #include "kv8_api.h"
+#include "kv8_quant.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kThreads = 128;
-
-// x * inv rounded to an integer (ties to even) in the low byte of the result, plus 128: |x * inv| <= 127
-// up to two roundings, so adding 1.5 * 2^23 + 128 leaves the integer in the low bits.
-__device__ __forceinline__ uint32_t code_word(float x, float inv) {
-    return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.0f + 128.0f));
-}
-__device__ __forceinline__ unsigned long long code_words(float x, float y, float inv) {
-    // (single products: the assembler joins a packed product and a packed addition into one rounding)
-    return add2(pk2(__fmul_rn(x, inv), __fmul_rn(y, inv)), pk2(12582912.0f + 128.0f, 12582912.0f + 128.0f));
-}
-// byte i of w, a code, as code - 128
-__device__ __forceinline__ float code_value(uint32_t w, int i) {
-    return __fadd_rn(__uint_as_float(prmt(w, 0x4b000000u, 0x7440u + i)), -8388736.0f);  // 2^23 + 128
-}
-
-struct Scales {
-    float scale, inv, ratio;
-    bool grew;
-};
-__device__ __forceinline__ Scales block_scale(float amax, float old, bool kept) {
-    Scales s;
-    s.scale = max_nan(old, amax < kKvTiny ? 0.0f : __fdiv_rn(amax, 127.0f));
-    if (!(s.scale <= 3.4028234e38f)) s.scale = __int_as_float(0x7fffffff);
-    const bool some = s.scale > 0.0f;
-    s.inv = some ? __fdiv_rn(1.0f, s.scale) : 0.0f;
-    s.ratio = some && kept ? __fdiv_rn(old, s.scale) : 0.0f;
-    s.grew = s.scale != old;
-    return s;
-}
-// four codes under a larger scale (a block without one holds zeros)
-__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
-    return pack4(code_word(code_value(w, 0), ratio), code_word(code_value(w, 1), ratio), code_word(code_value(w, 2), ratio),
-                 code_word(code_value(w, 3), ratio));
-}
+constexpr int kThreads = kKvThreads;
 
 // NB = D / 32.
 // CTAs per SM: the more, the more rows in flight and the shorter the last wave (prompts of 25k tokens, 8 heads of
@@ -73,9 +38,9 @@ __global__ void __launch_bounds__(kThreads, write_ctas(TYPE, NB)) kv8_write_kern
                                                              KvRows<const typename Elem<TYPE>::T> V,
                                                              int64_t n_tokens, const int32_t* cu, const int32_t* start,
                                                              int32_t* err) {
-    constexpr int D = NB * 32, kTurn = 36;  // bytes of a dim's 32 tokens in shared memory, padded
+    constexpr int D = NB * 32;
     __shared__ uint32_t red[2][4];
-    __shared__ __align__(16) uint8_t turn[D * kTurn];
+    __shared__ __align__(16) uint8_t turn[D * kKvTurn];
     const int h = blockIdx.x % c.n_kv, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
@@ -120,38 +85,11 @@ __global__ void __launch_bounds__(kThreads, write_ctas(TYPE, NB)) kv8_write_kern
     if (threadIdx.x == 0) *reinterpret_cast<float2*>(rec) = make_float2(sk.scale, sv.scale);
 
     // a block without a scale (zeros, or not finite) holds codes 128
-    const bool some_k = sk.inv > 0.0f, some_v = sv.inv > 0.0f;
+    const bool some_k = sk.inv > 0.0f;
     uint2* kr = reinterpret_cast<uint2*>(rec + kKvHead) + wid * NB * 32 + lane;
     uint8_t* vr = rec + kKvHead + kKvBlock * D;
-    if (kt < s.t0 && sk.grew) {  // kept tokens under the larger scale
-        uint2 q[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) q[n] = kr[n * 32];
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-            kr[n * 32] = some_k ? make_uint2(rescale4(q[n].x, sk.ratio), rescale4(q[n].y, sk.ratio)) : make_uint2(0x80808080u, 0x80808080u);
-    }
-    if (s.t0 > 0 && sv.grew) {
-        const int words = (s.t0 + 3) / 4;  // of a dim's 32 bytes: D words / 128 <= 2 NB a thread
-        uint32_t q[2 * NB];
-#pragma unroll
-        for (int n = 0; n < 2 * NB; ++n) {
-            const int i = n * kThreads + threadIdx.x, d = i / words;
-            if (d < D) q[n] = *(reinterpret_cast<const uint32_t*>(vr + d * 32) + i - d * words);
-        }
-#pragma unroll
-        for (int n = 0; n < 2 * NB; ++n) {
-            const int i = n * kThreads + threadIdx.x, d = i / words, x = i - d * words;
-            if (d >= D) continue;
-            uint32_t* at = reinterpret_cast<uint32_t*>(vr + d * 32) + x;
-            const uint32_t w = some_v ? rescale4(q[n], sv.ratio) : 0x80808080u;
-            if (4 * x + 4 <= s.t0) {
-                *at = w;
-            } else {  // the word's last bytes belong to new tokens
-                for (int e = 0; 4 * x + e < s.t0; ++e) reinterpret_cast<uint8_t*>(at)[e] = static_cast<uint8_t>(w >> (8 * e));
-            }
-        }
-    }
+    if (kt < s.t0 && sk.grew) rescale_keys<NB>(kr, sk);  // kept tokens under the larger scale
+    if (s.t0 > 0 && sv.grew) rescale_values<NB>(vr, s.t0, sv);
     if (kin) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -166,27 +104,7 @@ __global__ void __launch_bounds__(kThreads, write_ctas(TYPE, NB)) kv8_write_kern
             kr[n * 32] = q;
         }
     }
-    const bool whole = s.t0 == 0 && s.t1 == 32;
-    if (vin) {
-        auto put = [&](uint8_t* at, auto step) {
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const unsigned long long x = some_v ? code_words(v[n].get(2 * e), v[n].get(2 * e + 1), sv.inv) : (128ull << 32 | 128);
-                    at[(n * 32 + 2 * e) * step.value] = static_cast<uint8_t>(lo2(x));
-                    at[(n * 32 + 2 * e + 1) * step.value] = static_cast<uint8_t>(hi2(x));
-                }
-        };
-        if (whole) put(turn + (lane & 3) * 8 * kTurn + vt, std::integral_constant<int, kTurn>{});
-        else put(vr + (lane & 3) * 8 * 32 + vt, std::integral_constant<int, 32>{});  // part of a block: single bytes
-    }
-    if (!whole) return;
-    __syncthreads();
-    for (int i = threadIdx.x; i < D * 2; i += kThreads) {  // 16 tokens of a dim
-        const uint32_t* at = reinterpret_cast<const uint32_t*>(turn + (i >> 1) * kTurn + (i & 1) * 16);
-        reinterpret_cast<uint4*>(vr)[i] = make_uint4(at[0], at[1], at[2], at[3]);
-    }
+    write_values<TYPE, NB>(vr, turn, v, vt, vin, s.t0 == 0 && s.t1 == 32, sv);
 }
 
 template <int TYPE>

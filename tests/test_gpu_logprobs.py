@@ -1,0 +1,149 @@
+"""Log probabilities of given tokens, the most likely tokens, entropy and log-sum-exp (moe_token_logprobs) against the formulas
+in 64 bits. Tolerances count fp32 roundings (decode_ref.logprobs says which); token ids have to be equal."""
+import numpy as np
+import pytest
+import torch
+
+import decode_ref as R
+import kv8_ref as K
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import quantized_routed_expert_grouped_gb300 as mod
+    mod.lib()
+    return mod
+
+
+def check(m, x, ids, top, scale=1.0):
+    """x: device logits; ids: numpy [R, n]."""
+    got = m.token_logprobs(x, torch.from_numpy(ids.astype(np.int32)).cuda(), top=top, scale=scale)
+    lp, tl, ti, ent, lse = (None if t is None else t.cpu().numpy() for t in got)
+    x64 = x.double().cpu().numpy()
+    s = float(np.float32(scale))
+    elp, etl, eti, eent, else_, off, eoff = R.logprobs(x64, ids, top, s, 4096)
+    if top:
+        assert np.array_equal(ti, eti)
+    ulp = R.ULP
+
+    def near(a, e, bound):
+        some = ~np.isneginf(e)
+        assert np.array_equal(np.isneginf(a), ~some)
+        err, most = np.abs(a - np.where(some, e, 0))[some], np.broadcast_to(bound, e.shape)[some]
+        assert (err <= most).all(), float((err / most).max())
+
+    m_ = x64.max(1)
+    m_ = np.where(np.isneginf(m_), 0, m_)
+    ls = np.abs(np.where(np.isneginf(else_), 0, else_ - s * m_))
+    # the difference, its product, the logarithm's own error and rounding (2), the last difference
+    for a, e in ((lp, elp), (tl, etl)):
+        if a is not None and a.size:
+            near(a, e, off[:, None] + ulp * (3 * np.abs(np.where(np.isneginf(e), 0, e)) + 6 * ls[:, None] + 2))
+    near(ent, eent, eoff + ulp * (4 * np.abs(eent) + 4 * ls + 2))
+    near(lse, else_, off + ulp * (4 * ls + 2 * s * np.abs(m_) + 2))
+
+
+def ids_for(rng, R, V, n):
+    ids = rng.integers(0, V, (R, n))
+    ids[rng.random((R, n)) < 0.2] = -1
+    if R > 1:
+        ids[1, 0] = V  # past the end
+        ids[0, 0] = V - 1
+    return ids
+
+
+SIZES = [(1, 1), (3, 2), (2, 5), (5, 31), (4, 33), (3, 257), (2, 1000), (3, 4097), (2, 8191), (2, 8192), (3, 8193), (2, 16400), (5, 50001), (1, 131075),
+         (40, 40000), (330, 9001), (700, 2500)]
+
+
+@pytest.mark.parametrize("dtype", list(K.TYPES))
+@pytest.mark.parametrize("size", range(len(SIZES)))
+def test_random(m, size, dtype):
+    R_, V = SIZES[size]
+    rng = np.random.default_rng(size)
+    pad = [0, 1, 3, 8][size % 4]
+    x = (2.5 * rng.standard_normal((R_, V + pad))).astype(np.float32)
+    x[:, rng.integers(0, V)] += 8
+    if size % 3 == 1:
+        x[rng.random(x.shape) < 0.9] = -np.inf
+    dev = torch.from_numpy(x).to(K.TYPES[dtype]).cuda()[:, :V]
+    for top, n, scale in ((min(V, 20), 2, 1.0), (0, 1, 0.5), (min(V, 32), 1, 1 / 0.7), (1, 3, 1.0)):
+        check(m, dev, ids_for(rng, R_, V, n), top, scale)
+        if R_ * V > 1 << 20:
+            break
+
+
+@pytest.mark.parametrize("dtype", list(K.TYPES))
+@pytest.mark.parametrize("V", [7, 260, 9000, 70001])
+def test_hard_rows(m, V, dtype):
+    """Rows whose order, masks or ties are hard on a selection: each by the same rules."""
+    t = K.TYPES[dtype]
+    low = torch.finfo(t).min
+    rng = np.random.default_rng(V)
+    i = np.arange(V)
+    few = np.full(V, -np.inf)
+    few[rng.integers(0, V, 3)] = 1.0
+    lowest = np.full(V, low)
+    lowest[[0, V // 2, V - 1]] = [1.0, 2.0, 1.0]
+    zeros = np.where(rng.random(V) < 0.5, -0.0, 0.0)
+    mixed = np.where(i % 3 == 0, -np.inf, low)
+    rows = [np.full(V, -np.inf), np.full(V, 3.0), np.full(V, low), i * 10.0 / V, -i * 10.0 / V, few, lowest, zeros, mixed, np.round(rng.standard_normal(V)),
+            np.where(i == V - 1, 0.0, -np.inf), np.where(i < V // 2, -np.inf, 5.0 * i / V), np.where(i % 8 == 7, 4.0, -4.0)]
+    x = torch.from_numpy(np.stack(rows).astype(np.float64)).to(t).cuda()
+    for top in (1, 5, min(V, 32)):
+        check(m, x, ids_for(rng, len(rows), V, 2), top)
+    # one row alone: by a cluster
+    for r in range(len(rows)):
+        check(m, x[r:r + 1], ids_for(rng, 1, V, 1), min(V, 32))
+
+
+@pytest.mark.parametrize("V", [40, 70001])
+def test_not_finite(m, V):
+    """A NaN or +inf makes a row's numbers NaN, but leaves the other rows and the order of what is a number."""
+    x = torch.zeros((4, V), device="cuda")
+    x += torch.arange(V, device="cuda") % 7
+    x[1, 3] = float("nan")
+    x[2, 5] = float("inf")
+    x[3] = float("nan")
+    ids = torch.tensor([[1], [-1], [2], [0]], dtype=torch.int32, device="cuda")
+    lp, tl, ti, ent, lse = m.token_logprobs(x, ids, top=3)
+    assert torch.isfinite(lp[0]).all() and torch.isfinite(tl[0]).all() and torch.isfinite(ent[0]) and torch.isfinite(lse[0])
+    for r in (1, 2, 3):
+        assert torch.isnan(tl[r]).all() and torch.isnan(ent[r]) and torch.isnan(lse[r])
+    assert float(lp[1]) == float("-inf") and torch.isnan(lp[2:]).all()
+    assert ti.tolist() == [[6, 13, 20], [6, 13, 20], [5, 6, 13], [-1, -1, -1]]
+
+
+def test_many_ids_and_none(m):
+    rng = np.random.default_rng(3)
+    x = torch.from_numpy(rng.standard_normal((3, 901)).astype(np.float32)).cuda()
+    check(m, x, ids_for(rng, 3, 901, 700), 4)
+    a = m.token_logprobs(x)
+    b = m.token_logprobs(x, top=4)
+    assert a[0] is None and a[1] is None and a[2] is None and torch.equal(a[3], b[3]) and torch.equal(a[4], b[4])
+    none = m.token_logprobs(x[:0], torch.zeros((0, 2), dtype=torch.int32, device="cuda"), top=2)
+    assert [tuple(t.shape) for t in none] == [(0, 2), (0, 2), (0, 2), (0,), (0,)]
+
+
+def test_same_bits(m):
+    """Calls, streams and captured graphs give the same bits (the order of appended keys does not count)."""
+    rng = np.random.default_rng(5)
+    x = torch.from_numpy(np.round(4 * rng.standard_normal((6, 60000))).astype(np.float32)).cuda()
+    ids = torch.from_numpy(rng.integers(0, 60000, (6, 2)).astype(np.int32)).cuda()
+    want = m.token_logprobs(x, ids, top=32)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    runs = [m.token_logprobs(x, ids, top=32) for _ in range(20)] + [m.token_logprobs(x, ids, top=32, stream=s)]
+    s.synchronize()
+    buf = torch.zeros_like(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        runs.append(m.token_logprobs(buf, ids, top=32))
+    buf.copy_(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    for got in runs:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
