@@ -22,17 +22,24 @@
 
 #include "decode_api.h"
 
+#ifndef SMALLV
+#define SMALLV 256
+#endif
+#ifndef MINB
+#define MINB 4
+#endif
 namespace moe {
 
 namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256, kUnroll = 4, kTile = kThreads * kUnroll;  // vectors of a tile
+constexpr int kUnroll = 4;  // vectors of a thread's tile
+#ifndef SPAN
+#define SPAN 2
+#endif
+constexpr int span_of(int NT) { return NT == 32 ? 1 : SPAN; }  // tiles between two looks for the best keys
 constexpr int kTop = 32, kMaxCluster = 8;
-constexpr int kGroups = kThreads / 2;
-constexpr int kHot = 64;  // threads whose keys a list takes at once
-constexpr int kCap = kTop + kHot * (kUnroll * 8 + 1);
 constexpr float kFar = -1000.0f;  // an exponent whose power of two is 0
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
@@ -53,21 +60,30 @@ __device__ __forceinline__ unsigned long long key_of(float x, uint32_t index) {
     return o ? static_cast<unsigned long long>(o) << 32 | ~index : 0ull;
 }
 
-// Sums of e^t and t e^t (in base 2) next to a maximum.
+// Sums of 2^t and t 2^t, t = c x - r, next to a whole number r; and the largest x.
 struct Stats {
-    float m, s, u;
-    __device__ __forceinline__ void move(float m1, float c) {  // m1 >= m
-        const float d = fmaxf((m - (m1 == -INFINITY ? 0.0f : m1)) * c, kFar), f = ex2(d);
+    float r, s, u, m;
+    __device__ __forceinline__ void move(float to) {  // to >= r, and above -inf
+        const float d = fmaxf(r - to, kFar), f = ex2(d);
         u = fmaf(s, d, u) * f;
         s *= f;
-        m = m1;
+        r = to;
     }
-    __device__ __forceinline__ void join(Stats o, float c) {
-        const float m1 = fmaxf(m, o.m);
-        move(m1, c);
-        o.move(m1, c);
-        s += o.s;
-        u += o.u;
+    // of N lanes, the sums in lane 0
+    template <int N>
+    __device__ __forceinline__ void join() {
+        float to = r;
+#pragma unroll
+        for (int o = N / 2; o > 0; o >>= 1) {
+            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        if (to > -INFINITY) move(to);
+#pragma unroll
+        for (int o = N / 2; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            u += __shfl_xor_sync(0xffffffffu, u, o);
+        }
     }
 };
 
@@ -86,16 +102,51 @@ __device__ __forceinline__ float max_of(const RawVec<TYPE>& v, float mx) {  // (
     }
 }
 
+// A value far below any logit next to which it matters, and logits below it moved there (a NaN stays).
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const LogprobArgs a) {
+constexpr float kLow = TYPE == MOE_F16 ? -65504.0f : -1.329227995784916e36f;  // -2^120
+template <int TYPE>
+__device__ __forceinline__ void clamp_low(RawVec<TYPE>& v) {
+    if constexpr (TYPE != MOE_F32) {
+        using H = typename std::conditional<TYPE == MOE_F16, __half2, __nv_bfloat162>::type;
+        const uint32_t low = TYPE == MOE_F16 ? 0xfbfffbffu : 0xfb80fb80u;
+        H* h = reinterpret_cast<H*>(v.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __hmax2_nan(h[i], *reinterpret_cast<const H*>(&low));
+    }
+}
+
+// Keys in descending order over the lanes.
+__device__ __forceinline__ unsigned long long other_key(unsigned long long k, int o, bool more) {
+    const unsigned long long y = __shfl_xor_sync(0xffffffffu, k, o);
+    return (k > y) == more ? k : y;
+}
+__device__ __forceinline__ unsigned long long sorted_keys(unsigned long long k, int lane) {
+#pragma unroll 1
+    for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll 1
+        for (int o = n >> 1; o > 0; o >>= 1) k = other_key(k, o, !(lane & o) == !(lane & n));
+    return k;
+}
+// The 32 largest of two such lists (y's from the end).
+__device__ __forceinline__ unsigned long long merged_keys(unsigned long long k, unsigned long long y, int lane) {
+    k = k > y ? k : y;
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) k = other_key(k, o, !(lane & o));
+    return k;
+}
+
+template <int TYPE, int NT>
+__global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kernel(const LogprobArgs a) {
     using Raw = RawVec<TYPE>;
     using T = typename Elem<TYPE>::T;
-    constexpr int W = Raw::W;
+    constexpr int W = Raw::W, kTile = NT * kUnroll, kSpan = span_of(NT);  // vectors of a tile; tiles of a span
+    constexpr int kHot = NT < 64 ? NT : 64, kCap = kTop + kHot * (kSpan * kUnroll * W + 1);  // threads that append keys between two rankings, at most
     constexpr uint32_t kNone = TYPE == MOE_F32 ? 0xff800000u : TYPE == MOE_F16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf
-    __shared__ unsigned long long list[kCap];                // the best keys in order, then new ones
-    __shared__ __align__(16) unsigned long long work[kMaxCluster * kTop];
-    __shared__ unsigned long long bar;                       // a raised bar
-    __shared__ Stats stat[kThreads / 32 + 1];
+    __shared__ unsigned long long list[kCap];  // the best keys in order, then new ones
+    __shared__ __align__(16) unsigned long long work[NT];  // (NT = kMaxCluster * kTop where there are clusters)
+    __shared__ unsigned long long bar;  // a raised bar
+    __shared__ Stats stat[NT / 32 + 1];  // of the warps, of the CTA
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 31;
     const int C = a.cluster, rank = blockIdx.x % C, row = blockIdx.x / C;
@@ -115,161 +166,278 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const Logpr
     const int nv = (a.V - head) / W, tail = a.V - head - nv * W;
     const int v0 = static_cast<int>(static_cast<int64_t>(nv) * rank / C), v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / C);
     const T* xv = x + head;
-    Raw next[kUnroll];
-    auto load = [&](int at) {
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int v = at + i * kThreads + tid;
-            if (v < v1) {
-                next[i].load(xv + static_cast<int64_t>(v) * W, true);
-            } else {
-                next[i].w[0] = next[i].w[1] = next[i].w[2] = next[i].w[3] = kNone;
-            }
+    Stats st{-INFINITY, 0.0f, 0.0f, -INFINITY};
+    unsigned long long best = 0;  // the list's last key, 0 while it is not full
+    int pending = 0;              // threads that have appended since the list was in order
+    // the list in order again (count of its keys are valid and visible)
+    auto ranked = [&]() {
+        const int n = count, keep = min(n, a.top);
+        for (int i = tid; i < n; i += NT) {
+            const unsigned long long mine = list[i];
+            int above = 0;
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) above += list[j] > mine;
+            if (above < a.top) work[above] = mine;
         }
+        __syncthreads();
+        if (tid < keep) list[tid] = work[tid];
+        if (tid == 0) count = keep;
+        best = n >= a.top ? work[a.top - 1] : 0;
+        pending = 0;
+        __syncthreads();
     };
-    load(v0);
-    Stats st{-INFINITY, 0.0f, 0.0f};
-    unsigned long long best = 0;  // the bar: the list's last key, 0 while it is not full
     int at = v0;
-    do {
-        Raw cur[kUnroll];
+    Raw raw[kUnroll];  // the next tile
+    auto load = [&](int i, int from, bool whole) {
+        const int v = from + i * NT + tid;
+        if (whole || v < v1) raw[i].load(xv + static_cast<int64_t>(v) * W, true);
+        else raw[i].w[0] = raw[i].w[1] = raw[i].w[2] = raw[i].w[3] = kNone;
+    };
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) cur[i] = next[i];
-        // singles: of the row's start thread 0 .., of its end thread 32 ..
+    for (int i = 0; i < kUnroll; ++i) load(i, at, false);
+    do {
+        // singles: of the row's start threads 0 .., of its end threads 8 ..
         int single = -1;
         if (rank == 0 && at == v0 && tid < head) single = tid;
-        if (rank == C - 1 && at + kTile >= v1 && tid >= 32 && tid < 32 + tail) single = head + nv * W + tid - 32;
+        if (rank == C - 1 && at + kSpan * kTile >= v1 && tid >= 8 && tid < 8 + tail) single = head + nv * W + tid - 8;
         const float alone = single >= 0 ? Elem<TYPE>::get(gload(x + single)) : -INFINITY;
-        load(at + kTile);
-        // ---- statistics
-        float mx = alone == alone ? alone : -INFINITY;
+        float most = alone == alone ? alone : -INFINITY;  // of the span
+#pragma unroll 1
+        for (int from = at; from < min(at + kSpan * kTile, v1); from += kTile) {
+            float mx = max_of<TYPE>(raw[0], -INFINITY);
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) mx = max_of<TYPE>(cur[i], mx);
-        if (mx > st.m) st.move(mx, a.c);
-        const float mr = st.m == -INFINITY ? 0.0f : st.m;
-        const unsigned long long mm = pk2(-mr, -mr), cc = pk2(a.c, a.c);
-        unsigned long long s2 = 0, u2 = 0;
+            for (int i = 1; i < kUnroll; ++i) mx = max_of<TYPE>(raw[i], mx);
+            most = fmaxf(most, mx);
+            const float to = ceilf(mx * a.c);
+            if (to > st.r) st.move(to);
+            const float r = st.r == -INFINITY ? 0.0f : st.r;
+            const unsigned long long rr = pk2(-r, -r), cc = pk2(a.c, a.c);
+            unsigned long long s2 = 0, u2 = 0;
+            // t 2^t of a logit of -inf is 0: it is clamped, in pairs before the conversion where that can be (the clamped logit's power is 0
+            // and its t finite), else t by t
+            const float room = fmaf(-kLow<TYPE>, a.c, r);
+            const bool whole = from + 2 * kTile <= v1;
+            if (TYPE != MOE_F32 && room > 200.0f && room < 1e38f) {
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
+                for (int i = 0; i < kUnroll; ++i) {
+                    clamp_low<TYPE>(raw[i]);
 #pragma unroll
-            for (int e = 0; e < W / 2; ++e) {
-                const float2 t = up2(mul2(add2(pk2(cur[i].get(2 * e), cur[i].get(2 * e + 1)), mm), cc));
-                const unsigned long long p = pk2(ex2(t.x), ex2(t.y));
-                s2 = add2(s2, p);
-                u2 = fma2(p, pk2(fmaxf(t.x, kFar), fmaxf(t.y, kFar)), u2);
+                    for (int e = 0; e < W / 2; ++e) {
+                        const unsigned long long t = fma2(pk2(raw[i].get(2 * e), raw[i].get(2 * e + 1)), cc, rr);
+                        const float2 f = up2(t);
+                        const unsigned long long p = pk2(ex2(f.x), ex2(f.y));
+                        s2 = add2(s2, p);
+                        u2 = fma2(p, t, u2);
+                    }
+                    load(i, from + kTile, whole);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) {
+#pragma unroll
+                    for (int e = 0; e < W / 2; ++e) {
+                        const float2 t = up2(fma2(pk2(raw[i].get(2 * e), raw[i].get(2 * e + 1)), cc, rr));
+                        const unsigned long long p = pk2(ex2(t.x), ex2(t.y));
+                        s2 = add2(s2, p);
+                        u2 = fma2(p, pk2(fmaxf(t.x, kFar), fmaxf(t.y, kFar)), u2);
+                    }
+                    load(i, from + kTile, whole);
+                }
             }
-        const float2 sf = up2(s2), uf = up2(u2);
-        st.s += sf.x + sf.y;
-        st.u += uf.x + uf.y;
+            const float2 sf = up2(s2), uf = up2(u2);
+            st.s += sf.x + sf.y;
+            st.u += uf.x + uf.y;
+        }
+        st.m = fmaxf(st.m, most);
         if (single >= 0) {
-            const float t = (alone - mr) * a.c, p = ex2(t);
+            const float to = ceilf(alone * a.c);
+            if (to > st.r) st.move(to);
+            const float t = fmaf(alone, a.c, st.r == -INFINITY ? 0.0f : -st.r), p = ex2(t);
             st.s += p;
             st.u = fmaf(p, fmaxf(t, kFar), st.u);
         }
         // ---- the best keys
         if (a.top) {
-            const bool hot = order(mx) > static_cast<uint32_t>(best >> 32);
+            const uint32_t mine = at + tid < v1 || single >= 0 ? order(most) : 0;  // (0: nothing, or NaN alone)
+            bool hot = mine > static_cast<uint32_t>(best >> 32);
             const int n_hot = __syncthreads_count(hot);
             if (n_hot) {
+                // f(logit, index) for the tile's logits of this thread, read again
                 auto each = [&](auto f) {
-                    if (!hot) return;
-                    if (single >= 0) f(key_of(alone, static_cast<uint32_t>(single)));
+                    if (single >= 0) f(alone, static_cast<uint32_t>(single));
+#pragma unroll 1
+                    for (int v = at + tid; v < min(at + kSpan * kTile, v1); v += NT) {
+                        Raw r;
+                        r.load(xv + static_cast<int64_t>(v) * W, true);
 #pragma unroll
-                    for (int i = 0; i < kUnroll; ++i) {
-                        const int v = at + i * kThreads + tid;
-                        if (v >= v1) continue;
-#pragma unroll
-                        for (int e = 0; e < W; ++e) f(key_of(cur[i].get(e), static_cast<uint32_t>(head + v * W + e)));
+                        for (int e = 0; e < W; ++e) f(r.get(e), static_cast<uint32_t>(head + v * W + e));
                     }
                 };
-                unsigned long long least = best + 1;
-                if (n_hot > kHot) {
-                    unsigned long long k = 0;
-                    each([&](unsigned long long y) { k = y > k ? y : k; });
-                    const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, 1);
-                    if (!(tid & 1)) work[tid >> 1] = k > o ? k : o;
-                    if (tid == 0) bar = 0;
-                    __syncthreads();
-                    if (tid < kGroups) {
-                        const unsigned long long mine = work[tid];
-                        int above = 0;
-#pragma unroll 16
-                        for (int j = 0; j < kGroups; ++j) above += work[j] > mine;
-                        if (above == a.top - 1 && mine) bar = mine;
+                // the hot threads' keys of at least `low`, and of values of at least `least`: a warp takes its hot threads one by one, a
+                // word of the thread's tile a lane
+                auto append = [&](bool hot, float least, unsigned long long low) {
+                    auto put = [&](float y, uint32_t index) {
+                        if (y >= least) {
+                            const unsigned long long k = key_of(y, index);
+                            if (k >= low) list[atomicAdd(&count, 1)] = k;
+                        }
+                    };
+                    if (hot && single >= 0) put(alone, static_cast<uint32_t>(single));
+                    for (unsigned who = __ballot_sync(0xffffffffu, hot); who; who &= who - 1) {
+                        constexpr int kWords = kSpan * kUnroll * 4, kEach = (kWords + 31) / 32;
+                        const int v = at + (lane >> 2) * NT + (tid & ~31) + __ffs(who) - 1;
+                        uint32_t w[kEach];
+#pragma unroll
+                        for (int i = 0; i < kEach; ++i)
+                            if (i * 32 + lane < kWords && v + i * 8 * NT < v1)
+                                w[i] = gload(reinterpret_cast<const uint32_t*>(xv + static_cast<int64_t>(v + i * 8 * NT) * W) + (lane & 3));
+#pragma unroll
+                        for (int i = 0; i < kEach; ++i) {
+                            if (i * 32 + lane >= kWords || v + i * 8 * NT >= v1) continue;
+                            const uint32_t index = head + (v + i * 8 * NT) * W + (lane & 3) * (W / 4);
+                            if (TYPE == MOE_F32) {
+                                put(__uint_as_float(w[i]), index);
+                            } else {
+                                Raw r;
+                                r.w[0] = w[i];
+                                put(r.get(0), index);
+                                put(r.get(1), index + 1);
+                            }
+                        }
+                    }
+                };
+                if (best && n_hot <= kHot) {
+                    if (pending + n_hot > kHot) {
+                        ranked();
+                        hot = mine > static_cast<uint32_t>(best >> 32);
+                    }
+                    append(hot, unorder(static_cast<uint32_t>(best >> 32) + 1), 0);
+                    pending += n_hot;
+                } else {
+                    if (pending) ranked();
+                    // a bar: a maximum that `top` threads reach, as many in each warp
+                    constexpr int kWarps = NT / 32;
+                    bool few = kWarps > 1;
+                    if (kWarps > 1) {
+                        uint32_t m = mine, r = 0;
+                        for (int i = 0; i < a.top; i += kWarps) {
+                            r = __reduce_max_sync(0xffffffffu, m);
+                            if (m == r) m = 0;
+                        }
+                        uint32_t* low32 = reinterpret_cast<uint32_t*>(work);
+                        if (lane == 0) low32[tid >> 5] = r;
+                        __syncthreads();
+                        uint32_t least = low32[0];
+#pragma unroll
+                        for (int w = 1; w < kWarps; ++w) least = min(least, low32[w]);
+                        least = max(least, order(-INFINITY));  // (0: fewer threads than that have any)
+                        hot = mine >= least;
+                        few = __syncthreads_count(hot) <= kHot;
+                        if (few) append(hot, unorder(least), 0);
+                    }
+                    if (!few) {  // ties: the top-th best of the threads' best keys
+                        unsigned long long mine_key = 0;
+                        if (mine) each([&](float y, uint32_t index) {
+                            const unsigned long long z = key_of(y, index);
+                            mine_key = z > mine_key ? z : mine_key;
+                        });
+                        unsigned long long k = sorted_keys(mine_key, lane);
+#pragma unroll 1
+                        for (int half = kWarps / 2; half > 0; half >>= 1) {
+                            if ((tid >> 5) >= half && (tid >> 5) < 2 * half) work[tid - 32 * half] = k;
+                            __syncthreads();
+                            if ((tid >> 5) < half) k = merged_keys(k, work[tid ^ 31], lane);
+                            __syncthreads();
+                        }
+                        if (tid == a.top - 1) bar = k;  // (0: fewer threads than that have any)
+                        __syncthreads();
+                        append(mine_key && mine_key >= bar, -INFINITY, bar);
                     }
                     __syncthreads();
-                    least = bar > least ? bar : least;
+                    ranked();
                 }
-                each([&](unsigned long long y) {
-                    if (y >= least) list[atomicAdd(&count, 1)] = y;
-                });
-                __syncthreads();
-                const int n = count, keep = min(n, a.top);
-                for (int i = tid; i < n; i += kThreads) {
-                    const unsigned long long mine = list[i];
-                    int above = 0;
-#pragma unroll 4
-                    for (int j = 0; j < n; ++j) above += list[j] > mine;
-                    if (above < a.top) work[above] = mine;
-                }
-                __syncthreads();
-                if (tid < keep) list[tid] = work[tid];
-                if (tid == 0) count = keep;
-                best = n >= a.top ? work[a.top - 1] : 0;
-                __syncthreads();
             }
         }
-        at += kTile;
+        at += kSpan * kTile;
     } while (at < v1);
-
-    // ---- the CTA's, then the row's
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stats y;
-        y.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-        y.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-        y.u = __shfl_xor_sync(0xffffffffu, st.u, o);
-        // (the lower lane's first in both lanes, so that they agree)
-        if (lane & o) {
-            const Stats z = st;
-            st = y;
-            y = z;
-        }
-        st.join(y, a.c);
+    if (pending) {
+        __syncthreads();
+        ranked();
     }
-    if (lane == 0) stat[tid >> 5] = st;
-    __syncthreads();
-    st = stat[0];
-    for (int w = 1; w < kThreads / 32; ++w) st.join(stat[w], a.c);
-    if (C > 1) {
-        cg::cluster_group cluster = cg::this_cluster();
-        if (tid == 0) stat[kThreads / 32] = st;
-        cluster.sync();
-        if (rank == 0) {
-            const int from = tid / kTop, i = tid % kTop;  // (kMaxCluster * kTop threads)
-            unsigned long long mine = 0;
-            if (a.top && from < C && i < *cluster.map_shared_rank(&count, from)) mine = cluster.map_shared_rank(list, from)[i];
-            work[tid] = mine;
-            for (int r = 1; r < C; ++r) st.join(*cluster.map_shared_rank(stat + kThreads / 32, r), a.c);
+
+    // ---- the CTA's sums, then the row's
+    auto join = [&]() {
+        st.template join<32>();
+        if (NT > 32) {
+            if (lane == 0) stat[tid >> 5] = st;
             __syncthreads();
-            if (a.top) {
-                int above = 0, some = __syncthreads_count(mine != 0);
-#pragma unroll 16
-                for (int j = 0; j < C * kTop; ++j) above += work[j] > mine;
-                if (mine && above < a.top) list[above] = mine;
-                if (tid == 0) count = min(some, a.top);
-                __syncthreads();
+            if (tid < 32) {
+                st = stat[lane & (NT / 32 - 1)];
+                st.template join<NT / 32>();
             }
+        }
+        if (C > 1) {
+            cg::cluster_group cluster = cg::this_cluster();
+            if (tid == 0) stat[NT / 32] = st;
+            cluster.sync();
+            if (tid < 32) {
+                st = Stats{-INFINITY, 0.0f, 0.0f, -INFINITY};
+                if (lane < C) st = *cluster.map_shared_rank(stat + NT / 32, lane);
+                st.template join<kMaxCluster>();
+            }
+            cluster.sync();
+        }
+        if (tid == 0) stat[NT / 32] = st;
+        __syncthreads();
+        st = stat[NT / 32];
+    };
+    join();
+    // Where c times the row's largest logit is no number to subtract (a row that is masked by its type's lowest value): once more,
+    // with differences first.
+    const bool ends = fabsf(st.m) < INFINITY && !(fabsf(st.m * a.c) < 1.2676506e30f);
+    if (ends) {
+        const float m = st.m;
+        st = Stats{0.0f, 0.0f, 0.0f, m};
+        auto one = [&](float y) {
+            const float t = (y - m) * a.c, p = ex2(t);
+            st.s += p;
+            st.u = fmaf(p, fmaxf(t, kFar), st.u);
+        };
+        for (int v = v0 + tid; v < v1; v += NT) {
+            Raw y;
+            y.load(xv + static_cast<int64_t>(v) * W, true);
+#pragma unroll
+            for (int e = 0; e < W; ++e) one(y.get(e));
+        }
+        if (rank == 0 && tid < head) one(Elem<TYPE>::get(gload(x + tid)));
+        if (rank == C - 1 && tid < tail) one(Elem<TYPE>::get(gload(x + head + nv * W + tid)));
+        __syncthreads();
+        join();
+    }
+    if (C > 1 && a.top) {  // the row's best keys
+        cg::cluster_group cluster = cg::this_cluster();
+        if (rank == 0) {
+            const int from = tid / kTop, i = tid % kTop;  // (NT = kMaxCluster * kTop threads)
+            unsigned long long mine = 0;
+            if (from < C && i < a.top && i < *cluster.map_shared_rank(&count, from)) mine = cluster.map_shared_rank(list, from)[i];
+            if (from < C && i < a.top) work[from * a.top + i] = mine;
+            const int some = __syncthreads_count(mine != 0);
+            int above = 0;
+#pragma unroll 8
+            for (int j = 0; j < C * a.top; ++j) above += work[j] > mine;
+            if (mine && above < a.top) list[above] = mine;
+            if (tid == 0) count = min(some, a.top);
+            __syncthreads();
         }
         cluster.sync();
     }
     if (rank != 0) return;
     const bool none = st.s == 0.0f;
-    const float ls = logf(st.s);
+    const float l2 = log2f(st.s), ls = (l2 - (ends ? 0.0f : fmaf(st.m, a.c, -st.r))) * kLn2;  // log of the sum of e^(scale (x - m))
     auto logprob = [&](float v) { return none ? -INFINITY : (v - st.m) * a.scale - ls; };
-    for (int i = tid; i < a.n_ids; i += kThreads) {
+    for (int i = tid; i < a.n_ids; i += NT) {
         const int64_t to = static_cast<int64_t>(row) * a.n_ids + i;
-        if (i >= kThreads) {
+        if (i >= NT) {
             id = gload(a.ids + to);
             if (id >= 0 && id < a.V) given = Elem<TYPE>::get(gload(x + id));
         }
@@ -283,21 +451,22 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const Logpr
         a.top_logprobs[to] = has ? logprob(unorder(static_cast<uint32_t>(k >> 32))) : NAN;
     }
     if (tid == 0) {
-        if (a.entropy) a.entropy[row] = none ? 0.0f : ls - st.u * kLn2 / st.s;
+        if (a.entropy) a.entropy[row] = none ? 0.0f : (l2 - st.u / st.s) * kLn2;
         if (a.lse) a.lse[row] = none ? -INFINITY : fmaf(st.m, a.scale, ls);
     }
 }
 
 template <int TYPE>
 cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
-    constexpr int W = RawVec<TYPE>::W;
+    constexpr int W = RawVec<TYPE>::W, kTile = 256 * kUnroll;
     // CTAs of a row: until every SM has two, and while each still has a whole tile
     a.cluster = 1;
     while (a.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * a.cluster < 304 && a.V / W / a.cluster > kTile) a.cluster *= 2;
     a.c = a.scale * kLog2e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.cluster);
-    cfg.blockDim = dim3(kThreads);
+    const bool small = a.V / W <= SMALLV;
+    cfg.blockDim = dim3(small ? 32 : 256);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -307,7 +476,7 @@ cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE>, a);
+    return small ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 32>, a) : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 256>, a);
 }
 
 }  // namespace
