@@ -35,12 +35,10 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kUnroll = 4;  // vectors of a thread's tile
-#ifndef SPAN
-#define SPAN 2
-#endif
-constexpr int span_of(int NT) { return NT == 32 ? 1 : SPAN; }  // tiles between two looks for the best keys
+constexpr int kSpan = 2;    // tiles between two looks for the best keys: one is added while the next is on its way
 constexpr int kTop = 32, kMaxCluster = 8;
 constexpr float kFar = -1000.0f;  // an exponent whose power of two is 0
+constexpr float kSlack = 8.0f;    // powers of two above its reference that a thread's maximum may rise
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -60,7 +58,8 @@ __device__ __forceinline__ unsigned long long key_of(float x, uint32_t index) {
     return o ? static_cast<unsigned long long>(o) << 32 | ~index : 0ull;
 }
 
-// Sums of 2^t and t 2^t, t = c x - r, next to a whole number r; and the largest x.
+// Sums of 2^t and t 2^t, t = c x - r, next to a whole number r (at most kSlack below
+// the largest c x); and the largest x.
 struct Stats {
     float r, s, u, m;
     __device__ __forceinline__ void move(float to) {  // to >= r, and above -inf
@@ -87,18 +86,23 @@ struct Stats {
     }
 };
 
+// The largest of a thread's tile. (A NaN does not count.)
 template <int TYPE>
-__device__ __forceinline__ float max_of(const RawVec<TYPE>& v, float mx) {  // (a NaN does not count)
+__device__ __forceinline__ float max_of(const RawVec<TYPE> (&v)[kUnroll]) {
     if constexpr (TYPE == MOE_F32) {
+        float mx = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, v.get(e));
+        for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, v[i].get(e));
         return mx;
     } else {
         using H = typename std::conditional<TYPE == MOE_F16, __half2, __nv_bfloat162>::type;
-        const H* h = reinterpret_cast<const H*>(v.w);
-        const H a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        H a = *reinterpret_cast<const H*>(v[0].w);
+#pragma unroll
+        for (int i = 1; i < 4 * kUnroll; ++i) a = __hmax2(a, *reinterpret_cast<const H*>(&v[i >> 2].w[i & 3]));
         const float2 f = TYPE == MOE_F16 ? __half22float2(*reinterpret_cast<const __half2*>(&a)) : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&a));
-        return fmaxf(mx, fmaxf(f.x, f.y));
+        return fmaxf(fmaxf(f.x, f.y), -INFINITY);
     }
 }
 
@@ -140,17 +144,19 @@ template <int TYPE, int NT>
 __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kernel(const LogprobArgs a) {
     using Raw = RawVec<TYPE>;
     using T = typename Elem<TYPE>::T;
-    constexpr int W = Raw::W, kTile = NT * kUnroll, kSpan = span_of(NT);  // vectors of a tile; tiles of a span
-    constexpr int kHot = NT < 64 ? NT : 64, kCap = kTop + kHot * (kSpan * kUnroll * W + 1);  // threads that append keys between two rankings, at most
+    constexpr int W = Raw::W, kTile = NT * kUnroll;  // vectors of a tile
+    constexpr int kHot = NT == 32 ? 32 : 64, kCap = kTop + kHot * (kSpan * kUnroll * W + 1);  // threads' spans to be looked through at once, and their keys
     constexpr uint32_t kNone = TYPE == MOE_F32 ? 0xff800000u : TYPE == MOE_F16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf
     __shared__ unsigned long long list[kCap];  // the best keys in order, then new ones
-    __shared__ __align__(16) unsigned long long work[NT];  // (NT = kMaxCluster * kTop where there are clusters)
+    __shared__ __align__(16) unsigned long long work[NT == 32 ? kHot + kTop : NT];  // (NT = kMaxCluster * kTop where there are clusters)
     __shared__ unsigned long long bar;  // a raised bar
+    __shared__ uint32_t hot_max[kHot];  // spans of threads with logits above the bar: their maxima and first vectors
+    __shared__ int hot_at[kHot], hots;
     __shared__ Stats stat[NT / 32 + 1];  // of the warps, of the CTA
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 31;
     const int C = a.cluster, rank = blockIdx.x % C, row = blockIdx.x / C;
-    if (tid == 0) count = 0;
+    if (tid == 0) count = hots = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
@@ -168,7 +174,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
     const T* xv = x + head;
     Stats st{-INFINITY, 0.0f, 0.0f, -INFINITY};
     unsigned long long best = 0;  // the list's last key, 0 while it is not full
-    int pending = 0;              // threads that have appended since the list was in order
+    int pending = 0, listed = 0;  // hots, as all threads know it; keys in order
     // the list in order again (count of its keys are valid and visible)
     auto ranked = [&]() {
         const int n = count, keep = min(n, a.top);
@@ -183,76 +189,143 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
         if (tid < keep) list[tid] = work[tid];
         if (tid == 0) count = keep;
         best = n >= a.top ? work[a.top - 1] : 0;
-        pending = 0;
+        listed = keep;
         __syncthreads();
     };
-    int at = v0;
-    Raw raw[kUnroll];  // the next tile
-    auto load = [&](int i, int from, bool whole) {
-        const int v = from + i * NT + tid;
-        if (whole || v < v1) raw[i].load(xv + static_cast<int64_t>(v) * W, true);
-        else raw[i].w[0] = raw[i].w[1] = raw[i].w[2] = raw[i].w[3] = kNone;
-    };
+    // One thread's span, its first vector v, by a warp, a word or two a lane: keys of values of at least `least`, and of at least `low`.
+    auto look = [&](int v, float least, unsigned long long low) {
+        constexpr int kWords = kSpan * kUnroll * 4, kEach = (kWords + 31) / 32;
+        auto put = [&](float y, uint32_t index) {
+            if (y >= least) {
+                const unsigned long long k = key_of(y, index);
+                if (k >= low) list[atomicAdd(&count, 1)] = k;
+            }
+        };
+        v += (lane >> 2) * NT;
+        uint32_t w[kEach];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) load(i, at, false);
+        for (int i = 0; i < kEach; ++i)
+            if (i * 32 + lane < kWords && v + i * 8 * NT < v1)
+                w[i] = gload(reinterpret_cast<const uint32_t*>(xv + static_cast<int64_t>(v + i * 8 * NT) * W) + (lane & 3));
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (i * 32 + lane >= kWords || v + i * 8 * NT >= v1) continue;
+            const uint32_t index = head + (v + i * 8 * NT) * W + (lane & 3) * (W / 4);
+            if (TYPE == MOE_F32) {
+                put(__uint_as_float(w[i]), index);
+            } else {
+                Raw r;
+                r.w[0] = w[i];
+                put(r.get(0), index);
+                put(r.get(1), index + 1);
+            }
+        }
+    };
+    // The spans that wait (visible to all threads) are looked through: those that reach the top-th best of their maxima and the list.
+    auto flush = [&]() {
+        const int n = hots, keys = listed;  // (pending may count some that a flush has cooled)
+        for (int i = tid; i < n + keys; i += NT) work[i] = i < n ? static_cast<unsigned long long>(hot_max[i]) << 32 : list[i - n] & ~0xffffffffull;
+        if (tid == 0) bar = 0;
+        __syncthreads();
+        for (int i = tid; i < n + keys; i += NT) {
+            const unsigned long long mine = work[i];
+            int above = 0;
+#pragma unroll 8
+            for (int j = 0; j < n + keys; ++j) above += work[j] > mine || (work[j] == mine && j < i);
+            if (above == a.top - 1) bar = mine;
+        }
+        __syncthreads();
+        const uint32_t least = max(static_cast<uint32_t>(bar >> 32), order(-INFINITY));
+        for (int i = tid >> 5; i < n; i += NT / 32)
+            if (hot_max[i] >= least) look(hot_at[i], unorder(least), 0);
+        __syncthreads();
+        if (tid == 0) hots = 0;
+        pending = 0;
+        ranked();
+    };
+    int at = v0;
+    auto load = [&](Raw (&raw)[kUnroll], int from) {
+        const T* p = xv + static_cast<int64_t>(from + tid) * W;
+        if (from + kTile <= v1) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) raw[i].load(p + i * NT * W, true);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                if (from + i * NT + tid < v1) raw[i].load(p + i * NT * W, true);
+                else raw[i].w[0] = raw[i].w[1] = raw[i].w[2] = raw[i].w[3] = kNone;
+            }
+        }
+    };
+    float most;  // of a span
+    float r = 0.0f;  // st.r, or 0 while that is -inf
+    // t 2^t of a logit of -inf is 0: it is clamped, in pairs before the conversion where that can be (its power is 0 then, and its t
+    // finite), else t by t
+    auto room = [&](float r) {
+        const float t = fmaf(-kLow<TYPE>, a.c, r);
+        return TYPE != MOE_F32 && t > 200.0f && t < 1e38f;
+    };
+    bool clamped = room(0.0f);
+    auto add = [&](Raw (&raw)[kUnroll]) {
+        const float mx = max_of<TYPE>(raw);
+        most = fmaxf(most, mx);
+        // (2^kSlack is far from fp32's range: few tiles move the reference)
+        if (mx * a.c > st.r + kSlack) {
+            st.move(ceilf(mx * a.c));
+            r = st.r;
+            clamped = room(r);
+        }
+        const unsigned long long rr = pk2(-r, -r), cc = pk2(a.c, a.c);
+        unsigned long long s2 = 0, u2 = 0;
+        if (clamped) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                clamp_low<TYPE>(raw[i]);
+#pragma unroll
+                for (int e = 0; e < W / 2; ++e) {
+                    const unsigned long long t = fma2(pk2(raw[i].get(2 * e), raw[i].get(2 * e + 1)), cc, rr);
+                    const float2 f = up2(t);
+                    const unsigned long long p = pk2(ex2(f.x), ex2(f.y));
+                    s2 = add2(s2, p);
+                    u2 = fma2(p, t, u2);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+                for (int e = 0; e < W / 2; ++e) {
+                    const float2 t = up2(fma2(pk2(raw[i].get(2 * e), raw[i].get(2 * e + 1)), cc, rr));
+                    const unsigned long long p = pk2(ex2(t.x), ex2(t.y));
+                    s2 = add2(s2, p);
+                    u2 = fma2(p, pk2(fmaxf(t.x, kFar), fmaxf(t.y, kFar)), u2);
+                }
+        }
+        const float2 sf = up2(s2), uf = up2(u2);
+        st.s += sf.x + sf.y;
+        st.u += uf.x + uf.y;
+    };
+    Raw even[kUnroll], odd[kUnroll];
+    load(even, at);
     do {
         // singles: of the row's start threads 0 .., of its end threads 8 ..
         int single = -1;
         if (rank == 0 && at == v0 && tid < head) single = tid;
         if (rank == C - 1 && at + kSpan * kTile >= v1 && tid >= 8 && tid < 8 + tail) single = head + nv * W + tid - 8;
         const float alone = single >= 0 ? Elem<TYPE>::get(gload(x + single)) : -INFINITY;
-        float most = alone == alone ? alone : -INFINITY;  // of the span
-#pragma unroll 1
-        for (int from = at; from < min(at + kSpan * kTile, v1); from += kTile) {
-            float mx = max_of<TYPE>(raw[0], -INFINITY);
-#pragma unroll
-            for (int i = 1; i < kUnroll; ++i) mx = max_of<TYPE>(raw[i], mx);
-            most = fmaxf(most, mx);
-            const float to = ceilf(mx * a.c);
-            if (to > st.r) st.move(to);
-            const float r = st.r == -INFINITY ? 0.0f : st.r;
-            const unsigned long long rr = pk2(-r, -r), cc = pk2(a.c, a.c);
-            unsigned long long s2 = 0, u2 = 0;
-            // t 2^t of a logit of -inf is 0: it is clamped, in pairs before the conversion where that can be (the clamped logit's power is 0
-            // and its t finite), else t by t
-            const float room = fmaf(-kLow<TYPE>, a.c, r);
-            const bool whole = from + 2 * kTile <= v1;
-            if (TYPE != MOE_F32 && room > 200.0f && room < 1e38f) {
-#pragma unroll
-                for (int i = 0; i < kUnroll; ++i) {
-                    clamp_low<TYPE>(raw[i]);
-#pragma unroll
-                    for (int e = 0; e < W / 2; ++e) {
-                        const unsigned long long t = fma2(pk2(raw[i].get(2 * e), raw[i].get(2 * e + 1)), cc, rr);
-                        const float2 f = up2(t);
-                        const unsigned long long p = pk2(ex2(f.x), ex2(f.y));
-                        s2 = add2(s2, p);
-                        u2 = fma2(p, t, u2);
-                    }
-                    load(i, from + kTile, whole);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kUnroll; ++i) {
-#pragma unroll
-                    for (int e = 0; e < W / 2; ++e) {
-                        const float2 t = up2(fma2(pk2(raw[i].get(2 * e), raw[i].get(2 * e + 1)), cc, rr));
-                        const unsigned long long p = pk2(ex2(t.x), ex2(t.y));
-                        s2 = add2(s2, p);
-                        u2 = fma2(p, pk2(fmaxf(t.x, kFar), fmaxf(t.y, kFar)), u2);
-                    }
-                    load(i, from + kTile, whole);
-                }
-            }
-            const float2 sf = up2(s2), uf = up2(u2);
-            st.s += sf.x + sf.y;
-            st.u += uf.x + uf.y;
-        }
+        most = alone == alone ? alone : -INFINITY;
+        load(odd, at + kTile);
+        add(even);
+        load(even, at + 2 * kTile);
+        if (at + kTile < v1) add(odd);
         st.m = fmaxf(st.m, most);
         if (single >= 0) {
-            const float to = ceilf(alone * a.c);
-            if (to > st.r) st.move(to);
-            const float t = fmaf(alone, a.c, st.r == -INFINITY ? 0.0f : -st.r), p = ex2(t);
+            if (alone * a.c > st.r + kSlack) {
+                st.move(ceilf(alone * a.c));
+                r = st.r;
+                clamped = room(r);
+            }
+            const float t = fmaf(alone, a.c, -r), p = ex2(t);
             st.s += p;
             st.u = fmaf(p, fmaxf(t, kFar), st.u);
         }
@@ -260,7 +333,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
         if (a.top) {
             const uint32_t mine = at + tid < v1 || single >= 0 ? order(most) : 0;  // (0: nothing, or NaN alone)
             bool hot = mine > static_cast<uint32_t>(best >> 32);
-            const int n_hot = __syncthreads_count(hot);
+            int n_hot = __syncthreads_count(hot);
             if (n_hot) {
                 // f(logit, index) for the tile's logits of this thread, read again
                 auto each = [&](auto f) {
@@ -273,69 +346,48 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
                         for (int e = 0; e < W; ++e) f(r.get(e), static_cast<uint32_t>(head + v * W + e));
                     }
                 };
-                // the hot threads' keys of at least `low`, and of values of at least `least`: a warp takes its hot threads one by one, a
-                // word of the thread's tile a lane
-                auto append = [&](bool hot, float least, unsigned long long low) {
-                    auto put = [&](float y, uint32_t index) {
-                        if (y >= least) {
-                            const unsigned long long k = key_of(y, index);
-                            if (k >= low) list[atomicAdd(&count, 1)] = k;
-                        }
-                    };
-                    if (hot && single >= 0) put(alone, static_cast<uint32_t>(single));
-                    for (unsigned who = __ballot_sync(0xffffffffu, hot); who; who &= who - 1) {
-                        constexpr int kWords = kSpan * kUnroll * 4, kEach = (kWords + 31) / 32;
-                        const int v = at + (lane >> 2) * NT + (tid & ~31) + __ffs(who) - 1;
-                        uint32_t w[kEach];
-#pragma unroll
-                        for (int i = 0; i < kEach; ++i)
-                            if (i * 32 + lane < kWords && v + i * 8 * NT < v1)
-                                w[i] = gload(reinterpret_cast<const uint32_t*>(xv + static_cast<int64_t>(v + i * 8 * NT) * W) + (lane & 3));
-#pragma unroll
-                        for (int i = 0; i < kEach; ++i) {
-                            if (i * 32 + lane >= kWords || v + i * 8 * NT >= v1) continue;
-                            const uint32_t index = head + (v + i * 8 * NT) * W + (lane & 3) * (W / 4);
-                            if (TYPE == MOE_F32) {
-                                put(__uint_as_float(w[i]), index);
-                            } else {
-                                Raw r;
-                                r.w[0] = w[i];
-                                put(r.get(0), index);
-                                put(r.get(1), index + 1);
-                            }
-                        }
+                auto put_single = [&]() {
+                    if (single >= 0 && alone == alone) list[atomicAdd(&count, 1)] = key_of(alone, static_cast<uint32_t>(single));
+                };
+                auto wait = [&](bool hot) {  // the span is looked through later (a single at once)
+                    if (hot) {
+                        const int i = atomicAdd(&hots, 1);
+                        hot_max[i] = mine;
+                        hot_at[i] = at + tid;
+                        put_single();
                     }
                 };
                 if (best && n_hot <= kHot) {
                     if (pending + n_hot > kHot) {
-                        ranked();
+                        flush();
                         hot = mine > static_cast<uint32_t>(best >> 32);
                     }
-                    append(hot, unorder(static_cast<uint32_t>(best >> 32) + 1), 0);
+                    wait(hot);
                     pending += n_hot;
                 } else {
-                    if (pending) ranked();
+                    if (pending) flush();
                     // a bar: a maximum that `top` threads reach, as many in each warp
                     constexpr int kWarps = NT / 32;
-                    bool few = kWarps > 1;
-                    if (kWarps > 1) {
-                        uint32_t m = mine, r = 0;
-                        for (int i = 0; i < a.top; i += kWarps) {
-                            r = __reduce_max_sync(0xffffffffu, m);
-                            if (m == r) m = 0;
-                        }
-                        uint32_t* low32 = reinterpret_cast<uint32_t*>(work);
-                        if (lane == 0) low32[tid >> 5] = r;
-                        __syncthreads();
-                        uint32_t least = low32[0];
-#pragma unroll
-                        for (int w = 1; w < kWarps; ++w) least = min(least, low32[w]);
-                        least = max(least, order(-INFINITY));  // (0: fewer threads than that have any)
-                        hot = mine >= least;
-                        few = __syncthreads_count(hot) <= kHot;
-                        if (few) append(hot, unorder(least), 0);
+                    uint32_t m = mine, r = 0;
+                    for (int i = 0; i < a.top; i += kWarps) {
+                        r = __reduce_max_sync(0xffffffffu, m);
+                        if (m == r) m = 0;
                     }
-                    if (!few) {  // ties: the top-th best of the threads' best keys
+                    uint32_t* low32 = reinterpret_cast<uint32_t*>(work);
+                    if (lane == 0) low32[tid >> 5] = r;
+                    __syncthreads();
+                    uint32_t least = low32[0];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) least = min(least, low32[w]);
+                    least = max(least, order(-INFINITY));  // (0: fewer threads than that have any)
+                    hot = mine >= least;
+                    n_hot = __syncthreads_count(hot);
+                    if (n_hot <= min(kHot, NT - 1)) {
+                        wait(hot);
+                        pending = n_hot;
+                        __syncthreads();
+                        flush();
+                    } else {  // ties: the top-th best of the threads' best keys
                         unsigned long long mine_key = 0;
                         if (mine) each([&](float y, uint32_t index) {
                             const unsigned long long z = key_of(y, index);
@@ -351,10 +403,12 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
                         }
                         if (tid == a.top - 1) bar = k;  // (0: fewer threads than that have any)
                         __syncthreads();
-                        append(mine_key && mine_key >= bar, -INFINITY, bar);
+                        hot = mine_key && mine_key >= bar;
+                        if (hot) put_single();
+                        for (unsigned who = __ballot_sync(0xffffffffu, hot); who; who &= who - 1) look(at + (tid & ~31) + __ffs(who) - 1, -INFINITY, bar);
+                        __syncthreads();
+                        ranked();
                     }
-                    __syncthreads();
-                    ranked();
                 }
             }
         }
@@ -362,7 +416,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
     } while (at < v1);
     if (pending) {
         __syncthreads();
-        ranked();
+        flush();
     }
 
     // ---- the CTA's sums, then the row's
