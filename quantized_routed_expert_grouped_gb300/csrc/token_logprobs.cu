@@ -25,8 +25,11 @@
 #ifndef SMALLV
 #define SMALLV 256
 #endif
+#ifndef NTB
+#define NTB 256
+#endif
 #ifndef MINB
-#define MINB 4
+#define MINB (1024 / NTB)
 #endif
 namespace moe {
 
@@ -145,37 +148,30 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
     using Raw = RawVec<TYPE>;
     using T = typename Elem<TYPE>::T;
     constexpr int W = Raw::W, kTile = NT * kUnroll;  // vectors of a tile
-    constexpr int kHot = NT == 32 ? 32 : 64, kCap = kTop + kHot * (kSpan * kUnroll * W + 1);  // threads' spans to be looked through at once, and their keys
+    constexpr int kHot = NT == 32 ? 32 : NT == 128 ? 48 : 64, kCap = kTop + kHot * kSpan * kUnroll * W;  // threads' spans to be looked through at once, and their keys
     constexpr uint32_t kNone = TYPE == MOE_F32 ? 0xff800000u : TYPE == MOE_F16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf
     __shared__ unsigned long long list[kCap];  // the best keys in order, then new ones
-    __shared__ __align__(16) unsigned long long work[NT == 32 ? kHot + kTop : NT];  // (NT = kMaxCluster * kTop where there are clusters)
+    __shared__ __align__(16) unsigned long long work[NT == 32 ? kHot + kTop : kMaxCluster * kTop];
     __shared__ unsigned long long bar;  // a raised bar
     __shared__ uint32_t hot_max[kHot];  // spans of threads with logits above the bar: their maxima and first vectors
-    __shared__ int hot_at[kHot], hots;
+    __shared__ int hot_at[kHot], hots, listed;  // (listed: keys in order)
     __shared__ Stats stat[NT / 32 + 1];  // of the warps, of the CTA
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 31;
     const int C = a.cluster, rank = blockIdx.x % C, row = blockIdx.x / C;
-    if (tid == 0) count = hots = 0;
+    if (tid == 0) count = hots = listed = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
     const T* x = static_cast<const T*>(a.x) + row * a.stride;
-    // a given token's logit, on its way meanwhile
-    int id = -1;
-    float given = 0.0f;
-    if (rank == 0 && tid < a.n_ids) {
-        id = gload(a.ids + static_cast<int64_t>(row) * a.n_ids + tid);
-        if (id >= 0 && id < a.V) given = Elem<TYPE>::get(gload(x + id));
-    }
     const int head = min(a.V, static_cast<int>((-reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T)));
     const int nv = (a.V - head) / W, tail = a.V - head - nv * W;
     const int v0 = static_cast<int>(static_cast<int64_t>(nv) * rank / C), v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / C);
     const T* xv = x + head;
     Stats st{-INFINITY, 0.0f, 0.0f, -INFINITY};
-    unsigned long long best = 0;  // the list's last key, 0 while it is not full
-    int pending = 0, listed = 0;  // hots, as all threads know it; keys in order
-    // the list in order again (count of its keys are valid and visible)
+    uint32_t best = 0;  // the bar: order() of the list's last logit, 0 while the list is not full
+    int pending = 0;    // hots at most, as all threads know it
+    // the list in order again (its keys are visible)
     auto ranked = [&]() {
         const int n = count, keep = min(n, a.top);
         for (int i = tid; i < n; i += NT) {
@@ -187,9 +183,8 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
         }
         __syncthreads();
         if (tid < keep) list[tid] = work[tid];
-        if (tid == 0) count = keep;
-        best = n >= a.top ? work[a.top - 1] : 0;
-        listed = keep;
+        if (tid == 0) count = listed = keep;
+        best = n >= a.top ? static_cast<uint32_t>(work[a.top - 1] >> 32) : 0;
         __syncthreads();
     };
     // One thread's span, its first vector v, by a warp, a word or two a lane: keys of values of at least `least`, and of at least `low`.
@@ -258,48 +253,27 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
         }
     };
     float most;  // of a span
-    float r = 0.0f;  // st.r, or 0 while that is -inf
-    // t 2^t of a logit of -inf is 0: it is clamped, in pairs before the conversion where that can be (its power is 0 then, and its t
-    // finite), else t by t
-    auto room = [&](float r) {
-        const float t = fmaf(-kLow<TYPE>, a.c, r);
-        return TYPE != MOE_F32 && t > 200.0f && t < 1e38f;
-    };
-    bool clamped = room(0.0f);
     auto add = [&](Raw (&raw)[kUnroll]) {
         const float mx = max_of<TYPE>(raw);
         most = fmaxf(most, mx);
         // (2^kSlack is far from fp32's range: few tiles move the reference)
-        if (mx * a.c > st.r + kSlack) {
-            st.move(ceilf(mx * a.c));
-            r = st.r;
-            clamped = room(r);
-        }
+        if (mx * a.c > st.r + kSlack) st.move(ceilf(mx * a.c));
+        const float r = st.r == -INFINITY ? 0.0f : st.r;
         const unsigned long long rr = pk2(-r, -r), cc = pk2(a.c, a.c);
         unsigned long long s2 = 0, u2 = 0;
-        if (clamped) {
+        // (t 2^t of a logit of -inf is 0: 16-bit logits are clamped in pairs before the conversion, fp32's t one by one)
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                clamp_low<TYPE>(raw[i]);
+        for (int i = 0; i < kUnroll; ++i) {
+            clamp_low<TYPE>(raw[i]);
 #pragma unroll
-                for (int e = 0; e < W / 2; ++e) {
-                    const unsigned long long t = fma2(pk2(raw[i].get(2 * e), raw[i].get(2 * e + 1)), cc, rr);
-                    const float2 f = up2(t);
-                    const unsigned long long p = pk2(ex2(f.x), ex2(f.y));
-                    s2 = add2(s2, p);
-                    u2 = fma2(p, t, u2);
-                }
+            for (int e = 0; e < W / 2; ++e) {
+                unsigned long long t = fma2(pk2(raw[i].get(2 * e), raw[i].get(2 * e + 1)), cc, rr);
+                const float2 f = up2(t);
+                const unsigned long long p = pk2(ex2(f.x), ex2(f.y));
+                if (TYPE == MOE_F32) t = pk2(fmaxf(f.x, kFar), fmaxf(f.y, kFar));
+                s2 = add2(s2, p);
+                u2 = fma2(p, t, u2);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i)
-#pragma unroll
-                for (int e = 0; e < W / 2; ++e) {
-                    const float2 t = up2(fma2(pk2(raw[i].get(2 * e), raw[i].get(2 * e + 1)), cc, rr));
-                    const unsigned long long p = pk2(ex2(t.x), ex2(t.y));
-                    s2 = add2(s2, p);
-                    u2 = fma2(p, pk2(fmaxf(t.x, kFar), fmaxf(t.y, kFar)), u2);
-                }
         }
         const float2 sf = up2(s2), uf = up2(u2);
         st.s += sf.x + sf.y;
@@ -308,59 +282,29 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
     Raw even[kUnroll], odd[kUnroll];
     load(even, at);
     do {
-        // singles: of the row's start threads 0 .., of its end threads 8 ..
-        int single = -1;
-        if (rank == 0 && at == v0 && tid < head) single = tid;
-        if (rank == C - 1 && at + kSpan * kTile >= v1 && tid >= 8 && tid < 8 + tail) single = head + nv * W + tid - 8;
-        const float alone = single >= 0 ? Elem<TYPE>::get(gload(x + single)) : -INFINITY;
-        most = alone == alone ? alone : -INFINITY;
+        most = -INFINITY;
         load(odd, at + kTile);
         add(even);
         load(even, at + 2 * kTile);
         if (at + kTile < v1) add(odd);
         st.m = fmaxf(st.m, most);
-        if (single >= 0) {
-            if (alone * a.c > st.r + kSlack) {
-                st.move(ceilf(alone * a.c));
-                r = st.r;
-                clamped = room(r);
-            }
-            const float t = fmaf(alone, a.c, -r), p = ex2(t);
-            st.s += p;
-            st.u = fmaf(p, fmaxf(t, kFar), st.u);
-        }
         // ---- the best keys
         if (a.top) {
-            const uint32_t mine = at + tid < v1 || single >= 0 ? order(most) : 0;  // (0: nothing, or NaN alone)
-            bool hot = mine > static_cast<uint32_t>(best >> 32);
+            const uint32_t mine = at + tid < v1 ? order(most) : 0;
+            bool hot = mine > best;
             int n_hot = __syncthreads_count(hot);
             if (n_hot) {
-                // f(logit, index) for the tile's logits of this thread, read again
-                auto each = [&](auto f) {
-                    if (single >= 0) f(alone, static_cast<uint32_t>(single));
-#pragma unroll 1
-                    for (int v = at + tid; v < min(at + kSpan * kTile, v1); v += NT) {
-                        Raw r;
-                        r.load(xv + static_cast<int64_t>(v) * W, true);
-#pragma unroll
-                        for (int e = 0; e < W; ++e) f(r.get(e), static_cast<uint32_t>(head + v * W + e));
-                    }
-                };
-                auto put_single = [&]() {
-                    if (single >= 0 && alone == alone) list[atomicAdd(&count, 1)] = key_of(alone, static_cast<uint32_t>(single));
-                };
-                auto wait = [&](bool hot) {  // the span is looked through later (a single at once)
+                auto wait = [&](bool hot) {  // the span is looked through later
                     if (hot) {
                         const int i = atomicAdd(&hots, 1);
                         hot_max[i] = mine;
                         hot_at[i] = at + tid;
-                        put_single();
                     }
                 };
                 if (best && n_hot <= kHot) {
                     if (pending + n_hot > kHot) {
                         flush();
-                        hot = mine > static_cast<uint32_t>(best >> 32);
+                        hot = mine > best;
                     }
                     wait(hot);
                     pending += n_hot;
@@ -389,10 +333,16 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
                         flush();
                     } else {  // ties: the top-th best of the threads' best keys
                         unsigned long long mine_key = 0;
-                        if (mine) each([&](float y, uint32_t index) {
-                            const unsigned long long z = key_of(y, index);
-                            mine_key = z > mine_key ? z : mine_key;
-                        });
+#pragma unroll 1
+                        for (int v = at + tid; v < min(at + kSpan * kTile, v1); v += NT) {
+                            Raw y;
+                            y.load(xv + static_cast<int64_t>(v) * W, true);
+#pragma unroll
+                            for (int e = 0; e < W; ++e) {
+                                const unsigned long long z = key_of(y.get(e), static_cast<uint32_t>(head + v * W + e));
+                                mine_key = z > mine_key ? z : mine_key;
+                            }
+                        }
                         unsigned long long k = sorted_keys(mine_key, lane);
 #pragma unroll 1
                         for (int half = kWarps / 2; half > 0; half >>= 1) {
@@ -404,7 +354,6 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
                         if (tid == a.top - 1) bar = k;  // (0: fewer threads than that have any)
                         __syncthreads();
                         hot = mine_key && mine_key >= bar;
-                        if (hot) put_single();
                         for (unsigned who = __ballot_sync(0xffffffffu, hot); who; who &= who - 1) look(at + (tid & ~31) + __ffs(who) - 1, -INFINITY, bar);
                         __syncthreads();
                         ranked();
@@ -414,9 +363,38 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
         }
         at += kSpan * kTile;
     } while (at < v1);
-    if (pending) {
+    // a given token's logit, on its way meanwhile
+    int id = -1;
+    float given = 0.0f;
+    if (rank == 0 && tid < a.n_ids) {
+        id = gload(a.ids + static_cast<int64_t>(row) * a.n_ids + tid);
+        if (id >= 0 && id < a.V) given = Elem<TYPE>::get(gload(x + id));
+    }
+    // single logits: of the row's start threads 0 .., of its end threads 8 ..
+    int single = -1;
+    if (rank == 0 && tid < head) single = tid;
+    if (rank == C - 1 && tid >= 8 && tid < 8 + tail) single = head + nv * W + tid - 8;
+    if (a.top) {
         __syncthreads();
-        flush();
+        if (pending) flush();
+        if (C == 1 ? head + tail : rank == 0 ? head : rank == C - 1 ? tail : 0) {
+            unsigned long long k = 0;
+            if (single >= 0) k = key_of(Elem<TYPE>::get(gload(x + single)), static_cast<uint32_t>(single));
+            const bool more = k && (!best || k > list[a.top - 1]);
+            if (__syncthreads_count(more)) {
+                if (more) list[atomicAdd(&count, 1)] = k;
+                __syncthreads();
+                ranked();
+            }
+        }
+    }
+    if (single >= 0) {
+        const float y = Elem<TYPE>::get(gload(x + single));
+        st.m = fmaxf(st.m, y);
+        if (y * a.c > st.r + kSlack) st.move(ceilf(y * a.c));
+        const float t = fmaf(y, a.c, st.r == -INFINITY ? 0.0f : -st.r), p = ex2(t);
+        st.s += p;
+        st.u = fmaf(p, fmaxf(t, kFar), st.u);
     }
 
     // ---- the CTA's sums, then the row's
@@ -446,9 +424,9 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
         st = stat[NT / 32];
     };
     join();
-    // Where c times the row's largest logit is no number to subtract (a row that is masked by its type's lowest value): once more,
-    // with differences first.
-    const bool ends = fabsf(st.m) < INFINITY && !(fabsf(st.m * a.c) < 1.2676506e30f);
+    // Where c times the row's largest logit is no number to subtract, or a clamped logit would count next to it (rows that are masked by
+    // their type's lowest value; scales near 0 or far above 1): once more, with differences first.
+    const bool ends = fabsf(st.m) < INFINITY && !(fabsf(st.m * a.c) < 1.2676506e30f && (TYPE == MOE_F32 || ((st.m - kLow<TYPE>) * a.c > 250.0f && -kLow<TYPE> * a.c < 1e38f)));
     if (ends) {
         const float m = st.m;
         st = Stats{0.0f, 0.0f, 0.0f, m};
@@ -471,22 +449,27 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
     if (C > 1 && a.top) {  // the row's best keys
         cg::cluster_group cluster = cg::this_cluster();
         if (rank == 0) {
-            const int from = tid / kTop, i = tid % kTop;  // (NT = kMaxCluster * kTop threads)
-            unsigned long long mine = 0;
-            if (from < C && i < a.top && i < *cluster.map_shared_rank(&count, from)) mine = cluster.map_shared_rank(list, from)[i];
-            if (from < C && i < a.top) work[from * a.top + i] = mine;
-            const int some = __syncthreads_count(mine != 0);
-            int above = 0;
+            int some = 0;
+            for (int r = 0; r < C; ++r) some += *cluster.map_shared_rank(&count, r);
+            for (int i = tid; i < C * a.top; i += NT) {
+                const int from = i / a.top, k = i - from * a.top;
+                work[i] = k < *cluster.map_shared_rank(&count, from) ? cluster.map_shared_rank(list, from)[k] : 0;
+            }
+            __syncthreads();
+            for (int i = tid; i < C * a.top; i += NT) {
+                const unsigned long long mine = work[i];
+                int above = 0;
 #pragma unroll 8
-            for (int j = 0; j < C * a.top; ++j) above += work[j] > mine;
-            if (mine && above < a.top) list[above] = mine;
+                for (int j = 0; j < C * a.top; ++j) above += work[j] > mine;
+                if (mine && above < a.top) list[above] = mine;
+            }
             if (tid == 0) count = min(some, a.top);
             __syncthreads();
         }
         cluster.sync();
     }
     if (rank != 0) return;
-    const bool none = st.s == 0.0f;
+    const bool none = st.m == -INFINITY && st.s == st.s;  // (a row of NaN is none of -inf)
     const float l2 = log2f(st.s), ls = (l2 - (ends ? 0.0f : fmaf(st.m, a.c, -st.r))) * kLn2;  // log of the sum of e^(scale (x - m))
     auto logprob = [&](float v) { return none ? -INFINITY : (v - st.m) * a.scale - ls; };
     for (int i = tid; i < a.n_ids; i += NT) {
@@ -512,7 +495,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
 
 template <int TYPE>
 cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
-    constexpr int W = RawVec<TYPE>::W, kTile = 256 * kUnroll;
+    constexpr int W = RawVec<TYPE>::W, kTile = NTB * kUnroll;
     // CTAs of a row: until every SM has two, and while each still has a whole tile
     a.cluster = 1;
     while (a.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * a.cluster < 304 && a.V / W / a.cluster > kTile) a.cluster *= 2;
@@ -520,7 +503,7 @@ cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.cluster);
     const bool small = a.V / W <= SMALLV;
-    cfg.blockDim = dim3(small ? 32 : 256);
+    cfg.blockDim = dim3(small ? 32 : NTB);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -530,7 +513,7 @@ cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return small ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 32>, a) : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 256>, a);
+    return small ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 32>, a) : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, NTB>, a);
 }
 
 }  // namespace
