@@ -688,21 +688,28 @@ def _rope(rope, dev, D):
     return rope._fields
 
 
-def _heads(x, weight, out, N, D, like, dev, stream, name):
+def _heads(x, weight, out, N, D, dtype, dev, stream, name):
     """The fields of moe_heads, and the rows that they are written to."""
-    shape, xs = x.shape, x.stride()
-    if len(shape) != 3 or shape[0] != N or shape[2] != D or (N and xs[2] != 1) or x.dtype is not like.dtype:
-        raise MoeError(f"{name}: [{N}, heads, {D}] of {like.dtype}, contiguous in the last dimension, expected")
+    shape = x.shape
+    if len(shape) != 3 or x.dtype is not dtype or x.get_device() != dev:
+        raise MoeError(f"{name}: [{N}, heads, {D}] of {dtype} on device {dev} expected")
+    n, H, d = shape
+    xt, xh, xd = x.stride()
+    if n != N or d != D or (xd != 1 and N):
+        raise MoeError(f"{name}: [{N}, heads, {D}], contiguous in the last dimension, expected")
     if out is None:
-        out = _empty(stream, shape, x.dtype, x.device)
-        os = (shape[1] * D, D)
+        out = torch.empty(shape, dtype=dtype, device=x.device) if stream is None else _empty(stream, shape, dtype, x.device)
+        ot, oh = H * D, D
     else:
-        os = out.stride()
-        if out.shape != shape or out.dtype is not x.dtype or (N and os[2] != 1):
-            raise MoeError(f"{name}_out: {name}'s shape and type, contiguous in the last dimension, expected")
-    if weight is not None and (weight.shape != (D,) or not weight.is_contiguous()):
-        raise MoeError(f"{name}_weight: contiguous [{D}] expected")
-    return (_ptr(x, dev), _ptr(out, dev), 0 if weight is None else _ptr(weight, dev), xs[0], xs[1], os[0], os[1], shape[1]), out
+        ot, oh, od = out.stride()
+        if out.shape != shape or out.dtype is not dtype or (od != 1 and N) or out.get_device() != dev:
+            raise MoeError(f"{name}_out: {name}'s shape, type and device, contiguous in the last dimension, expected")
+    w = 0
+    if weight is not None:
+        w = weight.data_ptr()
+        if weight.numel() != D or weight.dim() != 1 or not weight.is_contiguous() or weight.get_device() != dev:
+            raise MoeError(f"{name}_weight: contiguous [{D}] on device {dev} expected")
+    return (x.data_ptr(), out.data_ptr(), w, xt, xh, ot, oh, H), out
 
 
 def _w_type(a, b):
@@ -718,13 +725,14 @@ def head_norm_rope(q, positions, rope=None, k=None, q_weight=None, k_weight=None
     k, [tokens, heads, head_dim], in one pass; positions int32 [tokens] (None without a rotation), negative ones turn back. Returns (q_out,
     k_out), k_out None without k; q_out may be q itself, k_out k. head_dim: a multiple of 16 up to 256."""
     dev = _device(q)
-    if len(q.shape) != 3:
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
         raise MoeError("q: [tokens, heads, head_dim] expected")
-    N, _, D = q.shape
+    N, _, D = shape
     if rope is not None and positions is None:
         raise MoeError("positions: expected with a rotation")
-    a, q_out = _heads(q, q_weight, q_out, N, D, q, dev, stream, "q")
-    b, k_out = (_NO_HEADS, None) if k is None else _heads(k, k_weight, k_out, N, D, q, dev, stream, "k")
+    a, q_out = _heads(q, q_weight, q_out, N, D, dtype, dev, stream, "q")
+    b, k_out = (_NO_HEADS, None) if k is None else _heads(k, k_weight, k_out, N, D, dtype, dev, stream, "k")
     c = _pack(_pack_heads, *a, *b, *_rope(rope, dev, D), 0 if positions is None else _ints(positions, "positions", N, dev), N, _elem(q),
               _w_type(q_weight, None if k is None else k_weight), D, eps)
     _launch(lib().moe_head_norm_rope, dev, stream, (q, k, q_weight, k_weight, positions, q_out, k_out, None if rope is None else rope.turns), c)
@@ -745,7 +753,7 @@ def kv8_append(k, v, pool, page_table, cu_tokens, start, rope=None, q=None, q_we
         raise MoeError(f"k, v: [tokens, {hkv}, {D}] of one type, contiguous in the last dimension, expected")
     if k_weight is not None and (k_weight.shape != (D,) or not k_weight.is_contiguous()):
         raise MoeError(f"k_weight: contiguous [{D}] expected")
-    a, q_out = (_NO_HEADS, None) if q is None else _heads(q, q_weight, q_out, N, D, k, dev, stream, "q")
+    a, q_out = (_NO_HEADS, None) if q is None else _heads(q, q_weight, q_out, N, D, k.dtype, dev, stream, "q")
     if n == 0 and N == 0:  # no sequences (the library takes one at least)
         return q_out
     x = _pack(_pack_append, *c, _ptr(k, dev), _ptr(v, dev), _elem(k), N, ks[0], ks[1], vs[0], vs[1], *a, *_rope(rope, dev, D),
@@ -768,22 +776,20 @@ def token_logprobs(logits, ids=None, top=0, scale=1.0, stream=None):
     if not 0 <= top <= 32:
         raise MoeError("top: 0 to 32 expected")
     R, V = shape
-    n = 0
+    n, given = 0, 0
     if ids is not None:
-        if ids.shape[:1] != (R,) or len(ids.shape) != 2:
+        if len(ids.shape) != 2 or ids.shape[0] != R:
             raise MoeError(f"ids: [{R}, n] expected")
         n = ids.shape[1]
-    # one allocation for what is fp32: entropy, lse, logprobs, top
-    f = _empty(stream, (R * (2 + n + top),), torch.float32, logits.device)
-    entropy, lse = f[:R], f[R:2 * R]
-    logprobs = None if ids is None else f[2 * R:(2 + n) * R].view(R, n)
-    top_ids = _empty(stream, (R, top), torch.int32, logits.device) if top else None
-    top_lp = f[(2 + n) * R:].view(R, top) if top else None
+        given = _ints(ids, "ids", R * n, dev)
+    device = logits.device
+    logprobs = None if ids is None else _empty(stream, (R, n), torch.float32, device)
+    top_lp, top_ids = (_empty(stream, (R, top), torch.float32, device), _empty(stream, (R, top), torch.int32, device)) if top else (None, None)
+    entropy, lse = _empty(stream, (R,), torch.float32, device), _empty(stream, (R,), torch.float32, device)
     if R:
-        at = f.data_ptr()
-        c = _pack(_pack_logprobs, _ptr(logits, dev), logits.stride(0) if R > 1 else V, _elem(logits), R, V, n, top, scale, 0 if not n else _ints(ids, "ids", R * n, dev),
-                  at + 8 * R, at + 4 * R * (2 + n), 0 if top_ids is None else top_ids.data_ptr(), at, at + 4 * R)
-        _launch(lib().moe_token_logprobs, dev, stream, (logits, ids, f, top_ids), c)
+        x = _pack(_pack_logprobs, logits.data_ptr(), logits.stride(0) if R > 1 else V, _elem(logits), R, V, n, top, scale, given,
+                  logprobs.data_ptr() if n else 0, top_lp.data_ptr() if top else 0, top_ids.data_ptr() if top else 0, entropy.data_ptr(), lse.data_ptr())
+        _launch(lib().moe_token_logprobs, dev, stream, (logits, ids, logprobs, top_lp, top_ids, entropy, lse), x)
     return logprobs, top_lp, top_ids, entropy, lse
 
 

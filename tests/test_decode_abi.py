@@ -92,12 +92,12 @@ def test_logprobs_refusals(m):  # noqa: F811
 
 def test_binding_refusals(m, monkeypatch):  # noqa: F811
     """Tensors of the wrong kind never reach the library."""
-    monkeypatch.setattr(m, "_device", lambda t: 0)
+    monkeypatch.setattr(m, "_device", lambda t: -1)
     monkeypatch.setattr(m, "_ptr", lambda t, dev: t.data_ptr())
     monkeypatch.setattr(m, "_launch", lambda *a: pytest.fail("launched"))
     r = m.Rope(64, device="cpu")
-    r._device = 0
     other = m.Rope(64, device="cpu")
+    other._device = 1
     q, pos, w = torch.zeros((3, 4, 64)), torch.zeros(3, dtype=torch.int32), torch.ones(64)
     pool, table = m.kv8_pool(2, 2, 64, 32, device="cpu"), torch.zeros((1, 2), dtype=torch.int32)
     k, cu, start = torch.zeros((3, 2, 64)), torch.tensor([0, 3], dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
@@ -142,9 +142,9 @@ def test_two_descriptions_agree(m):  # noqa: F811
 
 
 def test_empty_batches(m, monkeypatch):  # noqa: F811
-    monkeypatch.setattr(m, "_device", lambda t: 0)
+    monkeypatch.setattr(m, "_device", lambda t: -1)
     monkeypatch.setattr(m, "_ptr", lambda t, dev: t.data_ptr())
-    monkeypatch.setattr(m, "_current_device", lambda: 0)
+    monkeypatch.setattr(m, "_current_device", lambda: -1)
     monkeypatch.setattr(m, "_raw_stream", lambda dev: 0)
     pool, table = m.kv8_pool(2, 2, 64, 32, device="cpu"), torch.zeros((0, 3), dtype=torch.int32)
     none = torch.zeros(0, dtype=torch.int32)
