@@ -12,8 +12,7 @@ struct HeadRopeArgs {
     int64_t n;
     int D, w_type;
     float eps;
-    // of a token: warps for queries and for keys, heads of each warp
-    int qw, kw, qh, kh;
+    int tokens, warps, splits;  // of a CTA; of a token in a CTA; CTAs of a token
 };
 cudaError_t launch_head_norm_rope(HeadRopeArgs a, int type, cudaStream_t st);
 

@@ -1,52 +1,92 @@
 // head_rope.cu - norm and rotation of the heads of query and key rows in one pass (the mathematics and a lane's share are
 // in head_rope.cuh).
 //
-// Bound by memory: a value is read once and written once, with five instructions. A warp takes up to kHeadsOfWarp rounds of heads of
-// one token's queries or keys, so that its angles and weights serve several heads.
 #include "decode_api.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kThreads = 128;
+#ifndef RB
+#define RB 7
+#endif
+#ifndef MAXT
+#define MAXT 4
+#endif
+constexpr int kThreads = 128, kWarps = kThreads / 32, kMaxTokens = MAXT;
 
-template <int TYPE, int L>
-__global__ void __launch_bounds__(kThreads) head_norm_rope_kernel(const HeadRopeArgs a) {
-    const uint32_t id = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), per = a.qw + a.kw;
-    const uint32_t token = id / per;
-    const int part = static_cast<int>(id - token * per);
-    if (token >= a.n) return;
+template <int TYPE, int L, bool VEC>
+__global__ void __launch_bounds__(kThreads, RB) head_norm_rope_kernel(const HeadRopeArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    using Warp = RopeWarp<TYPE, L, VEC>;
+    constexpr int W = Warp::W, G = Warp::G;
+    // the CTA's tokens t0 .. t0 + n; this warp's first one, and its rounds r0 .. r1 of a token's (queries', then keys')
+    const int wid = threadIdx.x >> 5, tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits;
+    const int64_t t0 = static_cast<int64_t>(tile) * a.tokens;
+    const int n = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.n - t0));
+    const int first = wid / a.warps, rq = (a.q.n + G - 1) / G, rounds = rq + (a.k.n + G - 1) / G;
+    const int part = split * a.warps + wid - first * a.warps, parts = a.splits * a.warps;
+    const int r0 = rounds * part / parts, r1 = rounds * (part + 1) / parts;
+    const int q0 = r0 * G, q1 = min(a.q.n, r1 * G), k0 = max(r0 - rq, 0) * G, k1 = min(a.k.n, (r1 - rq) * G);
+    float *qw = sm + n * a.r.rot, *kw = qw + a.D;
+    Warp w(a.r, a.D);
     pdl_wait();
     pdl_trigger();
-    const bool keys = part >= a.qw;
-    const HeadSet& set = keys ? a.k : a.q;
-    const int each = keys ? a.kh : a.qh, h0 = (keys ? part - a.qw : part) * each;
-    rope_heads<TYPE, L>(set, a.r, a.D, a.w_type, a.eps, token, a.positions + token, 0, h0, min(set.n, h0 + each));
+    if (first < n) {
+        if (q0 < q1) w.start(a.q, t0 + first, q0, q1);
+        else if (k0 < k1) w.start(a.k, t0 + first, k0, k1);
+    }
+    const int half = a.r.rot / 2;
+    for (int i = threadIdx.x; i < n * half; i += kThreads) {
+        const int t = i / half;
+        put_angle<W>(sm + t * a.r.rot, a.r, gload(a.positions + t0 + t), i - t * half);
+    }
+    if (a.q.weight) put_weights<W>(qw, a.r, a.D, a.q.weight, a.w_type);
+    if (a.k.weight) put_weights<W>(kw, a.r, a.D, a.k.weight, a.w_type);
+    __syncthreads();
+    for (int t = first; t < n; t += kWarps / a.warps) {
+        const float* angles = sm + t * a.r.rot;
+        if (q0 < q1) {
+            if (t != first) w.start(a.q, t0 + t, q0, q1);
+            w.run(a.q, a.r, a.D, a.eps, angles, qw, t0 + t, q0, q1);
+        }
+        if (k0 < k1) {
+            if (t != first || q0 < q1) w.start(a.k, t0 + t, k0, k1);
+            w.run(a.k, a.r, a.D, a.eps, angles, kw, t0 + t, k0, k1);
+        }
+    }
 }
 
-template <int TYPE, int L>
+template <int TYPE, int L, bool VEC>
 cudaError_t rope_l(HeadRopeArgs& a, cudaStream_t st) {
     constexpr int G = 32 / L;
-    // rounds of heads of a warp: as few as give the device 16 warps an SM, 8 at most
-    const int64_t rounds = a.n * ((a.q.n + G - 1) / G + (a.k.n + G - 1) / G);
-    const int each = static_cast<int>(rounds / (152 * 16) < 1 ? 1 : rounds / (152 * 16) > 8 ? 8 : rounds / (152 * 16));
-    a.qh = a.kh = each * G;
-    a.qw = (a.q.n + a.qh - 1) / a.qh;
-    a.kw = (a.k.n + a.kh - 1) / a.kh;
-    const int64_t warps = a.n * (a.qw + a.kw);
-    return launch_kernel(head_norm_rope_kernel<TYPE, L>, dim3(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32))), dim3(kThreads), 0, st, true, a);
+    // Many tokens: up to eight a CTA, two a warp, so that weights and setting up serve several; few: a token's rounds over the
+    // CTA's warps, and over several CTAs.
+    const int rounds = (a.q.n + G - 1) / G + (a.k.n + G - 1) / G;
+    const int64_t each = a.n / (152 * 6);
+    a.tokens = static_cast<int>(each < 1 ? 1 : each > kMaxTokens ? kMaxTokens : each);
+    a.warps = a.tokens >= kWarps ? 1 : kWarps / a.tokens;  // of a token in a CTA
+    a.splits = 1;
+    while (a.n * a.splits < 152 * 2 && a.splits * a.warps < rounds) ++a.splits;
+    const int64_t grid = (a.n + a.tokens - 1) / a.tokens * a.splits;
+    return launch_kernel(head_norm_rope_kernel<TYPE, L, VEC>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), rope_smem(a.r.rot, a.D, a.tokens), st, true, a);
+}
+
+template <int TYPE, bool VEC>
+cudaError_t rope_v(HeadRopeArgs& a, cudaStream_t st) {
+    const int lanes = a.D / (2 * RawVec<TYPE, VEC>::W);
+    if (lanes <= 2) return rope_l<TYPE, 2, VEC>(a, st);
+    if (lanes <= 4) return rope_l<TYPE, 4, VEC>(a, st);
+    if (lanes <= 8) return rope_l<TYPE, 8, VEC>(a, st);
+    if (lanes <= 16) return rope_l<TYPE, 16, VEC>(a, st);
+    if constexpr (TYPE == MOE_F32) return rope_l<TYPE, 32, VEC>(a, st);
+    return cudaErrorInvalidValue;
 }
 
 template <int TYPE>
 cudaError_t rope_t(HeadRopeArgs& a, cudaStream_t st) {
-    const int lanes = a.D / (2 * RawVec<TYPE>::W);
-    if (lanes <= 2) return rope_l<TYPE, 2>(a, st);
-    if (lanes <= 4) return rope_l<TYPE, 4>(a, st);
-    if (lanes <= 8) return rope_l<TYPE, 8>(a, st);
-    if (lanes <= 16) return rope_l<TYPE, 16>(a, st);
-    if constexpr (TYPE == MOE_F32) return rope_l<TYPE, 32>(a, st);
-    return cudaErrorInvalidValue;
+    const bool vec = (a.q.n == 0 || (a.q.xvec && a.q.ovec)) && (a.k.n == 0 || (a.k.xvec && a.k.ovec));
+    return vec ? rope_v<TYPE, true>(a, st) : rope_v<TYPE, false>(a, st);
 }
 
 }  // namespace

@@ -6,12 +6,14 @@
 // A head is D / W vectors of 16 bytes (W = 8 elements of 16 bits, 4 of fp32). A lane holds two of them: s and
 // s + rot / 2W of the rotated dims, so that in both layouts a lane has whole pairs and a warp's accesses fill whole
 // sectors; the dims that stay follow, paired in the same way. L = a power of two >= D / 2W lanes hold a head, and the
-// 32 / L groups of a warp take heads of one token in turn: the W angles of a lane are the same for all of them, each group
-// computes its share, and they are exchanged by shuffles.
+// 32 / L groups of a warp take heads of one token in turn. The angles of a CTA's tokens and the weights lie in shared memory, in
+// the order in which lanes read them (chunks of 16 bytes, one after another over the lanes of a head): held in registers they
+// left a third of the warps.
 //
 // Angles. turns = f / 2 pi in units of 2^-64; position * turns, in 64 bits, drops whole turns by itself, so the angle of a
-// far position is as exact as that of a near one (what is left is the rounding to fp32: 9e-8 at half a turn). No table of
-// positions is read, and none limits them.
+// far position is as exact as that of a near one. The nearest quarter of a turn is taken off in whole numbers too; the rest, up
+// to pi / 4, goes to fp32 and into the Taylor polynomials of sine and cosine to the 9th and 10th power (what they leave out is below
+// 2^-29). No table of positions is read, and none limits them.
 #pragma once
 
 #include "internal.h"
@@ -39,21 +41,21 @@ struct HeadSet {
 
 #ifdef __CUDACC__
 
-// A vector of 16 bytes as it lies in memory.
-template <int TYPE>
+// 16 bytes as they lie in memory; VEC: they are aligned.
+template <int TYPE, bool VEC>
 struct RawVec {
     using T = typename Elem<TYPE>::T;
     static constexpr int W = 16 / static_cast<int>(sizeof(T));
     uint32_t w[4];
     __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0; }
-    __device__ __forceinline__ void load(const T* p, bool vec) {
-        if (vec) {
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC) {
             const uint4 v = gload(reinterpret_cast<const uint4*>(p));
             w[0] = v.x;
             w[1] = v.y;
             w[2] = v.z;
             w[3] = v.w;
-        } else if (TYPE == MOE_F32) {
+        } else if constexpr (TYPE == MOE_F32) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = gload(reinterpret_cast<const uint32_t*>(p) + i);
         } else {
@@ -69,40 +71,38 @@ struct RawVec {
         if (TYPE == MOE_BF16) return __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16);
         return __half2float(__ushort_as_half(static_cast<unsigned short>(e & 1 ? x >> 16 : x & 0xffffu)));
     }
-};
-
-template <int TYPE>
-__device__ __forceinline__ void store_vec(typename Elem<TYPE>::T* p, bool vec, const unsigned long long (&v)[RawVec<TYPE>::W / 2]) {
-    using E = Elem<TYPE>;
-    constexpr int W = RawVec<TYPE>::W;
-    uint32_t w[4];
+    // of packed pairs of fp32
+    __device__ __forceinline__ void put(const unsigned long long (&v)[W / 2]) {
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-        const float2 f = up2(v[i]);
-        if constexpr (TYPE == MOE_F32) {
-            w[2 * i] = __float_as_uint(f.x);
-            w[2 * i + 1] = __float_as_uint(f.y);
-        } else if constexpr (TYPE == MOE_F16) {
-            const __half2 h = __floats2half2_rn(f.x, f.y);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int i = 0; i < W / 2; ++i) {
+            const float2 f = up2(v[i]);
+            if constexpr (TYPE == MOE_F32) {
+                w[2 * i] = __float_as_uint(f.x);
+                w[2 * i + 1] = __float_as_uint(f.y);
+            } else if constexpr (TYPE == MOE_F16) {
+                const __half2 h = __floats2half2_rn(f.x, f.y);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (VEC) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if constexpr (TYPE == MOE_F32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
         } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                reinterpret_cast<uint16_t*>(p)[2 * i] = static_cast<uint16_t>(w[i]);
+                reinterpret_cast<uint16_t*>(p)[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+            }
         }
     }
-    if (vec) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if constexpr (TYPE == MOE_F32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = __uint_as_float(w[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            reinterpret_cast<uint16_t*>(p)[2 * i] = static_cast<uint16_t>(w[i]);
-            reinterpret_cast<uint16_t*>(p)[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
-        }
-    }
-}
+};
 
 // The two vectors of lane s of a head (W elements each), by their first dims, and the pairs that they hold.
 struct RopeUnit {
@@ -133,31 +133,33 @@ __device__ __forceinline__ int rope_pair(const RopeArgs& r, int W, int s, int j)
 // factor * (cos, sin) of the pair's angle at a position.
 __device__ __forceinline__ float2 rope_angle(const RopeArgs& r, int position, int pair) {
     const uint64_t at = gload(r.turns + pair) * static_cast<uint64_t>(static_cast<int64_t>(position));
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int64_t>(at)) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns, in [-1, 1]
-    return make_float2(c * r.factor, s * r.factor);
+    const uint32_t quarter = static_cast<uint32_t>((at + (1ull << 61)) >> 62);
+    const float t = static_cast<float>(static_cast<int64_t>(at - (static_cast<uint64_t>(quarter) << 62))) * 3.4061215800086834e-19f;  // 2 pi / 2^64
+    const float z = t * t;
+    const float s = t * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f) * r.factor;
+    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f) * r.factor;
+    const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;  // quarter turns: (c, s), (-s, c), (-c, -s), (s, -c)
+    return make_float2((quarter + 1) & 2 ? -x : x, quarter & 2 ? -y : y);
 }
 
-// The rotation of a lane's two vectors, in place, as packed pairs of fp32.
+// The rotation of a lane's two vectors, in place, as packed pairs of fp32; at: its angles' chunks, `lanes` apart.
 template <int W>
-__device__ __forceinline__ void rope_turn(unsigned long long (&a)[W / 2], unsigned long long (&b)[W / 2], const float (&c)[W], const float (&s)[W], int inter) {
-    if (!inter) {
+__device__ __forceinline__ void rope_turn(unsigned long long (&a)[W / 2], unsigned long long (&b)[W / 2], const float4* at, int lanes, int inter) {
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            const unsigned long long cc = pk2(c[2 * i], c[2 * i + 1]), ss = pk2(s[2 * i], s[2 * i + 1]), neg = pk2(-s[2 * i], -s[2 * i + 1]);
-            const unsigned long long x = fma2(b[i], neg, mul2(a[i], cc));
-            b[i] = fma2(a[i], ss, mul2(b[i], cc));
+    for (int i = 0; i < W / 2; ++i) {
+        const float4 f = at[i * lanes];
+        if (!inter) {
+            const unsigned long long c = pk2(f.x, f.y), s = pk2(f.z, f.w), neg = mul2(b[i], pk2(-1.0f, -1.0f));
+            const unsigned long long x = fma2(neg, s, mul2(a[i], c));
+            b[i] = fma2(a[i], s, mul2(b[i], c));
             a[i] = x;
-        }
-    } else {
-        auto one = [](unsigned long long& v, float c, float s) {
-            const float2 f = up2(v);
-            v = pk2(fmaf(-f.y, s, f.x * c), fmaf(f.x, s, f.y * c));
-        };
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            one(a[i], c[i], s[i]);
-            one(b[i], c[W / 2 + i], s[W / 2 + i]);
+        } else {  // two pairs of the first vector, or of the second
+            auto one = [](unsigned long long& v, float c, float s) {
+                const float2 x = up2(v);
+                v = pk2(fmaf(-x.y, s, x.x * c), fmaf(x.x, s, x.y * c));
+            };
+            one(i < W / 4 ? a[2 * i] : b[2 * i - W / 2], f.x, f.z);
+            one(i < W / 4 ? a[2 * i + 1] : b[2 * i + 1 - W / 2], f.y, f.w);
         }
     }
 }
@@ -186,90 +188,110 @@ __device__ __forceinline__ void weight_vec(const void* w, int w_type, int at, un
     }
 }
 
-// Heads h0 .. h1 of one row by the whole warp. L lanes a head, two rounds of 32 / L heads with their loads in flight.
-template <int TYPE, int L>
-__device__ __forceinline__ void rope_heads(const HeadSet& set, const RopeArgs& r, int D, int w_type, float eps, int64_t row, const int32_t* position, int at,
-                                           int h0, int h1) {
-    using Raw = RawVec<TYPE>;
+// The shared memory of a CTA: angles of up to T tokens, then the weights of queries and of keys.
+__host__ __device__ inline int rope_smem(int rot, int D, int T) { return (T * rot + 2 * D) * 4; }
+
+// One token's angles, rot / 4 chunks of two pairs (both cosines, both sines, as packed arithmetic takes them): chunk j / 2 of lane s at
+// (j / 2) * lanes + s.
+template <int W>
+__device__ __forceinline__ void put_angle(float* to, const RopeArgs& r, int position, int i) {
+    const int lanes = r.rot / (2 * W), s = i / W, j = i - s * W;
+    const float2 f = rope_angle(r, position, rope_pair(r, W, s, j));
+    to += ((j >> 1) * lanes + s) * 4 + (j & 1);
+    to[0] = f.x;
+    to[2] = f.y;
+}
+// A set's weights as fp32: chunk c (of four) of lane s at c * lanes + s; the second vector's after all of the first's.
+template <int W>
+__device__ __forceinline__ void put_weights(float* to, const RopeArgs& r, int D, const void* weight, int w_type) {
+    const int lanes = D / (2 * W);
+    for (int i = threadIdx.x; i < D; i += blockDim.x) {
+        const int s = i / (2 * W), e = i - s * 2 * W, v = e / W, j = e - v * W;
+        const RopeUnit u(r, D, W, s);
+        const int at = (v ? u.e1 : u.e0) + j;
+        const float w = w_type == MOE_F32 ? gload(static_cast<const float*>(weight) + at) : w_type == MOE_F16 ? __half2float(gload(static_cast<const __half*>(weight) + at))
+                                                                                                              : __bfloat162float(gload(static_cast<const __nv_bfloat16*>(weight) + at));
+        to[((v * (W / 4) + (j >> 2)) * lanes + s) * 4 + (j & 3)] = w;
+    }
+}
+
+// Heads h0 .. h1 of a row by the whole warp: start() sends for the first ones, run() does them. L lanes a head; angles: the
+// token's; weights: the set's.
+template <int TYPE, int L, bool VEC>
+struct RopeWarp {
+    using Raw = RawVec<TYPE, VEC>;
     using T = typename Elem<TYPE>::T;
-    constexpr int W = Raw::W, G = 32 / L, kAhead = 2;
-    const int lane = threadIdx.x & 31, s = lane & (L - 1), g = lane / L;
-    const RopeUnit u(r, D, W, s);
-    const T* x = static_cast<const T*>(set.x) + row * set.xt;
-    T* out = static_cast<T*>(set.out) + row * set.ot;
-    Raw raw[kAhead][2];
-    auto load = [&](int h) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            raw[i][0].clear();
-            raw[i][1].clear();
-            if (u.in && h + i * G < h1) {
-                const T* p = x + (h + i * G) * set.xh;
-                raw[i][0].load(p + u.e0, set.xvec);
-                raw[i][1].load(p + u.e1, set.xvec);
-            }
-        }
-    };
-    load(h0 + g);
-    float c[W], sn[W];
-    if (r.rot) {  // each group computes P of the lane's W angles
-        constexpr int P = G < W ? W / G : 1;
-        const int pos = position ? gload(position) : at;
-        float2 mine[P];
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            mine[i] = make_float2(1.0f, 0.0f);
-            if (u.turn && g * P + i < W) mine[i] = rope_angle(r, pos, rope_pair(r, W, s, g * P + i));
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            c[j] = __shfl_sync(0xffffffffu, mine[j % P].x, j / P * L + s);
-            sn[j] = __shfl_sync(0xffffffffu, mine[j % P].y, j / P * L + s);
-        }
+    static constexpr int W = Raw::W, G = 32 / L;  // elements of a vector, heads of a round
+    const RopeUnit u;
+    const int s, g;
+    Raw ra, rb;
+
+    __device__ __forceinline__ RopeWarp(const RopeArgs& r, int D) : u(r, D, W, threadIdx.x & (L - 1)), s(threadIdx.x & (L - 1)), g((threadIdx.x & 31) / L) {
+        ra.clear();  // (a lane without dims adds zeros to its head's sum)
+        rb.clear();
     }
-    unsigned long long w0[W / 2], w1[W / 2];
-    if (set.weight && u.in) {
-        weight_vec<W>(set.weight, w_type, u.e0, w0);
-        weight_vec<W>(set.weight, w_type, u.e1, w1);
+    __device__ __forceinline__ void start(const HeadSet& set, int64_t row, int h0, int h1) {
+        if (!u.in || h0 + g >= h1) return;
+        const T* x = static_cast<const T*>(set.x) + row * set.xt + (h0 + g) * set.xh + u.e0;
+        ra.load(x);
+        rb.load(x + u.e1 - u.e0);
     }
-    const float mean = 1.0f / static_cast<float>(D);
-    for (int h = h0 + g; h - g < h1; h += kAhead * G) {  // (a warp's lanes stay together)
-        unsigned long long a[kAhead][W / 2], b[kAhead][W / 2];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
+    __device__ __forceinline__ void run(const HeadSet& set, const RopeArgs& r, int D, float eps, const float* angles, const float* weights, int64_t row, int h0, int h1) {
+        const T* x = static_cast<const T*>(set.x) + row * set.xt + (h0 + g) * set.xh + u.e0;
+        T* out = static_cast<T*>(set.out) + row * set.ot + (h0 + g) * set.oh + u.e0;
+        const int64_t xs = G * set.xh, os = G * set.oh;
+        const int second = u.e1 - u.e0, lanes = D / (2 * W), turning = r.rot / (2 * W);
+        const float4* aw = reinterpret_cast<const float4*>(angles) + s;
+        const float4* ww = reinterpret_cast<const float4*>(weights) + s;
+        int left = u.in ? h1 - h0 - g : 0;  // heads from the lane's on
+#pragma unroll 1
+        for (int n = h1 - h0; n > 0; n -= G, left -= G) {  // (a warp's lanes stay together)
+            unsigned long long a[W / 2], b[W / 2];
 #pragma unroll
             for (int e = 0; e < W / 2; ++e) {
-                a[i][e] = pk2(raw[i][0].get(2 * e), raw[i][0].get(2 * e + 1));
-                b[i][e] = pk2(raw[i][1].get(2 * e), raw[i][1].get(2 * e + 1));
+                a[e] = pk2(ra.get(2 * e), ra.get(2 * e + 1));
+                b[e] = pk2(rb.get(2 * e), rb.get(2 * e + 1));
             }
-        load(h + kAhead * G);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+            x += xs;
+            if (left > G) {
+                ra.load(x);
+                rb.load(x + second);
+            }
             if (set.weight) {
-                unsigned long long s2 = 0;
+                unsigned long long s2 = mul2(a[0], a[0]);
 #pragma unroll
-                for (int e = 0; e < W / 2; ++e) s2 = fma2(b[i][e], b[i][e], fma2(a[i][e], a[i][e], s2));
+                for (int e = 1; e < W / 2; ++e) s2 = fma2(a[e], a[e], s2);
+#pragma unroll
+                for (int e = 0; e < W / 2; ++e) s2 = fma2(b[e], b[e], s2);
                 const float2 f = up2(s2);
                 float ss = f.x + f.y;
 #pragma unroll
                 for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float inv = rsqrtf(fmaf(ss, mean, eps));
+                const float inv = rsqrtf(fmaf(ss, 1.0f / static_cast<float>(D), eps));
                 const unsigned long long ii = pk2(inv, inv);
+                if (u.in) {
 #pragma unroll
-                for (int e = 0; e < W / 2; ++e) {
-                    a[i][e] = mul2(mul2(a[i][e], ii), w0[e]);
-                    b[i][e] = mul2(mul2(b[i][e], ii), w1[e]);
+                    for (int c = 0; c < W / 4; ++c) {
+                        const float4 p = ww[c * lanes], q = ww[(W / 4 + c) * lanes];
+                        a[2 * c] = mul2(mul2(a[2 * c], ii), pk2(p.x, p.y));
+                        a[2 * c + 1] = mul2(mul2(a[2 * c + 1], ii), pk2(p.z, p.w));
+                        b[2 * c] = mul2(mul2(b[2 * c], ii), pk2(q.x, q.y));
+                        b[2 * c + 1] = mul2(mul2(b[2 * c + 1], ii), pk2(q.z, q.w));
+                    }
                 }
             }
-            if (u.turn) rope_turn<W>(a[i], b[i], c, sn, r.inter);
-            if (u.in && h + i * G < h1) {
-                T* p = out + (h + i * G) * set.oh;
-                store_vec<TYPE>(p + u.e0, set.ovec, a[i]);
-                store_vec<TYPE>(p + u.e1, set.ovec, b[i]);
+            if (u.turn) rope_turn<W>(a, b, aw, turning, r.inter);
+            if (left > 0) {
+                Raw y;
+                y.put(a);
+                y.store(out);
+                y.put(b);
+                y.store(out + second);
             }
+            out += os;
         }
     }
-}
+};
 
 #endif
 

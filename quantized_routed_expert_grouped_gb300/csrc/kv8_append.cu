@@ -15,8 +15,8 @@ namespace {
 
 constexpr int kThreads = kKvThreads;
 
-// The angles of a block: per token, four chunks of two pairs (cos, sin, cos, sin) for each of the rot / 16 units, chunk by
-// chunk; a token's row is an odd multiple of 64 bytes, so that the eight lanes of an access (two tokens) share no bank.
+// The angles of a block: a token's row (put_angle) is an odd multiple of 64 bytes, so that the eight lanes of an access (two
+// tokens) share no bank.
 __host__ __device__ inline int angle_row(int rot) { return rot / 4 + (rot / 16 % 2 ? 0 : 4); }  // in float4
 
 template <int TYPE, int NB>
@@ -30,11 +30,9 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
     const bool kin = kt >= s.t0 && kt < s.t1, vin = vt >= s.t0 && vt < s.t1;
     const int row4 = angle_row(a.r.rot), units = a.r.rot / 16;
     if (a.r.rot) {
-        float2* to = reinterpret_cast<float2*>(angles);
         for (int i = threadIdx.x; i < (s.t1 - s.t0) * units * 8; i += kThreads) {
-            const int t = s.t0 + i / (units * 8), p = i - (t - s.t0) * units * 8, u = p >> 3, j = p & 7;
-            const int pos = a.positions ? gload(a.positions + s.row + t) : s.blk * 32 + t;
-            to[(t * row4 + (j >> 1) * units + u) * 2 + (j & 1)] = rope_angle(a.r, pos, rope_pair(a.r, 8, u, j));
+            const int t = s.t0 + i / (units * 8);
+            put_angle<8>(reinterpret_cast<float*>(angles + t * row4), a.r, a.positions ? gload(a.positions + s.row + t) : s.blk * 32 + t, i - (t - s.t0) * units * 8);
         }
         __syncthreads();
     }
@@ -94,17 +92,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
             const int u = 4 * n + (lane & 3);
-            if (!kin || u >= units) continue;
-            float c[8], sn[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 f = angles[kt * row4 + j * units + u];
-                c[2 * j] = f.x;
-                sn[2 * j] = f.y;
-                c[2 * j + 1] = f.z;
-                sn[2 * j + 1] = f.w;
-            }
-            rope_turn<8>(x[n][0], x[n][1], c, sn, a.r.inter);
+            if (kin && u < units) rope_turn<8>(x[n][0], x[n][1], angles + kt * row4 + u, units, a.r.inter);
         }
         float mk = 0.0f;
 #pragma unroll
@@ -165,6 +153,26 @@ constexpr int lanes_of(int type, int nb) {
     return n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : 32;
 }
 
+template <int TYPE, int NB, bool VEC>
+__device__ __forceinline__ void append_queries(const AppendArgs& a, const KvSlot& s, int h0, int h1, float* sm) {
+    using Warp = RopeWarp<TYPE, lanes_of(TYPE, NB), VEC>;
+    const int n = s.t1 - s.t0, half = a.r.rot / 2, first = s.t0 + (threadIdx.x >> 5);
+    float* qw = sm + n * a.r.rot;
+    Warp w(a.r, NB * 32);
+    if (first < s.t1) w.start(a.q, s.row + first, h0, h1);
+    for (int i = threadIdx.x; i < n * half; i += kThreads) {
+        const int t = i / half, at = s.t0 + t;
+        put_angle<Warp::W>(sm + t * a.r.rot, a.r, a.positions ? gload(a.positions + s.row + at) : s.blk * 32 + at, i - t * half);
+    }
+    if (a.q.weight) put_weights<Warp::W>(qw, a.r, NB * 32, a.q.weight, a.w_type);
+    __syncthreads();
+#pragma unroll 1
+    for (int t = first; t < s.t1; t += kThreads / 32) {
+        if (t != first) w.start(a.q, s.row + t, h0, h1);
+        w.run(a.q, a.r, NB * 32, a.eps, sm + (t - s.t0) * a.r.rot, qw, s.row + t, h0, h1);
+    }
+}
+
 template <int TYPE, int NB>
 __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendArgs a) {
     extern __shared__ __align__(16) float4 angles[];
@@ -179,8 +187,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendArgs a
         return;
     }
     const int h0 = (part - a.kparts) * a.qheads, h1 = min(a.q.n, h0 + a.qheads);
-    for (int t = s.t0 + (threadIdx.x >> 5); t < s.t1; t += kThreads / 32)
-        rope_heads<TYPE, lanes_of(TYPE, NB)>(a.q, a.r, NB * 32, a.w_type, a.eps, s.row + t, a.positions ? a.positions + s.row + t : nullptr, s.blk * 32 + t, h0, h1);
+    if (a.q.xvec && a.q.ovec) append_queries<TYPE, NB, true>(a, s, h0, h1, reinterpret_cast<float*>(angles));
+    else append_queries<TYPE, NB, false>(a, s, h0, h1, reinterpret_cast<float*>(angles));
 }
 
 template <int TYPE>
@@ -194,7 +202,8 @@ cudaError_t append_t(AppendArgs& a, cudaStream_t st) {
     a.kparts = (a.c.n_kv + a.kheads - 1) / a.kheads;
     a.qparts = (a.q.n + a.qheads - 1) / a.qheads;
     const unsigned grid = static_cast<unsigned>(slots * (a.kparts + a.qparts));
-    const size_t smem = a.r.rot ? 32 * angle_row(a.r.rot) * sizeof(float4) : 0;
+    const int keys = 32 * angle_row(a.r.rot) * static_cast<int>(sizeof(float4)), queries = rope_smem(a.r.rot, a.c.D, 32);
+    const size_t smem = a.q.n && queries > keys ? queries : keys;
     switch (a.c.D / 32) {
 #define MOE_KV8_CASE(NB) \
     case NB: return launch_kernel(kv8_append_kernel<TYPE, NB>, dim3(grid), dim3(kThreads), smem, st, true, a);

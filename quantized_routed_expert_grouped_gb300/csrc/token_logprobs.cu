@@ -50,6 +50,26 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// 16 bytes of a row.
+template <int TYPE>
+struct Vec16 {
+    static constexpr int W = 16 / static_cast<int>(sizeof(typename Elem<TYPE>::T));
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const typename Elem<TYPE>::T* p) {
+        const uint4 v = gload(reinterpret_cast<const uint4*>(p));
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if (TYPE == MOE_F32) return __uint_as_float(w[e & 3]);
+        const uint32_t x = w[(e >> 1) & 3];
+        if (TYPE == MOE_BF16) return __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16);
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(e & 1 ? x >> 16 : x & 0xffffu)));
+    }
+};
+
 // Larger for larger values, 0 for NaN (-0 counts as 0).
 __device__ __forceinline__ uint32_t order(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);
@@ -91,7 +111,7 @@ struct Stats {
 
 // The largest of a thread's tile. (A NaN does not count.)
 template <int TYPE>
-__device__ __forceinline__ float max_of(const RawVec<TYPE> (&v)[kUnroll]) {
+__device__ __forceinline__ float max_of(const Vec16<TYPE> (&v)[kUnroll]) {
     if constexpr (TYPE == MOE_F32) {
         float mx = -INFINITY;
 #pragma unroll
@@ -113,7 +133,7 @@ __device__ __forceinline__ float max_of(const RawVec<TYPE> (&v)[kUnroll]) {
 template <int TYPE>
 constexpr float kLow = TYPE == MOE_F16 ? -65504.0f : -1.329227995784916e36f;  // -2^120
 template <int TYPE>
-__device__ __forceinline__ void clamp_low(RawVec<TYPE>& v) {
+__device__ __forceinline__ void clamp_low(Vec16<TYPE>& v) {
     if constexpr (TYPE != MOE_F32) {
         using H = typename std::conditional<TYPE == MOE_F16, __half2, __nv_bfloat162>::type;
         const uint32_t low = TYPE == MOE_F16 ? 0xfbfffbffu : 0xfb80fb80u;
@@ -145,7 +165,7 @@ __device__ __forceinline__ unsigned long long merged_keys(unsigned long long k, 
 
 template <int TYPE, int NT>
 __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kernel(const LogprobArgs a) {
-    using Raw = RawVec<TYPE>;
+    using Raw = Vec16<TYPE>;
     using T = typename Elem<TYPE>::T;
     constexpr int W = Raw::W, kTile = NT * kUnroll;  // vectors of a tile
     constexpr int kHot = NT == 32 ? 32 : NT == 128 ? 48 : 64, kCap = kTop + kHot * kSpan * kUnroll * W;  // threads' spans to be looked through at once, and their keys
@@ -243,11 +263,11 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
         const T* p = xv + static_cast<int64_t>(from + tid) * W;
         if (from + kTile <= v1) {
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) raw[i].load(p + i * NT * W, true);
+            for (int i = 0; i < kUnroll; ++i) raw[i].load(p + i * NT * W);
         } else {
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
-                if (from + i * NT + tid < v1) raw[i].load(p + i * NT * W, true);
+                if (from + i * NT + tid < v1) raw[i].load(p + i * NT * W);
                 else raw[i].w[0] = raw[i].w[1] = raw[i].w[2] = raw[i].w[3] = kNone;
             }
         }
@@ -336,7 +356,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
 #pragma unroll 1
                         for (int v = at + tid; v < min(at + kSpan * kTile, v1); v += NT) {
                             Raw y;
-                            y.load(xv + static_cast<int64_t>(v) * W, true);
+                            y.load(xv + static_cast<int64_t>(v) * W);
 #pragma unroll
                             for (int e = 0; e < W; ++e) {
                                 const unsigned long long z = key_of(y.get(e), static_cast<uint32_t>(head + v * W + e));
@@ -437,7 +457,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
         };
         for (int v = v0 + tid; v < v1; v += NT) {
             Raw y;
-            y.load(xv + static_cast<int64_t>(v) * W, true);
+            y.load(xv + static_cast<int64_t>(v) * W);
 #pragma unroll
             for (int e = 0; e < W; ++e) one(y.get(e));
         }
@@ -495,7 +515,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
 
 template <int TYPE>
 cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
-    constexpr int W = RawVec<TYPE>::W, kTile = NTB * kUnroll;
+    constexpr int W = Vec16<TYPE>::W, kTile = NTB * kUnroll;
     // CTAs of a row: until every SM has two, and while each still has a whole tile
     a.cluster = 1;
     while (a.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * a.cluster < 304 && a.V / W / a.cluster > kTile) a.cluster *= 2;
