@@ -36,11 +36,7 @@ __global__ void __launch_bounds__(kThreads, RB) head_norm_rope_kernel(const Head
         if (q0 < q1) w.start(a.q, t0 + first, q0, q1);
         else if (k0 < k1) w.start(a.k, t0 + first, k0, k1);
     }
-    const int half = a.r.rot / 2;
-    for (int i = threadIdx.x; i < n * half; i += kThreads) {
-        const int t = i / half;
-        put_angle<W>(sm + t * a.r.rot, a.r, gload(a.positions + t0 + t), i - t * half);
-    }
+    if (a.r.rot) put_angles<W>(sm, a.r, n, a.r.rot, [&](int t) { return gload(a.positions + t0 + t); });
     if (a.q.weight) put_weights<W>(qw, a.r, a.D, a.q.weight, a.w_type);
     if (a.k.weight) put_weights<W>(kw, a.r, a.D, a.k.weight, a.w_type);
     __syncthreads();

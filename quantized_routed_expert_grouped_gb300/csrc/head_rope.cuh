@@ -130,14 +130,14 @@ __device__ __forceinline__ int rope_pair(const RopeArgs& r, int W, int s, int j)
     return j < W / 2 ? s * (W / 2) + j : r.rot / 4 + s * (W / 2) + j - W / 2;
 }
 
-// factor * (cos, sin) of the pair's angle at a position.
-__device__ __forceinline__ float2 rope_angle(const RopeArgs& r, int position, int pair) {
-    const uint64_t at = gload(r.turns + pair) * static_cast<uint64_t>(static_cast<int64_t>(position));
+// factor * (cos, sin) of position * turns.
+__device__ __forceinline__ float2 rope_angle(uint64_t turns, int position, float factor) {
+    const uint64_t at = turns * static_cast<uint64_t>(static_cast<int64_t>(position));
     const uint32_t quarter = static_cast<uint32_t>((at + (1ull << 61)) >> 62);
     const float t = static_cast<float>(static_cast<int64_t>(at - (static_cast<uint64_t>(quarter) << 62))) * 3.4061215800086834e-19f;  // 2 pi / 2^64
     const float z = t * t;
-    const float s = t * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f) * r.factor;
-    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f) * r.factor;
+    const float s = t * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f) * factor;
+    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f) * factor;
     const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;  // quarter turns: (c, s), (-s, c), (-c, -s), (s, -c)
     return make_float2((quarter + 1) & 2 ? -x : x, quarter & 2 ? -y : y);
 }
@@ -191,15 +191,22 @@ __device__ __forceinline__ void weight_vec(const void* w, int w_type, int at, un
 // The shared memory of a CTA: angles of up to T tokens, then the weights of queries and of keys.
 __host__ __device__ inline int rope_smem(int rot, int D, int T) { return (T * rot + 2 * D) * 4; }
 
-// One token's angles, rot / 4 chunks of two pairs (both cosines, both sines, as packed arithmetic takes them): chunk j / 2 of lane s at
-// (j / 2) * lanes + s.
-template <int W>
-__device__ __forceinline__ void put_angle(float* to, const RopeArgs& r, int position, int i) {
-    const int lanes = r.rot / (2 * W), s = i / W, j = i - s * W;
-    const float2 f = rope_angle(r, position, rope_pair(r, W, s, j));
-    to += ((j >> 1) * lanes + s) * 4 + (j & 1);
-    to[0] = f.x;
-    to[2] = f.y;
+// The angles of n tokens, by the CTA. A token's are rot / 4 chunks of two pairs (both cosines, both sines, as packed arithmetic takes
+// them), chunk j / 2 of lane s at (j / 2) * lanes + s; tokens lie `row` floats apart. A thread has one pair of every
+// so many tokens. place(t): the token's position.
+template <int W, typename F>
+__device__ __forceinline__ void put_angles(float* to, const RopeArgs& r, int n, int row, F place) {
+    const int half = r.rot / 2, lanes = r.rot / (2 * W), each = max(1, static_cast<int>(blockDim.x) / half);
+    const int first = threadIdx.x / half;  // (half <= blockDim.x)
+    if (first >= each) return;
+    const int i = threadIdx.x - first * half, s = i / W, j = i - s * W;
+    const uint64_t turns = gload(r.turns + rope_pair(r, W, s, j));
+    to += ((j >> 1) * lanes + s) * 4 + (j & 1) + first * row;
+    for (int t = first; t < n; t += each, to += each * row) {
+        const float2 f = rope_angle(turns, place(t), r.factor);
+        to[0] = f.x;
+        to[2] = f.y;
+    }
 }
 // A set's weights as fp32: chunk c (of four) of lane s at c * lanes + s; the second vector's after all of the first's.
 template <int W>

@@ -19,6 +19,11 @@ constexpr int kThreads = kKvThreads;
 // tokens) share no bank.
 __host__ __device__ inline int angle_row(int rot) { return rot / 4 + (rot / 16 % 2 ? 0 : 4); }  // in float4
 
+// What token t of the block turns by.
+__device__ __forceinline__ int turn_at(const AppendArgs& a, const KvSlot& s, int t) {
+    return a.positions ? gload(a.positions + s.row + t) : s.blk * kKvBlock + t;
+}
+
 template <int TYPE, int NB>
 __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& s, int h0, int h1, float4* angles) {
     constexpr int D = NB * 32, NU = (NB + 1) / 2;
@@ -30,10 +35,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
     const bool kin = kt >= s.t0 && kt < s.t1, vin = vt >= s.t0 && vt < s.t1;
     const int row4 = angle_row(a.r.rot), units = a.r.rot / 16;
     if (a.r.rot) {
-        for (int i = threadIdx.x; i < (s.t1 - s.t0) * units * 8; i += kThreads) {
-            const int t = s.t0 + i / (units * 8);
-            put_angle<8>(reinterpret_cast<float*>(angles + t * row4), a.r, a.positions ? gload(a.positions + s.row + t) : s.blk * 32 + t, i - (t - s.t0) * units * 8);
-        }
+        put_angles<8>(reinterpret_cast<float*>(angles + s.t0 * row4), a.r, s.t1 - s.t0, row4 * 4, [&](int t) { return turn_at(a, s, s.t0 + t); });
         __syncthreads();
     }
 #pragma unroll 1
@@ -156,14 +158,11 @@ constexpr int lanes_of(int type, int nb) {
 template <int TYPE, int NB, bool VEC>
 __device__ __forceinline__ void append_queries(const AppendArgs& a, const KvSlot& s, int h0, int h1, float* sm) {
     using Warp = RopeWarp<TYPE, lanes_of(TYPE, NB), VEC>;
-    const int n = s.t1 - s.t0, half = a.r.rot / 2, first = s.t0 + (threadIdx.x >> 5);
+    const int n = s.t1 - s.t0, first = s.t0 + (threadIdx.x >> 5);
     float* qw = sm + n * a.r.rot;
     Warp w(a.r, NB * 32);
     if (first < s.t1) w.start(a.q, s.row + first, h0, h1);
-    for (int i = threadIdx.x; i < n * half; i += kThreads) {
-        const int t = i / half, at = s.t0 + t;
-        put_angle<Warp::W>(sm + t * a.r.rot, a.r, a.positions ? gload(a.positions + s.row + at) : s.blk * 32 + at, i - t * half);
-    }
+    if (a.r.rot) put_angles<Warp::W>(sm, a.r, n, a.r.rot, [&](int t) { return turn_at(a, s, s.t0 + t); });
     if (a.q.weight) put_weights<Warp::W>(qw, a.r, NB * 32, a.q.weight, a.w_type);
     __syncthreads();
 #pragma unroll 1
@@ -173,8 +172,22 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, const KvSlot
     }
 }
 
+#ifndef MANY
+#define MANY (152 * 16)
+#endif
+#ifndef AC
+#define AC 7
+#endif
+#ifndef KH
+#define KH 8
+#endif
+#ifndef QH
+#define QH 16
+#endif
+constexpr int append_ctas(int type, int nb) { return nb <= 4 ? type == MOE_F32 ? 5 : AC : nb <= 6 ? 4 : 3; }
+
 template <int TYPE, int NB>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, append_ctas(TYPE, NB)) kv8_append_kernel(const AppendArgs a) {
     extern __shared__ __align__(16) float4 angles[];
     const int parts = a.kparts + a.qparts;
     const int slot = blockIdx.x / parts, part = blockIdx.x - slot * parts;
@@ -196,9 +209,9 @@ cudaError_t append_t(AppendArgs& a, cudaStream_t st) {
     const int64_t slots = kv8_slots(a.n_tokens, a.c.n_seqs);
     // Heads of a CTA: one of the keys, a round or two of the queries, where there are few blocks; with many, four and 32, which
     // the block's angles serve.
-    const bool many = slots * a.c.n_kv > 152 * 16;
-    a.kheads = many ? 4 : 1;
-    a.qheads = many ? 32 : 8;
+    const bool many = slots * a.c.n_kv > MANY;
+    a.kheads = many ? KH : 1;
+    a.qheads = many ? QH : 8;
     a.kparts = (a.c.n_kv + a.kheads - 1) / a.kheads;
     a.qparts = (a.q.n + a.qheads - 1) / a.qheads;
     const unsigned grid = static_cast<unsigned>(slots * (a.kparts + a.qparts));
