@@ -24,36 +24,49 @@ __device__ __forceinline__ int turn_at(const AppendArgs& a, const KvSlot& s, int
     return a.positions ? gload(a.positions + s.row + t) : s.blk * kKvBlock + t;
 }
 
+// the largest magnitude (a NaN stays)
+__device__ __forceinline__ float amax3(float m, float a, float b) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(a), "f"(b));
+    return d;
+}
+
 template <int TYPE, int NB>
 __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& s, int h0, int h1, float4* angles) {
-    constexpr int D = NB * 32, NU = (NB + 1) / 2;
+    constexpr int D = NB * 32, NU = (NB + 1) / 2, kUnits = D / 16;
     using T = typename Elem<TYPE>::T;
     __shared__ uint32_t red[2][4];
     __shared__ __align__(16) uint8_t turn[D * kKvTurn];
+    __shared__ __align__(16) float weights[D];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int g = lane >> 2, kt = 8 * (g >> 1) + 2 * wid + (g & 1), vt = wid * 8 + g;
     const bool kin = kt >= s.t0 && kt < s.t1, vin = vt >= s.t0 && vt < s.t1;
-    const int row4 = angle_row(a.r.rot), units = a.r.rot / 16;
-    if (a.r.rot) {
-        put_angles<8>(reinterpret_cast<float*>(angles + s.t0 * row4), a.r, s.t1 - s.t0, row4 * 4, [&](int t) { return turn_at(a, s, s.t0 + t); });
-        __syncthreads();
+    const int row4 = angle_row(a.r.rot), turning = a.r.rot / 16;
+    uint8_t* rec = kv8_record(a.c, s.b, s.blk, h0, a.err);
+    if (!rec) return;  // (the CTA's heads share the page)
+    if (a.r.rot) put_angles<8>(reinterpret_cast<float*>(angles + s.t0 * row4), a.r, s.t1 - s.t0, row4 * 4, [&](int t) { return turn_at(a, s, s.t0 + t); });
+    if (a.k_weight) put_weights<8>(weights, a.r, D, a.k_weight, a.w_type);
+    if (a.r.rot || a.k_weight) __syncthreads();
+    int e0[NU], e1[NU];  // a lane's units of its token, -1: none
+#pragma unroll
+    for (int n = 0; n < NU; ++n) {
+        const RopeUnit u(a.r, D, 8, 4 * n + (lane & 3));
+        e0[n] = u.in ? u.e0 : -1;
+        e1[n] = u.e1;
     }
+    const T* kb = static_cast<const T*>(a.k) + (s.row + kt) * a.kt + h0 * a.kh;
+    const T* vb = static_cast<const T*>(a.v) + (s.row + vt) * a.vt + h0 * a.vh + (lane & 3) * 8;
 #pragma unroll 1
-    for (int h = h0; h < h1; ++h) {
-        uint8_t* rec = kv8_record(a.c, s.b, s.blk, h, a.err);
-        if (!rec) return;  // (the CTA's heads share the page)
-        const T* kb = static_cast<const T*>(a.k) + (s.row + kt) * a.kt + h * a.kh;
-        const T* vb = static_cast<const T*>(a.v) + (s.row + vt) * a.vt + h * a.vh + (lane & 3) * 8;
+    for (int h = h0; h < h1; ++h, kb += a.kh, vb += a.vh, rec += a.c.page_blocks * a.c.rec) {
         const float2 old2 = s.t0 > 0 ? *reinterpret_cast<const float2*>(rec) : make_float2(0.0f, 0.0f);
         Raw8<TYPE> k[NU][2], v[NB];
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
-            const RopeUnit u(a.r, D, 8, 4 * n + (lane & 3));
             k[n][0].clear();
             k[n][1].clear();
-            if (kin && u.in) {
-                k[n][0].load(kb + u.e0, a.kvec);
-                k[n][1].load(kb + u.e1, a.kvec);
+            if (kin && e0[n] >= 0) {
+                k[n][0].load(kb + e0[n], a.kvec);
+                k[n][1].load(kb + e1[n], a.kvec);
             }
         }
 #pragma unroll
@@ -62,50 +75,54 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
             if (vin) v[n].load(vb + n * 32, a.vvec);
         }
         // ---- keys: norm, rotation
-        unsigned long long x[NU][2][4], s2 = 0;
+        unsigned long long x[NU][2][4];
 #pragma unroll
         for (int n = 0; n < NU; ++n)
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[n][w][e] = pk2(k[n][w].get(2 * e), k[n][w].get(2 * e + 1));
-                    s2 = fma2(x[n][w][e], x[n][w][e], s2);
-                }
+                for (int e = 0; e < 4; ++e) x[n][w][e] = pk2(k[n][w].get(2 * e), k[n][w].get(2 * e + 1));
         if (a.k_weight) {
+            unsigned long long s2 = 0;
+#pragma unroll
+            for (int n = 0; n < NU; ++n)
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s2 = fma2(x[n][w][e], x[n][w][e], s2);
             const float2 f = up2(s2);
             float ss = f.x + f.y;
             ss += __shfl_xor_sync(0xffffffffu, ss, 1);
             ss += __shfl_xor_sync(0xffffffffu, ss, 2);
             const float inv = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
+            const unsigned long long ii = pk2(inv, inv);
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
-                const RopeUnit u(a.r, D, 8, 4 * n + (lane & 3));
-                if (!u.in) continue;
+                if (e0[n] < 0) continue;
+                const float4* ww = reinterpret_cast<const float4*>(weights) + 4 * n + (lane & 3);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    unsigned long long ww[4];
-                    weight_vec<8>(a.k_weight, a.w_type, w ? u.e1 : u.e0, ww);
+                for (int w = 0; w < 2; ++w)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[n][w][e] = mul2(mul2(x[n][w][e], pk2(inv, inv)), ww[e]);
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        const float4 y = ww[(2 * w + e) * kUnits];
+                        x[n][w][2 * e] = mul2(mul2(x[n][w][2 * e], ii), pk2(y.x, y.y));
+                        x[n][w][2 * e + 1] = mul2(mul2(x[n][w][2 * e + 1], ii), pk2(y.z, y.w));
+                    }
             }
-        }
-#pragma unroll
-        for (int n = 0; n < NU; ++n) {
-            const int u = 4 * n + (lane & 3);
-            if (kin && u < units) rope_turn<8>(x[n][0], x[n][1], angles + kt * row4 + u, units, a.r.inter);
         }
         float mk = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NU; ++n)
+        for (int n = 0; n < NU; ++n) {
+            const int u = 4 * n + (lane & 3);
+            if (kin && u < turning) rope_turn<8>(x[n][0], x[n][1], angles + kt * row4 + u, turning, a.r.inter);
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 f = up2(x[n][w][e]);
-                    mk = max_nan(mk, max_nan(fabsf(f.x), fabsf(f.y)));
+                    mk = amax3(mk, f.x, f.y);
                 }
+        }
         uint32_t ak = __float_as_uint(mk), av = 0;  // magnitudes order as their bits do (a NaN is above all)
 #pragma unroll
         for (int n = 0; n < NB; ++n) av = v[n].amax(av);
@@ -126,8 +143,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
         if (kin) {
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
-                const RopeUnit u(a.r, D, 8, 4 * n + (lane & 3));
-                if (!u.in) continue;
+                if (e0[n] < 0) continue;
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     uint2 q = make_uint2(0x80808080u, 0x80808080u);  // a block without a scale (zeros, or not finite)
@@ -141,7 +157,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
                         q.x = pack4(lo2(y[0]), hi2(y[0]), lo2(y[1]), hi2(y[1]));
                         q.y = pack4(lo2(y[2]), hi2(y[2]), lo2(y[3]), hi2(y[3]));
                     }
-                    *reinterpret_cast<uint2*>(rec + kv8_k_at(D, kt, w ? u.e1 : u.e0)) = q;
+                    *reinterpret_cast<uint2*>(rec + kv8_k_at(D, kt, w ? e1[n] : e0[n])) = q;
                 }
             }
         }
@@ -179,7 +195,7 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, const KvSlot
 #define AC 7
 #endif
 #ifndef KH
-#define KH 8
+#define KH 4
 #endif
 #ifndef QH
 #define QH 16
