@@ -28,6 +28,9 @@
 #ifndef NTB
 #define NTB 256
 #endif
+#ifndef CLIM
+#define CLIM 304
+#endif
 #ifndef MINB
 #define MINB (1024 / NTB)
 #endif
@@ -163,24 +166,33 @@ __device__ __forceinline__ unsigned long long merged_keys(unsigned long long k, 
     return k;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 template <int TYPE, int NT>
 __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kernel(const LogprobArgs a) {
     using Raw = Vec16<TYPE>;
     using T = typename Elem<TYPE>::T;
     constexpr int W = Raw::W, kTile = NT * kUnroll;  // vectors of a tile
     constexpr int kHot = NT == 32 ? 32 : NT == 128 ? 48 : 64, kCap = kTop + kHot * kSpan * kUnroll * W;  // threads' spans to be looked through at once, and their keys
+    constexpr int kFew = 4 * (NT / 32);  // spans that are looked through sooner than sifted
     constexpr uint32_t kNone = TYPE == MOE_F32 ? 0xff800000u : TYPE == MOE_F16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf
-    __shared__ unsigned long long list[kCap];  // the best keys in order, then new ones
+    __shared__ __align__(16) unsigned long long list[kCap];  // the best keys in order, then new ones
     __shared__ __align__(16) unsigned long long work[NT == 32 ? kHot + kTop : kMaxCluster * kTop];
-    __shared__ unsigned long long bar;  // a raised bar
+    __shared__ unsigned long long bar;  // a raised bar: a key, order() of a value
+    __shared__ uint32_t raised;
     __shared__ uint32_t hot_max[kHot];  // spans of threads with logits above the bar: their maxima and first vectors
     __shared__ int hot_at[kHot], hots, listed;  // (listed: keys in order)
-    __shared__ Stats stat[NT / 32 + 1];  // of the warps, of the CTA
+    __shared__ Stats stat[NT / 32];                           // of the warps
+    __shared__ Stats all[2][kMaxCluster];                     // of the row's CTAs; once more
+    __shared__ unsigned long long best_of[NT == 32 ? 1 : kMaxCluster * kTop];  // their best keys
+    __shared__ int ids[NT];
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 31;
     const int C = a.cluster, rank = blockIdx.x % C, row = blockIdx.x / C;
     if (tid == 0) count = hots = listed = 0;
     __syncthreads();
+    if (C > 1) cluster_arrive();
     pdl_wait();
     pdl_trigger();
     const T* x = static_cast<const T*>(a.x) + row * a.stride;
@@ -191,72 +203,112 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
     Stats st{-INFINITY, 0.0f, 0.0f, -INFINITY};
     uint32_t best = 0;  // the bar: order() of the list's last logit, 0 while the list is not full
     int pending = 0;    // hots at most, as all threads know it
-    // the list in order again (its keys are visible)
-    auto ranked = [&]() {
-        const int n = count, keep = min(n, a.top);
-        for (int i = tid; i < n; i += NT) {
-            const unsigned long long mine = list[i];
-            int above = 0;
-#pragma unroll 8
-            for (int j = 0; j < n; ++j) above += list[j] > mine;
-            if (above < a.top) work[above] = mine;
-        }
-        __syncthreads();
-        if (tid < keep) list[tid] = work[tid];
-        if (tid == 0) count = listed = keep;
-        best = n >= a.top ? static_cast<uint32_t>(work[a.top - 1] >> 32) : 0;
-        __syncthreads();
-    };
-    // One thread's span, its first vector v, by a warp, a word or two a lane: keys of values of at least `least`, and of at least `low`.
-    auto look = [&](int v, float least, unsigned long long low) {
+    // Spans of threads (their first vectors; the second may be none, -1) by a warp, a word or two a lane of each: keys of values of at
+    // least `least`, and of at least `low`.
+    auto look = [&](int first, int second, float least, unsigned long long low) {
         constexpr int kWords = kSpan * kUnroll * 4, kEach = (kWords + 31) / 32;
+        uint32_t w[2][kEach];
+        auto fetch = [&](int v, uint32_t (&w)[kEach]) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (i * 32 + lane < kWords && v + i * 8 * NT < v1) w[i] = gload(reinterpret_cast<const uint32_t*>(xv + static_cast<int64_t>(v + i * 8 * NT) * W) + (lane & 3));
+        };
         auto put = [&](float y, uint32_t index) {
             if (y >= least) {
                 const unsigned long long k = key_of(y, index);
                 if (k >= low) list[atomicAdd(&count, 1)] = k;
             }
         };
-        v += (lane >> 2) * NT;
-        uint32_t w[kEach];
+        auto sift = [&](int v, const uint32_t (&w)[kEach]) {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (i * 32 + lane < kWords && v + i * 8 * NT < v1)
-                w[i] = gload(reinterpret_cast<const uint32_t*>(xv + static_cast<int64_t>(v + i * 8 * NT) * W) + (lane & 3));
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (i * 32 + lane >= kWords || v + i * 8 * NT >= v1) continue;
-            const uint32_t index = head + (v + i * 8 * NT) * W + (lane & 3) * (W / 4);
-            if (TYPE == MOE_F32) {
-                put(__uint_as_float(w[i]), index);
-            } else {
-                Raw r;
-                r.w[0] = w[i];
-                put(r.get(0), index);
-                put(r.get(1), index + 1);
+            for (int i = 0; i < kEach; ++i) {
+                if (i * 32 + lane >= kWords || v + i * 8 * NT >= v1) continue;
+                const uint32_t index = head + (v + i * 8 * NT) * W + (lane & 3) * (W / 4);
+                if (TYPE == MOE_F32) {
+                    put(__uint_as_float(w[i]), index);
+                } else {
+                    Raw r;
+                    r.w[0] = w[i];
+                    put(r.get(0), index);
+                    put(r.get(1), index + 1);
+                }
             }
-        }
+        };
+        const int mine = (lane >> 2) * NT;
+        fetch(first + mine, w[0]);
+        if (second >= 0) fetch(second + mine, w[1]);
+        sift(first + mine, w[0]);
+        if (second >= 0) sift(second + mine, w[1]);
     };
-    // The spans that wait (visible to all threads) are looked through: those that reach the top-th best of their maxima and the list.
-    auto flush = [&]() {
-        const int n = hots, keys = listed;  // (pending may count some that a flush has cooled)
-        for (int i = tid; i < n + keys; i += NT) work[i] = i < n ? static_cast<unsigned long long>(hot_max[i]) << 32 : list[i - n] & ~0xffffffffull;
-        if (tid == 0) bar = 0;
-        __syncthreads();
-        for (int i = tid; i < n + keys; i += NT) {
-            const unsigned long long mine = work[i];
+    // The spans that wait are looked through (of many, those that reach the top-th best of their maxima and the list); then the list is put in order.
+    // (What was appended before is visible. Keys below `low`, and values
+    // below `base`, an order(), do not count.)
+    auto flush = [&](unsigned long long low, uint32_t base) {
+        const int n = hots, keys = listed;
+        if (n) {
+            if (tid == 0) raised = base;
+            if (n > kFew) {
+                uint32_t* v = reinterpret_cast<uint32_t*>(work);
+                for (int i = tid; i < (n + keys + 3) / 4 * 4; i += NT) v[i] = i < n ? hot_max[i] : i < n + keys ? static_cast<uint32_t>(list[i - n] >> 32) : 0;
+                __syncthreads();
+                for (int i = tid; i < n + keys; i += NT) {
+                    const uint32_t mine = v[i];
+                    int above = 0, same = 0;
+#pragma unroll 4
+                    for (int j = 0; j < (n + keys + 3) / 4; ++j) {
+                        const uint4 y = reinterpret_cast<const uint4*>(v)[j];
+                        above += (y.x > mine) + (y.y > mine) + (y.z > mine) + (y.w > mine);
+                        same += (y.x == mine) + (y.y == mine) + (y.z == mine) + (y.w == mine);
+                    }
+                    if (above < a.top && above + same >= a.top && mine > base) raised = mine;
+                }
+            }
+            __syncthreads();
+            const uint32_t least = max(raised, best ? best + 1 : 0);  // (of a full list, what equals its last comes later)
+            const int mine = (tid >> 5) + lane * (NT / 32);
+            unsigned on = __ballot_sync(0xffffffffu, mine < n && hot_max[mine < n ? mine : 0] >= least);
+            while (on) {
+                const int first = __ffs(on) - 1;
+                on &= on - 1;
+                const int second = __ffs(on) - 1;
+                on &= on - 1;
+                look(hot_at[(tid >> 5) + first * (NT / 32)], second < 0 ? -1 : hot_at[(tid >> 5) + second * (NT / 32)], unorder(least), low);
+            }
+            __syncthreads();
+        }
+        const int m = count, keep = min(m, a.top);
+        for (int i = tid; i < m; i += NT) {
+            const unsigned long long mine = list[i];
             int above = 0;
-#pragma unroll 8
-            for (int j = 0; j < n + keys; ++j) above += work[j] > mine || (work[j] == mine && j < i);
-            if (above == a.top - 1) bar = mine;
+#pragma unroll 4
+            for (int j = 0; j < m / 2; ++j) {
+                const ulonglong2 y = reinterpret_cast<const ulonglong2*>(list)[j];
+                above += (y.x > mine) + (y.y > mine);
+            }
+            if (m & 1) above += list[m - 1] > mine;
+            if (above < a.top) work[above] = mine;
         }
         __syncthreads();
-        const uint32_t least = max(static_cast<uint32_t>(bar >> 32), order(-INFINITY));
-        for (int i = tid >> 5; i < n; i += NT / 32)
-            if (hot_max[i] >= least) look(hot_at[i], unorder(least), 0);
-        __syncthreads();
-        if (tid == 0) hots = 0;
+        if (tid < keep) list[tid] = work[tid];
+        if (tid == 0) {
+            count = listed = keep;
+            hots = 0;
+        }
+        best = m >= a.top ? static_cast<uint32_t>(work[a.top - 1] >> 32) : 0;
         pending = 0;
-        ranked();
+        __syncthreads();
+    };
+    // The 32 largest keys of the first n warps (a power of two), whose lanes have theirs in order; in the first warp.
+    auto merged_lists = [&](unsigned long long k, int n) {
+        const int wid = tid >> 5;
+#pragma unroll 1
+        for (int half = n / 2; half > 0; half >>= 1) {
+            if (wid >= half && wid < 2 * half) work[tid - 32 * half] = k;
+            __syncthreads();
+            if (wid < half) k = merged_keys(k, work[tid ^ 31], lane);
+            __syncthreads();
+        }
+        return k;
     };
     int at = v0;
     auto load = [&](Raw (&raw)[kUnroll], int from) {
@@ -301,39 +353,58 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
     };
     Raw even[kUnroll], odd[kUnroll];
     load(even, at);
-    do {
+    if (rank == 0 && tid < a.n_ids) ids[tid] = gload(a.ids + static_cast<int64_t>(row) * a.n_ids + tid);
+    for (;;) {
+        const bool last = at >= v1;
+        if (last && !pending) break;
         most = -INFINITY;
-        load(odd, at + kTile);
-        add(even);
-        load(even, at + 2 * kTile);
-        if (at + kTile < v1) add(odd);
-        st.m = fmaxf(st.m, most);
+        if (!last) {
+            load(odd, at + kTile);
+            add(even);
+            load(even, at + 2 * kTile);
+            if (at + kTile < v1) add(odd);
+            st.m = fmaxf(st.m, most);
+        }
         // ---- the best keys
         if (a.top) {
             const uint32_t mine = at + tid < v1 ? order(most) : 0;
             bool hot = mine > best;
-            int n_hot = __syncthreads_count(hot);
-            if (n_hot) {
-                auto wait = [&](bool hot) {  // the span is looked through later
-                    if (hot) {
-                        const int i = atomicAdd(&hots, 1);
-                        hot_max[i] = mine;
-                        hot_at[i] = at + tid;
-                    }
-                };
-                if (best && n_hot <= kHot) {
-                    if (pending + n_hot > kHot) {
-                        flush();
-                        hot = mine > best;
-                    }
-                    wait(hot);
-                    pending += n_hot;
-                } else {
-                    if (pending) flush();
-                    // a bar: a maximum that `top` threads reach, as many in each warp
-                    constexpr int kWarps = NT / 32;
+            const int n_hot = __syncthreads_count(hot);
+            const bool few = best && n_hot <= kHot;
+            auto wait = [&]() {  // the span is looked through later
+                if (!hot) return;
+                const int i = atomicAdd(&hots, 1);
+                hot_max[i] = mine;
+                hot_at[i] = at + tid;
+            };
+            // what is to be done, step by step (one place for each, since this code is fetched anew for a CTA's few passes)
+            enum { kNothing, kWait, kRaise, kTies, kFlush };
+            int now = kNothing, then = kNothing;
+            unsigned long long low = 0;
+            uint32_t base = order(-INFINITY);
+            if (last) {
+                now = kFlush;
+            } else if (n_hot && few && pending + n_hot <= kHot) {
+                wait();
+                pending += n_hot;
+            } else if (n_hot) {
+                now = few ? kWait : kRaise;
+                if (pending) {
+                    then = now;
+                    now = kFlush;
+                }
+            }
+            while (now != kNothing) {
+                if (now == kFlush) {
+                    flush(low, base);
+                    hot = mine > best;
+                    now = then;
+                    then = kNothing;
+                    continue;
+                }
+                if (now == kRaise) {  // a bar: a maximum that `top` threads reach, as many in each warp
                     uint32_t m = mine, r = 0;
-                    for (int i = 0; i < a.top; i += kWarps) {
+                    for (int i = 0; i < a.top; i += NT / 32) {
                         r = __reduce_max_sync(0xffffffffu, m);
                         if (m == r) m = 0;
                     }
@@ -342,19 +413,21 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
                     __syncthreads();
                     uint32_t least = low32[0];
 #pragma unroll
-                    for (int w = 1; w < kWarps; ++w) least = min(least, low32[w]);
-                    least = max(least, order(-INFINITY));  // (0: fewer threads than that have any)
-                    hot = mine >= least;
-                    n_hot = __syncthreads_count(hot);
-                    if (n_hot <= min(kHot, NT - 1)) {
-                        wait(hot);
-                        pending = n_hot;
-                        __syncthreads();
-                        flush();
-                    } else {  // ties: the top-th best of the threads' best keys
-                        unsigned long long mine_key = 0;
-#pragma unroll 1
-                        for (int v = at + tid; v < min(at + kSpan * kTile, v1); v += NT) {
+                    for (int w = 1; w < NT / 32; ++w) least = min(least, low32[w]);
+                    base = max(base, least);  // (0: fewer threads than that have any)
+                    hot = mine >= base;
+                    if (__syncthreads_count(hot) > min(kHot, NT - 1)) {
+                        now = kTies;
+                        continue;
+                    }
+                }
+                if (now == kTies) {  // the top-th best of the threads' best keys
+                    unsigned long long mine_key = 0;
+                    if (mine) {
+#pragma unroll 4
+                        for (int i = 0; i < kSpan * kUnroll; ++i) {
+                            const int v = at + i * NT + tid;
+                            if (v >= v1) break;
                             Raw y;
                             y.load(xv + static_cast<int64_t>(v) * W);
 #pragma unroll
@@ -363,49 +436,56 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
                                 mine_key = z > mine_key ? z : mine_key;
                             }
                         }
-                        unsigned long long k = sorted_keys(mine_key, lane);
-#pragma unroll 1
-                        for (int half = kWarps / 2; half > 0; half >>= 1) {
-                            if ((tid >> 5) >= half && (tid >> 5) < 2 * half) work[tid - 32 * half] = k;
-                            __syncthreads();
-                            if ((tid >> 5) < half) k = merged_keys(k, work[tid ^ 31], lane);
-                            __syncthreads();
-                        }
-                        if (tid == a.top - 1) bar = k;  // (0: fewer threads than that have any)
-                        __syncthreads();
-                        hot = mine_key && mine_key >= bar;
-                        for (unsigned who = __ballot_sync(0xffffffffu, hot); who; who &= who - 1) look(at + (tid & ~31) + __ffs(who) - 1, -INFINITY, bar);
-                        __syncthreads();
-                        ranked();
                     }
+                    const unsigned long long k = merged_lists(sorted_keys(mine_key, lane), NT / 32);
+                    if (tid == a.top - 1) bar = k;  // (0: fewer threads than that have any)
+                    __syncthreads();
+                    low = bar;
+                    base = order(-INFINITY);
+                    hot = mine_key && mine_key >= low;
+                }
+                wait();
+                pending += now == kWait ? n_hot : kHot;
+                if (now != kWait) {
+                    __syncthreads();
+                    now = kFlush;
+                } else {
+                    now = kNothing;
                 }
             }
         }
+        if (last) break;
         at += kSpan * kTile;
-    } while (at < v1);
+    }
     // a given token's logit, on its way meanwhile
     int id = -1;
     float given = 0.0f;
     if (rank == 0 && tid < a.n_ids) {
-        id = gload(a.ids + static_cast<int64_t>(row) * a.n_ids + tid);
+        id = ids[tid];
         if (id >= 0 && id < a.V) given = Elem<TYPE>::get(gload(x + id));
     }
     // single logits: of the row's start threads 0 .., of its end threads 8 ..
     int single = -1;
     if (rank == 0 && tid < head) single = tid;
     if (rank == C - 1 && tid >= 8 && tid < 8 + tail) single = head + nv * W + tid - 8;
-    if (a.top) {
-        __syncthreads();
-        if (pending) flush();
-        if (C == 1 ? head + tail : rank == 0 ? head : rank == C - 1 ? tail : 0) {
-            unsigned long long k = 0;
-            if (single >= 0) k = key_of(Elem<TYPE>::get(gload(x + single)), static_cast<uint32_t>(single));
-            const bool more = k && (!best || k > list[a.top - 1]);
-            if (__syncthreads_count(more)) {
-                if (more) list[atomicAdd(&count, 1)] = k;
-                __syncthreads();
-                ranked();
+    if (a.top && (C == 1 ? head + tail : rank == 0 ? head : rank == C - 1 ? tail : 0)) {
+        unsigned long long k = 0;
+        if (single >= 0) k = key_of(Elem<TYPE>::get(gload(x + single)), static_cast<uint32_t>(single));
+        const bool more = k && (!best || k > list[a.top - 1]);
+        if (__syncthreads_count(more)) {  // into its place (their keys are few)
+            if (more) list[atomicAdd(&count, 1)] = k;
+            __syncthreads();
+            const int m = count;
+            for (int i = tid; i < m; i += NT) {
+                const unsigned long long mine = list[i];
+                int above = 0;
+                for (int j = 0; j < m; ++j) above += list[j] > mine;
+                if (above < a.top) work[above] = mine;
             }
+            __syncthreads();
+            if (tid < min(m, a.top)) list[tid] = work[tid];
+            if (tid == 0) count = min(m, a.top);
+            __syncthreads();
         }
     }
     if (single >= 0) {
@@ -418,32 +498,41 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
     }
 
     // ---- the CTA's sums, then the row's
-    auto join = [&]() {
+    auto join = [&](int pass) {
         st.template join<32>();
         if (NT > 32) {
             if (lane == 0) stat[tid >> 5] = st;
             __syncthreads();
-            if (tid < 32) {
+        }
+        if (tid < 32) {  // to every CTA of the row, and the best keys to the first
+            if (NT > 32) {
                 st = stat[lane & (NT / 32 - 1)];
                 st.template join<NT / 32>();
             }
+            st.r = __shfl_sync(0xffffffffu, st.r, 0);
+            st.s = __shfl_sync(0xffffffffu, st.s, 0);
+            st.u = __shfl_sync(0xffffffffu, st.u, 0);
+            st.m = __shfl_sync(0xffffffffu, st.m, 0);
         }
         if (C > 1) {
             cg::cluster_group cluster = cg::this_cluster();
-            if (tid == 0) stat[NT / 32] = st;
-            cluster.sync();
+            if (!pass) cluster_wait();  // (they have all started)
+            if (tid < C) *cluster.map_shared_rank(&all[pass][rank], tid) = st;
+            if (NT > 32 && !pass && tid < a.top) *cluster.map_shared_rank(best_of + rank * a.top + tid, 0) = tid < count ? list[tid] : 0;
+            cluster_arrive();
+            cluster_wait();
             if (tid < 32) {
-                st = Stats{-INFINITY, 0.0f, 0.0f, -INFINITY};
-                if (lane < C) st = *cluster.map_shared_rank(stat + NT / 32, lane);
+                st = all[pass][lane & (kMaxCluster - 1)];
+                if ((lane & (kMaxCluster - 1)) >= C) st = Stats{-INFINITY, 0.0f, 0.0f, -INFINITY};
                 st.template join<kMaxCluster>();
             }
-            cluster.sync();
+            __syncthreads();
         }
-        if (tid == 0) stat[NT / 32] = st;
+        if (tid == 0) all[pass][0] = st;
         __syncthreads();
-        st = stat[NT / 32];
+        st = all[pass][0];
     };
-    join();
+    join(0);
     // Where c times the row's largest logit is no number to subtract, or a clamped logit would count next to it (rows that are masked by
     // their type's lowest value; scales near 0 or far above 1): once more, with differences first.
     const bool ends = fabsf(st.m) < INFINITY && !(fabsf(st.m * a.c) < 1.2676506e30f && (TYPE == MOE_F32 || ((st.m - kLow<TYPE>) * a.c > 250.0f && -kLow<TYPE> * a.c < 1e38f)));
@@ -464,31 +553,14 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
         if (rank == 0 && tid < head) one(Elem<TYPE>::get(gload(x + tid)));
         if (rank == C - 1 && tid < tail) one(Elem<TYPE>::get(gload(x + head + nv * W + tid)));
         __syncthreads();
-        join();
-    }
-    if (C > 1 && a.top) {  // the row's best keys
-        cg::cluster_group cluster = cg::this_cluster();
-        if (rank == 0) {
-            int some = 0;
-            for (int r = 0; r < C; ++r) some += *cluster.map_shared_rank(&count, r);
-            for (int i = tid; i < C * a.top; i += NT) {
-                const int from = i / a.top, k = i - from * a.top;
-                work[i] = k < *cluster.map_shared_rank(&count, from) ? cluster.map_shared_rank(list, from)[k] : 0;
-            }
-            __syncthreads();
-            for (int i = tid; i < C * a.top; i += NT) {
-                const unsigned long long mine = work[i];
-                int above = 0;
-#pragma unroll 8
-                for (int j = 0; j < C * a.top; ++j) above += work[j] > mine;
-                if (mine && above < a.top) list[above] = mine;
-            }
-            if (tid == 0) count = min(some, a.top);
-            __syncthreads();
-        }
-        cluster.sync();
+        join(1);
     }
     if (rank != 0) return;
+    if (NT > 32 && C > 1 && a.top) {
+        const unsigned long long k = merged_lists(tid >> 5 < C && lane < a.top ? best_of[(tid >> 5) * a.top + lane] : 0, C);
+        if (tid < a.top) list[tid] = k;
+        __syncthreads();
+    }
     const bool none = st.m == -INFINITY && st.s == st.s;  // (a row of NaN is none of -inf)
     const float l2 = log2f(st.s), ls = (l2 - (ends ? 0.0f : fmaf(st.m, a.c, -st.r))) * kLn2;  // log of the sum of e^(scale (x - m))
     auto logprob = [&](float v) { return none ? -INFINITY : (v - st.m) * a.scale - ls; };
@@ -502,8 +574,8 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
     }
     if (tid < a.top) {
         const int64_t to = static_cast<int64_t>(row) * a.top + tid;
-        const bool has = tid < count;
-        const unsigned long long k = has ? list[tid] : 0;
+        const unsigned long long k = C > 1 || tid < count ? list[tid] : 0;
+        const bool has = k != 0;
         a.top_ids[to] = has ? static_cast<int32_t>(~static_cast<uint32_t>(k)) : -1;
         a.top_logprobs[to] = has ? logprob(unorder(static_cast<uint32_t>(k >> 32))) : NAN;
     }
@@ -518,7 +590,7 @@ cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
     constexpr int W = Vec16<TYPE>::W, kTile = NTB * kUnroll;
     // CTAs of a row: until every SM has two, and while each still has a whole tile
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * a.cluster < 304 && a.V / W / a.cluster > kTile) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * a.cluster < CLIM && a.V / W / a.cluster > kTile) a.cluster *= 2;
     a.c = a.scale * kLog2e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.cluster);
