@@ -79,7 +79,7 @@ int moe_kv8_append(const moe_kv8_append_call* call, cudaStream_t stream);
  *   entropy[row] = -sum p log p, lse[row] = log sum e^(scale * x).
  * Logits of -inf have p = 0; a row of nothing else gives -inf, entropy 0, and the first indices. A row with a NaN or +inf
  * gives NaN for all but top_ids, in which NaN logits have no place (-1 behind the last). Sums are fp32. logits: rows row_stride
- * elements apart, on their element's boundary; 0 < vocab < 2^31, 0 <= top <= min(32, vocab), scale > 0 and finite.
+ * elements apart, on their element's boundary; 0 < vocab < 2^31, 0 <= top <= min(32, vocab), scale from 2^-100 to 2^100.
  * entropy and lse may be NULL; logprobs and ids where n_ids is 0, top_* where top is 0. Errors: MOE_E_NULL,
  * MOE_E_TYPE, MOE_E_SHAPE, MOE_E_CAP (rows * max(n_ids, 8) of 2^31 or more), MOE_E_ALIGN, MOE_E_CUDA. */
 typedef struct moe_logprobs_call {

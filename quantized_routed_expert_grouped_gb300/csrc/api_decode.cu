@@ -1,7 +1,5 @@
 // api_decode.cu - the C ABI of moe_decode.h: host-side argument checks and launches. Nothing here reads device memory or
 // allocates.
-#include <cmath>
-
 #include "api_checks.h"
 #include "decode_api.h"
 
@@ -87,7 +85,7 @@ int moe_kv8_append(const moe_kv8_append_call* c, cudaStream_t stream) {
 int moe_token_logprobs(const moe_logprobs_call* c, cudaStream_t stream) {
     if (!c) return MOE_E_NULL;
     if (!valid_elem(c->type)) return MOE_E_TYPE;
-    if (c->rows < 0 || c->vocab <= 0 || c->n_ids < 0 || c->top < 0 || c->top > 32 || c->top > c->vocab || !(c->scale > 0.0f) || !std::isfinite(c->scale) ||
+    if (c->rows < 0 || c->vocab <= 0 || c->n_ids < 0 || c->top < 0 || c->top > 32 || c->top > c->vocab || !(c->scale >= 0x1p-100f && c->scale <= 0x1p100f) ||
         (c->rows > 1 && c->row_stride < c->vocab))
         return MOE_E_SHAPE;
     if (static_cast<int64_t>(c->rows) * (c->n_ids > 8 ? c->n_ids : 8) > 0x7fffffff) return MOE_E_CAP;

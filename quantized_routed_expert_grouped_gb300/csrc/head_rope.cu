@@ -1,22 +1,19 @@
 // head_rope.cu - norm and rotation of the heads of query and key rows in one pass (the mathematics and a lane's share are
 // in head_rope.cuh).
 //
+// A CTA takes up to four tokens. Its warps compute the tokens' angles and lay out the weights in shared memory while
+// each one's first heads are on their way; then a warp takes a token's heads, round after round, with the next round's loads in flight.
+// Bound by memory where there are many rows, else by its chain of latencies.
 #include "decode_api.h"
 
 namespace moe {
 
 namespace {
 
-#ifndef RB
-#define RB 7
-#endif
-#ifndef MAXT
-#define MAXT 4
-#endif
-constexpr int kThreads = 128, kWarps = kThreads / 32, kMaxTokens = MAXT;
+constexpr int kThreads = 128, kWarps = kThreads / 32, kMaxTokens = 4;
 
 template <int TYPE, int L, bool VEC>
-__global__ void __launch_bounds__(kThreads, RB) head_norm_rope_kernel(const HeadRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 7) head_norm_rope_kernel(const HeadRopeArgs a) {
     extern __shared__ __align__(16) float sm[];
     using Warp = RopeWarp<TYPE, L, VEC>;
     constexpr int W = Warp::W, G = Warp::G;
@@ -56,8 +53,8 @@ __global__ void __launch_bounds__(kThreads, RB) head_norm_rope_kernel(const Head
 template <int TYPE, int L, bool VEC>
 cudaError_t rope_l(HeadRopeArgs& a, cudaStream_t st) {
     constexpr int G = 32 / L;
-    // Many tokens: up to eight a CTA, two a warp, so that weights and setting up serve several; few: a token's rounds over the
-    // CTA's warps, and over several CTAs.
+    // Many tokens: up to four a CTA, so that weights and setting up serve several (8191 tokens of 72 heads of 128: 51.7 us, with
+    // eight 52.1, with sixteen 57); few: a token's rounds over the CTA's warps, and over several CTAs.
     const int rounds = (a.q.n + G - 1) / G + (a.k.n + G - 1) / G;
     const int64_t each = a.n / (152 * 6);
     a.tokens = static_cast<int>(each < 1 ? 1 : each > kMaxTokens ? kMaxTokens : each);

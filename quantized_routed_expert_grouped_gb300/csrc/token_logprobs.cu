@@ -1,39 +1,33 @@
 // token_logprobs.cu - log probabilities of given tokens, the most likely tokens, entropy and log-sum-exp of rows of logits,
 // in one pass over them.
 //
-//   t_j = scale (x_j - m),  s = sum e^t_j,  u = sum t_j e^t_j;   lse = scale m + log s,  log p_j = t_j - log s,
-//   entropy = log s - u / s
+//   t_j = c x_j - r,  s = sum 2^t_j,  u = sum t_j 2^t_j   (c = scale log2 e);
+//   log p_j = scale (x_j - m) - l,  l = ln 2 (log2 s - (c m - r)),  lse = scale m + l,  entropy = ln 2 (log2 s - u / s)
 //
-// m is a thread's running maximum, moved once a tile (s and u are rescaled where it grows); threads, then the CTAs of a row,
-// join theirs. Differences come before the product with the scale, so that x_j = m gives 0 exactly and masks of the type's
-// lowest value overflow to -inf at most. In base 2: e^t = 2^((x - m) scale log2 e).
+// m is the row's largest logit. r is a whole number near c times the largest that a thread has seen (kSlack below it at most), so that a
+// logit's exponent is one fused product, rounded once, and what r is does not matter to the result; s and u are rescaled where r
+// moves, which few tiles need. Threads join theirs, then the CTAs of a row, always in the same order. t 2^t of a logit of -inf has to be 0: 16-bit logits
+// are clamped in pairs before they are converted, fp32's t one by one. Where that or c m leaves the range (rows masked by their type's lowest value,
+// scales near 0 or far above 1) the row's sums are taken a second time, differences first. Powers are the hardware's (2^-22 of
+// themselves); sums are fp32, eight of a thread's terms in a row at most before they are added to its two running ones.
 //
 // The most likely tokens. A logit and its index are one 64-bit key, larger for a larger logit and among equal ones for
-// the lower index, so that every order is strict and the result does not depend on timing. A CTA keeps its best `top` keys, the
-// last of which is the bar that a later tile's logit must pass (strictly: its index is higher); a tile with few threads above
-// the bar appends their keys and ranks the list anew. Where many are above it (a row's first tile), the bar first rises to the
-// top-th best of the maxima of 128 pairs of threads: at least `top` keys pass, and no more than 2 `top` threads have any, whatever the
-// logits are. Ranks are counts of larger keys.
+// the lower index: every order is strict, and nothing depends on timing. A CTA keeps its best `top` keys in order; the
+// last one's logit is the bar. Every span of two tiles the threads whose maximum is above it are noted (an equal logit comes later, and
+// loses); kHot of them, or the row's end, are looked through at once: of many only those that reach the top-th best of
+// their maxima and the list, a warp for a span, read again (from L2: kept in registers they cost a quarter of the warps).
+// While the list is not full, or more threads than kHot are above it, a new bar comes first: the least of the warps' maxima of
+// rank top / warps, which `top` threads reach; and where more than kHot reach that (ties: masked rows), the top-th best of
+// the threads' best keys, by sorting networks over lanes and merging over warps, so that never more than kHot spans are looked through,
+// whatever the logits are. Ranks are counts of larger keys.
 //
-// A row is read by a cluster of C CTAs (C a power of two up to 8, where rows are few), which join through distributed
-// shared memory: one launch, no workspace. Rows need no alignment: the elements before a row's first 16-byte boundary and after
-// its last one are taken singly, in its first and last tile.
+// A row is read by a cluster of C CTAs (a power of two up to 8, where rows are few); each sends its sums to all, and its list to the first,
+// through distributed shared memory, behind one barrier: one launch, no workspace. Rows need no alignment: what lies before a
+// row's first 16-byte boundary and after its last one is taken singly, at the end.
 #include <cooperative_groups.h>
 
 #include "decode_api.h"
 
-#ifndef SMALLV
-#define SMALLV 256
-#endif
-#ifndef NTB
-#define NTB 256
-#endif
-#ifndef CLIM
-#define CLIM 304
-#endif
-#ifndef MINB
-#define MINB (1024 / NTB)
-#endif
 namespace moe {
 
 namespace {
@@ -42,6 +36,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kUnroll = 4;  // vectors of a thread's tile
 constexpr int kSpan = 2;    // tiles between two looks for the best keys: one is added while the next is on its way
+constexpr int kWide = 256;  // threads of a CTA, but for short rows
 constexpr int kTop = 32, kMaxCluster = 8;
 constexpr float kFar = -1000.0f;  // an exponent whose power of two is 0
 constexpr float kSlack = 8.0f;    // powers of two above its reference that a thread's maximum may rise
@@ -170,12 +165,12 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 template <int TYPE, int NT>
-__global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(const LogprobArgs a) {
     using Raw = Vec16<TYPE>;
     using T = typename Elem<TYPE>::T;
     constexpr int W = Raw::W, kTile = NT * kUnroll;  // vectors of a tile
     constexpr int kHot = NT == 32 ? 32 : NT == 128 ? 48 : 64, kCap = kTop + kHot * kSpan * kUnroll * W;  // threads' spans to be looked through at once, and their keys
-    constexpr int kFew = 4 * (NT / 32);  // spans that are looked through sooner than sifted
+    constexpr int kFew = 2 * (NT / 32);  // spans that are looked through sooner than sifted
     constexpr uint32_t kNone = TYPE == MOE_F32 ? 0xff800000u : TYPE == MOE_F16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf
     __shared__ __align__(16) unsigned long long list[kCap];  // the best keys in order, then new ones
     __shared__ __align__(16) unsigned long long work[NT == 32 ? kHot + kTop : kMaxCluster * kTop];
@@ -587,15 +582,17 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : MINB) token_logprobs_kerne
 
 template <int TYPE>
 cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
-    constexpr int W = Vec16<TYPE>::W, kTile = NTB * kUnroll;
-    // CTAs of a row: until every SM has two, and while each still has a whole tile
+    constexpr int W = Vec16<TYPE>::W, kTile = kWide * kUnroll;
+    // CTAs of a row: until there are two for every SM, and while each has more than a tile (192 rows of 65,537, fp32, top 20: two of a row 23 us,
+    // four 31, as the keys are picked in each)
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * a.cluster < CLIM && a.V / W / a.cluster > kTile) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * a.cluster < 304 && a.V / W / a.cluster > kTile) a.cluster *= 2;
     a.c = a.scale * kLog2e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.cluster);
-    const bool small = a.V / W <= SMALLV;
-    cfg.blockDim = dim3(small ? 32 : NTB);
+    // a warp where one span of it holds the row (2000 rows of 2000, bf16, top 5: 13 us, by wide CTAs 22; of 8000: 26 and 23)
+    const bool small = a.V / W <= 32 * kUnroll * kSpan;
+    cfg.blockDim = dim3(small ? 32 : kWide);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -605,7 +602,7 @@ cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return small ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 32>, a) : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, NTB>, a);
+    return small ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 32>, a) : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, kWide>, a);
 }
 
 }  // namespace

@@ -79,7 +79,7 @@ def test_logprobs_refusals(m):  # noqa: F811
     assert m.lib().moe_token_logprobs(None, None) == NULL
     assert call(type=3) == TYPE
     for kw in (dict(rows=-1), dict(vocab=0), dict(vocab=-5), dict(n_ids=-1), dict(top=-1), dict(top=33), dict(top=5, vocab=4), dict(row_stride=99), dict(scale=0.0),
-               dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan)):
+               dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(scale=2.0 ** -101), dict(scale=2.0 ** 101)):
         assert call(**kw) == SHAPE, kw
     assert call(rows=1 << 28) == CAP and call(rows=1 << 20, n_ids=1 << 11) == CAP
     for name in ("logits", "ids", "logprobs", "top_logprobs", "top_ids"):
