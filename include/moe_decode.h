@@ -32,13 +32,13 @@ typedef struct moe_heads {
     void* out;
     const void* weight; /* [head_dim] of w_type, 16-byte aligned, or NULL: no norm */
     int64_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;
-    int32_t n_heads; /* 0: none (the other fields are not read) */
+    int32_t n_heads; /* at most 65535; 0: none (the other fields are not read) */
 } moe_heads;
 
 /* y = x * (1 / sqrt(mean(x^2) + eps)) * weight over a head's dims (where there is a weight), then the rotation, in
  * fp32 (squares too: they overflow above 1.8e19), rounded once to `type`. Row i is at positions[i], any 32-bit number. Errors:
  * MOE_E_NULL, MOE_E_TYPE, MOE_E_SHAPE (head_dim: a multiple of 16 from 16 to 256; rot, start; negative counts), MOE_E_CAP
- * (n_tokens * heads of 2^31 or more), MOE_E_ALIGN (x and out off their element's boundary, weights off 16 bytes,
+ * (more than 65535 heads of a set, n_tokens * heads of 2^31 or more), MOE_E_ALIGN (x and out off their element's boundary, weights off 16 bytes,
  * positions off 4, turns off 8), MOE_E_CUDA. */
 typedef struct moe_head_norm_call {
     moe_heads q, k;

@@ -20,6 +20,7 @@ int check_heads(const moe_heads& h, int eb, int64_t n, HeadSet& to) {
     to = HeadSet{};
     if (h.n_heads < 0) return MOE_E_SHAPE;
     if (h.n_heads == 0) return MOE_OK;
+    if (h.n_heads > 65535) return MOE_E_CAP;
     if (n > 0 && (!h.x || !h.out)) return MOE_E_NULL;
     to = HeadSet{h.x, h.out, h.weight, h.x_token_stride, h.x_head_stride, h.out_token_stride, h.out_head_stride, h.n_heads, false, false};
     if (off16(h.weight)) return MOE_E_ALIGN;

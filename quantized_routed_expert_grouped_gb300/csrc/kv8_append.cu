@@ -57,7 +57,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
     const T* kb = static_cast<const T*>(a.k) + (s.row + kt) * a.kt + h0 * a.kh;
     const T* vb = static_cast<const T*>(a.v) + (s.row + vt) * a.vt + h0 * a.vh + (lane & 3) * 8;
 #pragma unroll 1
-    for (int h = h0; h < h1; ++h, kb += a.kh, vb += a.vh, rec += a.c.page_blocks * a.c.rec) {
+    for (int h = h0; h < h1; ++h, kb += a.kh, vb += a.vh, rec += static_cast<int64_t>(a.c.page_blocks) * a.c.rec) {
         const float2 old2 = s.t0 > 0 ? *reinterpret_cast<const float2*>(rec) : make_float2(0.0f, 0.0f);
         Raw8<TYPE> k[NU][2], v[NB];
 #pragma unroll

@@ -6,7 +6,7 @@
 //
 // m is the row's largest logit. r is a whole number near c times the largest that a thread has seen (kSlack below it at most), so that a
 // logit's exponent is one fused product, rounded once, and what r is does not matter to the result; s and u are rescaled where r
-// moves, which few tiles need. Threads join theirs, then the CTAs of a row, always in the same order. t 2^t of a logit of -inf has to be 0: 16-bit logits
+// moves, which few tiles need. (It is above -2^24: what lies below has a power of 0 there, and nothing but such logits is a row for the second pass.) Threads join theirs, then the CTAs of a row, always in the same order. t 2^t of a logit of -inf has to be 0: 16-bit logits
 // are clamped in pairs before they are converted, fp32's t one by one. Where that or c m leaves the range (rows masked by their type's lowest value,
 // scales near 0 or far above 1) the row's sums are taken a second time, differences first. Powers are the hardware's (2^-22 of
 // themselves); sums are fp32, eight of a thread's terms in a row at most before they are added to its two running ones.
@@ -40,6 +40,7 @@ constexpr int kWide = 256;  // threads of a CTA, but for short rows
 constexpr int kTop = 32, kMaxCluster = 8;
 constexpr float kFar = -1000.0f;  // an exponent whose power of two is 0
 constexpr float kSlack = 8.0f;    // powers of two above its reference that a thread's maximum may rise
+constexpr float kReach = 16777216.0f;  // 2^24: c x and the whole number next to it differ by a half at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
         const float mx = max_of<TYPE>(raw);
         most = fmaxf(most, mx);
         // (2^kSlack is far from fp32's range: few tiles move the reference)
-        if (mx * a.c > st.r + kSlack) st.move(ceilf(mx * a.c));
+        if (mx * a.c > fmaxf(st.r + kSlack, -kReach)) st.move(ceilf(mx * a.c));
         const float r = st.r == -INFINITY ? 0.0f : st.r;
         const unsigned long long rr = pk2(-r, -r), cc = pk2(a.c, a.c);
         unsigned long long s2 = 0, u2 = 0;
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
     if (single >= 0) {
         const float y = Elem<TYPE>::get(gload(x + single));
         st.m = fmaxf(st.m, y);
-        if (y * a.c > st.r + kSlack) st.move(ceilf(y * a.c));
+        if (y * a.c > fmaxf(st.r + kSlack, -kReach)) st.move(ceilf(y * a.c));
         const float t = fmaf(y, a.c, st.r == -INFINITY ? 0.0f : -st.r), p = ex2(t);
         st.s += p;
         st.u = fmaf(p, fmaxf(t, kFar), st.u);
@@ -528,9 +529,9 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
         st = all[pass][0];
     };
     join(0);
-    // Where c times the row's largest logit is no number to subtract, or a clamped logit would count next to it (rows that are masked by
+    // Where c times the row's largest logit is too large to subtract, or a clamped logit would count next to it (rows that are masked by
     // their type's lowest value; scales near 0 or far above 1): once more, with differences first.
-    const bool ends = fabsf(st.m) < INFINITY && !(fabsf(st.m * a.c) < 1.2676506e30f && (TYPE == MOE_F32 || ((st.m - kLow<TYPE>) * a.c > 250.0f && -kLow<TYPE> * a.c < 1e38f)));
+    const bool ends = fabsf(st.m) < INFINITY && !(fabsf(st.m * a.c) < kReach && (TYPE == MOE_F32 || ((st.m - kLow<TYPE>) * a.c > 250.0f && -kLow<TYPE> * a.c < 1e38f)));
     if (ends) {
         const float m = st.m;
         st = Stats{0.0f, 0.0f, 0.0f, m};

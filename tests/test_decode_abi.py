@@ -21,7 +21,7 @@ def heads(m, **kw):  # noqa: F811
 
 BAD_ROPE = [(dict(rot=0), SHAPE), (dict(rot=-16), SHAPE), (dict(rot=24), SHAPE), (dict(rot=144), SHAPE), (dict(start=-8), SHAPE), (dict(start=4), SHAPE),
             (dict(start=72), SHAPE), (dict(start=2 ** 31 - 8), SHAPE), (dict(turns=20), ALIGN)]
-BAD_HEADS = [(dict(n_heads=-1), SHAPE), (dict(x=None), NULL), (dict(out=None), NULL), (dict(x=17), ALIGN), (dict(out=17), ALIGN), (dict(weight=24), ALIGN)]
+BAD_HEADS = [(dict(n_heads=-1), SHAPE), (dict(n_heads=65536), CAP), (dict(x=None), NULL), (dict(out=None), NULL), (dict(x=17), ALIGN), (dict(out=17), ALIGN), (dict(weight=24), ALIGN)]
 
 
 def test_head_norm_refusals(m):  # noqa: F811

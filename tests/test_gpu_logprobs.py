@@ -99,11 +99,11 @@ def test_hard_rows(m, V, dtype):
         check(m, x[r:r + 1], ids_for(rng, 1, V, 1), min(V, 32))
 
 
-@pytest.mark.parametrize("V", [40, 70001])
-def test_not_finite(m, V):
+@pytest.mark.parametrize("dtype", list(K.TYPES))
+@pytest.mark.parametrize("V", [40, 3000, 70001])
+def test_not_finite(m, V, dtype):
     """A NaN or +inf makes a row's numbers NaN, but leaves the other rows and the order of what is a number."""
-    x = torch.zeros((4, V), device="cuda")
-    x += torch.arange(V, device="cuda") % 7
+    x = (torch.zeros((4, V), device="cuda") + torch.arange(V, device="cuda") % 7).to(K.TYPES[dtype])
     x[1, 3] = float("nan")
     x[2, 5] = float("inf")
     x[3] = float("nan")
@@ -114,6 +114,41 @@ def test_not_finite(m, V):
         assert torch.isnan(tl[r]).all() and torch.isnan(ent[r]) and torch.isnan(lse[r])
     assert float(lp[1]) == float("-inf") and torch.isnan(lp[2:]).all()
     assert ti.tolist() == [[6, 13, 20], [6, 13, 20], [5, 6, 13], [-1, -1, -1]]
+
+
+@pytest.mark.parametrize("dtype", list(K.TYPES))
+@pytest.mark.parametrize("V", [50, 9001, 70001])
+def test_scales(m, V, dtype):
+    """Scales near 0 and far above 1, small and large logits: where c x leaves fp32's range, or clamped logits would count, too."""
+    rng = np.random.default_rng(V + 1)
+    x = rng.standard_normal((5, V))
+    x[1] *= 1e-3
+    x[2] *= 1000
+    x[3, rng.random(V) < 0.9] = -np.inf
+    x[4] = np.where(rng.random(V) < 0.5, -np.inf, torch.finfo(K.TYPES[dtype]).min)
+    dev = torch.from_numpy(x).to(K.TYPES[dtype]).cuda()
+    for scale in (2.0 ** -100, 2.0 ** -30, 1e-3, 1.0, 30.0, 2.0 ** 20, 2.0 ** 100):
+        check(m, dev[:3], ids_for(rng, 3, V, 2), min(V, 9), scale)
+        check(m, dev[3:4], ids_for(rng, 1, V, 2), 3, scale)
+    check(m, dev[4:], ids_for(rng, 1, V, 2), 3, 0.5)
+
+
+@pytest.mark.parametrize("dtype", list(K.TYPES))
+@pytest.mark.parametrize("V", [50, 9001, 140001])
+def test_mask_values(m, V, dtype):
+    """Masks by large negative numbers, where most threads see nothing else, and rows with one far larger logit."""
+    rng = np.random.default_rng(V + 2)
+    for mask in (-1e4, -6e4, -1e9, -1e30, -3e38):
+        x = rng.standard_normal((4, V))
+        x[:3][rng.random((3, V)) < 0.999] = mask
+        x[2] = mask
+        x[3, V // 2] = -mask
+        dev = torch.from_numpy(x).to(K.TYPES[dtype]).cuda()
+        if dtype == "f16" and mask < -65504:
+            dev = dev[:3]  # (-inf there, and the last row +inf)
+        for scale in (1.0, 0.1):
+            check(m, dev, ids_for(rng, dev.shape[0], V, 2), 3, scale)
+            check(m, dev[2:3], ids_for(rng, 1, V, 1), 2, scale)
 
 
 def test_many_ids_and_none(m):
