@@ -29,8 +29,8 @@ struct AppendArgs {
     int w_type;
     float eps;
     int32_t* err;
-    // of a block: CTAs for the key/value heads and for the query heads, heads of each
-    int kparts, kheads, qparts, qheads;
+    // of a block: CTAs for keys, for values and for queries, heads of each
+    int kparts, kheads, vparts, vheads, qparts, qheads;
 };
 cudaError_t launch_kv8_append(AppendArgs a, int type, cudaStream_t st);
 

@@ -2,10 +2,11 @@
 // normed and rotated beside them, in one launch. The codes and scales are those of kv8_cache.cu, of the fp32 keys that
 // the norm and the rotation give (they are not rounded to the rows' type first: one rounding less).
 //
-// The list is kv8_slots' blocks of 32 positions; a CTA takes one block for some key/value heads, or for some query heads, as
-// head_rope.cu does. For keys a token is four lanes, which hold D / 16 pairs of vectors of eight dims between them (NU = D / 64
-// rounded up each, as RopeUnit pairs them), so that the norm is two shuffles and a pair is a lane's own. The block's
-// angles are computed once a CTA, a (token, pair) a thread, into shared memory, and serve its heads.
+// The list is kv8_slots' blocks of 32 positions; a CTA takes a block for the keys, or the values, of some key/value heads, or for some
+// query heads, as head_rope.cu does. (Keys and values apart need fewer registers, and angles and weights are the keys' alone.) For keys a
+// token is four lanes, which hold D / 16 pairs of vectors of eight dims between them (NU = D / 64 rounded up each, as
+// RopeUnit pairs them), so that the norm is two shuffles and a pair is a lane's own. The block's angles are computed once a
+// CTA into shared memory, a pair a thread, and serve its heads. A record's two scales are written by the two CTAs.
 #include "decode_api.h"
 #include "kv8_quant.cuh"
 
@@ -31,19 +32,21 @@ __device__ __forceinline__ float amax3(float m, float a, float b) {
     return d;
 }
 
+// The block's largest magnitude, from the threads' (as bits: they order as magnitudes do, a NaN above all).
+__device__ __forceinline__ float block_max(uint32_t (&red)[4], uint32_t m) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();  // also: every thread has read the old scale
+    return __uint_as_float(max(max(red[0], red[1]), max(red[2], red[3])));
+}
+
 template <int TYPE, int NB>
-__device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& s, int h0, int h1, float4* angles) {
+__device__ __forceinline__ void append_keys(const AppendArgs& a, const KvSlot& s, int h0, int h1, uint8_t* rec, uint32_t (&red)[4], float* weights, float4* angles) {
     constexpr int D = NB * 32, NU = (NB + 1) / 2, kUnits = D / 16;
     using T = typename Elem<TYPE>::T;
-    __shared__ uint32_t red[2][4];
-    __shared__ __align__(16) uint8_t turn[D * kKvTurn];
-    __shared__ __align__(16) float weights[D];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int g = lane >> 2, kt = 8 * (g >> 1) + 2 * wid + (g & 1), vt = wid * 8 + g;
-    const bool kin = kt >= s.t0 && kt < s.t1, vin = vt >= s.t0 && vt < s.t1;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, kt = 8 * (g >> 1) + 2 * wid + (g & 1);
+    const bool kin = kt >= s.t0 && kt < s.t1;
     const int row4 = angle_row(a.r.rot), turning = a.r.rot / 16;
-    uint8_t* rec = kv8_record(a.c, s.b, s.blk, h0, a.err);
-    if (!rec) return;  // (the CTA's heads share the page)
     if (a.r.rot) put_angles<8>(reinterpret_cast<float*>(angles + s.t0 * row4), a.r, s.t1 - s.t0, row4 * 4, [&](int t) { return turn_at(a, s, s.t0 + t); });
     if (a.k_weight) put_weights<8>(weights, a.r, D, a.k_weight, a.w_type);
     if (a.r.rot || a.k_weight) __syncthreads();
@@ -55,11 +58,10 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
         e1[n] = u.e1;
     }
     const T* kb = static_cast<const T*>(a.k) + (s.row + kt) * a.kt + h0 * a.kh;
-    const T* vb = static_cast<const T*>(a.v) + (s.row + vt) * a.vt + h0 * a.vh + (lane & 3) * 8;
 #pragma unroll 1
-    for (int h = h0; h < h1; ++h, kb += a.kh, vb += a.vh, rec += static_cast<int64_t>(a.c.page_blocks) * a.c.rec) {
-        const float2 old2 = s.t0 > 0 ? *reinterpret_cast<const float2*>(rec) : make_float2(0.0f, 0.0f);
-        Raw8<TYPE> k[NU][2], v[NB];
+    for (int h = h0; h < h1; ++h, kb += a.kh, rec += static_cast<int64_t>(a.c.page_blocks) * a.c.rec) {
+        const float old = s.t0 > 0 ? *reinterpret_cast<const float*>(rec) : 0.0f;
+        Raw8<TYPE> k[NU][2];
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
             k[n][0].clear();
@@ -69,12 +71,6 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
                 k[n][1].load(kb + e1[n], a.kvec);
             }
         }
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            v[n].clear();
-            if (vin) v[n].load(vb + n * 32, a.vvec);
-        }
-        // ---- keys: norm, rotation
         unsigned long long x[NU][2][4];
 #pragma unroll
         for (int n = 0; n < NU; ++n)
@@ -123,23 +119,9 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
                     mk = amax3(mk, f.x, f.y);
                 }
         }
-        uint32_t ak = __float_as_uint(mk), av = 0;  // magnitudes order as their bits do (a NaN is above all)
-#pragma unroll
-        for (int n = 0; n < NB; ++n) av = v[n].amax(av);
-        ak = __reduce_max_sync(0xffffffffu, ak);
-        av = __reduce_max_sync(0xffffffffu, Raw8<TYPE>::float_bits(av));
-        if (lane == 0) {
-            red[0][wid] = ak;
-            red[1][wid] = av;
-        }
-        __syncthreads();  // also: every thread has read the old scales
-        ak = max(max(red[0][0], red[0][1]), max(red[0][2], red[0][3]));
-        av = max(max(red[1][0], red[1][1]), max(red[1][2], red[1][3]));
-        const Scales sk = block_scale(__uint_as_float(ak), old2.x, s.t0 > 0), sv = block_scale(__uint_as_float(av), old2.y, s.t0 > 0);
-        if (threadIdx.x == 0) *reinterpret_cast<float2*>(rec) = make_float2(sk.scale, sv.scale);
-        uint8_t* vr = rec + kKvHead + kKvBlock * D;
+        const Scales sk = block_scale(block_max(red, __float_as_uint(mk)), old, s.t0 > 0);
+        if (threadIdx.x == 0) *reinterpret_cast<float*>(rec) = sk.scale;
         if (kt < s.t0 && sk.grew) rescale_keys<NB>(reinterpret_cast<uint2*>(rec + kKvHead) + wid * NB * 32 + lane, sk);
-        if (s.t0 > 0 && sv.grew) rescale_values<NB>(vr, s.t0, sv);
         if (kin) {
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
@@ -161,6 +143,33 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const KvSlot& 
                 }
             }
         }
+        if (h + 1 < h1) __syncthreads();  // red is written again
+    }
+}
+
+template <int TYPE, int NB>
+__device__ __forceinline__ void append_values(const AppendArgs& a, const KvSlot& s, int h0, int h1, uint8_t* rec, uint32_t (&red)[4], uint8_t* turn) {
+    constexpr int D = NB * 32;
+    using T = typename Elem<TYPE>::T;
+    const int lane = threadIdx.x & 31, vt = (threadIdx.x >> 5) * 8 + (lane >> 2);
+    const bool vin = vt >= s.t0 && vt < s.t1;
+    const T* vb = static_cast<const T*>(a.v) + (s.row + vt) * a.vt + h0 * a.vh + (lane & 3) * 8;
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h, vb += a.vh, rec += static_cast<int64_t>(a.c.page_blocks) * a.c.rec) {
+        const float old = s.t0 > 0 ? *reinterpret_cast<const float*>(rec + 4) : 0.0f;
+        Raw8<TYPE> v[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            v[n].clear();
+            if (vin) v[n].load(vb + n * 32, a.vvec);
+        }
+        uint32_t av = 0;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) av = v[n].amax(av);
+        const Scales sv = block_scale(block_max(red, Raw8<TYPE>::float_bits(av)), old, s.t0 > 0);
+        if (threadIdx.x == 0) *reinterpret_cast<float*>(rec + 4) = sv.scale;
+        uint8_t* vr = rec + kKvHead + kKvBlock * D;
+        if (s.t0 > 0 && sv.grew) rescale_values<NB>(vr, s.t0, sv);
         write_values<TYPE, NB>(vr, turn, v, vt, vin, s.t0 == 0 && s.t1 == 32, sv);
         if (h + 1 < h1) __syncthreads();  // red and turn are written again
     }
@@ -188,24 +197,33 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, const KvSlot
     }
 }
 
-// CTAs an SM, by the registers that a thread's keys and values need (prompts of 25k tokens, 8 heads of 128, 32 query heads, bf16: seven
-// 117 us, six 122, without a limit 149).
-constexpr int append_ctas(int type, int nb) { return nb <= 4 ? type == MOE_F32 ? 5 : 7 : nb <= 6 ? 4 : 3; }
+// CTAs an SM, by the registers that a thread's keys need (prompts of 25k tokens, 8 heads of 128, 32 query heads, bf16: eight 108 us,
+// seven 112).
+constexpr int append_ctas(int type, int nb) { return nb <= 4 ? type == MOE_F32 ? 5 : 8 : nb <= 6 ? 4 : 3; }
 
 template <int TYPE, int NB>
 __global__ void __launch_bounds__(kThreads, append_ctas(TYPE, NB)) kv8_append_kernel(const AppendArgs a) {
     extern __shared__ __align__(16) float4 angles[];
-    const int parts = a.kparts + a.qparts;
+    constexpr int D = NB * 32;
+    __shared__ uint32_t red[4];
+    __shared__ __align__(16) uint8_t turn[D * kKvTurn];
+    __shared__ __align__(16) float weights[D];
+    const int parts = a.kparts + a.vparts + a.qparts;
     const int slot = blockIdx.x / parts, part = blockIdx.x - slot * parts;
     pdl_wait();
     pdl_trigger();
     const KvSlot s = kv8_slot(slot, a.cu, a.start, a.c.n_seqs, a.n_tokens, a.err);
     if (s.b < 0) return;
-    if (part < a.kparts) {
-        append_block<TYPE, NB>(a, s, part * a.kheads, min(a.c.n_kv, (part + 1) * a.kheads), angles);
+    if (part < a.kparts + a.vparts) {
+        const bool values = part >= a.kparts;
+        const int each = values ? a.vheads : a.kheads, h0 = (values ? part - a.kparts : part) * each, h1 = min(a.c.n_kv, h0 + each);
+        uint8_t* rec = kv8_record(a.c, s.b, s.blk, h0, a.err);
+        if (!rec) return;  // (the heads share the page)
+        if (values) append_values<TYPE, NB>(a, s, h0, h1, rec, red, turn);
+        else append_keys<TYPE, NB>(a, s, h0, h1, rec, red, weights, angles);
         return;
     }
-    const int h0 = (part - a.kparts) * a.qheads, h1 = min(a.q.n, h0 + a.qheads);
+    const int h0 = (part - a.kparts - a.vparts) * a.qheads, h1 = min(a.q.n, h0 + a.qheads);
     if (a.q.xvec && a.q.ovec) append_queries<TYPE, NB, true>(a, s, h0, h1, reinterpret_cast<float*>(angles));
     else append_queries<TYPE, NB, false>(a, s, h0, h1, reinterpret_cast<float*>(angles));
 }
@@ -213,14 +231,17 @@ __global__ void __launch_bounds__(kThreads, append_ctas(TYPE, NB)) kv8_append_ke
 template <int TYPE>
 cudaError_t append_t(AppendArgs& a, cudaStream_t st) {
     const int64_t slots = kv8_slots(a.n_tokens, a.c.n_seqs);
-    // Heads of a CTA: one of the keys, a round or two of the queries, where there are few blocks; with many, four and 16, which
-    // the block's angles serve (the same prompts: four 117 us, two 123, eight 125, one 160).
+    // Heads of a CTA. Keys: one where there are few blocks, with many eight, which the block's angles serve (the same prompts:
+    // eight 108 us, four 112; keys and values in one CTA, four heads each, 117). Queries: two rounds, or four. Values: two (64 windows of four:
+    // two 8.4 us, one 9.0, four 8.7).
     const bool many = slots * a.c.n_kv > 152 * 16;
-    a.kheads = many ? 4 : 1;
+    a.kheads = many ? 8 : 1;
+    a.vheads = 2;
     a.qheads = many ? 16 : 8;
     a.kparts = (a.c.n_kv + a.kheads - 1) / a.kheads;
+    a.vparts = (a.c.n_kv + a.vheads - 1) / a.vheads;
     a.qparts = (a.q.n + a.qheads - 1) / a.qheads;
-    const unsigned grid = static_cast<unsigned>(slots * (a.kparts + a.qparts));
+    const unsigned grid = static_cast<unsigned>(slots * (a.kparts + a.vparts + a.qparts));
     const int keys = 32 * angle_row(a.r.rot) * static_cast<int>(sizeof(float4)), queries = rope_smem(a.r.rot, a.c.D, 32);
     const size_t smem = a.q.n && queries > keys ? queries : keys;
     switch (a.c.D / 32) {
