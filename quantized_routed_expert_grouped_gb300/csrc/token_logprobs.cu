@@ -591,8 +591,9 @@ cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
     a.c = a.scale * kLog2e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.cluster);
-    // a warp where one span of it holds the row (2000 rows of 2000, bf16, top 5: 13 us, by wide CTAs 22; of 8000: 26 and 23)
-    const bool small = a.V / W <= 32 * kUnroll * kSpan;
+    // A warp where one span of it holds the row, for more rows than wide CTAs are resident, and few keys (2000 rows of 2000, bf16,
+    // top 5: 13 us, by wide CTAs 22; of 8000: 26 and 23; 300 rows of 2000, top 12: 8.7 and 7.2; 2000 of 2000, top 30: 43 and 32).
+    const bool small = a.V / W <= 32 * kUnroll * kSpan && a.rows > 152 * 4 && a.top <= 24;
     cfg.blockDim = dim3(small ? 32 : kWide);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];

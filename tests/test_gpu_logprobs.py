@@ -55,7 +55,7 @@ def ids_for(rng, R, V, n):
 
 
 SIZES = [(1, 1), (3, 2), (2, 5), (5, 31), (4, 33), (3, 257), (2, 1000), (3, 4097), (2, 8191), (2, 8192), (3, 8193), (2, 16400), (5, 50001), (1, 131075),
-         (40, 40000), (330, 9001), (700, 2500)]
+         (40, 40000), (330, 9001), (700, 2500), (701, 33), (801, 1), (650, 700), (900, 2044)]
 
 
 @pytest.mark.parametrize("dtype", list(K.TYPES))
@@ -94,6 +94,14 @@ def test_hard_rows(m, V, dtype):
     x = torch.from_numpy(np.stack(rows).astype(np.float64)).to(t).cuda()
     for top in (1, 5, min(V, 32)):
         check(m, x, ids_for(rng, len(rows), V, 2), top)
+    if V < 9000:  # many short rows: by warps
+        many = x.repeat(55, 1)
+        got = [m.token_logprobs(many, top=t) for t in (1, 5)]
+        for t, (_, tl, ti, ent, lse) in zip((1, 5), got):
+            _, tl1, ti1, _, _ = m.token_logprobs(x, top=t)
+            assert torch.equal(ti.view(55, *ti1.shape), ti1.expand(55, *ti1.shape)) and bool((ti >= 0).all())
+            assert torch.allclose(tl.view(55, *tl1.shape), tl1.expand(55, *tl1.shape), rtol=1e-6, atol=1e-5)
+        check(m, many[:len(rows) * 52], ids_for(rng, len(rows) * 52, V, 1), min(V, 24))
     # one row alone: by a cluster
     for r in range(len(rows)):
         check(m, x[r:r + 1], ids_for(rng, 1, V, 1), min(V, 32))
@@ -101,14 +109,17 @@ def test_hard_rows(m, V, dtype):
 
 @pytest.mark.parametrize("dtype", list(K.TYPES))
 @pytest.mark.parametrize("V", [40, 3000, 70001])
-def test_not_finite(m, V, dtype):
+@pytest.mark.parametrize("more", [0, 700])
+def test_not_finite(m, V, dtype, more):
     """A NaN or +inf makes a row's numbers NaN, but leaves the other rows and the order of what is a number."""
     x = (torch.zeros((4, V), device="cuda") + torch.arange(V, device="cuda") % 7).to(K.TYPES[dtype])
     x[1, 3] = float("nan")
     x[2, 5] = float("inf")
     x[3] = float("nan")
     ids = torch.tensor([[1], [-1], [2], [0]], dtype=torch.int32, device="cuda")
-    lp, tl, ti, ent, lse = m.token_logprobs(x, ids, top=3)
+    if more and V < 9000:  # (many short rows are taken by warps)
+        x, ids = torch.cat([x, x[:1].expand(more, V)]), torch.cat([ids, ids[:1].expand(more, 1)])
+    lp, tl, ti, ent, lse = (t[:4] for t in m.token_logprobs(x.contiguous(), ids.contiguous(), top=3))
     assert torch.isfinite(lp[0]).all() and torch.isfinite(tl[0]).all() and torch.isfinite(ent[0]) and torch.isfinite(lse[0])
     for r in (1, 2, 3):
         assert torch.isnan(tl[r]).all() and torch.isnan(ent[r]) and torch.isnan(lse[r])
@@ -128,7 +139,8 @@ def test_scales(m, V, dtype):
     x[4] = np.where(rng.random(V) < 0.5, -np.inf, torch.finfo(K.TYPES[dtype]).min)
     dev = torch.from_numpy(x).to(K.TYPES[dtype]).cuda()
     for scale in (2.0 ** -100, 2.0 ** -30, 1e-3, 1.0, 30.0, 2.0 ** 20, 2.0 ** 100):
-        check(m, dev[:3], ids_for(rng, 3, V, 2), min(V, 9), scale)
+        some = dev[:3].repeat(210 if V == 50 else 1, 1)  # (many short rows are taken by warps)
+        check(m, some, ids_for(rng, some.shape[0], V, 2), min(V, 9), scale)
         check(m, dev[3:4], ids_for(rng, 1, V, 2), 3, scale)
     check(m, dev[4:], ids_for(rng, 1, V, 2), 3, 0.5)
 
@@ -146,6 +158,8 @@ def test_mask_values(m, V, dtype):
         dev = torch.from_numpy(x).to(K.TYPES[dtype]).cuda()
         if dtype == "f16" and mask < -65504:
             dev = dev[:3]  # (-inf there, and the last row +inf)
+        if V == 50:
+            dev = dev.repeat(210, 1)  # (many short rows are taken by warps)
         for scale in (1.0, 0.1):
             check(m, dev, ids_for(rng, dev.shape[0], V, 2), 3, scale)
             check(m, dev[2:3], ids_for(rng, 1, V, 1), 2, scale)
