@@ -178,5 +178,5 @@ def test_large_offsets(m):
     assert torch.equal(rows, want)
     logits = far.as_strided((n, 5001), (apart, 1))
     logits.copy_(torch.randn((n, 5001), device="cuda"))
-    for a, b in zip(m.token_logprobs(logits, top=5)[1:], m.token_logprobs(logits.contiguous(), top=5)[1:]):
-        assert torch.equal(a, b)
+    # (not bit for bit against contiguous rows: what lies at another alignment is summed in another order)
+    check_logprobs(m, logits, np.array([[0], [5000], [-1], [17], [2500]]), 5)
