@@ -196,3 +196,17 @@ def test_rope_refusals(m):  # noqa: F811
     for kw in bad:
         with pytest.raises(m.MoeError):
             m.Rope(device="cpu", **kw)
+
+
+def test_other_device(m, monkeypatch):  # noqa: F811
+    """The library launches on the current device: tensors of another one are refused before the call."""
+    monkeypatch.setattr(m, "_device", lambda t: -1)
+    monkeypatch.setattr(m, "_ptr", lambda t, dev: t.data_ptr())
+    monkeypatch.setattr(m, "_current_device", lambda: 1)
+    monkeypatch.setattr(m, "_raw_stream", lambda dev: pytest.fail("launched"))
+    x, pos = torch.zeros((2, 2, 64)), torch.zeros(2, dtype=torch.int32)
+    pool, table = m.kv8_pool(2, 2, 64, 32, device="cpu"), torch.zeros((1, 2), dtype=torch.int32)
+    one, cu = torch.zeros(1, dtype=torch.int32), torch.tensor([0, 2], dtype=torch.int32)
+    for f in (lambda: m.head_norm_rope(x, pos), lambda: m.kv8_append(x, x, pool, table, cu, one), lambda: m.token_logprobs(x[0])):
+        with pytest.raises(m.MoeError, match="device"):
+            f()
