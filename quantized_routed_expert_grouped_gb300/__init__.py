@@ -10,7 +10,6 @@ q8_1 rows are uint8 tensors of shape [rows, cols/32, 36].
 from __future__ import annotations
 
 import ctypes
-import fractions
 import math
 import os
 import struct
@@ -615,7 +614,7 @@ _pack_heads = struct.Struct("@" + _HEADS * 2 + _ROPE + "Pqiiif").pack
 _pack_append = struct.Struct("@" + _CACHE + "0q" + _ROWS + _HEADS + _ROPE + "PPPPifP").pack
 _pack_logprobs = struct.Struct("@PqiiiiifPPPPPP").pack
 _NO_HEADS, _NO_ROPE = (0,) * 8, (0, 0, 0, 0, 0.0)
-_TWO_PI = 2 * fractions.Fraction("3.14159265358979323846264338327950288419716939937510")
+_TWO_PI = 2 * 314159265358979323846264338327950288419716939937510, 10 ** 50  # as a fraction
 
 
 class Rope:
@@ -645,9 +644,13 @@ class Rope:
         f, scaled = self._scaled(f, rot, theta, dict(scaling or {"kind": "none"}))
         self.inv_freq, self.factor = f, scaled if factor is None else float(factor)
         self.rot, self.start, self.interleaved = rot, start, bool(interleaved)
-        # fractions of a turn a position, in 64 bits (as int64 tensors hold them)
-        turns = [round(fractions.Fraction(x) / _TWO_PI * 2 ** 64) % 2 ** 64 for x in f]
-        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+        # fractions of a turn a position, rounded to 64 bits (as int64 tensors hold them)
+        turns = []
+        for x in f:
+            n, d = x.as_integer_ratio()
+            n, d = n * _TWO_PI[1] << 64, d * _TWO_PI[0]
+            turns.append(((2 * n + d) // (2 * d) + 2 ** 63) % 2 ** 64 - 2 ** 63)
+        self.turns = torch.tensor(turns, dtype=torch.int64, device=device)
         self._device = self.turns.get_device()
         self._fields = (self.turns.data_ptr(), rot, start, int(self.interleaved), self.factor)
 
