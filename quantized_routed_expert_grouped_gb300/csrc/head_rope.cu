@@ -3,7 +3,10 @@
 //
 // A CTA takes up to four tokens. Its warps compute the tokens' angles and lay out the weights in shared memory while
 // each one's first heads are on their way; then a warp takes a token's heads, round after round, with the next round's loads in flight.
-// Bound by memory where there are many rows, else by its chain of latencies.
+// Bound by memory where there are many rows, else by its chain of latencies. Measured (GB300, of 6703 GB/s that a copy
+// reaches): 8191 tokens of 72 heads of 128 dims, bf16, normed and rotated: 51.7 us for 302 MB read and written (5.8 TB/s; 54 % of
+// the issue slots, 24 warps an SM at 72 registers). With angles and weights in registers, 118 a thread, it took 63; without a limit on registers
+// 59. 256 tokens of 40 heads, fp32: 3.2 us; one token: 2.3 us.
 #include "decode_api.h"
 
 namespace moe {

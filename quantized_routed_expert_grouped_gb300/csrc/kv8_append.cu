@@ -7,6 +7,10 @@
 // token is four lanes, which hold D / 16 pairs of vectors of eight dims between them (NU = D / 64 rounded up each, as
 // RopeUnit pairs them), so that the norm is two shuffles and a pair is a lane's own. The block's angles are computed once a
 // CTA into shared memory, a pair a thread, and serve its heads. A record's two scales are written by the two CTAs.
+//
+// Bound by memory and by its instructions together. Measured (GB300, bf16): 25.5k tokens of seven prompts, 8 heads of 128 and
+// 32 query heads: 108 us for 575 MB (5.3 TB/s of the copy's 6.7; issue slots 58 %); keys and values alone 48 us, of which the rotation
+// takes 7 and the norm 4 (moe_kv8_write 31: its keys stay packed). 64 windows of four: 8.4 us; one token: 3.5 us.
 #include "decode_api.h"
 #include "kv8_quant.cuh"
 

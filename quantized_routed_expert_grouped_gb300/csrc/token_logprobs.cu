@@ -24,6 +24,11 @@
 // A row is read by a cluster of C CTAs (a power of two up to 8, where rows are few); each sends its sums to all, and its list to the first,
 // through distributed shared memory, behind one barrier: one launch, no workspace. Rows need no alignment: what lies before a
 // row's first 16-byte boundary and after its last one is taken singly, at the end.
+//
+// Bound by memory while it only sums (2047 rows of 131,075, bf16, 537 MB: 86 us, 6.2 TB/s of a copy's 6.7; fp32 1024 rows of
+// 131,072: 78 us, 6.8 TB/s); picking the best keys costs a barrier a span and a chain of latencies a row: top 1 104 us, top 5
+// 107, top 20 127 (issue slots 58 %). 192 rows of 65,537, fp32, top 20: 24 us; one row of 32,768: 7.3 us, of which 3 are picking
+// and 2 joining the cluster.
 #include <cooperative_groups.h>
 
 #include "decode_api.h"
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
     using Raw = Vec16<TYPE>;
     using T = typename Elem<TYPE>::T;
     constexpr int W = Raw::W, kTile = NT * kUnroll;  // vectors of a tile
-    constexpr int kHot = NT == 32 ? 32 : NT == 128 ? 48 : 64, kCap = kTop + kHot * kSpan * kUnroll * W;  // threads' spans to be looked through at once, and their keys
+    constexpr int kHot = NT == 32 ? 32 : 64, kCap = kTop + kHot * kSpan * kUnroll * W;  // threads' spans to be looked through at once, and their keys
     constexpr int kFew = 2 * (NT / 32);  // spans that are looked through sooner than sifted
     constexpr uint32_t kNone = TYPE == MOE_F32 ? 0xff800000u : TYPE == MOE_F16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf
     __shared__ __align__(16) unsigned long long list[kCap];  // the best keys in order, then new ones
