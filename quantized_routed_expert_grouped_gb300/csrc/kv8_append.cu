@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kThreads = kKvThreads;
 
-// The angles of a block: a token's row (put_angle) is an odd multiple of 64 bytes, so that the eight lanes of an access (two
+// The angles of a block: a token's row (put_angles) is an odd multiple of 64 bytes, so that the eight lanes of an access (two
 // tokens) share no bank.
 __host__ __device__ inline int angle_row(int rot) { return rot / 4 + (rot / 16 % 2 ? 0 : 4); }  // in float4
 
@@ -98,7 +98,7 @@ __device__ __forceinline__ void append_keys(const AppendArgs& a, const KvSlot& s
             const unsigned long long ii = pk2(inv, inv);
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
-                if (e0[n] < 0) continue;
+                if (e0[n] < 0 || !kin) continue;  // (no token there: zeros, which 1 / sqrt(0) would make NaN)
                 const float4* ww = reinterpret_cast<const float4*>(weights) + 4 * n + (lane & 3);
 #pragma unroll
                 for (int w = 0; w < 2; ++w)

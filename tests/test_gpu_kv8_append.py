@@ -206,6 +206,27 @@ def test_not_finite_and_zero(m):
     assert bool(torch.isfinite(k[32:, 2]).all()) and bool(torch.isfinite(v).all())
 
 
+@pytest.mark.parametrize("dtype", list(K.TYPES))
+def test_norm_without_eps(m, dtype):
+    """eps 0: the places of a block that hold no new token do not count; a key of zeros is 0 / 0, and makes its block NaN."""
+    c = Case(19, [3, 40], [7, 2], 2, 2, 96, 32, dtype)
+    rope = m.Rope(32, start=16)
+    q = c.append(m, rope=rope, q=c.q, q_weight=c.weights[0], k_weight=c.weights[1], eps=0.0)
+    assert int(c.err) == 0 and bool(torch.isfinite(q).all())
+    y, off = D.rope(c.k.double().cpu().numpy(), c.places, c.weights[1].double().cpu().numpy(), rope.inv_freq, 1.0, 16, False, 0.0)
+    k, v = m.kv8_read(c.pool, c.table, ints(c.cu), ints(c.starts), c.N, dtype=torch.float32)
+    got = K.Cache(c.pool.cpu().numpy(), c.ref.table)
+    for b, j in ((0, 0), (1, 1)):
+        rows = slice(c.cu[b], c.cu[b + 1])
+        for h in range(2):
+            step = got.codes(b, j, h, 0)[1] * (0.5 + 127 * 3 * D.ULP)
+            assert (np.abs(k[rows, h].cpu().numpy() - y[rows, h]) <= step + off[rows, h]).all()
+    c.k[8, 1] = 0
+    c.append(m, rope=rope, k_weight=c.weights[1], eps=0.0)
+    k, _ = m.kv8_read(c.pool, c.table, ints(c.cu), ints(c.starts), c.N, dtype=torch.float32)
+    assert bool(torch.isnan(k[7:, 1]).all()) and bool(torch.isfinite(k[:, 0]).all()) and bool(torch.isfinite(k[:7]).all())
+
+
 def test_empty(m):
     c = Case(17, [5], [0], 2, 2, 64, 64)
     before = c.pool.clone()
