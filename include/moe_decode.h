@@ -55,7 +55,7 @@ int moe_head_norm_rope(const moe_head_norm_call* call, cudaStream_t stream);
  * beside them. A key's fp32 result is quantised as it is, without a rounding to the rows' type; without norm and
  * rotation the records are moe_kv8_write's. Rotation positions: positions[i] of row i (a draft token may turn by its depth in a
  * tree), or NULL: the row's position in the cache. q: rows of n_tokens tokens like k and v, with q.out as moe_head_norm_rope
- * gives it (q.n_heads 0: none; rows of a sequence that is skipped are not written; q.out must not overlap k or v). The cache, the rows and the lists are as moe_kv8_write
+ * gives it (q.n_heads 0: none; rows of a sequence that is skipped are not written, those of a block without a page are; q.out must not overlap k or v). The cache, the rows and the lists are as moe_kv8_write
  * takes them, with its errors; MOE_E_CAP also counts the query heads. */
 typedef struct moe_kv8_append_call {
     moe_kv8_cache cache;

@@ -164,30 +164,6 @@ __device__ __forceinline__ void rope_turn(unsigned long long (&a)[W / 2], unsign
     }
 }
 
-template <int W>
-__device__ __forceinline__ void weight_vec(const void* w, int w_type, int at, unsigned long long (&v)[W / 2]) {
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-        float x, y;
-        if (w_type == MOE_F32) {
-            const float2 f = gload(reinterpret_cast<const float2*>(static_cast<const float*>(w) + at) + i);
-            x = f.x;
-            y = f.y;
-        } else {
-            const uint32_t u = gload(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(w) + at) + i);
-            if (w_type == MOE_BF16) {
-                x = __uint_as_float(u << 16);
-                y = __uint_as_float(u & 0xffff0000u);
-            } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-                x = f.x;
-                y = f.y;
-            }
-        }
-        v[i] = pk2(x, y);
-    }
-}
-
 // The shared memory of a CTA: angles of up to T tokens, then the weights of queries and of keys.
 __host__ __device__ inline int rope_smem(int rot, int D, int T) { return (T * rot + 2 * D) * 4; }
 

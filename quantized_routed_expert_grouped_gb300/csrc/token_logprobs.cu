@@ -30,6 +30,7 @@
 // 107, top 20 127 (issue slots 58 %). 192 rows of 65,537, fp32, top 20: 24 us; one row of 32,768: 7.3 us, of which 3 are picking
 // and 2 joining the cluster.
 #include <cooperative_groups.h>
+#include <type_traits>
 
 #include "decode_api.h"
 
@@ -167,7 +168,10 @@ __device__ __forceinline__ unsigned long long merged_keys(unsigned long long k, 
     return k;
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();  // (the aligned form takes a warp's lanes together)
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 template <int TYPE, int NT>
