@@ -29,8 +29,8 @@ struct AppendArgs {
     int w_type;
     float eps;
     int32_t* err;
-    // of a block: CTAs for keys, for values and for queries, heads of each
-    int kparts, kheads, vparts, vheads, qparts, qheads;
+    // of a block: CTAs for keys, for values and for queries, heads of each; its queries' tokens are split over 1 << qshift
+    int kparts, kheads, vparts, vheads, qparts, qheads, qshift;
 };
 cudaError_t launch_kv8_append(AppendArgs a, int type, cudaStream_t st);
 

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, append_ctas(TYPE, NB)) kv8_append_ke
     const int slot = blockIdx.x / parts, part = blockIdx.x - slot * parts;
     pdl_wait();
     pdl_trigger();
-    const KvSlot s = kv8_slot(slot, a.cu, a.start, a.c.n_seqs, a.n_tokens, a.err);
+    KvSlot s = kv8_slot(slot, a.cu, a.start, a.c.n_seqs, a.n_tokens, a.err);
     if (s.b < 0) return;
     if (part < a.kparts + a.vparts) {
         const bool values = part >= a.kparts;
@@ -227,7 +227,13 @@ __global__ void __launch_bounds__(kThreads, append_ctas(TYPE, NB)) kv8_append_ke
         else append_keys<TYPE, NB>(a, s, h0, h1, rec, red, weights, angles);
         return;
     }
-    const int h0 = (part - a.kparts - a.vparts) * a.qheads, h1 = min(a.q.n, h0 + a.qheads);
+    const int qpart = part - a.kparts - a.vparts, h0 = (qpart >> a.qshift) * a.qheads, h1 = min(a.q.n, h0 + a.qheads);
+    if (a.qshift) {  // these tokens of the block alone
+        const int split = 1 << a.qshift, each = (s.t1 - s.t0 + split - 1) >> a.qshift;
+        s.t0 += (qpart & (split - 1)) * each;
+        s.t1 = min(s.t1, s.t0 + each);
+        if (s.t0 >= s.t1) return;
+    }
     if (a.q.xvec && a.q.ovec) append_queries<TYPE, NB, true>(a, s, h0, h1, reinterpret_cast<float*>(angles));
     else append_queries<TYPE, NB, false>(a, s, h0, h1, reinterpret_cast<float*>(angles));
 }
@@ -236,15 +242,20 @@ template <int TYPE>
 cudaError_t append_t(AppendArgs& a, cudaStream_t st) {
     const int64_t slots = kv8_slots(a.n_tokens, a.c.n_seqs);
     // Heads of a CTA. Keys: one where there are few blocks, with many eight, which the block's angles serve (the same prompts:
-    // eight 108 us, four 112; keys and values in one CTA, four heads each, 117). Queries: two rounds, or four. Values: two (64 windows of four:
-    // two 8.4 us, one 9.0, four 8.7).
+    // eight 108 us, four 112; keys and values in one CTA, four heads each, 117). Queries: two rounds of a warp, or four (the same: half as
+    // many 2 % longer, twice 6 %; 16 heads of 192, fp32: 4 155 us, 16 180), 8 and 32 heads at most. Values: two (64 windows of four: two 8.4 us, one 9.0,
+    // four 8.7).
     const bool many = slots * a.c.n_kv > 152 * 16;
     a.kheads = many ? 8 : 1;
     a.vheads = 2;
-    a.qheads = many ? 16 : 8;
+    const int round = 32 / lanes_of(TYPE, a.c.D / 32);
+    a.qheads = many ? round > 8 ? 32 : 4 * round : round > 4 ? 8 : 2 * round;
+    // Few blocks of several tokens: a block's over two or four CTAs (12 prompts of 286 to 621, 16 query heads of 128, fp16:
+    // 13.9 us, undivided 19.9; 51 windows of 1 to 22, 20 of 256: two 12.7, four 15.1, undivided 14.1).
+    a.qshift = many || a.n_tokens <= 4 * a.c.n_seqs ? 0 : a.n_tokens <= 16 * a.c.n_seqs ? 1 : 2;
     a.kparts = (a.c.n_kv + a.kheads - 1) / a.kheads;
     a.vparts = (a.c.n_kv + a.vheads - 1) / a.vheads;
-    a.qparts = (a.q.n + a.qheads - 1) / a.qheads;
+    a.qparts = (a.q.n + a.qheads - 1) / a.qheads << a.qshift;
     const unsigned grid = static_cast<unsigned>(slots * (a.kparts + a.vparts + a.qparts));
     const int keys = 32 * angle_row(a.r.rot) * static_cast<int>(sizeof(float4)), queries = rope_smem(a.r.rot, a.c.D, 32);
     const size_t smem = a.q.n && queries > keys ? queries : keys;
