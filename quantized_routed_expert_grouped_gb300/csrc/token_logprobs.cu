@@ -1,5 +1,5 @@
 // token_logprobs.cu - log probabilities of given tokens, the most likely tokens, entropy and log-sum-exp of rows of logits,
-// in one pass over them.
+// in one pass over them. (Short rows: token_logprobs_short.cu.)
 //
 //   t_j = c x_j - r,  s = sum 2^t_j,  u = sum t_j 2^t_j   (c = scale log2 e);
 //   log p_j = scale (x_j - m) - l,  l = ln 2 (log2 s - (c m - r)),  lse = scale m + l,  entropy = ln 2 (log2 s - u / s)
@@ -32,7 +32,7 @@
 #include <cooperative_groups.h>
 #include <type_traits>
 
-#include "decode_api.h"
+#include "token_logprobs.cuh"
 
 namespace moe {
 
@@ -42,49 +42,11 @@ namespace cg = cooperative_groups;
 
 constexpr int kUnroll = 4;  // vectors of a thread's tile
 constexpr int kSpan = 2;    // tiles between two looks for the best keys: one is added while the next is on its way
-constexpr int kWide = 256;  // threads of a CTA, but for short rows
+constexpr int NT = 256;     // threads of a CTA
 constexpr int kTop = 32, kMaxCluster = 8;
-constexpr float kFar = -1000.0f;  // an exponent whose power of two is 0
 constexpr float kSlack = 8.0f;    // powers of two above its reference that a thread's maximum may rise
 constexpr float kReach = 16777216.0f;  // 2^24: c x and the whole number next to it differ by a half at most
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// 16 bytes of a row.
-template <int TYPE>
-struct Vec16 {
-    static constexpr int W = 16 / static_cast<int>(sizeof(typename Elem<TYPE>::T));
-    uint32_t w[4];
-    __device__ __forceinline__ void load(const typename Elem<TYPE>::T* p) {
-        const uint4 v = gload(reinterpret_cast<const uint4*>(p));
-        w[0] = v.x;
-        w[1] = v.y;
-        w[2] = v.z;
-        w[3] = v.w;
-    }
-    __device__ __forceinline__ float get(int e) const {
-        if (TYPE == MOE_F32) return __uint_as_float(w[e & 3]);
-        const uint32_t x = w[(e >> 1) & 3];
-        if (TYPE == MOE_BF16) return __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16);
-        return __half2float(__ushort_as_half(static_cast<unsigned short>(e & 1 ? x >> 16 : x & 0xffffu)));
-    }
-};
-
-// Larger for larger values, 0 for NaN (-0 counts as 0).
-__device__ __forceinline__ uint32_t order(float x) {
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    return x == x ? b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u) : 0u;
-}
-__device__ __forceinline__ float unorder(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
-__device__ __forceinline__ unsigned long long key_of(float x, uint32_t index) {
-    const uint32_t o = order(x);
-    return o ? static_cast<unsigned long long>(o) << 32 | ~index : 0ull;
-}
 
 // Sums of 2^t and t 2^t, t = c x - r, next to a whole number r (at most kSlack below
 // the largest c x); and the largest x.
@@ -148,49 +110,29 @@ __device__ __forceinline__ void clamp_low(Vec16<TYPE>& v) {
     }
 }
 
-// Keys in descending order over the lanes.
-__device__ __forceinline__ unsigned long long other_key(unsigned long long k, int o, bool more) {
-    const unsigned long long y = __shfl_xor_sync(0xffffffffu, k, o);
-    return (k > y) == more ? k : y;
-}
-__device__ __forceinline__ unsigned long long sorted_keys(unsigned long long k, int lane) {
-#pragma unroll 1
-    for (int n = 2; n <= 32; n <<= 1)
-#pragma unroll 1
-        for (int o = n >> 1; o > 0; o >>= 1) k = other_key(k, o, !(lane & o) == !(lane & n));
-    return k;
-}
-// The 32 largest of two such lists (y's from the end).
-__device__ __forceinline__ unsigned long long merged_keys(unsigned long long k, unsigned long long y, int lane) {
-    k = k > y ? k : y;
-#pragma unroll 1
-    for (int o = 16; o > 0; o >>= 1) k = other_key(k, o, !(lane & o));
-    return k;
-}
-
 __device__ __forceinline__ void cluster_arrive() {
     __syncwarp();  // (the aligned form takes a warp's lanes together)
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
-template <int TYPE, int NT>
-__global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(const LogprobArgs a) {
+template <int TYPE>
+__global__ void __launch_bounds__(NT, 4) token_logprobs_kernel(const LogprobArgs a) {
     using Raw = Vec16<TYPE>;
     using T = typename Elem<TYPE>::T;
     constexpr int W = Raw::W, kTile = NT * kUnroll;  // vectors of a tile
-    constexpr int kHot = NT == 32 ? 32 : 64, kCap = kTop + kHot * kSpan * kUnroll * W;  // threads' spans to be looked through at once, and their keys
+    constexpr int kHot = 64, kCap = kTop + kHot * kSpan * kUnroll * W;  // threads' spans to be looked through at once, and their keys
     constexpr int kFew = 2 * (NT / 32);  // spans that are looked through sooner than sifted
     constexpr uint32_t kNone = TYPE == MOE_F32 ? 0xff800000u : TYPE == MOE_F16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf
     __shared__ __align__(16) unsigned long long list[kCap];  // the best keys in order, then new ones
-    __shared__ __align__(16) unsigned long long work[NT == 32 ? kHot + kTop : kMaxCluster * kTop];
+    __shared__ __align__(16) unsigned long long work[kMaxCluster * kTop];
     __shared__ unsigned long long bar;  // a raised bar: a key, order() of a value
     __shared__ uint32_t raised;
     __shared__ uint32_t hot_max[kHot];  // spans of threads with logits above the bar: their maxima and first vectors
     __shared__ int hot_at[kHot], hots, listed;  // (listed: keys in order)
     __shared__ Stats stat[NT / 32];                           // of the warps
     __shared__ Stats all[2][kMaxCluster];                     // of the row's CTAs; once more
-    __shared__ unsigned long long best_of[NT == 32 ? 1 : kMaxCluster * kTop];  // their best keys
+    __shared__ unsigned long long best_of[kMaxCluster * kTop];  // their best keys
     __shared__ int ids[NT];
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -310,7 +252,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
         for (int half = n / 2; half > 0; half >>= 1) {
             if (wid >= half && wid < 2 * half) work[tid - 32 * half] = k;
             __syncthreads();
-            if (wid < half) k = merged_keys(k, work[tid ^ 31], lane);
+            if (wid < half) k = merged_keys<1>(k, work[tid ^ 31], lane);
             __syncthreads();
         }
         return k;
@@ -421,7 +363,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
                     for (int w = 1; w < NT / 32; ++w) least = min(least, low32[w]);
                     base = max(base, least);  // (0: fewer threads than that have any)
                     hot = mine >= base;
-                    if (__syncthreads_count(hot) > min(kHot, NT - 1)) {
+                    if (__syncthreads_count(hot) > kHot) {
                         now = kTies;
                         continue;
                     }
@@ -442,7 +384,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
                             }
                         }
                     }
-                    const unsigned long long k = merged_lists(sorted_keys(mine_key, lane), NT / 32);
+                    const unsigned long long k = merged_lists(sorted_keys<1>(mine_key, lane), NT / 32);
                     if (tid == a.top - 1) bar = k;  // (0: fewer threads than that have any)
                     __syncthreads();
                     low = bar;
@@ -505,15 +447,11 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
     // ---- the CTA's sums, then the row's
     auto join = [&](int pass) {
         st.template join<32>();
-        if (NT > 32) {
-            if (lane == 0) stat[tid >> 5] = st;
-            __syncthreads();
-        }
+        if (lane == 0) stat[tid >> 5] = st;
+        __syncthreads();
         if (tid < 32) {  // to every CTA of the row, and the best keys to the first
-            if (NT > 32) {
-                st = stat[lane & (NT / 32 - 1)];
-                st.template join<NT / 32>();
-            }
+            st = stat[lane & (NT / 32 - 1)];
+            st.template join<NT / 32>();
             st.r = __shfl_sync(0xffffffffu, st.r, 0);
             st.s = __shfl_sync(0xffffffffu, st.s, 0);
             st.u = __shfl_sync(0xffffffffu, st.u, 0);
@@ -523,7 +461,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
             cg::cluster_group cluster = cg::this_cluster();
             if (!pass) cluster_wait();  // (they have all started)
             if (tid < C) *cluster.map_shared_rank(&all[pass][rank], tid) = st;
-            if (NT > 32 && !pass && tid < a.top) *cluster.map_shared_rank(best_of + rank * a.top + tid, 0) = tid < count ? list[tid] : 0;
+            if (!pass && tid < a.top) *cluster.map_shared_rank(best_of + rank * a.top + tid, 0) = tid < count ? list[tid] : 0;
             cluster_arrive();
             cluster_wait();
             if (tid < 32) {
@@ -561,7 +499,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
         join(1);
     }
     if (rank != 0) return;
-    if (NT > 32 && C > 1 && a.top) {
+    if (C > 1 && a.top) {
         const unsigned long long k = merged_lists(tid >> 5 < C && lane < a.top ? best_of[(tid >> 5) * a.top + lane] : 0, C);
         if (tid < a.top) list[tid] = k;
         __syncthreads();
@@ -592,7 +530,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 4) token_logprobs_kernel(c
 
 template <int TYPE>
 cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
-    constexpr int W = Vec16<TYPE>::W, kTile = kWide * kUnroll;
+    constexpr int W = Vec16<TYPE>::W, kTile = NT * kUnroll;
     // CTAs of a row: until there are two for every SM, and while each has more than a tile (192 rows of 65,537, fp32, top 20: two of a row 23 us,
     // four 31, as the keys are picked in each)
     a.cluster = 1;
@@ -600,10 +538,7 @@ cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
     a.c = a.scale * kLog2e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.cluster);
-    // A warp where one span of it holds the row, for more rows than wide CTAs are resident, and few keys (2000 rows of 2000, bf16,
-    // top 5: 13 us, by wide CTAs 22; of 8000: 26 and 23; 300 rows of 2000, top 12: 8.7 and 7.2; 2000 of 2000, top 30: 43 and 32).
-    const bool small = a.V / W <= 32 * kUnroll * kSpan && a.rows > 152 * 4 && a.top <= 24;
-    cfg.blockDim = dim3(small ? 32 : kWide);
+    cfg.blockDim = dim3(NT);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -613,12 +548,13 @@ cudaError_t logprobs_t(LogprobArgs a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return small ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 32>, a) : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, kWide>, a);
+    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int type, cudaStream_t st) {
+    if (logprobs_short(a, type)) return launch_token_logprobs_short(a, type, st);
     if (type == MOE_F32) return logprobs_t<MOE_F32>(a, st);
     if (type == MOE_F16) return logprobs_t<MOE_F16>(a, st);
     return logprobs_t<MOE_BF16>(a, st);

@@ -165,6 +165,38 @@ def test_mask_values(m, V, dtype):
             check(m, dev[2:3], ids_for(rng, 1, V, 1), 2, scale)
 
 
+@pytest.mark.parametrize("dtype", list(K.TYPES))
+@pytest.mark.parametrize("size", [(620, 1030), (5, 1030), (620, 4100), (3, 4100), (610, 8200), (609, 12300), (2, 16390), (609, 24590)])
+def test_row_sizes(m, size, dtype):
+    """Rows about the sizes where their number of warps changes, for many and for few of them, at odd addresses."""
+    R_, V = size
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy(rng.standard_normal((R_, V + 3)).astype(np.float32)).to(K.TYPES[dtype]).cuda()[:, 1:V + 1]
+    for v in (V, V - 7, V - 2):
+        check(m, x[:, :v], ids_for(rng, R_, v, 2), 17)
+
+
+@pytest.mark.parametrize("dtype", list(K.TYPES))
+@pytest.mark.parametrize("size", [(700, 1000), (2, 1000), (700, 2040), (2, 2040), (620, 8000), (2, 16000)])
+def test_best_in_few_places(m, size, dtype):
+    """The large logits lie close together, in a pattern that few threads see: far more of them than `top` in some rows, far
+    fewer in others, all equal in some."""
+    R_, V = size
+    W = 4 if dtype == "f32" else 8
+    rng = np.random.default_rng(R_ + V)
+    i = np.arange(V)
+    x = np.full((R_, V), -10.0)
+    for r in range(R_):
+        period, width = [(32, 9), (64, 9), (128, 15), (32, 2), (128, 1), (1 << 30, 5)][r % 6]
+        on = (i // W) % period < width
+        x[r, on] = [rng.standard_normal(on.sum()), 2.0, np.round(rng.standard_normal(on.sum()))][r // 6 % 3]
+        if r % 5 == 4:
+            x[r, ~on] = -np.inf
+    dev = torch.from_numpy(x).to(K.TYPES[dtype]).cuda()
+    for top in (1, 20, 32):
+        check(m, dev, ids_for(rng, R_, V, 1), top)
+
+
 def test_many_ids_and_none(m):
     rng = np.random.default_rng(3)
     x = torch.from_numpy(rng.standard_normal((3, 901)).astype(np.float32)).cuda()
