@@ -45,7 +45,7 @@ struct LogprobArgs {
     float *entropy, *lse;
     int cluster;  // CTAs of a row
 };
-bool logprobs_short(const LogprobArgs& a, int type);  // whether rows are few enough bytes, for their number, for the next
+bool logprobs_short(const LogprobArgs& a, int type);  // whether rows are short enough for the next
 cudaError_t launch_token_logprobs_short(const LogprobArgs& a, int type, cudaStream_t st);
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int type, cudaStream_t st);
 

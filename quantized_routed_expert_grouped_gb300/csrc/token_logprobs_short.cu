@@ -21,9 +21,9 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 4, kCap = 128;  // rows of a CTA at most; keys of a list
-// Bytes of a row, of few and of many rows (by CTAs of 256 threads, with bf16, top 5 and 20: 300 rows of 32 KB 10.3 and 14.1 us, here 8.1 and 8.4;
-// of 64 KB 10.8 and 17.0, here 12.2 and 13.1; 2000 rows of 32 KB 30.9 and 38.8, here 27.4 and 28.8; of 64 KB 45.8 and 57.8, here 57.7 and 59.8).
-constexpr int kFew = 32 * 1024, kMany = 48 * 1024;
+// Bytes of a row at most (bf16, top 5 and 20, by the other kernel and here: 15 rows of 43 KB 8.5 and 10.3 us, 8.9 and 9.3; 192 of 48 KB 11.2 and 15.0,
+// 9.7 and 10.4; 2000 of 32 KB 30.9 and 38.8, 27.4 and 28.8; of 64 KB 45.8 and 57.8, 57.7 and 59.8).
+constexpr int kRowBytes = 48 * 1024;
 
 __device__ __forceinline__ void copy16(void* to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from) : "memory");
@@ -286,7 +286,7 @@ cudaError_t short_g(LogprobArgs a, cudaStream_t st) {
     a.c = a.scale * kLog2e;
     if (G == 1) return launch_kernel(token_logprobs_short_kernel<TYPE, G>, dim3((a.rows + kRows - 1) / kRows), dim3(kRows * 32), kRows * bytes, st, true, a);
     if (bytes > 44 * 1024) {  // (with the rest above what every launch may have)
-        const cudaError_t e = cudaFuncSetAttribute(token_logprobs_short_kernel<TYPE, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMany);
+        const cudaError_t e = cudaFuncSetAttribute(token_logprobs_short_kernel<TYPE, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowBytes);
         if (e != cudaSuccess) return e;
     }
     return launch_kernel(token_logprobs_short_kernel<TYPE, G>, dim3(a.rows), dim3(G * 32), bytes, st, true, a);
@@ -303,7 +303,7 @@ cudaError_t short_t(const LogprobArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-bool logprobs_short(const LogprobArgs& a, int type) { return row_bytes(a, type) <= (many(a) ? kMany : kFew); }
+bool logprobs_short(const LogprobArgs& a, int type) { return row_bytes(a, type) <= kRowBytes; }
 
 cudaError_t launch_token_logprobs_short(const LogprobArgs& a, int type, cudaStream_t st) {
     if (type == MOE_F32) return short_t<MOE_F32>(a, st);
