@@ -202,8 +202,8 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, const KvSlot
 }
 
 // CTAs an SM, by the registers that a thread's keys need (prompts of 25k tokens, 8 heads of 128, 32 query heads, bf16: eight 108 us,
-// seven 112).
-constexpr int append_ctas(int type, int nb) { return nb <= 4 ? type == MOE_F32 ? 5 : 8 : nb <= 6 ? 4 : 3; }
+// seven 112; 4 and 16 heads of 256: five 125, three 153, six, which spill, 125; 192, fp32: six 130, four 155; one token of 192: 4.5 and 4.3).
+constexpr int append_ctas(int type, int nb) { return nb <= 4 ? type == MOE_F32 ? 5 : 8 : nb <= 6 ? 6 : 5; }
 
 template <int TYPE, int NB>
 __global__ void __launch_bounds__(kThreads, append_ctas(TYPE, NB)) kv8_append_kernel(const AppendArgs a) {
@@ -242,17 +242,19 @@ template <int TYPE>
 cudaError_t append_t(AppendArgs& a, cudaStream_t st) {
     const int64_t slots = kv8_slots(a.n_tokens, a.c.n_seqs);
     // Heads of a CTA. Keys: one where there are few blocks, with many eight, which the block's angles serve (the same prompts:
-    // eight 108 us, four 112; keys and values in one CTA, four heads each, 117). Queries: two rounds of a warp, or four (the same: half as
-    // many 2 % longer, twice 6 %; 16 heads of 192, fp32: 4 155 us, 16 180), 8 and 32 heads at most. Values: two (64 windows of four: two 8.4 us, one 9.0,
-    // four 8.7).
+    // eight 108 us, four 112; keys and values in one CTA, four heads each, 117). Values: two (64 windows of four: two 8.4 us, one 9.0, four 8.7).
     const bool many = slots * a.c.n_kv > 152 * 16;
     a.kheads = many ? 8 : 1;
     a.vheads = 2;
+    // Queries: two rounds of a warp, eight heads at most; where that makes many CTAs four rounds, 32 heads (the prompts: half as many
+    // 2 % longer, twice 6 %; 16 heads of 192, fp32: 4 155 us, 16 180; 26 prompts of 495 to 657, 32 heads of 160 and 4 key heads: 4 102, 2 120).
+    // Else a block of several tokens over two or four CTAs (12 prompts of 286 to 621, 16 query heads of 128, fp16: 13.9 us, undivided 19.9; four of 1200,
+    // 32 heads: 27.5 and 39; 51 windows of 1 to 22, 20 of 256: two 12.7, four 15.1, undivided 14.1).
     const int round = 32 / lanes_of(TYPE, a.c.D / 32);
-    a.qheads = many ? round > 8 ? 32 : 4 * round : round > 4 ? 8 : 2 * round;
-    // Few blocks of several tokens: a block's over two or four CTAs (12 prompts of 286 to 621, 16 query heads of 128, fp16:
-    // 13.9 us, undivided 19.9; 51 windows of 1 to 22, 20 of 256: two 12.7, four 15.1, undivided 14.1).
-    a.qshift = many || a.n_tokens <= 4 * a.c.n_seqs ? 0 : a.n_tokens <= 16 * a.c.n_seqs ? 1 : 2;
+    a.qheads = round > 4 ? 8 : 2 * round;
+    const bool many_q = many || slots * ((a.q.n + a.qheads - 1) / a.qheads) > 152 * 16;
+    if (many_q) a.qheads = round > 8 ? 32 : 4 * round;
+    a.qshift = many_q || a.n_tokens <= 4 * a.c.n_seqs ? 0 : a.n_tokens <= 16 * a.c.n_seqs ? 1 : 2;
     a.kparts = (a.c.n_kv + a.kheads - 1) / a.kheads;
     a.vparts = (a.c.n_kv + a.vheads - 1) / a.vheads;
     a.qparts = (a.q.n + a.qheads - 1) / a.qheads << a.qshift;

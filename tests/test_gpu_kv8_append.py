@@ -207,6 +207,21 @@ def test_not_finite_and_zero(m):
 
 
 @pytest.mark.parametrize("dtype", list(K.TYPES))
+@pytest.mark.parametrize("shape", [([5, 64], [500, 470], 600, 2, 32), ([31, 0, 62], [9, 6, 11], 7, 1, 256), ([0, 30, 7], [40, 3, 70], 9, 3, 192),
+                                   ([3, 9], [1500, 1100], 33, 1, 160), ([1] * 5, [5, 4, 6, 5, 4], 3, 2, 224)])
+def test_query_parts(m, shape, dtype):
+    """Queries by few and by many CTAs, a block's tokens by one, two and four, heads that leave part of a warp's round."""
+    starts, counts, hq, hkv, d = shape
+    c = Case(21, starts, counts, hq, hkv, d, 64, dtype)
+    rope = m.Rope(16, start=d - 16)
+    want = c.pool.clone()
+    q = c.append(m, rope=rope, q=c.q, q_weight=c.weights[0], k_weight=c.weights[1], q_out=torch.full_like(c.q, 5.0))
+    c.append(m, want, rope=rope, k_weight=c.weights[1])
+    assert int(c.err) == 0 and torch.equal(c.pool, want)
+    assert torch.equal(q, m.head_norm_rope(c.q, ints(c.places), rope, q_weight=c.weights[0])[0])
+
+
+@pytest.mark.parametrize("dtype", list(K.TYPES))
 def test_norm_without_eps(m, dtype):
     """eps 0: the places of a block that hold no new token do not count; a key of zeros is 0 / 0, and makes its block NaN."""
     c = Case(19, [3, 40], [7, 2], 2, 2, 96, 32, dtype)
