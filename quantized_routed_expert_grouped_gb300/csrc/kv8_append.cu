@@ -202,7 +202,7 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, const KvSlot
 }
 
 // CTAs an SM, by the registers that a thread's keys need (prompts of 25k tokens, 8 heads of 128, 32 query heads, bf16: eight 108 us,
-// seven 112; 4 and 16 heads of 256: five 125, three 153, six, which spill, 125; 192, fp32: six 130, four 155; one token of 192: 4.5 and 4.3).
+// seven 112; 4 and 16 heads of 256: five 125, three 153, six, which spill, 125; 192, fp32: six 130, four 155; three tokens of 192: 4.5 and 4.3).
 constexpr int append_ctas(int type, int nb) { return nb <= 4 ? type == MOE_F32 ? 5 : 8 : nb <= 6 ? 6 : 5; }
 
 template <int TYPE, int NB>

@@ -11,9 +11,9 @@
 // the list holds (ties, masked rows), the top-th best value is found by halving, and of those that equal it the first are taken,
 // in the order of their indices: never more work than a pass over the row for each bit of a value.
 //
-// Bound by its instructions (six or seven a logit; a row of its own 3 us of latencies). Measured (GB300): bf16, top 20: 2000 rows of 2000 8.3 us (by
-// CTAs of 256 threads, which read a row twice at its best keys, 24), of 16,000 28.8 (39); fp32: 8000 of 19 10 us (37), of 1000 15.8 (66), of 4000
-// 39 us for 128 MB (97).
+// Bound by its instructions (17.7 a lane and logit of 16,000 in bf16, top 20, 71 % of the issue slots; fused products and clamps in pairs, as in
+// token_logprobs.cu, take as long), a row of its own by 3 us of latencies. Measured (GB300): bf16, top 20: 2000 rows of 2000 8.3 us (by
+// the other kernel 24), of 16,000 28.9 (39); fp32: 8000 of 19 10 us (37), of 1000 15.8 (66), of 4000 39 us for 128 MB (97).
 #include "token_logprobs.cuh"
 
 namespace moe {
