@@ -620,20 +620,22 @@ _TWO_PI = 2 * 314159265358979323846264338327950288419716939937510, 10 ** 50  # a
 class Rope:
     """A rotation of heads by position, kept between calls: dims start .. start + rot of a head are rot / 2 pairs, dims
     (start + i, start + i + rot / 2), or interleaved (start + 2 i, start + 2 i + 1), and pair i turns by position * f_i.
-    rot is a multiple of 16, start of 8. f_i = theta^(-2 i / rot), or inv_freq[i] where given (say, frequencies that
-    were rounded to fp32). scaling: None, or for long contexts
+    rot is a multiple of 16, start of 8. f_i = theta^(-2 i / rot) (theta 10000 where not given), or inv_freq[i] where given (say,
+    frequencies that were rounded to fp32). scaling: None, or for long contexts
       {"kind": "linear", "scale": s}: all divided by s;
       {"kind": "yarn", "scale": s, "original": o, "fast": 32, "slow": 1}: pairs that turn less than `slow` times over the
         original length o are divided by s, those that turn more than `fast` times are kept, with a line in i between (whose
-        ends are moved outward to whole pairs); the rotated dims are multiplied by 0.1 log s + 1;
+        ends are moved outward to whole pairs); the rotated dims are multiplied by 0.1 log s + 1. The ends come from theta: with
+        inv_freq, which have to be its powers (to 2^-7 of themselves), it has to be given;
       {"kind": "bands", "scale": s, "original": o, "low": 1, "high": 4}: the same by low and high, with a line in the number
         of turns, and without a factor.
     factor (of the rotated dims) overrides the scaling's. Angles are exact to 1e-7 at any 32-bit position."""
 
-    def __init__(self, rot, theta=10000.0, start=0, interleaved=False, scaling=None, inv_freq=None, factor=None, device="cuda"):
+    def __init__(self, rot, theta=None, start=0, interleaved=False, scaling=None, inv_freq=None, factor=None, device="cuda"):
         if rot <= 0 or rot % 16 or start < 0 or start % 8:
             raise MoeError("rot: a multiple of 16, start: a multiple of 8, expected")
         if inv_freq is None:
+            theta = 10000.0 if theta is None else theta
             if not (theta > 0 and math.isfinite(theta)):
                 raise MoeError("theta: a positive number expected")
             f = [float(theta) ** (-2 * i / rot) for i in range(rot // 2)]
@@ -672,8 +674,10 @@ class Rope:
             keep = [min(max((t - p["low"]) / (p["high"] - p["low"]), 0.0), 1.0) for t in turns]
             factor = 1.0
         else:
-            if theta <= 1:
-                raise MoeError("scaling: yarn takes a theta above 1")
+            if theta is None or not 1 < theta < math.inf:
+                raise MoeError("scaling: yarn takes a theta above 1, with inv_freq the one whose powers they are")
+            if any(not abs(x * float(theta) ** (2 * i / rot) - 1) <= 2.0 ** -7 for i, x in enumerate(f)):
+                raise MoeError("scaling: yarn takes frequencies that are theta's powers")
             at = [rot * math.log(p["original"] / (2 * math.pi * p[r])) / (2 * math.log(theta)) for r in ("fast", "slow")]
             lo, hi = max(math.floor(at[0]), 0), math.ceil(at[1])
             keep = [1 - (min(max((i - lo) / (hi - lo), 0.0), 1.0) if hi > lo else float(i > lo)) for i in range(rot // 2)]

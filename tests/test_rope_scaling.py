@@ -1,0 +1,43 @@
+"""The frequencies of a Rope with a scaling for long contexts, against the scalings' definitions written apart from the
+package's code, pair by pair."""
+import math
+
+import pytest
+
+from test_kv8_abi import m  # noqa: F401
+
+
+def powers(rot, theta):
+    return [theta ** (-2.0 * i / rot) for i in range(rot // 2)]
+
+
+def turns(f, original):
+    """How many times a pair turns over the original length."""
+    return original * f / (2 * math.pi)
+
+
+def test_yarn_of_given_frequencies(m):  # noqa: F811
+    """Given frequencies get the scaling that the theta whose powers they are gives them; without that theta, or where they are
+    not its powers, there is no line between the pairs that turn often and seldom, and the call is refused."""
+    yarn = {"kind": "yarn", "scale": 16, "original": 8192}
+    for rot, theta in ((128, 500000.0), (64, 10000.0), (32, 1e6)):
+        f = powers(rot, theta)
+        want = m.Rope(rot, theta=theta, scaling=yarn, device="cpu")
+        got = m.Rope(rot, theta=theta, inv_freq=f, scaling=yarn, device="cpu")
+        assert got.inv_freq == want.inv_freq and got.factor == want.factor
+        rounded = [x * (1 + 2.0 ** -8 * (-1) ** i) for i, x in enumerate(f)]  # as bf16 has them, at most
+        got = m.Rope(rot, theta=theta, inv_freq=rounded, scaling=yarn, device="cpu")
+        assert all(math.isclose(x / r, y / p) for x, r, y, p in zip(got.inv_freq, rounded, want.inv_freq, f))
+        for kw in (dict(), dict(theta=2 * theta), dict(theta=1.0), dict(theta=0.0), dict(theta=math.nan)):
+            with pytest.raises(m.MoeError):
+                m.Rope(rot, inv_freq=f, scaling=yarn, device="cpu", **kw)
+        with pytest.raises(m.MoeError):
+            m.Rope(rot, theta=theta, inv_freq=[-x for x in f], scaling=yarn, device="cpu")
+    # without a line there is nothing to find: no theta is needed, and none is looked at
+    f = powers(64, 500000.0)
+    for kw in (dict(), dict(theta=7.0)):
+        assert m.Rope(64, inv_freq=f, device="cpu", **kw).inv_freq == f
+        assert m.Rope(64, inv_freq=f, scaling={"kind": "linear", "scale": 4}, device="cpu", **kw).inv_freq == [x / 4 for x in f]
+    bands = {"kind": "bands", "scale": 8, "original": 8192}
+    assert m.Rope(64, inv_freq=f, scaling=bands, device="cpu").inv_freq == m.Rope(64, theta=500000.0, scaling=bands, device="cpu").inv_freq
+    assert m.Rope(64, device="cpu").inv_freq == powers(64, 10000.0)
