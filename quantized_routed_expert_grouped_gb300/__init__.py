@@ -626,7 +626,7 @@ class Rope:
       {"kind": "yarn", "scale": s, "original": o, "fast": 32, "slow": 1}: pairs that turn less than `slow` times over the
         original length o are divided by s, those that turn more than `fast` times are kept, with a line in i between (whose
         ends are moved outward to whole pairs); the rotated dims are multiplied by 0.1 log s + 1. The ends come from theta: with
-        inv_freq, which have to be its powers (to 2^-7 of themselves), it has to be given;
+        inv_freq, which have to be its powers (to 2^-7 of themselves), it has to be given. fast is above slow, s at least 1;
       {"kind": "bands", "scale": s, "original": o, "low": 1, "high": 4}: the same by low and high, with a line in the number
         of turns, and without a factor.
     factor (of the rotated dims) overrides the scaling's. Angles are exact to 1e-7 at any 32-bit position."""
@@ -674,6 +674,8 @@ class Rope:
             keep = [min(max((t - p["low"]) / (p["high"] - p["low"]), 0.0), 1.0) for t in turns]
             factor = 1.0
         else:
+            if p["fast"] <= p["slow"] or s < 1:
+                raise MoeError("scaling: yarn takes fast above slow, and a scale of at least 1")
             if theta is None or not 1 < theta < math.inf:
                 raise MoeError("scaling: yarn takes a theta above 1, with inv_freq the one whose powers they are")
             if any(not abs(x * float(theta) ** (2 * i / rot) - 1) <= 2.0 ** -7 for i, x in enumerate(f)):

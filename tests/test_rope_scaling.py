@@ -41,3 +41,14 @@ def test_yarn_of_given_frequencies(m):  # noqa: F811
     bands = {"kind": "bands", "scale": 8, "original": 8192}
     assert m.Rope(64, inv_freq=f, scaling=bands, device="cpu").inv_freq == m.Rope(64, theta=500000.0, scaling=bands, device="cpu").inv_freq
     assert m.Rope(64, device="cpu").inv_freq == powers(64, 10000.0)
+
+
+def test_yarn_refusals(m):  # noqa: F811
+    """Bounds in the wrong order have no line between them, and below a scale of 1 the factor is less than 1, at last negative."""
+    for kw in (dict(fast=1.0, slow=32.0), dict(fast=1.0), dict(slow=32.0), dict(fast=4.0, slow=4.0), dict(scale=0.5), dict(scale=1e-5)):
+        with pytest.raises(m.MoeError):
+            m.Rope(64, scaling={"kind": "yarn", "scale": 4, "original": 4096, **kw}, device="cpu")
+    one = m.Rope(64, scaling={"kind": "yarn", "scale": 1, "original": 4096}, device="cpu")
+    assert one.factor == 1.0 and all(math.isclose(a, b) for a, b in zip(one.inv_freq, powers(64, 10000.0)))
+    short = m.Rope(64, scaling={"kind": "linear", "scale": 0.5}, device="cpu")
+    assert short.inv_freq == [2 * x for x in powers(64, 10000.0)] and short.factor == 1.0
