@@ -682,7 +682,8 @@ class Rope:
                 raise MoeError("scaling: yarn takes frequencies that are theta's powers")
             at = [rot * math.log(p["original"] / (2 * math.pi * p[r])) / (2 * math.log(theta)) for r in ("fast", "slow")]
             lo, hi = max(math.floor(at[0]), 0), math.ceil(at[1])
-            keep = [1 - (min(max((i - lo) / (hi - lo), 0.0), 1.0) if hi > lo else float(i > lo)) for i in range(rot // 2)]
+            # (hi <= lo: pair 0, where a line starts at the earliest, lies behind its end)
+            keep = [1 - min(max((i - lo) / (hi - lo), 0.0), 1.0) if hi > lo else 0.0 for i in range(rot // 2)]
             factor = 0.1 * math.log(s) + 1
         return [x * k + x / s * (1 - k) for x, k in zip(f, keep)], factor
 

@@ -52,3 +52,31 @@ def test_yarn_refusals(m):  # noqa: F811
     assert one.factor == 1.0 and all(math.isclose(a, b) for a, b in zip(one.inv_freq, powers(64, 10000.0)))
     short = m.Rope(64, scaling={"kind": "linear", "scale": 0.5}, device="cpu")
     assert short.inv_freq == [2 * x for x in powers(64, 10000.0)] and short.factor == 1.0
+
+
+def yarn_share(i, rot, theta, original, fast, slow):
+    """How much of pair i's frequency is divided: none up to the last whole pair (pair 0 at least) before the place where pairs turn
+    `fast` times, all from the first whole one behind the place where they turn `slow` times, a line in i between."""
+    def place(r):  # a real index, by halving (pairs turn less and less)
+        lo, hi = -10.0 * rot, 10.0 * rot
+        for _ in range(200):
+            mid = (lo + hi) / 2
+            lo, hi = (mid, hi) if turns(theta ** (-2 * mid / rot), original) > r else (lo, mid)
+        return lo
+    first, last = max(0, math.floor(place(fast))), math.ceil(place(slow))
+    return 1.0 if i >= last else 0.0 if i <= first else (i - first) / (last - first)
+
+
+@pytest.mark.parametrize("rot,theta,original,fast,slow,scale", [
+    (64, 10000.0, 4096, 32.0, 1.0, 4.0), (128, 500000.0, 8192, 32.0, 1.0, 16.0), (128, 1e6, 32768, 32.0, 1.0, 4.0), (32, 10000.0, 100, 32.0, 1.0, 2.0),
+    (96, 150000.0, 4096, 32.0, 1.0, 32.0), (64, 10000.0, 1 << 20, 32.0, 1.0, 8.0), (16, 100.0, 2048, 8.0, 2.0, 40.0), (64, 10000.0, 7, 32.0, 1.0, 2.0),
+    # shorter than a turn of the first pair: all pairs turn less than `slow` times
+    (64, 10000.0, 6, 32.0, 1.0, 2.0), (64, 10000.0, 1, 2.0, 1.0, 4.0), (64, 10000.0, 2, 2.0, 1.0, 1.0)])
+def test_yarn_line(m, rot, theta, original, fast, slow, scale):  # noqa: F811
+    got = m.Rope(rot, theta=theta, scaling={"kind": "yarn", "scale": scale, "original": original, "fast": fast, "slow": slow}, device="cpu")
+    assert math.isclose(got.factor, 0.1 * math.log(scale) + 1)
+    for i, (f, y) in enumerate(zip(powers(rot, theta), got.inv_freq)):
+        share = yarn_share(i, rot, theta, original, fast, slow)
+        assert math.isclose(y, f * (1 - share) + f / scale * share, rel_tol=1e-9), i
+        if turns(f, original) < slow * (1 - 1e-9) * theta ** (-2 / rot):  # (a pair further: the ends are moved outward)
+            assert math.isclose(y, f / scale)
