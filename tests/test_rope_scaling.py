@@ -80,3 +80,13 @@ def test_yarn_line(m, rot, theta, original, fast, slow, scale):  # noqa: F811
         assert math.isclose(y, f * (1 - share) + f / scale * share, rel_tol=1e-9), i
         if turns(f, original) < slow * (1 - 1e-9) * theta ** (-2 / rot):  # (a pair further: the ends are moved outward)
             assert math.isclose(y, f / scale)
+
+
+def test_bands_line(m):  # noqa: F811
+    """A line in the number of turns, of pairs that turn either way."""
+    f = powers(64, 10000.0)
+    f = [-x if i % 3 == 1 else x for i, x in enumerate(f)]
+    got = m.Rope(64, inv_freq=f, scaling={"kind": "bands", "scale": 8, "original": 1024, "low": 1, "high": 4}, device="cpu")
+    for x, y in zip(f, got.inv_freq):
+        keep = min(max((abs(turns(x, 1024)) - 1) / 3, 0), 1)
+        assert math.isclose(y, x * keep + x / 8 * (1 - keep)), x
