@@ -667,7 +667,7 @@ class Rope:
             return [x / s for x in f], 1.0
         if not all(x is not None and x > 0 for x in p.values()):
             raise MoeError(f"scaling: {kind} takes positive {', '.join(p)}")
-        turns = [p["original"] * x / (2 * math.pi) for x in f]
+        turns = [p["original"] * abs(x) / (2 * math.pi) for x in f]
         if kind == "bands":
             if p["high"] <= p["low"]:
                 raise MoeError("scaling: high above low expected")
