@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 import struct
 
@@ -632,19 +633,26 @@ class Rope:
     factor (of the rotated dims) overrides the scaling's. Angles are exact to 1e-7 at any 32-bit position."""
 
     def __init__(self, rot, theta=None, start=0, interleaved=False, scaling=None, inv_freq=None, factor=None, device="cuda"):
-        if rot <= 0 or rot % 16 or start < 0 or start % 8:
-            raise MoeError("rot: a multiple of 16, start: a multiple of 8, expected")
-        if inv_freq is None:
-            theta = 10000.0 if theta is None else theta
-            if not (theta > 0 and math.isfinite(theta)):
-                raise MoeError("theta: a positive number expected")
-            f = [float(theta) ** (-2 * i / rot) for i in range(rot // 2)]
-        else:
-            f = [float(x) for x in inv_freq]
-        if len(f) != rot // 2 or not all(math.isfinite(x) for x in f):
-            raise MoeError(f"inv_freq: {rot // 2} finite numbers expected")
-        f, scaled = self._scaled(f, rot, theta, dict(scaling or {"kind": "none"}))
-        self.inv_freq, self.factor = f, scaled if factor is None else float(factor)
+        try:
+            rot, start = operator.index(rot), operator.index(start)
+            if rot <= 0 or rot % 16 or start < 0 or start % 8:
+                raise MoeError("rot: a multiple of 16, start: a multiple of 8, expected")
+            if inv_freq is None:
+                theta = 10000.0 if theta is None else theta
+                if not (theta > 0 and math.isfinite(theta)):
+                    raise MoeError("theta: a positive number expected")
+                f = [float(theta) ** (-2 * i / rot) for i in range(rot // 2)]
+            else:
+                f = [float(x) for x in inv_freq]
+            if len(f) != rot // 2 or not all(math.isfinite(x) for x in f):
+                raise MoeError(f"inv_freq: {rot // 2} finite numbers expected")
+            f, scaled = self._scaled(f, rot, theta, dict(scaling or {"kind": "none"}))
+            factor = scaled if factor is None else float(factor)
+        except (TypeError, ValueError, OverflowError) as e:
+            raise MoeError(f"rope: an argument is not of its kind, or out of its range: {e}") from None
+        if not all(math.isfinite(x) for x in f) or not abs(factor) <= 3.4028234663852886e38:
+            raise MoeError("rope: frequencies out of range, or a factor that fp32 does not hold")
+        self.inv_freq, self.factor = f, factor
         self.rot, self.start, self.interleaved = rot, start, bool(interleaved)
         # fractions of a turn a position, rounded to 64 bits (as int64 tensors hold them)
         turns = []

@@ -90,3 +90,18 @@ def test_bands_line(m):  # noqa: F811
     for x, y in zip(f, got.inv_freq):
         keep = min(max((abs(turns(x, 1024)) - 1) / 3, 0), 1)
         assert math.isclose(y, x * keep + x / 8 * (1 - keep)), x
+
+
+def test_numbers_out_of_range(m):  # noqa: F811
+    """Numbers that give no frequency or no factor, or are none, are argument errors."""
+    far, yarn = {"kind": "linear", "scale": 1e-320}, {"kind": "yarn", "scale": 4, "original": 4096}
+    bad = [dict(factor=math.nan), dict(factor=math.inf), dict(factor=1e39), dict(factor="x"), dict(theta=1e-320), dict(theta="x"), dict(theta=math.nan), dict(theta=10 ** 400),
+           dict(scaling=far), dict(scaling={"kind": "linear", "scale": "4"}), dict(scaling={"kind": "linear", "scale": 10 ** 400}), dict(scaling={**yarn, "original": math.inf}),
+           dict(scaling={**yarn, "fast": math.inf}), dict(scaling={**yarn, "fast": math.nan}), dict(scaling={**yarn, "original": 10 ** 400}), dict(scaling={**yarn, "slow": 1e-320}),
+           dict(scaling={**yarn, "original": "4096"}), dict(scaling={**yarn, "scale": None}), dict(scaling="linear"), dict(inv_freq=[10 ** 400] * 32), dict(inv_freq=["x"] * 32),
+           dict(inv_freq=5), dict(rot=64.0), dict(rot="64"), dict(start=8.0), dict(start=None)]
+    for kw in bad:
+        with pytest.raises(m.MoeError):
+            m.Rope(**{"rot": 64, "device": "cpu", **kw})
+            pytest.fail(f"not refused: {kw}")
+    assert m.Rope(64, factor=-2, theta=1e-300, device="cpu").factor == -2.0
