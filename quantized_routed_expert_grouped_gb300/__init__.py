@@ -662,7 +662,11 @@ class Rope:
             turns.append(((2 * n + d) // (2 * d) + 2 ** 63) % 2 ** 64 - 2 ** 63)
         self.turns = torch.tensor(turns, dtype=torch.int64, device=device)
         self._device = self.turns.get_device()
-        self._fields = (self.turns.data_ptr(), rot, start, int(self.interleaved), self.factor)
+        self._fields = (rot, start, int(self.interleaved), self.factor)  # (without the address: a copy has its own)
+
+    def __setstate__(self, state):  # (loading may move tensors to another device)
+        self.__dict__.update(state)
+        self._device = self.turns.get_device()
 
     @staticmethod
     def _scaled(f, rot, theta, p):
@@ -703,7 +707,7 @@ def _rope(rope, dev, D):
         raise MoeError(f"rope: on device {dev} expected")
     if rope.start + rope.rot > D:
         raise MoeError(f"rope: dims {rope.start} .. {rope.start + rope.rot} of heads of {D}")
-    return rope._fields
+    return (rope.turns.data_ptr(), *rope._fields)
 
 
 def _heads(x, weight, out, N, D, dtype, dev, stream, name):

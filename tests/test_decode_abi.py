@@ -210,3 +210,15 @@ def test_other_device(m, monkeypatch):  # noqa: F811
     for f in (lambda: m.head_norm_rope(x, pos), lambda: m.kv8_append(x, x, pool, table, cu, one), lambda: m.token_logprobs(x[0])):
         with pytest.raises(m.MoeError, match="device"):
             f()
+
+
+def test_copies_of_a_rope(m):  # noqa: F811
+    """A copied or unpickled Rope names its own frequencies' memory, not that of the one it was made from."""
+    import copy
+    import pickle
+    r = m.Rope(64, start=8, interleaved=True, factor=0.5, device="cpu")
+    for c in (copy.copy(r), copy.deepcopy(r), pickle.loads(pickle.dumps(r))):
+        assert torch.equal(c.turns, r.turns) and m._rope(c, -1, 128) == (c.turns.data_ptr(), 64, 8, 1, 0.5)
+    assert copy.deepcopy(r).turns.data_ptr() != r.turns.data_ptr()
+    r._device = 5  # as one saved on another device and loaded onto this one
+    assert pickle.loads(pickle.dumps(r))._device == -1
