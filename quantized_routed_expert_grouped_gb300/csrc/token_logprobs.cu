@@ -505,7 +505,10 @@ __global__ void __launch_bounds__(NT, 4) token_logprobs_kernel(const LogprobArgs
         __syncthreads();
     }
     const bool none = st.m == -INFINITY && st.s == st.s;  // (a row of NaN is none of -inf)
-    const float l2 = log2f(st.s), ls = (l2 - (ends ? 0.0f : fmaf(st.m, a.c, -st.r))) * kLn2;  // log of the sum of e^(scale (x - m))
+    // The log of the sum of e^(scale (x - m)), and the entropy: of at least 0, but each a difference of numbers of up to kSlack and a half, whose
+    // rounding falls on either side where one token has all of the probability.
+    auto above0 = [](float v) { return v < 0.0f ? 0.0f : v; };  // (a NaN stays)
+    const float l2 = log2f(st.s), ls = above0((l2 - (ends ? 0.0f : fmaf(st.m, a.c, -st.r))) * kLn2);
     auto logprob = [&](float v) { return none ? -INFINITY : (v - st.m) * a.scale - ls; };
     for (int i = tid; i < a.n_ids; i += NT) {
         const int64_t to = static_cast<int64_t>(row) * a.n_ids + i;
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(NT, 4) token_logprobs_kernel(const LogprobArgs
         a.top_logprobs[to] = has ? logprob(unorder(static_cast<uint32_t>(k >> 32))) : NAN;
     }
     if (tid == 0) {
-        if (a.entropy) a.entropy[row] = none ? 0.0f : (l2 - st.u / st.s) * kLn2;
+        if (a.entropy) a.entropy[row] = none ? 0.0f : above0((l2 - st.u / st.s) * kLn2);
         if (a.lse) a.lse[row] = none ? -INFINITY : fmaf(st.m, a.scale, ls);
     }
 }
