@@ -723,9 +723,9 @@ def _heads(x, weight, out, N, D, dtype, dev, stream, name):
         out = torch.empty(shape, dtype=dtype, device=x.device) if stream is None else _empty(stream, shape, dtype, x.device)
         ot, oh = H * D, D
     else:
-        ot, oh, od = out.stride()
-        if out.shape != shape or out.dtype is not dtype or (od != 1 and N) or out.get_device() != dev:
+        if out.shape != shape or out.dtype is not dtype or (out.stride(2) != 1 and N) or out.get_device() != dev:
             raise MoeError(f"{name}_out: {name}'s shape, type and device, contiguous in the last dimension, expected")
+        ot, oh, _ = out.stride()
     w = 0
     if weight is not None:
         w = weight.data_ptr()
@@ -770,7 +770,7 @@ def kv8_append(k, v, pool, page_table, cu_tokens, start, rope=None, q=None, q_we
     they were."""
     c, dev = _kv8_cache(pool, page_table)
     hkv, D, n = c[2], c[3], c[8]
-    N, ks, vs = k.shape[0], k.stride(), v.stride()
+    N, ks, vs = k.shape[0] if k.dim() else 0, k.stride(), v.stride()
     if k.shape != (N, hkv, D) or v.shape != k.shape or v.dtype is not k.dtype or (N and (ks[2] != 1 or vs[2] != 1)):
         raise MoeError(f"k, v: [tokens, {hkv}, {D}] of one type, contiguous in the last dimension, expected")
     if k_weight is not None and (k_weight.shape != (D,) or not k_weight.is_contiguous()):

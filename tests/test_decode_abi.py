@@ -222,3 +222,22 @@ def test_copies_of_a_rope(m):  # noqa: F811
     assert copy.deepcopy(r).turns.data_ptr() != r.turns.data_ptr()
     r._device = 5  # as one saved on another device and loaded onto this one
     assert pickle.loads(pickle.dumps(r))._device == -1
+
+
+def test_ranks_refused(m, monkeypatch):  # noqa: F811
+    """Tensors with too few or too many dimensions are argument errors like any other."""
+    monkeypatch.setattr(m, "_device", lambda t: -1)
+    monkeypatch.setattr(m, "_ptr", lambda t, dev: t.data_ptr())
+    monkeypatch.setattr(m, "_launch", lambda *a: pytest.fail("launched"))
+    q, pos = torch.zeros((3, 4, 64)), torch.zeros(3, dtype=torch.int32)
+    pool, table = m.kv8_pool(2, 2, 64, 32, device="cpu"), torch.zeros((1, 2), dtype=torch.int32)
+    k, cu, start = torch.zeros((3, 2, 64)), torch.tensor([0, 3], dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    one = torch.zeros(())
+    for other in (one, q[0, 0], q[0], q[None]):
+        for f in (lambda: m.head_norm_rope(other, pos), lambda: m.head_norm_rope(q, pos, k=other), lambda: m.head_norm_rope(q, pos, q_out=other),
+                  lambda: m.head_norm_rope(q, pos, k=q, k_out=other), lambda: m.kv8_append(other, k, pool, table, cu, start), lambda: m.kv8_append(k, other, pool, table, cu, start),
+                  lambda: m.kv8_append(k, k, pool, table, cu, start, q=other), lambda: m.kv8_append(k, k, pool, table, cu, start, q=q, q_out=other),
+                  lambda: m.token_logprobs(other) if other.dim() != 2 else m.token_logprobs(q), lambda: m.token_logprobs(q[0, :2], other.int()),
+                  lambda: m.head_norm_rope(q, pos, q_weight=other), lambda: m.kv8_append(k, k, pool, table, cu, start, k_weight=other[..., None])):
+            with pytest.raises(m.MoeError):
+                f()
