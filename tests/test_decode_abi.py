@@ -238,6 +238,6 @@ def test_ranks_refused(m, monkeypatch):  # noqa: F811
                   lambda: m.head_norm_rope(q, pos, k=q, k_out=other), lambda: m.kv8_append(other, k, pool, table, cu, start), lambda: m.kv8_append(k, other, pool, table, cu, start),
                   lambda: m.kv8_append(k, k, pool, table, cu, start, q=other), lambda: m.kv8_append(k, k, pool, table, cu, start, q=q, q_out=other),
                   lambda: m.token_logprobs(other) if other.dim() != 2 else m.token_logprobs(q), lambda: m.token_logprobs(q[0, :2], other.int()),
-                  lambda: m.head_norm_rope(q, pos, q_weight=other), lambda: m.kv8_append(k, k, pool, table, cu, start, k_weight=other[..., None])):
+                  lambda: m.head_norm_rope(q, pos, q_weight=other[..., None]), lambda: m.kv8_append(k, k, pool, table, cu, start, k_weight=other[..., None])):
             with pytest.raises(m.MoeError):
                 f()
