@@ -76,7 +76,7 @@ int moe_kv8_append(const moe_kv8_append_call* call, cudaStream_t stream);
  *   logprobs[row][i] = log p[ids[row][i]] (-inf for an id outside [0, vocab)),
  *   top_ids[row][0 .. top): the largest logits' indices in descending order, among equal ones the lower first (-0 equals
  *     0), and top_logprobs[row][..] their log p,
- *   entropy[row] = -sum p log p, lse[row] = log sum e^(scale * x).
+ *   entropy[row] = -sum p log p, lse[row] = log sum e^(scale * x); log p is at most 0 and the entropy at least 0, rounded too.
  * Logits of -inf have p = 0; a row of nothing else gives -inf, entropy 0, and the first indices. A row with a NaN or +inf
  * gives NaN for all but top_ids, in which NaN logits have no place (-1 behind the last). Sums are fp32. logits: rows row_stride
  * elements apart, on their element's boundary; 0 < vocab < 2^31, 0 <= top <= min(32, vocab), scale from 2^-100 to 2^100.

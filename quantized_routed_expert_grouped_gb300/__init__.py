@@ -766,8 +766,8 @@ def kv8_append(k, v, pool, page_table, cu_tokens, start, rope=None, q=None, q_we
     """kv8_write of keys that are normed (k_weight [head_dim]) and rotated on the way, and the queries of the same tokens, q
     [tokens, heads, head_dim], normed and rotated beside them: one launch from the projection's rows to what kv8_attention
     takes. positions int32 [tokens]: what each row turns by (a draft token by its depth in a tree), None: its
-    position in the cache. Returns q_out (None without q); q_out may be q itself. Rows of q_out of a sequence that is refused (err) are left as
-    they were."""
+    position in the cache. Returns q_out (None without q); q_out may be q itself. Rows of q_out of a sequence that is refused (err), and
+    rows behind the last sequence, are left as they were."""
     c, dev = _kv8_cache(pool, page_table)
     hkv, D, n = c[2], c[3], c[8]
     N, ks, vs = k.shape[0] if k.dim() else 0, k.stride(), v.stride()
@@ -789,7 +789,7 @@ def kv8_append(k, v, pool, page_table, cu_tokens, start, rope=None, q=None, q_we
 def token_logprobs(logits, ids=None, top=0, scale=1.0, stream=None):
     """Of rows of logits [rows, vocab], with p = softmax(scale * logits): log p of the given tokens, ids int32 [rows, n] (-inf for
     an id outside the vocabulary, such as -1 for none); the `top` (up to 32) most likely tokens' log p and ids, equal logits in order of
-    their ids; the entropy; and the log-sum-exp. Returns (logprobs fp32 [rows, n], top_logprobs fp32 [rows, top], top_ids
+    their ids; the entropy; and the log-sum-exp. Log p is at most 0, the entropy at least 0. Returns (logprobs fp32 [rows, n], top_logprobs fp32 [rows, top], top_ids
     int32 [rows, top], entropy fp32 [rows], lse fp32 [rows]), None for what was not asked for."""
     dev = _device(logits)
     shape = logits.shape

@@ -57,7 +57,8 @@ template <int TYPE, int L, bool VEC>
 cudaError_t rope_l(HeadRopeArgs& a, cudaStream_t st) {
     constexpr int G = 32 / L;
     // Many tokens: up to four a CTA, so that weights and setting up serve several (8191 tokens of 72 heads of 128: 51.7 us, with
-    // eight 52.1, with sixteen 57); few: a token's rounds over the CTA's warps, and over several CTAs.
+    // eight 52.1, with sixteen 57); few: a token's rounds over the CTA's warps, and over several CTAs. Three a CTA (2736 to 3647 tokens) leave a warp in
+    // four without any: 3000 tokens take 22.5 us, 3400, a second wave of CTAs, 32.0, 4000, four a CTA, 26.7.
     const int rounds = (a.q.n + G - 1) / G + (a.k.n + G - 1) / G;
     const int64_t each = a.n / (152 * 6);
     a.tokens = static_cast<int>(each < 1 ? 1 : each > kMaxTokens ? kMaxTokens : each);

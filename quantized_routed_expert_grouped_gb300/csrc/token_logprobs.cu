@@ -9,7 +9,9 @@
 // moves, which few tiles need. (It is above -2^24: what lies below has a power of 0 there, and nothing but such logits is a row for the second pass.) Threads join theirs, then the CTAs of a row, always in the same order. t 2^t of a logit of -inf has to be 0: 16-bit logits
 // are clamped in pairs before they are converted, fp32's t one by one. Where that or c m leaves the range (rows masked by their type's lowest value,
 // scales near 0 or far above 1) the row's sums are taken a second time, differences first. Powers are the hardware's (2^-22 of
-// themselves); sums are fp32, eight of a thread's terms in a row at most before they are added to its two running ones.
+// themselves); sums are fp32: a thread's terms of a tile in two halves (of eight in fp32, of sixteen in 16 bits), which are then added to its two
+// running ones; the second pass, which few rows need, adds them to those one by one. Joined sums are not next to the row's largest logit, so what
+// cannot be below 0 is held there at the end.
 //
 // The most likely tokens. A logit and its index are one 64-bit key, larger for a larger logit and among equal ones for
 // the lower index: every order is strict, and nothing depends on timing. A CTA keeps its best `top` keys in order; the

@@ -11,8 +11,9 @@
 // the list holds (ties, masked rows), the top-th best value is found by halving, and of those that equal it the first are taken,
 // in the order of their indices: never more work than a pass over the row for each bit of a value.
 //
-// Bound by its instructions (17.7 a lane and logit of 16,000 in bf16, top 20, 71 % of the issue slots; fused products and clamps in pairs, as in
-// token_logprobs.cu, take as long), a row of its own by 3 us of latencies. Measured (GB300): bf16, top 20: 2000 rows of 2000 8.3 us (by
+// Bound by its instructions (17.7 a lane and logit of 16,000 in bf16, top 20, 71 % of the issue slots: 13.6 are the copies and the two passes, which
+// a row without the best tokens takes too, 2.3 the bar and the first key, 1.8 the other nineteen; the other kernel's one pass takes 8.6 in all. Fused
+// products and clamps in pairs, as there, take as long), a row of its own by 3 us of latencies. Measured (GB300): bf16, top 20: 2000 rows of 2000 8.3 us (by
 // the other kernel 24), of 16,000 28.9 (39); fp32: 8000 of 19 10 us (37), of 1000 15.8 (66), of 4000 39 us for 128 MB (97).
 #include "token_logprobs.cuh"
 
@@ -21,8 +22,17 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 4, kCap = 128;  // rows of a CTA at most; keys of a list
-// Bytes of a row at most (bf16, top 5 and 20, by the other kernel and here: 15 rows of 43 KB 8.5 and 10.3 us, 8.9 and 9.3; 192 of 48 KB 11.2 and 15.0,
-// 9.7 and 10.4; 2000 of 32 KB 30.9 and 38.8, 27.4 and 28.8; of 64 KB 45.8 and 57.8, 57.7 and 59.8).
+// Bytes of a row at most: a rule on the bytes alone. Measured, bf16, us by the other kernel / here:
+//   rows, KB      top 0          top 1          top 5          top 20
+//   1 of 32       3.0 / 4.6      5.3 / 5.9      5.4 / 6.0      6.6 / 6.4
+//   4 of 43       3.0 / 5.4      5.5 / 6.8      6.4 / 7.0      8.4 / 7.5
+//   64 of 43      3.7 / 5.6      6.4 / 7.0      7.4 / 7.2      9.9 / 7.7
+//   192 of 43     6.1 / 6.6      9.4 / 7.9      9.6 / 8.2      14.1 / 8.6
+//   608 of 32     5.5 / 8.7      8.1 / 10.5     9.1 / 10.9     14.6 / 11.6
+//   2000 of 32    20.7 / 21.1    29.5 / 25.5    29.6 / 26.2    37.7 / 27.6
+//   2000 of 43    24.2 / 31.7    34.7 / 37.3    38.0 / 38.2    48.9 / 40.1
+// It gains with many of the best tokens and with hundreds of rows; few rows near the limit lose by it up to 1.3 us with the best token or five, and calls without
+// the best tokens up to 2.6, thousands of rows 7.5: there a rule on `top` too would choose the other kernel.
 constexpr int kRowBytes = 48 * 1024;
 
 __device__ __forceinline__ void copy16(void* to, const void* from) {
